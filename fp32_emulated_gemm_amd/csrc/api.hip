@@ -20,6 +20,7 @@
 
 #include "../../include/sgemm_emu.h"
 #include "launch.hpp"
+#include "ops.hpp"
 
 using namespace sgemm_emu_dev;
 
@@ -629,6 +630,71 @@ int gemm_noalloc(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, c
 }
 
 }  // namespace
+
+namespace sgemm_emu_dev {
+
+int current_cus(int *num_cus) { return current_device(num_cus); }
+
+// The N x K planes path of gemm_common for planes padded with zeros to a K
+// that is a multiple of 64 (16-byte aligned rows): 64 x 64 tiles or stream-K by
+// the same rules, A split into workspace planes for wide N, and a K tail that
+// the kernel masks in A.
+int gemm_padded_planes(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes,
+                       const float *bias, float *C, int64_t ldc, hipStream_t stream)
+{
+    int num_cus = 0, dev = 0, rc;
+    if ((rc = current_device(&num_cus, &dev)) != SGEMM_EMU_OK) return rc;
+    const int64_t kpad = (K + 63) / 64 * 64;
+    GemmArgs g{};
+    g.M = M; g.N = N; g.K = K; g.ka = K;
+    g.A = A; g.lda = lda;
+    g.B0 = planes; g.B1 = planes + N * kpad; g.B2 = planes + 2 * N * kpad; g.ldb = kpad;
+    g.C = C; g.ldc = ldc;
+    g.bias = bias;
+    g.act = SGEMM_EMU_ACT_NONE;
+    g.num_cus = num_cus;
+    g.splits = 1;
+    const int skg = gemm_streamk_grid(M, N, kpad, num_cus);
+    if (skg == 0 && gemm_tile64_pays(M, N, K, num_cus, false))
+        return launched(launch_gemm_tile64(g, 5, B_PLANES_NK, stream));
+#ifdef SGEMM_EMU_SERIAL_LDS
+    const bool presplit_a = false;
+#else
+    const bool presplit_a = skg == 0 && kpad == K && M >= kPresplitMinRows && N >= kPresplitAMinCols &&
+                            (uint64_t)M * (uint64_t)K <= kPresplitMaxElems;
+#endif
+    const size_t aplane = presplit_a ? ((size_t)M * (size_t)K * sizeof(uint16_t) + 255) & ~(size_t)255 : 0;
+    const size_t part = skg > 0 ? (size_t)skg * kSkSlotBytes : 0;
+    WsLease lease;
+    char *ws = nullptr;
+    if (aplane + part > 0) ws = (char *)acquire_workspace(dev, stream, 3 * aplane + part, lease);
+    if (ws == nullptr && skg > 0) return stream_capturing(stream) ? SGEMM_EMU_ECAPTURE : SGEMM_EMU_ENOMEM;
+    hipError_t e = hipSuccess;
+    if (ws != nullptr && presplit_a) {
+        uint16_t *Q0 = (uint16_t *)ws, *Q1 = (uint16_t *)(ws + aplane), *Q2 = (uint16_t *)(ws + 2 * aplane);
+        e = launch_split(M, K, A, lda, Q0, Q1, Q2, K, num_cus, stream, false);
+        if (e == hipSuccess) {
+            g.A0 = Q0; g.A1 = Q1; g.A2 = Q2; g.lda = K;
+            g.done = lease.event();
+            e = launch_gemm_planes(g, 5, stream);
+        }
+        lease.release(e == hipSuccess && g.done != nullptr);
+        return launched(e);
+    }
+    if (skg > 0) {
+        g.sk_grid = skg;
+        g.sk_flags = lease.flags;
+        g.sk_epoch = lease.epoch;
+        g.partials = (float *)ws;
+    }
+    g.K = kpad;
+    g.done = lease.event();
+    e = launch_gemm(g, 5, B_PLANES_NK, stream, false);
+    lease.release(e == hipSuccess && g.done != nullptr && launch_done_attached(g, B_PLANES_NK));
+    return launched(e);
+}
+
+}  // namespace sgemm_emu_dev
 
 extern "C" {
 

@@ -1,0 +1,550 @@
+// ops_api.hip -- the C ABI declared in include/sgemm_emu_ops.h: argument
+// validation, the workspace layouts, and the order of the kernels.
+//
+// As in api.hip every argument is checked before the first HIP call.  Scratch
+// memory is the caller's: each call lays its buffers out in `ws` with the same
+// code that its *_workspace function sizes them with (Carve).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/sgemm_emu_ops.h"
+#include "ops.hpp"
+
+using namespace sgemm_emu_dev;
+
+namespace {
+
+constexpr int64_t kMaxBytes = INT64_MAX / 8;
+constexpr int64_t kMaxLd = ((int64_t)1 << 32) / (128 * 4) - 64;   // as the GEMM's: 128-row tiles in 32-bit offsets
+constexpr int64_t kMaxExtent = 65535 * 64;                        // grid extents of 64-wide tiles
+constexpr int64_t kMaxAdapters = 65535;
+// Rows up to which the forward calls read the weight once, without tiles.
+constexpr int64_t kFewRows = 64;
+
+int64_t size_of(int dtype) { return dtype == SGEMM_EMU_F32 ? 4 : 2; }
+bool dtype_ok(int dtype) { return dtype == SGEMM_EMU_F32 || dtype == SGEMM_EMU_BF16; }
+bool extent_ok(int64_t v) { return v >= 0 && v <= kMaxExtent; }
+
+// A rows x cols operand: its leading dimension, extent, pointer and alignment.
+int check_operand(int dtype, int64_t rows, int64_t cols, const void *p, int64_t ld, bool optional = false)
+{
+    if (optional && p == nullptr) return SGEMM_EMU_OK;
+    if (ld < (cols > 1 ? cols : 1) || ld > kMaxLd) return SGEMM_EMU_EINVAL;
+    if (rows > 1 && cols > 0 && rows - 1 > (kMaxBytes - cols) / ld) return SGEMM_EMU_EINVAL;
+    if (rows > 0 && cols > 0 && p == nullptr) return SGEMM_EMU_ENULL;
+    if ((uintptr_t)p % (uintptr_t)size_of(dtype) != 0) return SGEMM_EMU_EINVAL;
+    return SGEMM_EMU_OK;
+}
+
+int check_vector(int64_t n, const void *p, int64_t elem, bool optional)
+{
+    if (p == nullptr) return optional || n == 0 ? SGEMM_EMU_OK : SGEMM_EMU_ENULL;
+    return (uintptr_t)p % (uintptr_t)elem != 0 ? SGEMM_EMU_EINVAL : SGEMM_EMU_OK;
+}
+
+#define CHECK(call)                                 \
+    do {                                            \
+        const int rc_ = (call);                     \
+        if (rc_ != SGEMM_EMU_OK) return rc_;        \
+    } while (0)
+
+#define LAUNCH(call)                                          \
+    do {                                                      \
+        if ((call) != hipSuccess) return SGEMM_EMU_ELAUNCH;   \
+    } while (0)
+
+// Lays buffers out one after another, 256-byte aligned; without a base it only
+// adds up their sizes.
+struct Carve {
+    char *base;
+    int64_t bytes = 0;
+    explicit Carve(void *ws) : base((char *)ws) {}
+    template <class T>
+    T *take(int64_t n)
+    {
+        T *const p = base != nullptr && n > 0 ? (T *)(base + bytes) : nullptr;
+        bytes += round_up(n * (int64_t)sizeof(T), 256);
+        return p;
+    }
+};
+
+int check_ws(const void *ws, int64_t ws_bytes, int64_t need)
+{
+    if (need == 0) return SGEMM_EMU_OK;
+    if (ws == nullptr) return SGEMM_EMU_ENULL;
+    if ((uintptr_t)ws % 256 != 0 || ws_bytes < need) return SGEMM_EMU_EINVAL;
+    return SGEMM_EMU_OK;
+}
+
+// bfloat16 operands that the GEMM reads as they lie.
+bool direct(const void *p, int64_t ld, int64_t K) { return K % 8 == 0 && ld % 8 == 0 && aligned(p, 16); }
+// The K that a bfloat16 product runs over: operands are padded copies unless K is a multiple of 8.
+int64_t bf16_k(int64_t K) { return K % 8 == 0 ? K : pad_k(K); }
+
+// C = A B^T + bias, FP32 through nine products.
+int product_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes,
+                const float *bias, float *C, int64_t ldc, int num_cus, hipStream_t stream)
+{
+    if (M == 0 || N == 0) return SGEMM_EMU_OK;
+    if (K == 0) {
+        LAUNCH(launch_zero(M, N, C, ldc, bias, SGEMM_EMU_ACT_NONE, num_cus, stream));
+        return SGEMM_EMU_OK;
+    }
+    return gemm_padded_planes(M, N, K, A, lda, planes, bias, C, ldc, stream);
+}
+
+// ---------------------------------------------------------------- gated projection
+
+int check_gated(int dtype, int64_t M, int64_t F, int64_t K, int gate)
+{
+    if (!dtype_ok(dtype) || !extent_ok(M) || !extent_ok(2 * F) || !extent_ok(K)) return SGEMM_EMU_EINVAL;
+    if (gate < SGEMM_EMU_GATE_SILU || gate > SGEMM_EMU_GATE_RELU) return SGEMM_EMU_EINVAL;
+    return SGEMM_EMU_OK;
+}
+
+// Few rows read W in one pass; pre-activations to keep come from the tiles.
+bool gated_few(int64_t M, int64_t K, const void *Z) { return M <= kFewRows && Z == nullptr && K > 0; }
+
+struct GatedWs {
+    uint16_t *plan, *x;   // W and X laid out
+    float *z;             // FP32 pre-activations
+    int64_t bytes;
+};
+GatedWs gated_ws(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                 const void *plan, const void *Z, void *ws)
+{
+    Carve c(ws);
+    GatedWs w{};
+    if (M == 0 || F == 0 || gated_few(M, K, Z)) return w;
+    if (dtype == SGEMM_EMU_F32) {
+        if (plan == nullptr) w.plan = c.take<uint16_t>(3 * 2 * F * pad_k(K));
+        if (Z == nullptr) w.z = c.take<float>(M * 2 * F);
+    } else {
+        if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(2 * F * pad_k(K));
+        if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
+    }
+    w.bytes = c.bytes;
+    return w;
+}
+
+struct GatedBackWs {
+    void *dz, *dzt;          // M x pad(2F), 2F x pad(M)
+    uint16_t *wt, *xt;       // W^T and X^T laid out
+    float *sums, *part_x, *part_w;
+    int64_t bytes;
+};
+GatedBackWs gated_back_ws(int dtype, int64_t M, int64_t F, int64_t K, int num_cus, void *ws)
+{
+    Carve c(ws);
+    GatedBackWs w{};
+    const int64_t size = size_of(dtype), comps = dtype == SGEMM_EMU_F32 ? 3 : 1, n2 = 2 * F;
+    w.dz = c.take<char>(M * pad_k(n2) * size);
+    w.dzt = c.take<char>(n2 * pad_k(M) * size);
+    w.wt = c.take<uint16_t>(comps * K * pad_k(n2));
+    w.xt = c.take<uint16_t>(comps * K * pad_k(M));
+    w.sums = c.take<float>(gate_tiles(M) * n2);
+    if (dtype == SGEMM_EMU_BF16) {
+        w.part_x = c.take<float>(bf16_gemm_partial_floats(M, K, pad_k(n2), true, num_cus));
+        w.part_w = c.take<float>(bf16_gemm_partial_floats(n2, K, pad_k(M), true, num_cus));
+    }
+    w.bytes = c.bytes;
+    return w;
+}
+
+// ---------------------------------------------------------------- adapters
+
+int check_adapters(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r)
+{
+    if (!dtype_ok(dtype) || !extent_ok(M) || !extent_ok(N) || !extent_ok(K) || !extent_ok(r)) return SGEMM_EMU_EINVAL;
+    if (n < 0 || n > kMaxAdapters) return SGEMM_EMU_EINVAL;
+    if (n > 0 && r > 0 && ((K > 0 && r > kMaxBytes / n / K) || (N > 0 && r > kMaxBytes / n / N))) return SGEMM_EMU_EINVAL;
+    return SGEMM_EMU_OK;
+}
+
+struct AdapterWs {
+    uint16_t *plan, *x;
+    float *s;
+    int64_t bytes;
+};
+AdapterWs adapter_ws(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, const void *W,
+                     int64_t ldw, const void *plan, int64_t n, int64_t r, const float *S, void *ws)
+{
+    Carve c(ws);
+    AdapterWs w{};
+    if (M == 0 || N == 0) return w;
+    if (n > 0 && r > 0 && S == nullptr) w.s = c.take<float>(M * rank_pad(r));
+    if (!(M <= kFewRows || K == 0)) {
+        if (dtype == SGEMM_EMU_F32) {
+            if (plan == nullptr) w.plan = c.take<uint16_t>(3 * N * pad_k(K));
+        } else {
+            if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(N * pad_k(K));
+            if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
+        }
+    }
+    w.bytes = c.bytes;
+    return w;
+}
+
+struct AdapterBackWs {
+    void *up_t, *down_t;       // n x r x N, n x K x r
+    float *p;                  // M x pad16(r)
+    uint16_t *dy;              // dY laid out
+    int32_t *offs, *rows;
+    float *part_down, *part_up;
+    int64_t bytes;
+};
+AdapterBackWs adapter_back_ws(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r, int num_cus, void *ws)
+{
+    Carve c(ws);
+    AdapterBackWs w{};
+    const int64_t size = size_of(dtype);
+    if (dtype == SGEMM_EMU_BF16) w.dy = c.take<uint16_t>(M * pad_k(N));
+    if (n > 0 && r > 0) {
+        w.up_t = c.take<char>(n * r * N * size);
+        w.down_t = c.take<char>(n * r * K * size);
+        w.p = c.take<float>(M * rank_pad(r));
+        w.offs = c.take<int32_t>(n + 1);
+        w.rows = c.take<int32_t>(M);
+        w.part_down = c.take<float>(lowrank_grad_floats(M, K, n, r, num_cus));
+        w.part_up = c.take<float>(lowrank_grad_floats(M, N, n, r, num_cus));
+    }
+    w.bytes = c.bytes;
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sgemm_emu_few_rows(void) { return (int)kFewRows; }
+
+int64_t sgemm_emu_plan_bytes(int dtype, int64_t rows, int64_t cols, int transposed)
+{
+    if (!dtype_ok(dtype) || !extent_ok(rows) || !extent_ok(cols) || (transposed != 0 && transposed != 1))
+        return SGEMM_EMU_EINVAL;
+    const int64_t comps = dtype == SGEMM_EMU_F32 ? 3 : 1;
+    return 2 * comps * (transposed ? cols * pad_k(rows) : rows * pad_k(cols));
+}
+
+int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, int64_t ldw, int transposed,
+                          void *plan, sgemm_emu_stream_t stream)
+{
+    const int64_t bytes = sgemm_emu_plan_bytes(dtype, rows, cols, transposed);
+    if (bytes < 0) return (int)bytes;
+    CHECK(check_operand(dtype, rows, cols, W, ldw));
+    if (bytes > 0 && plan == nullptr) return SGEMM_EMU_ENULL;
+    if ((uintptr_t)plan % 16 != 0) return SGEMM_EMU_EINVAL;
+    if (bytes == 0) return SGEMM_EMU_OK;
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    hipStream_t s = (hipStream_t)stream;
+    uint16_t *P = (uint16_t *)plan;
+    if (dtype == SGEMM_EMU_F32) {
+        if (transposed) {
+            const int64_t rp = pad_k(rows), plane = cols * rp;
+            LAUNCH(launch_split_transpose(rows, cols, (const float *)W, ldw, P, P + plane, P + 2 * plane, rp, num_cus,
+                                          s, false, rp));
+        } else {
+            LAUNCH(launch_split_padded(rows, cols, (const float *)W, ldw, P, s));
+        }
+    } else if (transposed) {
+        LAUNCH(launch_transpose_padded(rows, cols, (const uint16_t *)W, ldw, P, s));
+    } else {
+        LAUNCH(launch_copy_padded(rows, cols, (const uint16_t *)W, ldw, P, s));
+    }
+    return SGEMM_EMU_OK;
+}
+
+int64_t sgemm_emu_gated_linear_workspace(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx,
+                                         const void *W, int64_t ldw, const void *plan, const void *Z)
+{
+    CHECK(check_gated(dtype, M, F, K, SGEMM_EMU_GATE_SILU));
+    return gated_ws(dtype, M, F, K, X, ldx, W, ldw, plan, Z, nullptr).bytes;
+}
+
+int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *W,
+                           int64_t ldw, const void *plan, const void *bias, int gate, void *H, int64_t ldh, void *Z,
+                           int64_t ldz, void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream)
+{
+    CHECK(check_gated(dtype, M, F, K, gate));
+    CHECK(check_operand(dtype, M, K, X, ldx));
+    CHECK(check_operand(dtype, 2 * F, K, W, ldw));
+    CHECK(check_vector(2 * F, bias, size_of(dtype), true));
+    CHECK(check_operand(dtype, M, F, H, ldh));
+    CHECK(check_operand(dtype, M, 2 * F, Z, ldz, true));
+    if ((uintptr_t)plan % 16 != 0) return SGEMM_EMU_EINVAL;
+    const GatedWs w = gated_ws(dtype, M, F, K, X, ldx, W, ldw, plan, Z, ws);
+    CHECK(check_ws(ws, ws_bytes, w.bytes));
+    if (M == 0 || F == 0) return SGEMM_EMU_OK;
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    hipStream_t s = (hipStream_t)stream;
+    if (gated_few(M, K, Z)) {
+        FewRows a{};
+        a.M = M; a.N = F; a.K = K;
+        a.X = X; a.ldx = ldx; a.W = W; a.ldw = ldw;
+        a.bias = bias; a.gate = gate;
+        a.Y = H; a.ldy = ldh;
+        LAUNCH(launch_few_rows(dtype, a, num_cus, s));
+        return SGEMM_EMU_OK;
+    }
+    if (dtype == SGEMM_EMU_F32) {
+        if (w.plan != nullptr) LAUNCH(launch_split_padded(2 * F, K, (const float *)W, ldw, w.plan, s));
+        float *z = w.z != nullptr ? w.z : (float *)Z;
+        const int64_t ld = w.z != nullptr ? 2 * F : ldz;
+        CHECK(product_f32(M, 2 * F, K, (const float *)X, ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
+                          (const float *)bias, z, ld, num_cus, s));
+        LAUNCH(launch_gate(M, F, z, ld, gate, (float *)H, ldh, s));
+        return SGEMM_EMU_OK;
+    }
+    Bf16Gemm g{};
+    g.M = M; g.N = 2 * F; g.K = bf16_k(K);
+    g.A = (const uint16_t *)X; g.lda = ldx;
+    if (w.x != nullptr) {
+        LAUNCH(launch_copy_padded(M, K, (const uint16_t *)X, ldx, w.x, s));
+        g.A = w.x; g.lda = pad_k(K);
+    }
+    g.B = (const uint16_t *)W; g.ldb = ldw;
+    if (plan != nullptr) {
+        g.B = (const uint16_t *)plan; g.ldb = pad_k(K);
+    } else if (w.plan != nullptr) {
+        LAUNCH(launch_copy_padded(2 * F, K, (const uint16_t *)W, ldw, w.plan, s));
+        g.B = w.plan; g.ldb = pad_k(K);
+    }
+    g.bias = (const uint16_t *)bias;
+    g.C = (uint16_t *)H; g.ldc = ldh;
+    g.gate = gate;
+    g.Z = (uint16_t *)Z; g.ldz = ldz;
+    LAUNCH(launch_bf16_gemm(g, num_cus, s));
+    return SGEMM_EMU_OK;
+}
+
+int64_t sgemm_emu_gated_linear_backward_workspace(int dtype, int64_t M, int64_t F, int64_t K)
+{
+    CHECK(check_gated(dtype, M, F, K, SGEMM_EMU_GATE_SILU));
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    return gated_back_ws(dtype, M, F, K, num_cus, nullptr).bytes;
+}
+
+int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx,
+                                    const void *W, int64_t ldw, const void *Z, int64_t ldz, int gate, const void *dH,
+                                    int64_t lddh, void *dX, int64_t lddx, void *dW, int64_t lddw, void *dbias,
+                                    void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream)
+{
+    CHECK(check_gated(dtype, M, F, K, gate));
+    CHECK(check_operand(dtype, M, K, X, ldx, dW == nullptr));
+    CHECK(check_operand(dtype, 2 * F, K, W, ldw, dX == nullptr));
+    CHECK(check_operand(dtype, M, 2 * F, Z, ldz));
+    CHECK(check_operand(dtype, M, F, dH, lddh));
+    CHECK(check_operand(dtype, M, K, dX, lddx, true));
+    CHECK(check_operand(dtype, 2 * F, K, dW, lddw, true));
+    CHECK(check_vector(2 * F, dbias, size_of(dtype), true));
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    const GatedBackWs w = gated_back_ws(dtype, M, F, K, num_cus, ws);
+    CHECK(check_ws(ws, ws_bytes, w.bytes));
+    hipStream_t s = (hipStream_t)stream;
+    const int64_t n2 = 2 * F, n2p = pad_k(n2), mp = pad_k(M);
+    if (M > 0 && F > 0)
+        LAUNCH(launch_gate_backward(dtype, M, F, Z, ldz, dH, lddh, gate, dX != nullptr ? w.dz : nullptr, n2p,
+                                    dW != nullptr ? w.dzt : nullptr, dbias != nullptr ? w.sums : nullptr, s));
+    if (dbias != nullptr && F > 0) LAUNCH(launch_sum_tiles(dtype, gate_tiles(M), n2, w.sums, dbias, s));
+    if (dX != nullptr && M > 0 && K > 0) {
+        if (n2 > 0) CHECK(sgemm_emu_plan_weight(dtype, n2, K, W, ldw, 1, w.wt, stream));
+        if (dtype == SGEMM_EMU_F32) {
+            CHECK(product_f32(M, K, n2, (const float *)w.dz, n2p, w.wt, nullptr, (float *)dX, lddx, num_cus, s));
+        } else {
+            Bf16Gemm g{};
+            g.M = M; g.N = K; g.K = n2p;
+            g.A = (const uint16_t *)w.dz; g.lda = n2p;
+            g.B = w.wt; g.ldb = n2p;
+            g.C = (uint16_t *)dX; g.ldc = lddx;
+            g.gate = -1;
+            g.partials = w.part_x;
+            LAUNCH(launch_bf16_gemm(g, num_cus, s));
+        }
+    }
+    if (dW != nullptr && F > 0 && K > 0) {
+        if (M > 0) CHECK(sgemm_emu_plan_weight(dtype, M, K, X, ldx, 1, w.xt, stream));
+        if (dtype == SGEMM_EMU_F32) {
+            CHECK(product_f32(n2, K, M, (const float *)w.dzt, mp, w.xt, nullptr, (float *)dW, lddw, num_cus, s));
+        } else {
+            Bf16Gemm g{};
+            g.M = n2; g.N = K; g.K = mp;
+            g.A = (const uint16_t *)w.dzt; g.lda = mp;
+            g.B = w.xt; g.ldb = mp;
+            g.C = (uint16_t *)dW; g.ldc = lddw;
+            g.gate = -1;
+            g.partials = w.part_w;
+            LAUNCH(launch_bf16_gemm(g, num_cus, s));
+        }
+    }
+    return SGEMM_EMU_OK;
+}
+
+int64_t sgemm_emu_adapter_linear_workspace(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+                                           const void *W, int64_t ldw, const void *plan, int64_t n, int64_t r,
+                                           const float *S)
+{
+    CHECK(check_adapters(dtype, M, N, K, n, r));
+    return adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, S, nullptr).bytes;
+}
+
+int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, const void *W,
+                             int64_t ldw, const void *plan, const void *bias, int64_t n, int64_t r, const void *down,
+                             const void *up, const float *scale, const int32_t *ids, void *Y, int64_t ldy, float *S,
+                             void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream)
+{
+    CHECK(check_adapters(dtype, M, N, K, n, r));
+    CHECK(check_operand(dtype, M, K, X, ldx));
+    CHECK(check_operand(dtype, N, K, W, ldw));
+    CHECK(check_vector(N, bias, size_of(dtype), true));
+    CHECK(check_operand(dtype, M, N, Y, ldy));
+    const bool low = n > 0 && r > 0;
+    if (low) {
+        CHECK(check_vector(K, down, size_of(dtype), false));
+        CHECK(check_vector(N, up, size_of(dtype), false));
+        CHECK(check_vector(n, scale, 4, true));
+        CHECK(check_vector(M, ids, 4, false));
+        if ((uintptr_t)S % 16 != 0) return SGEMM_EMU_EINVAL;
+    }
+    if ((uintptr_t)plan % 16 != 0) return SGEMM_EMU_EINVAL;
+    const AdapterWs w = adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, S, ws);
+    CHECK(check_ws(ws, ws_bytes, w.bytes));
+    if (M == 0 || (N == 0 && (!low || S == nullptr))) return SGEMM_EMU_OK;
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    hipStream_t s = (hipStream_t)stream;
+    const Adapters ad{ids, n, r, down, up, scale};
+    if (low) {
+        if (S == nullptr) S = w.s;
+        LAUNCH(launch_shrink(dtype, M, K, X, ldx, ad, S, num_cus, s));
+        if (N == 0) return SGEMM_EMU_OK;
+    }
+    if (M <= kFewRows || K == 0) {
+        FewRows a{};
+        a.M = M; a.N = N; a.K = K;
+        a.X = X; a.ldx = ldx; a.W = W; a.ldw = ldw;
+        a.bias = bias; a.gate = -1;
+        a.Y = Y; a.ldy = ldy;
+        a.ad = low ? &ad : nullptr;
+        a.S = low ? S : nullptr;
+        LAUNCH(launch_few_rows(dtype, a, num_cus, s));
+        return SGEMM_EMU_OK;
+    }
+    if (dtype == SGEMM_EMU_F32) {
+        if (w.plan != nullptr) LAUNCH(launch_split_padded(N, K, (const float *)W, ldw, w.plan, s));
+        CHECK(product_f32(M, N, K, (const float *)X, ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
+                          (const float *)bias, (float *)Y, ldy, num_cus, s));
+        if (low) LAUNCH(launch_expand(dtype, M, N, S, ad, Y, ldy, num_cus, s));
+        return SGEMM_EMU_OK;
+    }
+    Bf16Gemm g{};
+    g.M = M; g.N = N; g.K = bf16_k(K);
+    g.A = (const uint16_t *)X; g.lda = ldx;
+    if (w.x != nullptr) {
+        LAUNCH(launch_copy_padded(M, K, (const uint16_t *)X, ldx, w.x, s));
+        g.A = w.x; g.lda = pad_k(K);
+    }
+    g.B = (const uint16_t *)W; g.ldb = ldw;
+    if (plan != nullptr) {
+        g.B = (const uint16_t *)plan; g.ldb = pad_k(K);
+    } else if (w.plan != nullptr) {
+        LAUNCH(launch_copy_padded(N, K, (const uint16_t *)W, ldw, w.plan, s));
+        g.B = w.plan; g.ldb = pad_k(K);
+    }
+    g.bias = (const uint16_t *)bias;
+    g.C = (uint16_t *)Y; g.ldc = ldy;
+    g.gate = -1;
+    if (low) {
+        g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
+        g.up = (const uint16_t *)up;
+        g.S = S;
+    }
+    LAUNCH(launch_bf16_gemm(g, num_cus, s));
+    return SGEMM_EMU_OK;
+}
+
+int64_t sgemm_emu_adapter_linear_backward_workspace(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r)
+{
+    CHECK(check_adapters(dtype, M, N, K, n, r));
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    return adapter_back_ws(dtype, M, N, K, n, r, num_cus, nullptr).bytes;
+}
+
+int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+                                      const void *plan_t, int64_t n, int64_t r, const void *down, const void *up,
+                                      const float *scale, const int32_t *ids, const float *S, const void *dY,
+                                      int64_t lddy, void *dX, int64_t lddx, void *d_down, void *d_up, void *ws,
+                                      int64_t ws_bytes, sgemm_emu_stream_t stream)
+{
+    CHECK(check_adapters(dtype, M, N, K, n, r));
+    const bool low = n > 0 && r > 0;
+    CHECK(check_operand(dtype, M, K, X, ldx, d_down == nullptr));
+    CHECK(check_operand(dtype, M, N, dY, lddy));
+    CHECK(check_operand(dtype, M, K, dX, lddx, true));
+    if (dX != nullptr && M > 0 && N > 0 && K > 0 && plan_t == nullptr) return SGEMM_EMU_ENULL;
+    if ((uintptr_t)plan_t % 16 != 0) return SGEMM_EMU_EINVAL;
+    if (low) {
+        CHECK(check_vector(K, down, size_of(dtype), false));
+        CHECK(check_vector(N, up, size_of(dtype), false));
+        CHECK(check_vector(n, scale, 4, true));
+        CHECK(check_vector(M, ids, 4, false));
+        CHECK(check_vector(M, S, 16, d_up == nullptr));
+        CHECK(check_vector(K, d_down, size_of(dtype), true));
+        CHECK(check_vector(N, d_up, size_of(dtype), true));
+    }
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    const AdapterBackWs w = adapter_back_ws(dtype, M, N, K, n, r, num_cus, ws);
+    CHECK(check_ws(ws, ws_bytes, w.bytes));
+    hipStream_t s = (hipStream_t)stream;
+    // P = scale up^T dY is the shrink of dY by the transposed up factors, and dX
+    // the forward of dY through W^T with the factors' roles exchanged.
+    const Adapters back{ids, n, r, w.up_t, w.down_t, scale};
+    const bool need_dx = dX != nullptr && M > 0 && K > 0, need_down = low && d_down != nullptr && K > 0,
+               need_up = low && d_up != nullptr && N > 0;
+    if (low && M > 0 && (need_dx || need_down)) {
+        if (N > 0) LAUNCH(launch_transpose_bank(dtype, n, N, r, up, w.up_t, s));
+        LAUNCH(launch_shrink(dtype, M, N, dY, lddy, back, w.p, num_cus, s));
+    }
+    if (need_dx) {
+        if (low) LAUNCH(launch_transpose_bank(dtype, n, r, K, down, w.down_t, s));
+        if (dtype == SGEMM_EMU_F32) {
+            CHECK(product_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, nullptr, (float *)dX, lddx,
+                              num_cus, s));
+            if (low) LAUNCH(launch_expand(dtype, M, K, w.p, back, dX, lddx, num_cus, s));
+        } else {
+            Bf16Gemm g{};
+            g.M = M; g.N = K; g.K = bf16_k(N);
+            g.A = (const uint16_t *)dY; g.lda = lddy;
+            if (!direct(dY, lddy, N)) {
+                if (N > 0) LAUNCH(launch_copy_padded(M, N, (const uint16_t *)dY, lddy, w.dy, s));
+                g.A = w.dy; g.lda = pad_k(N);
+            }
+            g.B = (const uint16_t *)plan_t; g.ldb = pad_k(N);
+            g.C = (uint16_t *)dX; g.ldc = lddx;
+            g.gate = -1;
+            if (low) {
+                g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
+                g.up = (const uint16_t *)w.down_t;
+                g.S = w.p;
+            }
+            LAUNCH(launch_bf16_gemm(g, num_cus, s));
+        }
+    }
+    if (need_down || need_up) {
+        LAUNCH(launch_group(M, ids, n, w.offs, w.rows, s));
+        if (need_down)
+            LAUNCH(launch_lowrank_grad(dtype, M, K, n, r, w.p, X, ldx, w.offs, w.rows, false, d_down, w.part_down,
+                                       num_cus, s));
+        if (need_up)
+            LAUNCH(launch_lowrank_grad(dtype, M, N, n, r, S, dY, lddy, w.offs, w.rows, true, d_up, w.part_up, num_cus,
+                                       s));
+    }
+    return SGEMM_EMU_OK;
+}
+
+}  // extern "C"

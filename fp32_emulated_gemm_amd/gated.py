@@ -1,0 +1,170 @@
+"""The gated feed-forward projection of a transformer block (forward, input and
+parameter gradients), for float32 tensors on the emulated GEMM and for bfloat16
+tensors:
+
+    H = act(Z[:, :F]) * Z[:, F:],   Z = X W^T + bias,
+
+W [2F, K]: the gate's F rows, then the up projection's F rows.  Both projections,
+the activation and the product are one call (sgemm_emu_gated_linear); the
+backward pass (sgemm_emu_gated_linear_backward) is deterministic.
+"""
+import torch
+
+from . import ops
+from .linear import Linear
+from .ops import GATES, WeightPlan, addr, check_tensor, current_stream, ok, ops_lib, rows_of, scratch
+
+
+def plan_weight(weight, backward=False):
+    """The layout of a fixed weight for gated_linear's `plan` (see ops.WeightPlan)."""
+    return WeightPlan(weight, backward=backward)
+
+
+def _forward(x, xld, weight, wld, bias, gate, plan, keep):
+    """H and, with `keep`, the pre-activations Z."""
+    L = ops_lib()
+    dt = ops.DTYPES[x.dtype]
+    (M, K), F = x.shape, weight.shape[0] // 2
+    h = torch.empty((M, F), dtype=x.dtype, device=x.device)
+    z = torch.empty((M, 2 * F), dtype=x.dtype, device=x.device) if keep else None
+    fwd = None if plan is None else addr(plan.forward)
+    xp, wp, zp, ws, nws = addr(x), addr(weight), addr(z), None, 0
+    if M > ops.FEW_ROWS or keep or K == 0:
+        ws, nws = scratch(ok(L.sgemm_emu_gated_linear_workspace(dt, M, F, K, xp, xld, wp, wld, fwd, zp),
+                             "sgemm_emu_gated_linear_workspace"), x.device)
+    ok(L.sgemm_emu_gated_linear(dt, M, F, K, xp, xld, wp, wld, fwd, addr(bias), gate, addr(h), max(F, 1), zp,
+                                max(2 * F, 1), addr(ws), nws, current_stream()), "sgemm_emu_gated_linear")
+    return h, z
+
+
+class _GatedFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, gate, plan):
+        x, xld = rows_of(x)
+        weight, wld = rows_of(weight)
+        bias = None if bias is None else bias.contiguous()
+        h, z = _forward(x, xld, weight, wld, bias, gate, plan, True)
+        ctx.save_for_backward(x, weight, z)
+        ctx.gate, ctx.has_bias = gate, bias is not None
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        x, weight, z = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        L = ops_lib()
+        dt = ops.DTYPES[x.dtype]
+        (M, K), F = x.shape, weight.shape[0] // 2
+        (x, xld), (weight, wld), (dh, dhld) = rows_of(x), rows_of(weight), rows_of(dh)
+        dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if need_x else None
+        dw = torch.empty((2 * F, K), dtype=x.dtype, device=x.device) if need_w else None
+        db = torch.empty((2 * F,), dtype=x.dtype, device=x.device) if need_b and ctx.has_bias else None
+        ws, nws = scratch(ok(L.sgemm_emu_gated_linear_backward_workspace(dt, M, F, K),
+                             "sgemm_emu_gated_linear_backward_workspace"), x.device)
+        ok(L.sgemm_emu_gated_linear_backward(dt, M, F, K, addr(x), xld, addr(weight), wld, addr(z), max(2 * F, 1),
+                                             ctx.gate, addr(dh), dhld, addr(dx), max(K, 1), addr(dw), max(K, 1),
+                                             addr(db), addr(ws), nws, current_stream()),
+           "sgemm_emu_gated_linear_backward")
+        return dx, dw, db, None, None
+
+
+def gated_linear(x, weight, bias=None, gate="silu", plan=None):
+    """act(x Wg^T + bg) * (x Wu^T + bu) for x[..., K], weight[2F, K] = [Wg; Wu], bias[2F] or None,
+    all float32 or all bfloat16 on the current HIP device.  gate: "silu", "gelu" (exact), "gelu_tanh",
+    "sigmoid" or "relu".  `plan` (plan_weight(weight)) spares laying out a weight that does not change.
+    Differentiable in x, weight and bias."""
+    if gate not in GATES:
+        raise ValueError(f"unknown gate {gate!r} (one of {', '.join(GATES)})")
+    if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
+        raise TypeError("gated_linear expects torch tensors")
+    if x.dtype not in ops.DTYPES:
+        raise TypeError(f"x: expected dtype float32 or bfloat16, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x: expected at least one dimension")
+    check_tensor(weight, "weight", x.dtype, (None, x.shape[-1]))
+    if weight.shape[0] % 2 != 0:
+        raise ValueError(f"weight: expected an even number of rows (gate, then up), got {weight.shape[0]}")
+    x2d = x if x.dim() == 2 else x.reshape(-1, x.shape[-1]) if x.shape[-1] else x.new_empty(x.shape[:-1].numel(), 0)
+    check_tensor(x2d, "x", x.dtype, (None, None))
+    if bias is not None:
+        check_tensor(bias, "bias", x.dtype, (weight.shape[0],))
+    if plan is not None:
+        plan.check(weight)
+    ops_lib()
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad
+                                    or (bias is not None and bias.requires_grad)):
+        h = _GatedFn.apply(x2d, weight, bias, GATES[gate], plan)
+    else:
+        (xr, xld), (wr, wld) = rows_of(x2d), rows_of(weight)
+        h, _ = _forward(xr, xld, wr, wld, None if bias is None else bias.contiguous(), GATES[gate], plan, False)
+    return h if x.dim() == 2 else h.reshape(*x.shape[:-1], weight.shape[0] // 2)
+
+
+class GatedLinear(torch.nn.Module):
+    """gated_linear as a module: `weight` [2 out_features, in_features] (gate rows, then up rows) and
+    `bias` [2 out_features], trainable.  fix_weights() freezes them and keeps their layout."""
+
+    def __init__(self, in_features, out_features, bias=True, gate="silu", device=None, dtype=None):
+        super().__init__()
+        if gate not in GATES:
+            raise ValueError(f"unknown gate {gate!r} (one of {', '.join(GATES)})")
+        self.in_features, self.out_features, self.gate = in_features, out_features, gate
+        self.weight = torch.nn.Parameter(torch.empty((2 * out_features, in_features), device=device, dtype=dtype))
+        self.bias = torch.nn.Parameter(torch.zeros(2 * out_features, device=device, dtype=dtype)) if bias else None
+        self._plan = None
+        bound = in_features ** -0.5 if in_features else 0.0
+        torch.nn.init.uniform_(self.weight, -bound, bound)
+
+    @classmethod
+    def from_linears(cls, gate_proj, up_proj, gate="silu"):
+        """From two torch.nn.Linear layers of one shape: act(gate_proj(x)) * up_proj(x)."""
+        if gate_proj.weight.shape != up_proj.weight.shape or (gate_proj.bias is None) != (up_proj.bias is None):
+            raise ValueError("gate_proj and up_proj differ in shape or bias")
+        m = cls(gate_proj.in_features, gate_proj.out_features, gate_proj.bias is not None, gate,
+                gate_proj.weight.device, gate_proj.weight.dtype)
+        with torch.no_grad():
+            m.weight.copy_(torch.cat((gate_proj.weight, up_proj.weight)))
+            if m.bias is not None:
+                m.bias.copy_(torch.cat((gate_proj.bias, up_proj.bias)))
+        return m
+
+    def fix_weights(self):
+        """Freeze the parameters and lay the weight out once for the calls to come."""
+        for p in self.parameters():
+            p.requires_grad_(False)
+        self._plan = (plan_weight(self.weight), self.weight._version)
+        return self
+
+    def forward(self, x):
+        plan = None
+        if self._plan is not None:
+            plan, version = self._plan
+            if version != self.weight._version or plan.device != self.weight.device:
+                raise RuntimeError("the weight changed after fix_weights(); call it again")
+        return gated_linear(x, self.weight, self.bias, self.gate, plan)
+
+    def extra_repr(self):
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"bias={self.bias is not None}, gate={self.gate}")
+
+
+class GatedFeedForward(torch.nn.Module):
+    """A float32 feed-forward block on the emulated GEMM: GatedLinear, then a fixed-weight Linear
+    (down projection)."""
+
+    def __init__(self, features, hidden, bias=True, gate="silu", device=None):
+        super().__init__()
+        self.up = GatedLinear(features, hidden, bias, gate, device, torch.float32)
+        self.down = Linear(hidden, features, bias, device=device)
+
+    @classmethod
+    def from_linears(cls, gate_proj, up_proj, down_proj, gate="silu"):
+        m = cls.__new__(cls)
+        torch.nn.Module.__init__(m)
+        m.up = GatedLinear.from_linears(gate_proj, up_proj, gate)
+        m.down = Linear.from_linear(down_proj)
+        return m
+
+    def forward(self, x):
+        return self.down(self.up(x))

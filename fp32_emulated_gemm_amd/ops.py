@@ -1,0 +1,144 @@
+"""Python binding of the operators in ``include/sgemm_emu_ops.h``: the gated
+feed-forward projection and the linear layer with low-rank adapters.
+
+Thin ctypes marshalling with the C names and argument order; every step runs in
+the library's HIP kernels.  The tensor functions that check their arguments,
+allocate outputs and differentiate are in ``gated`` and ``adapters``.
+"""
+import ctypes
+
+import torch
+
+from . import SgemmEmuError, lib
+
+SGEMM_EMU_F32 = 0
+SGEMM_EMU_BF16 = 1
+SGEMM_EMU_GATE_SILU = 0
+SGEMM_EMU_GATE_GELU = 1        # exact (erf) form
+SGEMM_EMU_GATE_GELU_TANH = 2
+SGEMM_EMU_GATE_SIGMOID = 3
+SGEMM_EMU_GATE_RELU = 4
+
+DTYPES = {torch.float32: SGEMM_EMU_F32, torch.bfloat16: SGEMM_EMU_BF16}
+GATES = {"silu": SGEMM_EMU_GATE_SILU, "gelu": SGEMM_EMU_GATE_GELU, "gelu_tanh": SGEMM_EMU_GATE_GELU_TANH,
+         "sigmoid": SGEMM_EMU_GATE_SIGMOID, "relu": SGEMM_EMU_GATE_RELU}
+
+OPS_EXPORTS = ("sgemm_emu_plan_bytes", "sgemm_emu_plan_weight", "sgemm_emu_gated_linear_workspace",
+               "sgemm_emu_gated_linear", "sgemm_emu_gated_linear_backward_workspace",
+               "sgemm_emu_gated_linear_backward", "sgemm_emu_adapter_linear_workspace", "sgemm_emu_adapter_linear",
+               "sgemm_emu_adapter_linear_backward_workspace", "sgemm_emu_adapter_linear_backward",
+               "sgemm_emu_few_rows")
+
+_OPS = None
+FEW_ROWS = None   # sgemm_emu_few_rows(), set when the library is first used
+
+
+def ops_lib():
+    """The library with the operators' signatures set (once)."""
+    global _OPS, FEW_ROWS
+    if _OPS is None:
+        L = lib()
+        i64, vp, ci = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
+        dims3 = [ci, i64, i64, i64]
+        L.sgemm_emu_plan_bytes.argtypes = [ci, i64, i64, ci]
+        L.sgemm_emu_plan_weight.argtypes = [ci, i64, i64, vp, i64, ci, vp, vp]
+        L.sgemm_emu_gated_linear_workspace.argtypes = dims3 + [vp, i64, vp, i64, vp, vp]
+        L.sgemm_emu_gated_linear.argtypes = dims3 + [vp, i64, vp, i64, vp, vp, ci, vp, i64, vp, i64, vp, i64, vp]
+        L.sgemm_emu_gated_linear_backward_workspace.argtypes = dims3
+        L.sgemm_emu_gated_linear_backward.argtypes = dims3 + [vp, i64, vp, i64, vp, i64, ci, vp, i64, vp, i64, vp,
+                                                              i64, vp, vp, i64, vp]
+        L.sgemm_emu_adapter_linear_workspace.argtypes = dims3 + [vp, i64, vp, i64, vp, i64, i64, vp]
+        L.sgemm_emu_adapter_linear.argtypes = dims3 + [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64,
+                                                       vp, vp, i64, vp]
+        L.sgemm_emu_adapter_linear_backward_workspace.argtypes = dims3 + [i64, i64]
+        L.sgemm_emu_adapter_linear_backward.argtypes = dims3 + [vp, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp, i64,
+                                                                vp, i64, vp, vp, vp, i64, vp]
+        L.sgemm_emu_few_rows.argtypes = []
+        for name in OPS_EXPORTS:
+            getattr(L, name).restype = i64 if name.endswith(("_workspace", "_bytes")) else ci
+        FEW_ROWS = L.sgemm_emu_few_rows()
+        _OPS = L
+    return _OPS
+
+
+def ok(status, where):
+    """Raise SgemmEmuError for a negative status or size; else return it."""
+    if status < 0:
+        raise SgemmEmuError(int(status), where)
+    return status
+
+
+# ---------------------------------------------------------------- tensor arguments
+
+def check_tensor(t, name, dtype, shape):
+    """A tensor of `dtype` and `shape` (None: any extent) on the current HIP device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected shape {tuple('any' if w is None else w for w in shape)}, "
+                         f"got {tuple(t.shape)}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current HIP device, got {t.device}")
+
+
+def rows_of(t):
+    """A 2-D tensor whose rows lie one after another with unit stride along columns (itself, or a
+    contiguous copy of a transposed, expanded or overlapping one), and its leading dimension."""
+    rows, cols = t.shape
+    ld = t.stride(0)
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and ld < cols):
+        t = t.contiguous()
+        ld = cols
+    return t, max(ld, cols, 1)
+
+
+def scratch(nbytes, device):
+    """Workspace of a call and its size: torch's allocator keeps it in the stream's order."""
+    if nbytes == 0:
+        return None, 0
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+
+
+def addr(t):
+    return None if t is None else t.data_ptr() or None
+
+
+def current_stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+class WeightPlan:
+    """A weight laid out for the products (sgemm_emu_plan_weight): `forward` holds W (None where a
+    bfloat16 weight is read as it lies), `backward` W^T (None unless asked for).  It holds the
+    values of the weight at the time: lay a changed weight out again."""
+
+    __slots__ = ("dtype", "shape", "device", "forward", "backward")
+
+    def __init__(self, weight, forward=True, backward=False):
+        w = weight.detach()
+        if w.dtype not in DTYPES:
+            raise TypeError(f"weight: expected dtype float32 or bfloat16, got {w.dtype}")
+        check_tensor(w, "weight", w.dtype, (None, None))
+        w, ld = rows_of(w)
+        self.dtype, self.shape, self.device = w.dtype, tuple(w.shape), w.device
+        # a bfloat16 weight with 16-byte aligned rows needs no layout for the forward product
+        lies = w.dtype == torch.bfloat16 and w.shape[1] % 8 == 0 and ld % 8 == 0 and w.data_ptr() % 16 == 0
+        self.forward = self._lay_out(w, ld, 0) if forward and not lies else None
+        self.backward = self._lay_out(w, ld, 1) if backward else None
+
+    @staticmethod
+    def _lay_out(w, ld, transposed):
+        L, dt = ops_lib(), DTYPES[w.dtype]
+        rows, cols = w.shape
+        nbytes = ok(L.sgemm_emu_plan_bytes(dt, rows, cols, transposed), "sgemm_emu_plan_bytes")
+        plan = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=w.device)
+        ok(L.sgemm_emu_plan_weight(dt, rows, cols, addr(w), ld, transposed, plan.data_ptr(), current_stream()),
+           "sgemm_emu_plan_weight")
+        return plan
+
+    def check(self, weight):
+        if self.dtype != weight.dtype or self.shape != tuple(weight.shape) or self.device != weight.device:
+            raise ValueError(f"plan: laid out for a {self.dtype} weight of shape {self.shape} on {self.device}, got "
+                             f"{weight.dtype} {tuple(weight.shape)} on {weight.device}")
