@@ -27,12 +27,10 @@ def _forward(x, xld, weight, wld, a, b, ids, scale, bias, plan, keep):
     (M, K), N, (n, r) = x.shape, weight.shape[0], a.shape[:2]
     y = torch.empty((M, N), dtype=x.dtype, device=x.device)
     low = n > 0 and r > 0
-    few = M <= ops.FEW_ROWS
-    s = torch.empty((M, -(-r // 16) * 16), dtype=torch.float32, device=x.device) if low and (keep or few) else None
+    s = torch.empty((M, -(-r // 16) * 16), dtype=torch.float32, device=x.device) if low and keep else None
     fwd = None if plan is None else addr(plan.forward)
-    xp, wp, sp, ws, nws = addr(x), addr(weight), addr(s), None, 0
-    if not few:
-        ws, nws = scratch(ok(L.sgemm_emu_adapter_linear_workspace(dt, M, N, K, xp, xld, wp, wld, fwd, n, r, sp),
+    xp, wp, sp = addr(x), addr(weight), addr(s)
+    ws, nws = scratch(ok(L.sgemm_emu_adapter_linear_workspace(dt, M, N, K, xp, xld, wp, wld, fwd, n, r, sp),
                              "sgemm_emu_adapter_linear_workspace"), x.device)
     ok(L.sgemm_emu_adapter_linear(dt, M, N, K, xp, xld, wp, wld, fwd, addr(bias), n, r, addr(a), addr(b), addr(scale),
                                   addr(ids), addr(y), max(N, 1), sp, addr(ws), nws, current_stream()),

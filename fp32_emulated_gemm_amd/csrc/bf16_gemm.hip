@@ -101,107 +101,101 @@ __device__ __forceinline__ void mfma_part(f32x16_t (&acc)[T::NI][T::MI], const F
 }
 
 // Add the adapters' part: acc[n][m] += up[i][n][:] . S[m][:] for the rows m of
-// adapter i, one adapter of the wave's rows after another (ascending ids).
-// S is split into two BF16 parts (16 significant bits; the rest lies 2^-8 below
-// the output's own rounding), up is exact.  A lane keeps its old value unless
-// its row belongs to the adapter, so Inf or NaN in one adapter's weights never
-// reach another's rows.
+// adapter i, one adapter of the wave's rows after another (in order of their
+// first row).  S comes in two BF16 parts (16 significant bits; the rest lies
+// 2^-8 below the output's own rounding), up is exact.  A lane keeps its old
+// value unless its row belongs to the adapter: zero times Inf or NaN in one
+// adapter's weights never reaches another's rows.
 template <class T>
 __device__ __forceinline__ void add_adapters(f32x16_t (&acc)[T::NI][T::MI], const Bf16Gemm &g, int64_t m0w,
                                              int64_t n0w, int lane)
 {
     int id[T::MI];
-    int64_t row[T::MI];
+    const uint16_t *srow[T::MI], *urow[T::NI];
+    uint32_t todo[T::MI];
 #pragma unroll
     for (int i = 0; i < T::MI; ++i) {
         const int64_t m = m0w + i * 32 + (lane & 31);
-        row[i] = lmin(m, g.M - 1);
+        srow[i] = g.S + lmin(m, g.M - 1) * 2 * g.rp + 8 * (lane >> 5);
         const int v = m < g.M ? g.ids[m] : -1;
         id[i] = v >= 0 && v < g.n ? v : -1;
+        todo[i] = (uint32_t)__ballot(id[i] >= 0);
     }
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j)
+        urow[j] = g.up + lmin(n0w + j * 32 + (lane & 31), g.N - 1) * g.r + 8 * (lane >> 5);
     const bool vec = g.r % 8 == 0 && ((uintptr_t)g.up % 16) == 0;
-    int last = -1;
     for (;;) {
-        int next = 0x7FFFFFFF;
+        int me = -1;
 #pragma unroll
-        for (int i = 0; i < T::MI; ++i)
-            if (id[i] > last && id[i] < next) next = id[i];
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) next = imin(next, __shfl_xor(next, s));
-        next = __builtin_amdgcn_readfirstlane(next);
-        if (next == 0x7FFFFFFF) break;
-        last = next;
+        for (int i = T::MI - 1; i >= 0; --i)
+            if (todo[i] != 0) me = __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo[i]));
+        if (me < 0) break;
+        bool own[T::MI];
 #pragma unroll
         for (int i = 0; i < T::MI; ++i) {
-            f32x16_t add[T::NI];
+            own[i] = id[i] == me;
+            todo[i] &= ~(uint32_t)__ballot(own[i]);
+        }
+        const int64_t bank = (int64_t)me * g.N * g.r;
+        for (int64_t rc = 0; rc < g.rp; rc += 16) {
+            u32x4_t up[T::NI], hi[T::MI], lo[T::MI];
 #pragma unroll
-            for (int j = 0; j < T::NI; ++j) add[j] = acc[j][i];
-            for (int64_t rc = 0; rc < g.rp; rc += 16) {
+            for (int j = 0; j < T::NI; ++j) {
+                const uint16_t *p = urow[j] + bank + rc;
                 const int64_t r0 = rc + 8 * (lane >> 5);
-                const f32x4_t *s = reinterpret_cast<const f32x4_t *>(g.S + row[i] * g.rp + r0);
-                const f32x4_t s0 = s[0], s1 = s[1];
-                uint16_t hi[8], lo[8];
+                up[j] = u32x4_t{0, 0, 0, 0};
+                if (vec) {
+                    if (r0 < g.r) up[j] = *reinterpret_cast<const u32x4_t *>(p);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    split_hi_lo(s0[e], hi[e], lo[e]);
-                    split_hi_lo(s1[e], hi[4 + e], lo[4 + e]);
-                }
-                u32x4_t vh, vl;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    vh[e] = (uint32_t)hi[2 * e] | ((uint32_t)hi[2 * e + 1] << 16);
-                    vl[e] = (uint32_t)lo[2 * e] | ((uint32_t)lo[2 * e + 1] << 16);
-                }
-#pragma unroll
-                for (int j = 0; j < T::NI; ++j) {
-                    const int64_t n = lmin(n0w + j * 32 + (lane & 31), g.N - 1);
-                    const uint16_t *p = g.up + ((int64_t)next * g.N + n) * g.r + r0;
-                    u32x4_t v = {0, 0, 0, 0};
-                    if (vec) {
-                        if (r0 < g.r) v = *reinterpret_cast<const u32x4_t *>(p);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (r0 + e < g.r) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
-                    }
-                    const bf16x8_t up = __builtin_bit_cast(bf16x8_t, v);
-                    add[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(up, __builtin_bit_cast(bf16x8_t, vl), add[j], 0,
-                                                                     0, 0);
-                    add[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(up, __builtin_bit_cast(bf16x8_t, vh), add[j], 0,
-                                                                     0, 0);
+                    for (int e = 0; e < 8; ++e)
+                        if (r0 + e < g.r) up[j][e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
                 }
             }
 #pragma unroll
-            for (int j = 0; j < T::NI; ++j)
+            for (int i = 0; i < T::MI; ++i) {
+                hi[i] = *reinterpret_cast<const u32x4_t *>(srow[i] + rc);
+                lo[i] = *reinterpret_cast<const u32x4_t *>(srow[i] + g.rp + rc);
+            }
 #pragma unroll
-                for (int q = 0; q < 16; ++q) acc[j][i][q] = id[i] == last ? add[j][q] : acc[j][i][q];
+            for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+                for (int j = 0; j < T::NI; ++j) {
+                    const bf16x8_t u = __builtin_bit_cast(bf16x8_t, up[j]);
+                    f32x16_t t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u, __builtin_bit_cast(bf16x8_t, lo[i]),
+                                                                         acc[j][i], 0, 0, 0);
+                    t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u, __builtin_bit_cast(bf16x8_t, hi[i]), t, 0, 0, 0);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) acc[j][i][q] = own[i] ? t[q] : acc[j][i][q];
+                }
         }
     }
 }
 
 // One wave's TM x W block of BF16 results in LDS (rows of PITCH elements) ->
 // rows m0w.., columns c0.. of a matrix of `cols` columns: 128-bit stores where
-// the matrix allows them.
+// the matrix allows them, else a row's elements by consecutive lanes.
 template <class T, int W>
 __device__ __forceinline__ void flush_block(const uint16_t *buf, uint16_t *out, int64_t ld, int64_t M, int64_t cols,
                                             int64_t m0w, int64_t c0, int lane)
 {
-    constexpr int PER_ROW = W / 8, ROWS = 64 / PER_ROW;            // lanes per row, rows per pass
-    const bool vec = ((uintptr_t)out % 16) == 0 && ld % 8 == 0;
-    const int64_t c = c0 + (lane % PER_ROW) * 8;
+    if (((uintptr_t)out % 16) == 0 && ld % 8 == 0 && c0 + W <= cols) {
+        constexpr int PER_ROW = W / 8, ROWS = 64 / PER_ROW;        // lanes per row, rows per pass
 #pragma unroll 4
-    for (int p = 0; p < T::TM / ROWS; ++p) {
-        const int row = p * ROWS + lane / PER_ROW;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(buf + row * T::PITCH + (lane % PER_ROW) * 8);
-        const int64_t m = m0w + row;
-        if (m >= M) continue;
-        uint16_t *dst = out + m * ld + c;
-        if (vec && c + 8 <= cols) {
-            *reinterpret_cast<u32x4_t *>(dst) = v;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < cols) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        for (int p = 0; p < T::TM / ROWS; ++p) {
+            const int row = p * ROWS + lane / PER_ROW, c = (lane % PER_ROW) * 8;
+            const u32x4_t v = *reinterpret_cast<const u32x4_t *>(buf + row * T::PITCH + c);
+            if (m0w + row < M) *reinterpret_cast<u32x4_t *>(out + (m0w + row) * ld + c0 + c) = v;
+        }
+    } else {
+        constexpr int ROWS = 64 / W;
+        const int c = lane % W;
+#pragma unroll 8
+        for (int p = 0; p < T::TM / ROWS; ++p) {
+            const int row = p * ROWS + lane / W;
+            const uint16_t v = buf[row * T::PITCH + c];
+            if (m0w + row < M && c0 + c < cols) out[(m0w + row) * ld + c0 + c] = v;
         }
     }
 }
@@ -350,21 +344,22 @@ __device__ __forceinline__ void gemm_tile(const Bf16Gemm &g, uint16_t *lds)
         }
         constexpr int W = T::TN / 2;
         if (g.Z != nullptr) {
+            // pre-activations stay in 32 bits: a lane's four are 16 bytes of a row
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {                                        // gate block, then up block
+            for (int i = 0; i < T::MI; ++i) {
+                const int64_t m = m0w + i * 32 + mlane;
+                if (m >= g.M) continue;
 #pragma unroll
-                for (int i = 0; i < T::MI; ++i)
+                for (int j = 0; j < T::NI; ++j)
 #pragma unroll
-                    for (int j = 0; j < T::NI; ++j)
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const f32x16_t &v = acc[j][i];
-                            const int b = 8 * s + 4 * q;
-                            put4<T>(out, i * 32 + mlane, j * 16 + 8 * q + 4 * half, v[b], v[b + 1], v[b + 2], v[b + 3]);
-                        }
-                wave_fence();
-                flush_block<T, W>(out, g.Z + s * F, g.ldz, g.M, F, m0w, f0w, lane);
-                wave_fence();
+                    for (int q = 0; q < 4; ++q) {
+                        const int64_t f = f0w + j * 16 + 8 * (q & 1) + 4 * half;
+                        // rows are padded to a multiple of 8, so four always fit
+                        if (f < F)
+                            *reinterpret_cast<f32x4_t *>(g.Z + m * g.ldz + (q >> 1) * (g.ldz / 2) + f) =
+                                f32x4_t{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2],
+                                        acc[j][i][4 * q + 3]};
+                    }
             }
         }
 #pragma unroll

@@ -90,93 +90,98 @@ __global__ __launch_bounds__(256) void transpose_kernel(int64_t rows, int64_t co
 // ---------------------------------------------------------------- gate
 
 template <int GATE>
-__global__ __launch_bounds__(256) void gate_kernel(int64_t M, int64_t F, const float *Z, int64_t ldz, float *H,
-                                                   int64_t ldh)
+__global__ __launch_bounds__(256) void gate_kernel(int64_t M, int64_t F, const float *Z, int64_t ldz, int64_t up,
+                                                   float *H, int64_t ldh)
 {
     const int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (f >= F) return;
     for (int64_t m = blockIdx.y; m < M; m += gridDim.y)
-        H[m * ldh + f] = gate_act<GATE>(Z[m * ldz + f]) * Z[m * ldz + F + f];
+        H[m * ldh + f] = gate_act<GATE>(Z[m * ldz + f]) * Z[m * ldz + up + f];
 }
 
 // 64 rows x 64 outputs per workgroup; a thread takes four consecutive outputs
-// of four rows.  The tile of dZ waits in LDS for its transpose and the column
-// sums, which take the unrounded values.
+// of four rows, loaded before any is used.  The tile of dZ waits in LDS for its
+// transpose and the column sums, which take the unrounded values.
 template <class T, int GATE>
-__global__ __launch_bounds__(256) void gate_backward_kernel(int64_t M, int64_t F, const T *Z, int64_t ldz, const T *dH,
-                                                            int64_t lddh, bool vec, T *dZ, int64_t ldd, T *dZt,
-                                                            int64_t mp, float *sums)
+__global__ __launch_bounds__(256) void gate_backward_kernel(int64_t M, int64_t F, const float *Z, const T *dH,
+                                                            int64_t lddh, bool vec_h, T *dZ, T *dZt, float *sums)
 {
     __shared__ float tile[2][64][65];
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     const int64_t f0 = (int64_t)blockIdx.y * 64, m0 = (int64_t)blockIdx.x * 64;
     const int tc = (threadIdx.x & 15) * 4, tr = threadIdx.x >> 4;
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    auto load4 = [&](const T *p, int64_t f, float (&v)[4]) {
-        if (vec && f + 4 <= F) {
-            if constexpr (sizeof(T) == 4) {
-                const f32x4_t x = *reinterpret_cast<const f32x4_t *>(p);
+    const int64_t f = f0 + tc, zup = (F + 7) / 8 * 8, dup = (F + 31) / 32 * 32, mp = (M + 63) / 64 * 64;
+    f32x4_t zg[4], zu[4];
+    float dh[4][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = x[e];
+    for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + tr + 16 * i;
+        zg[i] = zu[i] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dh[i][e] = 0.0f;
+        if (m < M && f < F) {                    // Z's rows are padded: four always fit
+            zg[i] = *reinterpret_cast<const f32x4_t *>(Z + m * 2 * zup + f);
+            zu[i] = *reinterpret_cast<const f32x4_t *>(Z + m * 2 * zup + zup + f);
+            const T *p = dH + m * lddh + f;
+            if (vec_h && f + 4 <= F) {
+                if constexpr (sizeof(T) == 4) {
+                    const f32x4_t x = *reinterpret_cast<const f32x4_t *>(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dh[i][e] = x[e];
+                } else {
+                    const u32x2 x = *reinterpret_cast<const u32x2 *>(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dh[i][e] = bf2f((uint16_t)(x[e >> 1] >> (16 * (e & 1))));
+                }
             } else {
-                const u32x2 x = *reinterpret_cast<const u32x2 *>(p);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = bf2f((uint16_t)(x[e >> 1] >> (16 * (e & 1))));
+                for (int e = 0; e < 4; ++e)
+                    if (f + e < F) dh[i][e] = Elem<T>::load(p + e);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = f + e < F ? Elem<T>::load(p + e) : 0.0f;
         }
-    };
-    auto store4 = [&](T *p, int64_t f, const float (&v)[4]) {
-        if (vec && f + 4 <= F) {
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4_t *>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-            else *reinterpret_cast<u32x2 *>(p) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (f + e < F) p[e] = Elem<T>::store(v[e]);
-        }
-    };
-    const int64_t f = f0 + tc;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = tr + 16 * i;
-        const int64_t m = m0 + row;
-        float zg[4] = {0, 0, 0, 0}, zu[4] = {0, 0, 0, 0}, dh[4] = {0, 0, 0, 0}, dg[4], du[4];
-        if (m < M && f < F) {
-            load4(Z + m * ldz + f, f, zg);
-            load4(Z + m * ldz + F + f, f, zu);
-            load4(dH + m * lddh + f, f, dh);
-        }
+        float dg[4], du[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float a, d;
-            gate_act_grad<GATE>(zg[e], a, d);
-            dg[e] = dh[e] * zu[e] * d;
-            du[e] = dh[e] * a;
+            gate_act_grad<GATE>(zg[i][e], a, d);
+            const bool in = m0 + row < M && f + e < F;      // the padding of Z may hold anything
+            dg[e] = in ? dh[i][e] * zu[i][e] * d : 0.0f;
+            du[e] = in ? dh[i][e] * a : 0.0f;
             tile[0][row][tc + e] = dg[e];
             tile[1][row][tc + e] = du[e];
         }
-        if (dZ != nullptr && m < M && f < F) {
-            store4(dZ + m * ldd + f, f, dg);
-            store4(dZ + m * ldd + F + f, f, du);
+        // a tile reaches past dup only where dup is not a multiple of 64
+        if (dZ != nullptr && m0 + row < M && f < dup) {
+            T *const p = dZ + (m0 + row) * 2 * dup + f;
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<f32x4_t *>(p) = f32x4_t{dg[0], dg[1], dg[2], dg[3]};
+                *reinterpret_cast<f32x4_t *>(p + dup) = f32x4_t{du[0], du[1], du[2], du[3]};
+            } else {
+                *reinterpret_cast<u32x2 *>(p) = u32x2{pack2(dg[0], dg[1]), pack2(dg[2], dg[3])};
+                *reinterpret_cast<u32x2 *>(p + dup) = u32x2{pack2(du[0], du[1]), pack2(du[2], du[3])};
+            }
         }
-    }
-    if (dZ != nullptr && blockIdx.y == gridDim.y - 1) {
-        // the pitch's padding
-        const int64_t pad = ldd - 2 * F;
-        for (int64_t o = threadIdx.x; o < 64 * pad; o += 256)
-            if (m0 + o / pad < M) dZ[(m0 + o / pad) * ldd + 2 * F + o % pad] = Elem<T>::store(0.0f);
     }
     __syncthreads();
     if (dZt != nullptr) {
-        const int lo = threadIdx.x & 63, hi = threadIdx.x >> 6;
+        // four rows of the tile are 16 (8) bytes of a transposed row
+        const int q = (threadIdx.x & 15) * 4, hi = threadIdx.x >> 4;
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int c = hi + 4 * i;
-                if (f0 + c < F) dZt[(s * F + f0 + c) * mp + m0 + lo] = Elem<T>::store(tile[s][lo][c]);
+            for (int i = 0; i < 4; ++i) {
+                const int c = hi + 16 * i;
+                if (f0 + c < F) {
+                    T *const p = dZt + (s * F + f0 + c) * mp + m0 + q;
+                    const float v0 = tile[s][q][c], v1 = tile[s][q + 1][c], v2 = tile[s][q + 2][c],
+                                v3 = tile[s][q + 3][c];
+                    if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4_t *>(p) = f32x4_t{v0, v1, v2, v3};
+                    else *reinterpret_cast<u32x2 *>(p) = u32x2{pack2(v0, v1), pack2(v2, v3)};
+                }
             }
     }
     if (sums != nullptr && threadIdx.x < 128) {
@@ -188,37 +193,38 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(int64_t M, int64_t F
     }
 }
 
+// out[c] = the tiles' sums: 16 threads per column, each over a run of tiles,
+// added in order.
 template <class T>
-__global__ __launch_bounds__(256) void sum_tiles_kernel(int64_t tiles, int64_t cols, const float *sums, T *out)
+__global__ __launch_bounds__(1024) void sum_tiles_kernel(int64_t tiles, int64_t cols, const float *sums, T *out)
 {
-    // 64 columns, four threads each over a quarter of the tiles, added in order
-    __shared__ float part[4][64];
-    const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-    const int q = threadIdx.x >> 6;
+    __shared__ float part[16][64];
+    const int l = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + l;
     float v = 0.0f;
-    if (c < cols)
-        for (int64_t t = tiles * q / 4; t < tiles * (q + 1) / 4; ++t) v += sums[t * cols + c];
-    part[q][threadIdx.x & 63] = v;
+    if (c < cols) {
+        const int64_t end = tiles * (q + 1) / 16;
+#pragma unroll 8
+        for (int64_t t = tiles * q / 16; t < end; ++t) v += sums[t * cols + c];
+    }
+    part[q][l] = v;
     __syncthreads();
     if (q == 0 && c < cols) {
-        const int l = threadIdx.x & 63;
-        out[c] = Elem<T>::store(((part[0][l] + part[1][l]) + part[2][l]) + part[3][l]);
+#pragma unroll
+        for (int k = 1; k < 16; ++k) v += part[k][l];
+        out[c] = Elem<T>::store(v);
     }
 }
 
 template <class T>
-hipError_t gate_backward_t(int64_t M, int64_t F, const T *Z, int64_t ldz, const T *dH, int64_t lddh, int gate, T *dZ,
-                           int64_t ldd, T *dZt, float *sums, hipStream_t stream)
+hipError_t gate_backward_t(int64_t M, int64_t F, const float *Z, const T *dH, int64_t lddh, int gate, T *dZ, T *dZt,
+                           float *sums, hipStream_t stream)
 {
     const dim3 grid((unsigned)gate_tiles(M), (unsigned)((F + 63) / 64));
-    // four elements at once: every row of every operand, gate and up half, aligned to them
-    const uintptr_t a = 4 * sizeof(T);
-    const bool vec = F % 4 == 0 && ldz % 4 == 0 && lddh % 4 == 0 && ldd % 4 == 0 && aligned(Z, a) && aligned(dH, a) &&
-                     aligned(dZ, a);
-    const int64_t mp = pad_k(M);
-#define LAUNCH(G)                                                                                                     \
-    hipLaunchKernelGGL((gate_backward_kernel<T, G>), grid, dim3(256), 0, stream, M, F, Z, ldz, dH, lddh, vec, dZ, ldd, \
-                       dZt, mp, sums)
+    const bool vec_h = lddh % 4 == 0 && aligned(dH, 4 * sizeof(T));
+#define LAUNCH(G)                                                                                                 \
+    hipLaunchKernelGGL((gate_backward_kernel<T, G>), grid, dim3(256), 0, stream, M, F, Z, dH, lddh, vec_h, dZ, dZt, \
+                       sums)
     switch (gate) {
     case kSilu: LAUNCH(kSilu); break;
     case kGelu: LAUNCH(kGelu); break;
@@ -252,11 +258,10 @@ hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int
 }
 
 hipError_t launch_transpose_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,
-                                   hipStream_t stream)
+                                   int64_t out_rows, int64_t ldp, hipStream_t stream)
 {
-    const int64_t rp = pad_k(rows);
-    hipLaunchKernelGGL((transpose_kernel<uint16_t>), dim3((unsigned)(rp / 64), (unsigned)((cols + 63) / 64)), dim3(256),
-                       0, stream, rows, cols, rp, X, ldx, (int64_t)0, P, rp, (int64_t)0);
+    hipLaunchKernelGGL((transpose_kernel<uint16_t>), dim3((unsigned)((out_rows + 63) / 64), (unsigned)((cols + 63) / 64)),
+                       dim3(256), 0, stream, rows, cols, out_rows, X, ldx, (int64_t)0, P, ldp, (int64_t)0);
     return hipGetLastError();
 }
 
@@ -273,41 +278,54 @@ hipError_t launch_transpose_bank(int dtype, int64_t n, int64_t rows, int64_t col
     return hipGetLastError();
 }
 
-hipError_t launch_gate(int64_t M, int64_t F, const float *Z, int64_t ldz, int gate, float *H, int64_t ldh,
+hipError_t launch_gate(int64_t M, int64_t F, const float *Z, int64_t ldz, int64_t up, int gate, float *H, int64_t ldh,
                        hipStream_t stream)
 {
     const dim3 grid((unsigned)((F + 255) / 256), (unsigned)(M < 16384 ? M : 16384));
+#define LAUNCH(G) hipLaunchKernelGGL((gate_kernel<G>), grid, dim3(256), 0, stream, M, F, Z, ldz, up, H, ldh)
     switch (gate) {
-    case kSilu: hipLaunchKernelGGL((gate_kernel<kSilu>), grid, dim3(256), 0, stream, M, F, Z, ldz, H, ldh); break;
-    case kGelu: hipLaunchKernelGGL((gate_kernel<kGelu>), grid, dim3(256), 0, stream, M, F, Z, ldz, H, ldh); break;
-    case kGeluTanh:
-        hipLaunchKernelGGL((gate_kernel<kGeluTanh>), grid, dim3(256), 0, stream, M, F, Z, ldz, H, ldh);
-        break;
-    case kSigmoid: hipLaunchKernelGGL((gate_kernel<kSigmoid>), grid, dim3(256), 0, stream, M, F, Z, ldz, H, ldh); break;
-    case kRelu: hipLaunchKernelGGL((gate_kernel<kRelu>), grid, dim3(256), 0, stream, M, F, Z, ldz, H, ldh); break;
+    case kSilu: LAUNCH(kSilu); break;
+    case kGelu: LAUNCH(kGelu); break;
+    case kGeluTanh: LAUNCH(kGeluTanh); break;
+    case kSigmoid: LAUNCH(kSigmoid); break;
+    case kRelu: LAUNCH(kRelu); break;
     default: return hipErrorInvalidValue;
     }
+#undef LAUNCH
     return hipGetLastError();
 }
 
-hipError_t launch_gate_backward(int dtype, int64_t M, int64_t F, const void *Z, int64_t ldz, const void *dH,
-                                int64_t lddh, int gate, void *dZ, int64_t ldd, void *dZt, float *sums,
-                                hipStream_t stream)
+__global__ __launch_bounds__(256) void copy_z_kernel(int64_t M, int64_t F, const float *Z, int64_t pitch, float *out)
+{
+    const int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (f >= 2 * F) return;
+    for (int64_t m = blockIdx.y; m < M; m += gridDim.y)
+        out[m * pitch + (f < F ? f : pitch / 2 + f - F)] = Z[m * 2 * F + f];
+}
+
+hipError_t launch_copy_z(int64_t M, int64_t F, const float *Z, float *out, hipStream_t stream)
+{
+    hipLaunchKernelGGL(copy_z_kernel, dim3((unsigned)((2 * F + 255) / 256), (unsigned)(M < 16384 ? M : 16384)),
+                       dim3(256), 0, stream, M, F, Z, z_pitch(F), out);
+    return hipGetLastError();
+}
+
+hipError_t launch_gate_backward(int dtype, int64_t M, int64_t F, const float *Z, const void *dH, int64_t lddh,
+                                int gate, void *dZ, void *dZt, float *sums, hipStream_t stream)
 {
     if (dtype == kF32)
-        return gate_backward_t<float>(M, F, (const float *)Z, ldz, (const float *)dH, lddh, gate, (float *)dZ, ldd,
-                                      (float *)dZt, sums, stream);
-    return gate_backward_t<uint16_t>(M, F, (const uint16_t *)Z, ldz, (const uint16_t *)dH, lddh, gate, (uint16_t *)dZ,
-                                     ldd, (uint16_t *)dZt, sums, stream);
+        return gate_backward_t<float>(M, F, Z, (const float *)dH, lddh, gate, (float *)dZ, (float *)dZt, sums, stream);
+    return gate_backward_t<uint16_t>(M, F, Z, (const uint16_t *)dH, lddh, gate, (uint16_t *)dZ, (uint16_t *)dZt, sums,
+                                     stream);
 }
 
 hipError_t launch_sum_tiles(int dtype, int64_t tiles, int64_t cols, const float *sums, void *out, hipStream_t stream)
 {
     const dim3 grid((unsigned)((cols + 63) / 64));
     if (dtype == kF32)
-        hipLaunchKernelGGL((sum_tiles_kernel<float>), grid, dim3(256), 0, stream, tiles, cols, sums, (float *)out);
+        hipLaunchKernelGGL((sum_tiles_kernel<float>), grid, dim3(1024), 0, stream, tiles, cols, sums, (float *)out);
     else
-        hipLaunchKernelGGL((sum_tiles_kernel<uint16_t>), grid, dim3(256), 0, stream, tiles, cols, sums,
+        hipLaunchKernelGGL((sum_tiles_kernel<uint16_t>), grid, dim3(1024), 0, stream, tiles, cols, sums,
                            (uint16_t *)out);
     return hipGetLastError();
 }

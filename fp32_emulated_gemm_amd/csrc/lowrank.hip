@@ -1,11 +1,11 @@
 // lowrank.hip -- few-row products and the low-rank parts of the adapters.
 //
-// dot_tile, shared by the few-row product and the shrink: a workgroup's eight
+// dot_tile, shared by the few-row products and the shrink: a workgroup's eight
 // waves split K; each reads rows of both operands straight into the fragments
 // of a 16 x 16 MFMA (128 bits of consecutive k per lane, four lanes of a row in
-// one 64-byte segment, two segments per wave and step), and the waves' sums are
-// added through LDS in wave order.  There is no reuse to stage: with few rows
-// of X the weight passes once, and the time is its bytes'.
+// one 64-byte segment), and the waves' sums are added through LDS in wave
+// order.  There is no reuse to stage: with few rows of X the weight passes
+// once, and the time is its bytes' and the latency of the loads.
 // FP32 operands take the FP32 matrix instruction (FP32 products, FP32 sums): a
 // lane's four consecutive k are the k of four instructions, the same for both
 // operands, so their order inside a step does not matter.
@@ -17,6 +17,8 @@ namespace sgemm_emu_dev {
 namespace {
 
 constexpr int WAVES = 8;                         // of a dot_tile workgroup
+constexpr int NT = 64 * WAVES;
+constexpr uint32_t OUT_OF_RANGE = 0xFFFFFFF0u;   // past every descriptor: reads zeros
 
 template <class T>
 __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c)
@@ -32,51 +34,75 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c)
     }
 }
 
-// VEC elements of a row from k on, zeros past K.  ALIGNED: rows are 16-byte
-// aligned and K is a multiple of VEC, so a load is whole or empty.
+// B blocks of 16 rows of an operand: each block's descriptor and this lane's row
+// offset in it (row l & 15), or OUT_OF_RANGE for a row that reads zeros.
+template <int B>
+struct Rows {
+    rsrc_t r[B];
+    uint32_t off[B];
+};
+
+// VEC elements of a row from k on, zeros from ke on.  ALIGNED: rows are 16-byte
+// aligned and every K bound is a multiple of VEC, so a load is whole or empty.
 template <class T, bool ALIGNED>
-__device__ __forceinline__ u32x4_t load_k(const T *row, int64_t k, int64_t K)
+__device__ __forceinline__ u32x4_t load_k(rsrc_t r, uint32_t row, int64_t k, int64_t ke)
 {
     constexpr int V = Elem<T>::VEC;
-    u32x4_t v = {0, 0, 0, 0};
+    const uint32_t off = row + (uint32_t)(k * (int64_t)sizeof(T));
+    const bool none = row == OUT_OF_RANGE;
     if constexpr (ALIGNED) {
-        if (k < K) v = *reinterpret_cast<const u32x4_t *>(row + k);
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (k + e < K) v[e] = __float_as_uint(row[k + e]);
+        return bload_u32x4(r, none || k >= ke ? OUT_OF_RANGE : off, 0);
     } else {
+        u32x4_t v = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (k + e < K) v[e >> 1] |= (uint32_t)row[k + e] << (16 * (e & 1));
+        for (int e = 0; e < V; ++e) {
+            const uint32_t o = none || k + e >= ke ? OUT_OF_RANGE : off + e * (uint32_t)sizeof(T);
+            if constexpr (sizeof(T) == 4) v[e] = bload_u32(r, o, 0);
+            else v[e >> 1] |= bload_u16(r, o, 0) << (16 * (e & 1));
+        }
+        return v;
     }
-    return v;
 }
 
-// acc[nb][mb] += rows of W (w[nb], 16 per block) times rows of X (x[mb]) over
-// this wave's share of K: lane l holds row l & 15 of each block.
+// acc[nb][mb] += rows of W times rows of X over this wave's share of [kb, ke).
+// Two neighbouring steps of a row are one wave's, so it reads 128 bytes of
+// each.  DEPTH steps' loads are in flight while a step multiplies.
 template <class T, int NB, int MB, bool AW, bool AX>
-__device__ __forceinline__ void dot_tile(f32x4_t (&acc)[NB][MB], const T *const (&w)[NB], const T *const (&x)[MB],
-                                         int64_t K, int wave, int lane)
+__device__ __forceinline__ void dot_tile(f32x4_t (&acc)[NB][MB], const Rows<NB> &w, const Rows<MB> &x, int64_t kb,
+                                         int64_t ke, int wave, int lane)
 {
-    constexpr int V = Elem<T>::VEC, STEP = 8 * V, U = 2;
-    const int64_t first = (int64_t)wave * STEP + (lane >> 4) * V;
-    for (int64_t k = first; k - first + wave * STEP < K; k += (int64_t)WAVES * STEP) {
-        u32x4_t fw[U][NB], fx[U][MB];
+    constexpr int V = Elem<T>::VEC, STEP = 4 * V, DEPTH = !AW || !AX ? 2 : NB + MB <= 3 ? 8 : 4;
+    u32x4_t fw[DEPTH][NB], fx[DEPTH][MB];
+    // step i of this wave starts at k = kb + first(i)
+    auto first = [&](int64_t i) { return ((i >> 1) * (2 * WAVES) + wave * 2 + (i & 1)) * STEP; };
+    auto load = [&](int d, int64_t i) {
+        const int64_t k = kb + first(i) + (lane >> 4) * V;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int nb = 0; nb < NB; ++nb) fw[d][nb] = load_k<T, AW>(w.r[nb], w.off[nb], k, ke);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) fw[u][nb] = load_k<T, AW>(w[nb], k + u * 4 * V, K);
+        for (int mb = 0; mb < MB; ++mb) fx[d][mb] = load_k<T, AX>(x.r[mb], x.off[mb], k, ke);
+    };
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) fx[u][mb] = load_k<T, AX>(x[mb], k + u * 4 * V, K);
-        }
+    for (int d = 0; d < DEPTH; ++d) load(d, d);
+    for (int64_t i = 0; kb + first(i) < ke; i += DEPTH) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int d = 0; d < DEPTH; ++d) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = mfma16<T>(fw[u][nb], fx[u][mb], acc[nb][mb]);
+                for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = mfma16<T>(fw[d][nb], fx[d][mb], acc[nb][mb]);
+            load(d, i + DEPTH + d);
+        }
     }
+}
+
+template <int NB, int MB>
+__device__ __forceinline__ void clear(f32x4_t (&acc)[NB][MB])
+{
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = f32x4_t{};
 }
 
 template <int NB, int MB>
@@ -100,93 +126,289 @@ __device__ __forceinline__ float get_sum(const float *lds, int n, int m)
     return v;
 }
 
-// ---------------------------------------------------------------- few rows
+// Blocks b of rows r0 + 16 b + (l & 15) of an operand of `rows` rows; rows past
+// it re-read the last one (their results are dropped).
+template <class T, int B>
+__device__ __forceinline__ Rows<B> rows_at(const T *p, int64_t ld, int64_t r0, int64_t rows, int lane)
+{
+    Rows<B> q;
+    const rsrc_t r = make_rsrc(p + r0 * ld, 0xFFFFFFF0ll);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        q.r[b] = r;
+        q.off[b] = (uint32_t)((lmin(r0 + b * 16 + (lane & 15), rows - 1) - r0) * ld * (int64_t)sizeof(T));
+    }
+    return q;
+}
 
-// GATE < 0: NB blocks of 16 rows of W; else NB / 2 blocks of gate rows, then
-// the NB / 2 blocks of up rows of the same outputs.
+// ---------------------------------------------------------------- gated, one pass
+// NB / 2 blocks of 16 gate rows, then the NB / 2 blocks of up rows of the same
+// outputs; the whole K in one workgroup.
 template <class T, int NB, int MB, int GATE, bool AW, bool AX>
-__global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(FewRows a, Adapters ad)
+__global__ __launch_bounds__(NT) void few_gated_kernel(FewRows a)
 {
     __shared__ __attribute__((aligned(16))) float lds[WAVES * NB * MB * 256];
-    constexpr int OUT = (GATE < 0 ? NB : NB / 2) * 16;              // outputs per row of the workgroup
+    constexpr int OUT = NB / 2 * 16;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * OUT, m0 = (int64_t)blockIdx.y * (16 * MB);
-    const T *W = (const T *)a.W, *X = (const T *)a.X;
-    const T *w[NB], *x[MB];
+    const int64_t n0 = (int64_t)blockIdx.x * OUT, F = a.N;
+    Rows<NB> w = rows_at<T, NB>((const T *)a.W, a.ldw, n0, F, lane);
+    const rsrc_t up = make_rsrc((const T *)a.W + (F + n0) * a.ldw, 0xFFFFFFF0ll);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const int b = GATE < 0 ? nb : nb % (NB / 2);
-        int64_t row = lmin(n0 + b * 16 + (lane & 15), a.N - 1);
-        if (GATE >= 0 && nb >= NB / 2) row += a.N;
-        w[nb] = W + row * a.ldw;
+    for (int b = 0; b < NB / 2; ++b) {
+        w.r[NB / 2 + b] = up;
+        w.off[NB / 2 + b] = w.off[b];
     }
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) x[mb] = X + lmin(m0 + mb * 16 + (lane & 15), a.M - 1) * a.ldx;
+    const Rows<MB> x = rows_at<T, MB>((const T *)a.X, a.ldx, 0, a.M, lane);
     f32x4_t acc[NB][MB];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = f32x4_t{};
-    dot_tile<T, NB, MB, AW, AX>(acc, w, x, a.K, wave, lane);
+    clear<NB, MB>(acc);
+    dot_tile<T, NB, MB, AW, AX>(acc, w, x, 0, a.K, wave, lane);
     put_sums<NB, MB>(lds, acc, wave, lane);
     __syncthreads();
     const T *bias = (const T *)a.bias;
     T *Y = (T *)a.Y;
-    for (int o = threadIdx.x; o < OUT * 16 * MB; o += 64 * WAVES) {
+    for (int o = threadIdx.x; o < OUT * 16 * MB; o += NT) {
         const int n = o % OUT, m = o / OUT;
-        if (n0 + n >= a.N || m0 + m >= a.M) continue;
-        float v = get_sum<NB, MB>(lds, n, m);
-        if (bias != nullptr) v += Elem<T>::load(bias + n0 + n);
-        if constexpr (GATE >= 0) {
-            float u = get_sum<NB, MB>(lds, OUT + n, m);
-            if (bias != nullptr) u += Elem<T>::load(bias + a.N + n0 + n);
-            v = gate_act<GATE>(v) * u;
-        } else if (a.S != nullptr) {
-            const int32_t i = ad.ids[m0 + m];
-            if (i >= 0 && i < ad.n) {
-                const T *up = (const T *)ad.up + ((int64_t)i * a.N + n0 + n) * ad.r;
-                const float *s = a.S + (m0 + m) * ((ad.r + 15) / 16 * 16);
-                float d = 0.0f;
-                for (int64_t j = 0; j < ad.r; ++j) d = __builtin_fmaf(s[j], Elem<T>::load(up + j), d);
-                v += d;
-            }
+        if (n0 + n >= F || m >= a.M) continue;
+        float v = get_sum<NB, MB>(lds, n, m), u = get_sum<NB, MB>(lds, OUT + n, m);
+        if (bias != nullptr) {
+            v += Elem<T>::load(bias + n0 + n);
+            u += Elem<T>::load(bias + F + n0 + n);
         }
-        Y[(m0 + m) * a.ldy + n0 + n] = Elem<T>::store(v);
+        Y[m * a.ldy + n0 + n] = Elem<T>::store(gate_act<GATE>(v) * u);
     }
 }
 
-template <class T, int NB, int MB, int GATE>
-void launch_few_rows_al(const FewRows &a, hipStream_t stream)
+// ---------------------------------------------------------------- K slices
+// partials[slice][m][n] of X W^T, 32 rows of W per workgroup, beside the
+// shrink's workgroups (they come first; nothing here depends on them).
+template <class T>
+struct Tokens {
+    int64_t M, N, K;
+    const T *X;
+    int64_t ldx;
+    const T *W;
+    int64_t ldw;
+    float *partials;
+    int64_t k_per_slice;
+    int n_blocks;
+    int shrink_blocks;        // workgroups of the shrink: (16-row tile, row)
+    Adapters ad;
+    float *S;
+    int64_t rp;
+};
+
+// One workgroup per row of a 16-row tile: the first row of an adapter multiplies
+// the tile's rows of that adapter, the others end.
+template <class T, bool AX, bool AD>
+__device__ __forceinline__ void shrink_row(const Tokens<T> &a, int block, float *lds, int wave, int lane)
 {
-    constexpr int OUT = (GATE < 0 ? NB : NB / 2) * 16, V = Elem<T>::VEC;
-    const dim3 grid((unsigned)((a.N + OUT - 1) / OUT), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
-    const bool aw = a.K % V == 0 && a.ldw % V == 0 && aligned(a.W, 16);
-    const bool ax = a.K % V == 0 && a.ldx % V == 0 && aligned(a.X, 16);
-    const Adapters ad = a.ad != nullptr ? *a.ad : Adapters{};
-    const dim3 block(64 * WAVES);
-    if (aw && ax) hipLaunchKernelGGL((few_rows_kernel<T, NB, MB, GATE, true, true>), grid, block, 0, stream, a, ad);
-    else if (aw) hipLaunchKernelGGL((few_rows_kernel<T, NB, MB, GATE, true, false>), grid, block, 0, stream, a, ad);
-    else hipLaunchKernelGGL((few_rows_kernel<T, NB, MB, GATE, false, false>), grid, block, 0, stream, a, ad);
+    const int64_t m0 = (int64_t)(block >> 4) * 16;
+    const int mine = block & 15;
+    const int64_t m = m0 + (lane & 15);
+    int32_t id = -1;
+    if (m < a.M) {
+        id = a.ad.ids[m];
+        if (id >= a.ad.n) id = -1;
+    }
+    if (m0 + mine >= a.M) return;
+    const int32_t me = __builtin_amdgcn_readlane(id, mine);
+    if (me < 0) {
+        for (int64_t j = threadIdx.x; j < a.rp; j += NT) a.S[(m0 + mine) * a.rp + j] = 0.0f;
+        return;
+    }
+    const uint32_t own = (uint32_t)(__ballot(id == me) & 0xFFFFu);
+    if ((own & ((1u << mine) - 1u)) != 0) return;                    // an earlier row computes it
+    Rows<1> x = rows_at<T, 1>(a.X, a.ldx, m0, a.M, lane);
+    if (!((own >> (lane & 15)) & 1u)) x.off[0] = OUT_OF_RANGE;
+    const T *down = (const T *)a.ad.down + (int64_t)me * a.ad.r * a.K;
+    const float scale = a.ad.scale != nullptr ? a.ad.scale[me] : 1.0f;
+    for (int64_t r0 = 0; r0 < a.rp; r0 += 16) {
+        const Rows<1> w = rows_at<T, 1>(down, a.K, r0, a.ad.r, lane);
+        f32x4_t acc[1][1];
+        clear<1, 1>(acc);
+        dot_tile<T, 1, 1, AD, AX>(acc, w, x, 0, a.K, wave, lane);
+        put_sums<1, 1>(lds, acc, wave, lane);
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            const int n = threadIdx.x & 15, row = threadIdx.x >> 4;
+            if ((own >> row) & 1u)
+                a.S[(m0 + row) * a.rp + r0 + n] = r0 + n < a.ad.r ? scale * get_sum<1, 1>(lds, n, row) : 0.0f;
+        }
+        __syncthreads();
+    }
 }
 
-template <class T, int NB, int GATE>
-void launch_few_rows_mb(const FewRows &a, hipStream_t stream)
+template <class T, int MB, bool AW, bool AX, bool AD>
+__global__ __launch_bounds__(NT) void tokens_kernel(Tokens<T> a)
 {
-    if (a.M <= 16) launch_few_rows_al<T, NB, 1, GATE>(a, stream);
-    else if (a.M <= 32) launch_few_rows_al<T, NB, 2, GATE>(a, stream);
-    else launch_few_rows_al<T, NB, 4, GATE>(a, stream);
+    constexpr int NB = 2;
+    __shared__ __attribute__((aligned(16))) float lds[WAVES * NB * MB * 256];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int block = (int)blockIdx.x;
+    if (block < a.shrink_blocks) {
+        shrink_row<T, AX, AD>(a, block, lds, wave, lane);
+        return;
+    }
+    block -= a.shrink_blocks;
+    const int64_t n0 = (int64_t)(block % a.n_blocks) * (16 * NB), slice = block / a.n_blocks;
+    const int64_t kb = slice * a.k_per_slice, ke = lmin(kb + a.k_per_slice, a.K);
+    const Rows<NB> w = rows_at<T, NB>(a.W, a.ldw, n0, a.N, lane);
+    const Rows<MB> x = rows_at<T, MB>(a.X, a.ldx, 0, a.M, lane);
+    f32x4_t acc[NB][MB];
+    clear<NB, MB>(acc);
+    dot_tile<T, NB, MB, AW, AX>(acc, w, x, kb, ke, wave, lane);
+    put_sums<NB, MB>(lds, acc, wave, lane);
+    __syncthreads();
+    float *const part = a.partials + slice * a.M * a.N;
+    for (int o = threadIdx.x; o < 16 * NB * 16 * MB; o += NT) {
+        const int n = o % (16 * NB), m = o / (16 * NB);
+        if (n0 + n < a.N && m < a.M) part[(int64_t)m * a.N + n0 + n] = get_sum<NB, MB>(lds, n, m);
+    }
+}
+
+// Y[m][n] = sum of the slices in order + bias + up[i][n] . S[m].
+template <class T>
+__global__ __launch_bounds__(256) void tokens_finish_kernel(Tokens<T> a, int slices, const T *bias, T *Y, int64_t ldy)
+{
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
+    if (n >= a.N) return;
+    const int64_t plane = a.M * a.N;
+    const float *p = a.partials + m * a.N + n;
+    float v = 0.0f;
+    for (int s = 0; s < slices; ++s) v += p[s * plane];
+    if (bias != nullptr) v += Elem<T>::load(bias + n);
+    if (a.shrink_blocks > 0) {
+        const int32_t i = a.ad.ids[m];
+        if (i >= 0 && i < a.ad.n) {
+            const T *up = (const T *)a.ad.up + ((int64_t)i * a.N + n) * a.ad.r;
+            const float *s = a.S + m * a.rp;
+            constexpr int V = Elem<T>::VEC;
+            float d = 0.0f;
+            if (a.ad.r % V == 0 && ((uintptr_t)a.ad.up % 16) == 0) {
+                for (int64_t j = 0; j < a.ad.r; j += V) {
+                    const u32x4_t u = *reinterpret_cast<const u32x4_t *>(up + j);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        float f;
+                        if constexpr (sizeof(T) == 4) f = __uint_as_float(u[e]);
+                        else f = bf2f((uint16_t)(u[e >> 1] >> (16 * (e & 1))));
+                        d = __builtin_fmaf(s[j + e], f, d);
+                    }
+                }
+            } else {
+                for (int64_t j = 0; j < a.ad.r; ++j) d = __builtin_fmaf(s[j], Elem<T>::load(up + j), d);
+            }
+            v += d;
+        }
+    }
+    Y[m * ldy + n] = Elem<T>::store(v);
+}
+
+// H[m][f] = act(gate) * up of the slices' sums + bias (a.N = 2F).
+template <class T, int GATE>
+__global__ __launch_bounds__(256) void gated_finish_kernel(Tokens<T> a, int slices, const T *bias, T *H, int64_t ldh)
+{
+    const int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x, m = blockIdx.y, F = a.N / 2;
+    if (f >= F) return;
+    const int64_t plane = a.M * a.N;
+    const float *p = a.partials + m * a.N + f;
+    float g = 0.0f, u = 0.0f;
+    for (int s = 0; s < slices; ++s) {
+        g += p[s * plane];
+        u += p[s * plane + F];
+    }
+    if (bias != nullptr) {
+        g += Elem<T>::load(bias + f);
+        u += Elem<T>::load(bias + F + f);
+    }
+    H[m * ldh + f] = Elem<T>::store(gate_act<GATE>(g) * u);
+}
+
+template <class T>
+bool rows_aligned(const void *p, int64_t ld, int64_t K)
+{
+    return K % Elem<T>::VEC == 0 && ld % Elem<T>::VEC == 0 && aligned(p, 16);
+}
+
+// K slices of a few-row product over n_blocks blocks of 32 weight rows: about
+// two workgroups per CU, each with a step or more for every wave.
+int token_slices(int dtype, int64_t N, int64_t K, int num_cus)
+{
+    const int64_t blocks = (N + 31) / 32, least = WAVES * (dtype == kF32 ? 16 : 32);
+    int64_t s = 2 * (int64_t)num_cus / (blocks > 0 ? blocks : 1);
+    if (s > K / least) s = K / least;
+    return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+}
+
+template <class T>
+Tokens<T> make_tokens(const FewRows &a, int64_t N, int slices)
+{
+    Tokens<T> t{};
+    t.M = a.M; t.N = N; t.K = a.K;
+    t.X = (const T *)a.X; t.ldx = a.ldx;
+    t.W = (const T *)a.W; t.ldw = a.ldw;
+    t.partials = a.partials;
+    // slices begin at whole 128-byte pairs of steps
+    t.k_per_slice = round_up((a.K + slices - 1) / slices, 8 * Elem<T>::VEC);
+    t.n_blocks = (int)((N + 31) / 32);
+    if (a.ad != nullptr) {
+        t.ad = *a.ad;
+        t.S = a.S;
+        t.rp = rank_pad(a.ad->r);
+        t.shrink_blocks = (int)((a.M + 15) / 16 * 16);
+    }
+    return t;
+}
+
+template <class T, int MB>
+void launch_tokens_mb(const Tokens<T> &t, int slices, hipStream_t stream)
+{
+    const dim3 grid((unsigned)(t.shrink_blocks + t.n_blocks * slices)), block(NT);
+    const bool aw = rows_aligned<T>(t.W, t.ldw, t.K), ax = rows_aligned<T>(t.X, t.ldx, t.K);
+    const bool ad = rows_aligned<T>(t.ad.down, t.K, t.K);
+    if (aw && ax && ad) hipLaunchKernelGGL((tokens_kernel<T, MB, true, true, true>), grid, block, 0, stream, t);
+    else hipLaunchKernelGGL((tokens_kernel<T, MB, false, false, false>), grid, block, 0, stream, t);
+}
+
+template <class T>
+void launch_tokens(const Tokens<T> &t, int slices, hipStream_t stream)
+{
+    if (t.M <= 16) launch_tokens_mb<T, 1>(t, slices, stream);
+    else if (t.M <= 32) launch_tokens_mb<T, 2>(t, slices, stream);
+    else launch_tokens_mb<T, 4>(t, slices, stream);
+}
+
+template <class T, int NB, int MB, int GATE>
+void launch_few_gated_al(const FewRows &a, hipStream_t stream)
+{
+    constexpr int OUT = NB / 2 * 16;
+    const dim3 grid((unsigned)((a.N + OUT - 1) / OUT)), block(NT);
+    const bool aw = rows_aligned<T>(a.W, a.ldw, a.K), ax = rows_aligned<T>(a.X, a.ldx, a.K);
+    if (aw && ax) hipLaunchKernelGGL((few_gated_kernel<T, NB, MB, GATE, true, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((few_gated_kernel<T, NB, MB, GATE, false, false>), grid, block, 0, stream, a);
 }
 
 template <class T, int GATE>
-void launch_few_rows_nb(const FewRows &a, int num_cus, hipStream_t stream)
+void launch_few_gated(const FewRows &a, int num_cus, hipStream_t stream)
 {
-    if constexpr (GATE >= 0) {
-        if (a.N >= (int64_t)32 * num_cus) launch_few_rows_mb<T, 4, GATE>(a, stream);
-        else launch_few_rows_mb<T, 2, GATE>(a, stream);
+    if (a.partials != nullptr) {
+        const int slices = token_slices(sizeof(T) == 4 ? kF32 : kBF16, 2 * a.N, a.K, num_cus);
+        const Tokens<T> t = make_tokens<T>(a, 2 * a.N, slices);
+        launch_tokens<T>(t, slices, stream);
+        hipLaunchKernelGGL((gated_finish_kernel<T, GATE>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256),
+                           0, stream, t, slices, (const T *)a.bias, (T *)a.Y, a.ldy);
+        return;
+    }
+    const bool wide = a.N >= (int64_t)32 * num_cus;
+    if (a.M <= 16) {
+        if (wide) launch_few_gated_al<T, 4, 1, GATE>(a, stream);
+        else launch_few_gated_al<T, 2, 1, GATE>(a, stream);
+    } else if (a.M <= 32) {
+        if (wide) launch_few_gated_al<T, 4, 2, GATE>(a, stream);
+        else launch_few_gated_al<T, 2, 2, GATE>(a, stream);
     } else {
-        if (a.N >= (int64_t)64 * num_cus) launch_few_rows_mb<T, 4, GATE>(a, stream);
-        else if (a.N >= (int64_t)32 * num_cus) launch_few_rows_mb<T, 2, GATE>(a, stream);
-        else launch_few_rows_mb<T, 1, GATE>(a, stream);
+        if (wide) launch_few_gated_al<T, 4, 4, GATE>(a, stream);
+        else launch_few_gated_al<T, 2, 4, GATE>(a, stream);
     }
 }
 
@@ -194,77 +416,91 @@ template <class T>
 hipError_t launch_few_rows_t(const FewRows &a, int num_cus, hipStream_t stream)
 {
     switch (a.gate) {
-    case kSilu: launch_few_rows_nb<T, kSilu>(a, num_cus, stream); break;
-    case kGelu: launch_few_rows_nb<T, kGelu>(a, num_cus, stream); break;
-    case kGeluTanh: launch_few_rows_nb<T, kGeluTanh>(a, num_cus, stream); break;
-    case kSigmoid: launch_few_rows_nb<T, kSigmoid>(a, num_cus, stream); break;
-    case kRelu: launch_few_rows_nb<T, kRelu>(a, num_cus, stream); break;
-    default: launch_few_rows_nb<T, -1>(a, num_cus, stream);
+    case kSilu: launch_few_gated<T, kSilu>(a, num_cus, stream); break;
+    case kGelu: launch_few_gated<T, kGelu>(a, num_cus, stream); break;
+    case kGeluTanh: launch_few_gated<T, kGeluTanh>(a, num_cus, stream); break;
+    case kSigmoid: launch_few_gated<T, kSigmoid>(a, num_cus, stream); break;
+    case kRelu: launch_few_gated<T, kRelu>(a, num_cus, stream); break;
+    default: {
+        const int slices = token_slices(sizeof(T) == 4 ? kF32 : kBF16, a.N, a.K, num_cus);
+        const Tokens<T> t = make_tokens<T>(a, a.N, slices);
+        launch_tokens<T>(t, slices, stream);
+        hipLaunchKernelGGL((tokens_finish_kernel<T>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256), 0,
+                           stream, t, slices, (const T *)a.bias, (T *)a.Y, a.ldy);
+    }
     }
     return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- shrink
 // S[t] = scale[i] down[i] X[t].  A workgroup takes 16 MB rows and walks the
-// adapters that occur in them (ascending ids): each pass multiplies all the
-// tile's rows by that adapter's r rows and keeps the rows that belong to it.
-// Rows of one request are neighbours, so a tile of a prompt holds one or two
-// adapters; gridDim.y workgroups share a tile's adapters where every row may
-// have its own (single tokens).
+// adapters that occur in them, in order of their first row: each pass multiplies
+// all the tile's rows by that adapter's r rows and keeps the rows that belong to
+// it.  Rows of one request are neighbours, so a tile of a prompt holds one or
+// two adapters.  FP32 keeps S as floats; bfloat16 as two BF16 parts (rp high
+// parts, then rp low parts per row, 16 significant bits), which is how the GEMM
+// epilogue multiplies it.
+template <class T>
+__device__ __forceinline__ void put_s(float *S, int64_t rp, int64_t m, int64_t j, float v)
+{
+    if constexpr (sizeof(T) == 4) {
+        S[m * rp + j] = v;
+    } else {
+        uint16_t *const row = (uint16_t *)S + m * 2 * rp;
+        uint16_t hi, lo;
+        split_hi_lo(v, hi, lo);
+        row[j] = hi;
+        row[rp + j] = lo;
+    }
+}
+
+template <class T>
+__device__ __forceinline__ float get_s(const float *S, int64_t rp, int64_t m, int64_t j)
+{
+    if constexpr (sizeof(T) == 4) {
+        return S[m * rp + j];
+    } else {
+        const uint16_t *const row = (const uint16_t *)S + m * 2 * rp;
+        return bf2f(row[j]) + bf2f(row[rp + j]);
+    }
+}
+
 template <class T, int NB, int MB, bool AL>
-__global__ __launch_bounds__(64 * WAVES) void shrink_kernel(int64_t M, int64_t K, const T *X, int64_t ldx, Adapters ad,
-                                                            float *S, int64_t rp)
+__global__ __launch_bounds__(NT) void shrink_kernel(int64_t M, int64_t K, const T *X, int64_t ldx, Adapters ad,
+                                                    float *S, int64_t rp)
 {
     __shared__ __attribute__((aligned(16))) float lds[WAVES * NB * MB * 256];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t m0 = (int64_t)blockIdx.x * (16 * MB);
     constexpr int ROWS = 16 * MB;
-    int id = -1;
+    const int64_t m0 = (int64_t)blockIdx.x * ROWS;
+    int32_t id = -1;
     if (lane < ROWS && m0 + lane < M) {
-        const int v = ad.ids[m0 + lane];
-        id = v >= 0 && v < ad.n ? v : -1;
+        id = ad.ids[m0 + lane];
+        if (id >= ad.n) id = -1;
     }
-    const T *x[MB];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) x[mb] = X + lmin(m0 + mb * 16 + (lane & 15), M - 1) * ldx;
-
-    if (blockIdx.y == 0) {
-        // rows without an adapter
-        for (int64_t o = threadIdx.x; o < ROWS * rp; o += 64 * WAVES) {
-            const int64_t m = m0 + o / rp;
-            if (m < M) {
-                const int v = ad.ids[m];
-                if (!(v >= 0 && v < ad.n)) S[m * rp + o % rp] = 0.0f;
-            }
-        }
-    }
-    int last = -1;
-    for (unsigned slot = 0;; ++slot) {
-        int next = id > last ? id : 0x7FFFFFFF;
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) next = imin(next, __shfl_xor(next, s));
-        next = __builtin_amdgcn_readfirstlane(next);
-        if (next == 0x7FFFFFFF) break;
-        last = next;
-        if (slot % gridDim.y != blockIdx.y) continue;
-        const T *down = (const T *)ad.down + (int64_t)next * ad.r * K;
-        const float scale = ad.scale != nullptr ? ad.scale[next] : 1.0f;
+    const Rows<MB> x = rows_at<T, MB>(X, ldx, m0, M, lane);
+    uint64_t todo = __ballot(id >= 0);
+    const uint64_t none = __ballot(id < 0 && lane < ROWS && m0 + lane < M);
+    if (none != 0)
+        for (int64_t o = threadIdx.x; o < ROWS * rp; o += NT)
+            if ((none >> (o / rp)) & 1) put_s<T>(S, rp, m0 + o / rp, o % rp, 0.0f);
+    while (todo != 0) {
+        const int32_t me = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(todo));
+        const uint64_t own = __ballot(id == me);
+        todo &= ~own;
+        const T *down = (const T *)ad.down + (int64_t)me * ad.r * K;
+        const float scale = ad.scale != nullptr ? ad.scale[me] : 1.0f;
         for (int64_t r0 = 0; r0 < rp; r0 += 16 * NB) {
-            const T *w[NB];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) w[nb] = down + lmin(r0 + nb * 16 + (lane & 15), ad.r - 1) * K;
+            const Rows<NB> w = rows_at<T, NB>(down, K, r0, ad.r, lane);
             f32x4_t acc[NB][MB];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = f32x4_t{};
-            dot_tile<T, NB, MB, AL, AL>(acc, w, x, K, wave, lane);
+            clear<NB, MB>(acc);
+            dot_tile<T, NB, MB, AL, AL>(acc, w, x, 0, K, wave, lane);
             put_sums<NB, MB>(lds, acc, wave, lane);
             __syncthreads();
-            for (int o = threadIdx.x; o < 16 * NB * ROWS; o += 64 * WAVES) {
+            for (int o = threadIdx.x; o < 16 * NB * ROWS; o += NT) {
                 const int n = o % (16 * NB), m = o / (16 * NB);
-                if (m0 + m < M && r0 + n < rp && ad.ids[m0 + m] == next)
-                    S[(m0 + m) * rp + r0 + n] = r0 + n < ad.r ? scale * get_sum<NB, MB>(lds, n, m) : 0.0f;
+                if (r0 + n < rp && ((own >> m) & 1))
+                    put_s<T>(S, rp, m0 + m, r0 + n, r0 + n < ad.r ? scale * get_sum<NB, MB>(lds, n, m) : 0.0f);
             }
             __syncthreads();
         }
@@ -272,52 +508,48 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(int64_t M, int64_t K
 }
 
 template <class T, int NB, int MB>
-void launch_shrink_mb(int64_t M, int64_t K, const T *X, int64_t ldx, const Adapters &ad, float *S, bool few,
-                      hipStream_t stream)
+void launch_shrink_mb(int64_t M, int64_t K, const T *X, int64_t ldx, const Adapters &ad, float *S, hipStream_t stream)
 {
-    constexpr int V = Elem<T>::VEC;
-    const dim3 grid((unsigned)((M + 16 * MB - 1) / (16 * MB)), few ? 16 * MB : 1);
-    const bool al = K % V == 0 && ldx % V == 0 && aligned(X, 16) && aligned(ad.down, 16);
-    if (al)
-        hipLaunchKernelGGL((shrink_kernel<T, NB, MB, true>), grid, dim3(64 * WAVES), 0, stream, M, K, X, ldx, ad, S,
+    const dim3 grid((unsigned)((M + 16 * MB - 1) / (16 * MB)));
+    if (rows_aligned<T>(X, ldx, K) && aligned(ad.down, 16))
+        hipLaunchKernelGGL((shrink_kernel<T, NB, MB, true>), grid, dim3(NT), 0, stream, M, K, X, ldx, ad, S,
                            rank_pad(ad.r));
     else
-        hipLaunchKernelGGL((shrink_kernel<T, NB, MB, false>), grid, dim3(64 * WAVES), 0, stream, M, K, X, ldx, ad, S,
+        hipLaunchKernelGGL((shrink_kernel<T, NB, MB, false>), grid, dim3(NT), 0, stream, M, K, X, ldx, ad, S,
                            rank_pad(ad.r));
 }
 
 template <class T, int NB>
-void launch_shrink_nb(int64_t M, int64_t K, const T *X, int64_t ldx, const Adapters &ad, float *S, hipStream_t stream)
+void launch_shrink_nb(int64_t M, int64_t K, const T *X, int64_t ldx, const Adapters &ad, float *S, int num_cus,
+                      hipStream_t stream)
 {
-    // every row of a small batch may have its own adapter: one workgroup each
-    if (M <= 256) launch_shrink_mb<T, NB, 1>(M, K, X, ldx, ad, S, true, stream);
-    else launch_shrink_mb<T, NB, 2>(M, K, X, ldx, ad, S, false, stream);
+    if (M <= (int64_t)32 * num_cus) launch_shrink_mb<T, NB, 1>(M, K, X, ldx, ad, S, stream);
+    else launch_shrink_mb<T, NB, 2>(M, K, X, ldx, ad, S, stream);
 }
 
 template <class T>
-hipError_t launch_shrink_t(int64_t M, int64_t K, const T *X, int64_t ldx, const Adapters &ad, float *S,
+hipError_t launch_shrink_t(int64_t M, int64_t K, const T *X, int64_t ldx, const Adapters &ad, float *S, int num_cus,
                            hipStream_t stream)
 {
-    if (ad.r <= 16) launch_shrink_nb<T, 1>(M, K, X, ldx, ad, S, stream);
-    else if (ad.r <= 32) launch_shrink_nb<T, 2>(M, K, X, ldx, ad, S, stream);
-    else launch_shrink_nb<T, 4>(M, K, X, ldx, ad, S, stream);
+    if (ad.r <= 16) launch_shrink_nb<T, 1>(M, K, X, ldx, ad, S, num_cus, stream);
+    else if (ad.r <= 32) launch_shrink_nb<T, 2>(M, K, X, ldx, ad, S, num_cus, stream);
+    else launch_shrink_nb<T, 4>(M, K, X, ldx, ad, S, num_cus, stream);
     return hipGetLastError();
 }
 
-// ---------------------------------------------------------------- expand
+// ---------------------------------------------------------------- expand (FP32)
 
-template <class T>
 __global__ __launch_bounds__(256) void expand_kernel(int64_t M, int64_t N, const float *S, int64_t rp, Adapters ad,
-                                                     T *Y, int64_t ldy)
+                                                     float *Y, int64_t ldy)
 {
     for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
         const int32_t i = ad.ids[m];
         const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
         if (!(i >= 0 && i < ad.n) || n >= N) continue;
-        const T *up = (const T *)ad.up + ((int64_t)i * N + n) * ad.r;
+        const float *up = (const float *)ad.up + ((int64_t)i * N + n) * ad.r;
         float d = 0.0f;
-        for (int64_t j = 0; j < ad.r; ++j) d = __builtin_fmaf(S[m * rp + j], Elem<T>::load(up + j), d);
-        Y[m * ldy + n] = Elem<T>::store(Elem<T>::load(Y + m * ldy + n) + d);
+        for (int64_t j = 0; j < ad.r; ++j) d = __builtin_fmaf(S[m * rp + j], up[j], d);
+        Y[m * ldy + n] += d;
     }
 }
 
@@ -371,80 +603,108 @@ __global__ __launch_bounds__(GROUP_NT) void group_kernel(int64_t M, const int32_
 }
 
 // ---------------------------------------------------------------- gradients of the low-rank factors
-// G[i] = sum over adapter i's rows t of L[t] (x) R[t] (r x C).  The rows,
-// grouped by adapter (group_kernel), are cut into chunks of CH; workgroup
-// (column block, chunk) sums the pieces of the adapters that its chunk meets,
-// each into slot chunk + i of the partials (chunks and adapters both ascend
-// along the list, so a piece's slot is its own), and a second kernel adds each
-// adapter's slots in order.  t is the k of an FP32 MFMA, so both operands are
-// read as they lie: rows of R 128 bits per lane, a lane's elements going to as
-// many instructions.
+// G[i] = sum over adapter i's rows t of L[t] (x) R[t] (r x C), for one or two
+// jobs (the two factors) in one launch.  The rows, grouped by adapter
+// (group_kernel), are cut into chunks of CH; workgroup (column block, chunk)
+// sums the pieces of the adapters that its chunk meets, each into slot
+// chunk + i of the partials (chunks and adapters both ascend along the list, so
+// a piece's slot is its own), and a second kernel adds each adapter's slots in
+// order.  t is the k of an FP32 MFMA, so both operands are read as they lie:
+// rows of R 128 bits per lane, a lane's elements going to as many instructions.
 constexpr int GRAD_WAVES = 4;
 
+template <class T>
+struct GradJob {
+    const float *L;           // as put_s writes it
+    const T *R;
+    int64_t ldr, C;
+    T *G;
+    float *partials;
+    int blocks;               // column blocks
+    bool vec, transposed;
+};
+template <class T>
+struct GradJobs {
+    GradJob<T> job[2];
+    int64_t n, r, rp, CH;
+    const int32_t *offs, *rows;
+};
+
 template <class T, int RB>
-__global__ __launch_bounds__(64 * GRAD_WAVES) void lowrank_grad_kernel(int64_t C, int64_t n, int64_t r, int64_t rp,
-                                                                       const float *L, const T *R, int64_t ldr,
-                                                                       bool vec, const int32_t *offs,
-                                                                       const int32_t *rows, int64_t CH,
-                                                                       float *partials)
+__global__ __launch_bounds__(64 * GRAD_WAVES) void lowrank_grad_kernel(GradJobs<T> a)
 {
-    constexpr int V = Elem<T>::VEC;
+    constexpr int V = Elem<T>::VEC, U = 4;
     __shared__ __attribute__((aligned(16))) f32x4_t lds[GRAD_WAVES][RB][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * (16 * V) + (lane & 15) * V, r0 = (int64_t)blockIdx.z * (16 * RB);
-    const int64_t total = offs[n], first = (int64_t)blockIdx.y * CH, end = lmin(first + CH, total);
+    const bool second = (int)blockIdx.x >= a.job[0].blocks;
+    const GradJob<T> &g = a.job[second ? 1 : 0];
+    const int64_t C = g.C, c = (int64_t)(blockIdx.x - (second ? a.job[0].blocks : 0)) * (16 * V) + (lane & 15) * V;
+    const int64_t r0 = (int64_t)blockIdx.z * (16 * RB);
+    const int64_t total = a.offs[a.n], first = (int64_t)blockIdx.y * a.CH, end = lmin(first + a.CH, total);
     if (first >= end) return;
     // the adapter that holds position `first`: the last i with offs[i] <= first
-    int64_t lo = 0, hi = n - 1;
+    int64_t lo = 0, hi = a.n - 1;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) >> 1;
-        if (offs[mid] <= first) lo = mid;
+        if (a.offs[mid] <= first) lo = mid;
         else hi = mid - 1;
     }
-    for (int64_t i = lo; i < n && offs[i] < end; ++i) {
-        const int64_t pb = offs[i] > first ? offs[i] : first, pe = lmin(offs[i + 1], end);
+    const bool vec = g.vec && c + V <= C;
+    for (int64_t i = lo; i < a.n && a.offs[i] < end; ++i) {
+        const int64_t pb = a.offs[i] > first ? a.offs[i] : first, pe = lmin(a.offs[i + 1], end);
         if (pb >= pe) continue;
         f32x4_t acc[RB][V];
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[b][e] = f32x4_t{};
-        for (int64_t p = pb + wave * 4; p < pe; p += GRAD_WAVES * 4) {
-            const int64_t q = p + (lane >> 4);
-            float l[RB], x[V];
+        // U groups of four rows at a time: their indices, then their loads
+        for (int64_t p = pb + wave * 4; p < pe; p += GRAD_WAVES * 4 * U) {
+            int64_t t[U];
+            bool in[U];
 #pragma unroll
-            for (int b = 0; b < RB; ++b) l[b] = 0.0f;
+            for (int u = 0; u < U; ++u) {
+                const int64_t q = p + u * GRAD_WAVES * 4 + (lane >> 4);
+                in[u] = q < pe;
+                t[u] = a.rows[in[u] ? q : pe - 1];
+            }
+            float l[U][RB], x[U][V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = 0.0f;
-            if (q < pe) {
-                const int64_t t = rows[q];
+            for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int b = 0; b < RB; ++b) {
                     const int64_t rr = r0 + b * 16 + (lane & 15);
-                    if (rr < rp) l[b] = L[t * rp + rr];
+                    l[u][b] = get_s<T>(g.L, a.rp, t[u], rr < a.rp ? rr : 0);
                 }
-                const T *src = R + t * ldr + c;
-                if (vec && c + V <= C) {
+                const T *src = g.R + t[u] * g.ldr + c;
+                if (vec) {
                     const u32x4_t v = *reinterpret_cast<const u32x4_t *>(src);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        if constexpr (sizeof(T) == 4) x[e] = __uint_as_float(v[e]);
-                        else x[e] = bf2f((uint16_t)(v[e >> 1] >> (16 * (e & 1))));
+                        if constexpr (sizeof(T) == 4) x[u][e] = __uint_as_float(v[e]);
+                        else x[u][e] = bf2f((uint16_t)(v[e >> 1] >> (16 * (e & 1))));
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        if (c + e < C) x[e] = Elem<T>::load(src + e);
+                    for (int e = 0; e < V; ++e) x[u][e] = c + e < C ? Elem<T>::load(src + e) : 0.0f;
                 }
             }
 #pragma unroll
-            for (int b = 0; b < RB; ++b)
+            for (int u = 0; u < U; ++u) {
+                // rows past the piece count zero times zero
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    acc[b][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(l[b], x[e], acc[b][e], 0, 0, 0);
+                for (int b = 0; b < RB; ++b) l[u][b] = in[u] ? l[u][b] : 0.0f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[u][e] = in[u] ? x[u][e] : 0.0f;
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        acc[b][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(l[u][b], x[u][e], acc[b][e], 0, 0, 0);
+            }
         }
         // waves in order; result (rank row 4 (lane >> 4) + k, column c + e)
-        float *const part = partials + ((int64_t)blockIdx.y + i) * r * C;
+        float *const part = g.partials + ((int64_t)blockIdx.y + i) * a.r * C;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             __syncthreads();
@@ -458,7 +718,7 @@ __global__ __launch_bounds__(64 * GRAD_WAVES) void lowrank_grad_kernel(int64_t C
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int64_t rr = r0 + b * 16 + 4 * (lane >> 4) + k;
-                    if (rr < r && c + e < C) part[rr * C + c + e] = v[k];
+                    if (rr < a.r && c + e < C) part[rr * C + c + e] = v[k];
                 }
             }
         }
@@ -466,55 +726,81 @@ __global__ __launch_bounds__(64 * GRAD_WAVES) void lowrank_grad_kernel(int64_t C
 }
 
 template <class T>
-__global__ __launch_bounds__(256) void lowrank_grad_sum_kernel(int64_t C, int64_t r, const int32_t *offs, int64_t CH,
-                                                               const float *partials, bool transposed, T *G)
+__global__ __launch_bounds__(256) void lowrank_grad_sum_kernel(GradJobs<T> a)
 {
-    const int64_t i = blockIdx.y, o = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (o >= r * C) return;
-    const int64_t pb = offs[i], pe = offs[i + 1];
+    const GradJob<T> &g = a.job[blockIdx.z];
+    const int64_t i = blockIdx.y, o = (int64_t)blockIdx.x * 256 + threadIdx.x, C = g.C;
+    if (o >= a.r * C) return;
+    const int64_t pb = a.offs[i], pe = a.offs[i + 1];
     float v = 0.0f;
     if (pb < pe)
-        for (int64_t ch = pb / CH; ch <= (pe - 1) / CH; ++ch) v += partials[(ch + i) * r * C + o];
+        for (int64_t ch = pb / a.CH; ch <= (pe - 1) / a.CH; ++ch) v += g.partials[(ch + i) * a.r * C + o];
     const int64_t rr = o / C, c = o % C;
-    G[i * r * C + (transposed ? c * r + rr : o)] = Elem<T>::store(v);
+    g.G[i * a.r * C + (g.transposed ? c * a.r + rr : o)] = Elem<T>::store(v);
 }
 
-int64_t grad_chunk(int64_t M, int64_t C, int64_t r, int vec, int num_cus)
+// Rows per chunk: about four workgroups per CU over the column blocks.
+int64_t grad_chunk(int64_t M, int64_t C0, int64_t C1, int64_t r, int vec, int num_cus)
 {
-    if (M == 0 || C == 0) return 16;
-    const int64_t blocks = ((C + 16 * vec - 1) / (16 * vec)) * ((r + 63) / 64);
+    const int64_t blocks = ((C0 + 16 * vec - 1) / (16 * vec) + (C1 + 16 * vec - 1) / (16 * vec)) * ((r + 63) / 64);
+    if (M == 0 || blocks == 0) return 16;
     int64_t chunks = (4 * (int64_t)num_cus + blocks - 1) / blocks;
     if (chunks > (M + 63) / 64) chunks = (M + 63) / 64;
     return round_up((M + chunks - 1) / chunks, 16);
 }
 
 template <class T>
-hipError_t launch_lowrank_grad_t(int64_t M, int64_t C, int64_t n, int64_t r, const float *L, const T *R, int64_t ldr,
-                                 const int32_t *offs, const int32_t *rows, bool transposed, T *G, float *partials,
-                                 int num_cus, hipStream_t stream)
+hipError_t launch_lowrank_grad_t(const LowrankGrads &q, int num_cus, hipStream_t stream)
 {
     constexpr int V = Elem<T>::VEC;
-    const int64_t CH = grad_chunk(M, C, r, V, num_cus), chunks = (M + CH - 1) / CH, rp = rank_pad(r);
-    const bool vec = ldr % V == 0 && aligned(R, 16);
-    const unsigned cb = (unsigned)((C + 16 * V - 1) / (16 * V));
-    const dim3 block(64 * GRAD_WAVES);
-    if (M > 0) {
-        if (r <= 16)
-            hipLaunchKernelGGL((lowrank_grad_kernel<T, 1>), dim3(cb, (unsigned)chunks, 1), block, 0, stream, C, n, r,
-                               rp, L, R, ldr, vec, offs, rows, CH, partials);
-        else if (r <= 32)
-            hipLaunchKernelGGL((lowrank_grad_kernel<T, 2>), dim3(cb, (unsigned)chunks, 1), block, 0, stream, C, n, r,
-                               rp, L, R, ldr, vec, offs, rows, CH, partials);
+    GradJobs<T> a{};
+    a.n = q.n; a.r = q.r; a.rp = rank_pad(q.r);
+    a.offs = q.offs; a.rows = q.rows;
+    int jobs = 0;
+    int64_t most = 0, blocks = 0;
+    const int64_t C0 = q.down ? q.K : 0, C1 = q.up ? q.N : 0;
+    a.CH = grad_chunk(q.M, C0, C1, q.r, V, num_cus);
+    const int64_t slots = (q.M + a.CH - 1) / a.CH + q.n;
+    auto add = [&](const float *L, const void *R, int64_t ldr, int64_t C, void *G, float *partials, bool transposed) {
+        GradJob<T> &g = a.job[jobs++];
+        g.L = L; g.R = (const T *)R; g.ldr = ldr; g.C = C;
+        g.G = (T *)G; g.partials = partials;
+        g.blocks = (int)((C + 16 * V - 1) / (16 * V));
+        g.vec = ldr % V == 0 && aligned(R, 16);
+        g.transposed = transposed;
+        blocks += g.blocks;
+        if (C > most) most = C;
+    };
+    if (q.down) add(q.P, q.X, q.ldx, q.K, q.down, q.partials, false);
+    if (q.up) add(q.S, q.dY, q.lddy, q.N, q.up, q.partials + slots * q.r * C0, true);
+    if (jobs == 0) return hipSuccess;
+    if (q.M > 0) {
+        const unsigned chunks = (unsigned)((q.M + a.CH - 1) / a.CH);
+        const dim3 block(64 * GRAD_WAVES);
+        if (q.r <= 16)
+            hipLaunchKernelGGL((lowrank_grad_kernel<T, 1>), dim3((unsigned)blocks, chunks, 1), block, 0, stream, a);
+        else if (q.r <= 32)
+            hipLaunchKernelGGL((lowrank_grad_kernel<T, 2>), dim3((unsigned)blocks, chunks, 1), block, 0, stream, a);
         else
-            hipLaunchKernelGGL((lowrank_grad_kernel<T, 4>), dim3(cb, (unsigned)chunks, (unsigned)((r + 63) / 64)),
-                               block, 0, stream, C, n, r, rp, L, R, ldr, vec, offs, rows, CH, partials);
+            hipLaunchKernelGGL((lowrank_grad_kernel<T, 4>), dim3((unsigned)blocks, chunks, (unsigned)((q.r + 63) / 64)),
+                               block, 0, stream, a);
     }
-    hipLaunchKernelGGL((lowrank_grad_sum_kernel<T>), dim3((unsigned)((r * C + 255) / 256), (unsigned)n), dim3(256), 0,
-                       stream, C, r, offs, CH, partials, transposed, G);
+    hipLaunchKernelGGL((lowrank_grad_sum_kernel<T>),
+                       dim3((unsigned)((q.r * most + 255) / 256), (unsigned)q.n, (unsigned)jobs), dim3(256), 0, stream,
+                       a);
     return hipGetLastError();
 }
 
 }  // namespace
+
+int64_t few_rows_partial_floats(int dtype, int64_t M, int64_t N, int64_t K, int gate, int num_cus)
+{
+    if (gate < 0) return token_slices(dtype, N, K, num_cus) * M * N;
+    // a gated product with enough outputs for a workgroup per CU runs in one pass
+    if (N >= (int64_t)16 * num_cus) return 0;
+    const int s = token_slices(dtype, 2 * N, K, num_cus);
+    return s > 1 ? s * M * 2 * N : 0;
+}
 
 hipError_t launch_few_rows(int dtype, const FewRows &a, int num_cus, hipStream_t stream)
 {
@@ -525,22 +811,15 @@ hipError_t launch_few_rows(int dtype, const FewRows &a, int num_cus, hipStream_t
 hipError_t launch_shrink(int dtype, int64_t M, int64_t K, const void *X, int64_t ldx, const Adapters &ad, float *S,
                          int num_cus, hipStream_t stream)
 {
-    (void)num_cus;
-    return dtype == kF32 ? launch_shrink_t<float>(M, K, (const float *)X, ldx, ad, S, stream)
-                         : launch_shrink_t<uint16_t>(M, K, (const uint16_t *)X, ldx, ad, S, stream);
+    return dtype == kF32 ? launch_shrink_t<float>(M, K, (const float *)X, ldx, ad, S, num_cus, stream)
+                         : launch_shrink_t<uint16_t>(M, K, (const uint16_t *)X, ldx, ad, S, num_cus, stream);
 }
 
-hipError_t launch_expand(int dtype, int64_t M, int64_t N, const float *S, const Adapters &ad, void *Y, int64_t ldy,
-                         int num_cus, hipStream_t stream)
+hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &ad, float *Y, int64_t ldy,
+                         hipStream_t stream)
 {
-    (void)num_cus;
     const dim3 grid((unsigned)((N + 255) / 256), (unsigned)(M < 32768 ? M : 32768));
-    if (dtype == kF32)
-        hipLaunchKernelGGL((expand_kernel<float>), grid, dim3(256), 0, stream, M, N, S, rank_pad(ad.r), ad, (float *)Y,
-                           ldy);
-    else
-        hipLaunchKernelGGL((expand_kernel<uint16_t>), grid, dim3(256), 0, stream, M, N, S, rank_pad(ad.r), ad,
-                           (uint16_t *)Y, ldy);
+    hipLaunchKernelGGL(expand_kernel, grid, dim3(256), 0, stream, M, N, S, rank_pad(ad.r), ad, Y, ldy);
     return hipGetLastError();
 }
 
@@ -550,23 +829,24 @@ hipError_t launch_group(int64_t M, const int32_t *ids, int64_t n, int32_t *offs,
     return hipGetLastError();
 }
 
-int64_t lowrank_grad_floats(int64_t M, int64_t C, int64_t n, int64_t r, int num_cus)
+int64_t lowrank_grad_floats(int dtype, int64_t M, int64_t K, int64_t N, int64_t n, int64_t r, int num_cus)
 {
-    // the chunk of either type's column blocks, whichever makes more slots
-    const int64_t a = grad_chunk(M, C, r, 4, num_cus), b = grad_chunk(M, C, r, 8, num_cus);
-    const int64_t CH = a < b ? a : b;
-    return ((M + CH - 1) / CH + n) * r * C;
+    // the most slots of any choice of the two gradients
+    const int vec = dtype == kF32 ? 4 : 8;
+    int64_t most = 0;
+    for (int which = 1; which < 4; ++which) {
+        const int64_t C0 = which & 1 ? K : 0, C1 = which & 2 ? N : 0;
+        const int64_t CH = grad_chunk(M, C0, C1, r, vec, num_cus);
+        const int64_t floats = ((M + CH - 1) / CH + n) * r * (C0 + C1);
+        if (floats > most) most = floats;
+    }
+    return most;
 }
 
-hipError_t launch_lowrank_grad(int dtype, int64_t M, int64_t C, int64_t n, int64_t r, const float *L, const void *R,
-                               int64_t ldr, const int32_t *offs, const int32_t *rows, bool transposed, void *G,
-                               float *partials, int num_cus, hipStream_t stream)
+hipError_t launch_lowrank_grad(int dtype, const LowrankGrads &q, int num_cus, hipStream_t stream)
 {
-    if (dtype == kF32)
-        return launch_lowrank_grad_t<float>(M, C, n, r, L, (const float *)R, ldr, offs, rows, transposed, (float *)G,
-                                            partials, num_cus, stream);
-    return launch_lowrank_grad_t<uint16_t>(M, C, n, r, L, (const uint16_t *)R, ldr, offs, rows, transposed,
-                                           (uint16_t *)G, partials, num_cus, stream);
+    return dtype == kF32 ? launch_lowrank_grad_t<float>(q, num_cus, stream)
+                         : launch_lowrank_grad_t<uint16_t>(q, num_cus, stream);
 }
 
 }  // namespace sgemm_emu_dev

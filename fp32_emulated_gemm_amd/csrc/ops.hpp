@@ -24,30 +24,41 @@ struct Adapters {
 };
 inline int64_t rank_pad(int64_t r) { return round_up(r, 16); }   // row pitch of S (zeros past r)
 
-// S[t][0..rp) = scale[i] * down[i] X[t] (zeros for rows without an adapter),
-// float32, rp = rank_pad(r).
+// S[t][0..rp) = scale[i] * down[i] X[t] (zeros for rows without an adapter and
+// past r), rp = rank_pad(r): floats for FP32; for bfloat16 rp high and rp low
+// BF16 parts in a row's 4 rp bytes.
 hipError_t launch_shrink(int dtype, int64_t M, int64_t K, const void *X, int64_t ldx, const Adapters &ad, float *S,
                          int num_cus, hipStream_t stream);
 
-// Y[t] += up[i] S[t] for the rows that have an adapter.
-hipError_t launch_expand(int dtype, int64_t M, int64_t N, const float *S, const Adapters &ad, void *Y, int64_t ldy,
-                         int num_cus, hipStream_t stream);
+// FP32: Y[t] += up[i] S[t] for the rows that have an adapter.
+hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &ad, float *Y, int64_t ldy,
+                         hipStream_t stream);
 
 // offs[0..n]: where each adapter's rows start in rows[]; rows[]: the row
 // numbers that have an adapter, grouped by it, ascending inside a group.
 hipError_t launch_group(int64_t M, const int32_t *ids, int64_t n, int32_t *offs, int32_t *rows, hipStream_t stream);
 
-// G[i] = sum over the adapter's rows t of L[t][0..r) (x) R[t][0..C): n x r x C,
-// or n x C x r with `transposed`, in the operands' type.  L float32 with pitch
-// rank_pad(r); partials: lowrank_grad_floats() floats.
-int64_t lowrank_grad_floats(int64_t M, int64_t C, int64_t n, int64_t r, int num_cus);
-hipError_t launch_lowrank_grad(int dtype, int64_t M, int64_t C, int64_t n, int64_t r, const float *L, const void *R,
-                               int64_t ldr, const int32_t *offs, const int32_t *rows, bool transposed, void *G,
-                               float *partials, int num_cus, hipStream_t stream);
+// down[i] = sum over the adapter's rows of P[t] (x) X[t] (n x r x K), up[i] = sum
+// of dY[t] (x) S[t] (n x N x r); either may be null.  P, S as launch_shrink writes
+// them; partials: lowrank_grad_floats() floats.
+struct LowrankGrads {
+    int64_t M, K, N, n, r;
+    const float *P, *S;
+    const void *X;
+    int64_t ldx;
+    const void *dY;
+    int64_t lddy;
+    const int32_t *offs, *rows;
+    void *down, *up;
+    float *partials;
+};
+int64_t lowrank_grad_floats(int dtype, int64_t M, int64_t K, int64_t N, int64_t n, int64_t r, int num_cus);
+hipError_t launch_lowrank_grad(int dtype, const LowrankGrads &q, int num_cus, hipStream_t stream);
 
 // ---------------------------------------------------------------- few rows
-// Y = X W^T + bias (+ up[i] S[t]), or, with gate >= 0, the gated product of a
-// weight of 2F rows (N = F).  Any M; made for few rows.
+// At most kFewRows rows: Y = X W^T + bias + up[i] (scale[i] down[i] X[t]), or,
+// with gate >= 0, the gated product of a weight of 2F rows (N = F).
+constexpr int64_t kFewRows = 64;
 struct FewRows {
     int64_t M, N, K;
     const void *X;
@@ -59,8 +70,10 @@ struct FewRows {
     void *Y;
     int64_t ldy;
     const Adapters *ad;     // or null
-    const float *S;
+    float *S;               // with adapters: M x rank_pad(r) floats of scratch
+    float *partials;        // few_rows_partial_floats() floats (null where that is 0)
 };
+int64_t few_rows_partial_floats(int dtype, int64_t M, int64_t N, int64_t K, int gate, int num_cus);
 hipError_t launch_few_rows(int dtype, const FewRows &a, int num_cus, hipStream_t stream);
 
 // ---------------------------------------------------------------- bfloat16 GEMM
@@ -76,12 +89,12 @@ struct Bf16Gemm {
     uint16_t *C;             // M x N, or M x N/2 with a gate
     int64_t ldc;
     int gate;                // -1: none; else B holds F = N/2 gate rows, then F up rows
-    uint16_t *Z;             // with a gate: M x N pre-activations (gate | up), or null
+    float *Z;                // with a gate: pre-activations (see z_pitch), or null
     int64_t ldz;
-    const int32_t *ids;      // adapters (or null): rows' ids, S (M x rp), up (n x N x r)
+    const int32_t *ids;      // adapters (or null): rows' ids, up (n x N x r)
     int64_t n, r, rp;
     const uint16_t *up;
-    const float *S;
+    const uint16_t *S;       // M x 2 rp: high parts, low parts
     float *partials;         // K slices: splits x M x N floats
     int splits;
     int64_t k_per_split;
@@ -99,24 +112,31 @@ hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64
 // bfloat16 rows x cols -> rows x pad_k(cols), zeros past cols.
 hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,
                               hipStream_t stream);
-// bfloat16 rows x cols -> cols x pad_k(rows), zeros past rows.
+// bfloat16 rows x cols -> cols x out_rows with pitch ldp, zeros past rows.
 hipError_t launch_transpose_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,
-                                   hipStream_t stream);
+                                   int64_t out_rows, int64_t ldp, hipStream_t stream);
 // src n x rows x cols -> dst n x cols x rows (contiguous).
 hipError_t launch_transpose_bank(int dtype, int64_t n, int64_t rows, int64_t cols, const void *src, void *dst,
                                  hipStream_t stream);
 
-// H = act(Z[:, :F]) * Z[:, F:], float32.
-hipError_t launch_gate(int64_t M, int64_t F, const float *Z, int64_t ldz, int gate, float *H, int64_t ldh,
+// Pre-activations Z are floats whatever the call's type: rows of z_pitch(F), the
+// gate's from column 0, the up projection's from column z_pitch(F) / 2.
+inline int64_t z_pitch(int64_t F) { return 2 * round_up(F, 8); }
+
+// H = act(gate) * up of Z's halves, `up` columns apart, float32.
+hipError_t launch_gate(int64_t M, int64_t F, const float *Z, int64_t ldz, int64_t up, int gate, float *H, int64_t ldh,
                        hipStream_t stream);
 
-// dZ (M x 2F, pitch ldd, columns 2F..ldd zero; null: skipped), its transpose
-// (2F x pad_k(M), zeros past M; null: skipped) and the column sums' partials
-// (gate_tiles(M) x 2F floats; null: skipped) from Z and dH.
+// Z (M x 2F) -> rows of z_pitch(F).
+hipError_t launch_copy_z(int64_t M, int64_t F, const float *Z, float *out, hipStream_t stream);
+
+// From Z and dH: dZ (rows of dz_pitch(F): gate from 0, up from dz_pitch / 2,
+// zeros between and after), its transpose (2F x pad_k(M), zeros past M), and the
+// column sums' partials (gate_tiles(M) x 2F floats); each may be null.
+inline int64_t dz_pitch(int64_t F) { return 2 * round_up(F, 32); }
 inline int64_t gate_tiles(int64_t M) { return (M + 63) / 64; }
-hipError_t launch_gate_backward(int dtype, int64_t M, int64_t F, const void *Z, int64_t ldz, const void *dH,
-                                int64_t lddh, int gate, void *dZ, int64_t ldd, void *dZt, float *sums,
-                                hipStream_t stream);
+hipError_t launch_gate_backward(int dtype, int64_t M, int64_t F, const float *Z, const void *dH, int64_t lddh,
+                                int gate, void *dZ, void *dZt, float *sums, hipStream_t stream);
 // out[c] = sum over t of sums[t][c], t ascending.
 hipError_t launch_sum_tiles(int dtype, int64_t tiles, int64_t cols, const float *sums, void *out, hipStream_t stream);
 

@@ -18,8 +18,6 @@ constexpr int64_t kMaxBytes = INT64_MAX / 8;
 constexpr int64_t kMaxLd = ((int64_t)1 << 32) / (128 * 4) - 64;   // as the GEMM's: 128-row tiles in 32-bit offsets
 constexpr int64_t kMaxExtent = 65535 * 64;                        // grid extents of 64-wide tiles
 constexpr int64_t kMaxAdapters = 65535;
-// Rows up to which the forward calls read the weight once, without tiles.
-constexpr int64_t kFewRows = 64;
 
 int64_t size_of(int dtype) { return dtype == SGEMM_EMU_F32 ? 4 : 2; }
 bool dtype_ok(int dtype) { return dtype == SGEMM_EMU_F32 || dtype == SGEMM_EMU_BF16; }
@@ -107,18 +105,20 @@ bool gated_few(int64_t M, int64_t K, const void *Z) { return M <= kFewRows && Z 
 
 struct GatedWs {
     uint16_t *plan, *x;   // W and X laid out
-    float *z;             // FP32 pre-activations
+    float *z;             // FP32 pre-activations, or few rows' K slices
     int64_t bytes;
 };
 GatedWs gated_ws(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *W, int64_t ldw,
-                 const void *plan, const void *Z, void *ws)
+                 const void *plan, const void *Z, int num_cus, void *ws)
 {
     Carve c(ws);
     GatedWs w{};
-    if (M == 0 || F == 0 || gated_few(M, K, Z)) return w;
-    if (dtype == SGEMM_EMU_F32) {
+    if (M == 0 || F == 0) return w;
+    if (gated_few(M, K, Z)) {
+        w.z = c.take<float>(few_rows_partial_floats(dtype, M, F, K, SGEMM_EMU_GATE_SILU, num_cus));
+    } else if (dtype == SGEMM_EMU_F32) {
         if (plan == nullptr) w.plan = c.take<uint16_t>(3 * 2 * F * pad_k(K));
-        if (Z == nullptr) w.z = c.take<float>(M * 2 * F);
+        w.z = c.take<float>(M * 2 * F);
     } else {
         if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(2 * F * pad_k(K));
         if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
@@ -128,8 +128,8 @@ GatedWs gated_ws(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int6
 }
 
 struct GatedBackWs {
-    void *dz, *dzt;          // M x pad(2F), 2F x pad(M)
-    uint16_t *wt, *xt;       // W^T and X^T laid out
+    void *dz, *dzt;          // M x dz_pitch(F), 2F x pad(M)
+    uint16_t *wt, *xt;       // W^T (columns as dz's) and X^T laid out
     float *sums, *part_x, *part_w;
     int64_t bytes;
 };
@@ -137,18 +137,36 @@ GatedBackWs gated_back_ws(int dtype, int64_t M, int64_t F, int64_t K, int num_cu
 {
     Carve c(ws);
     GatedBackWs w{};
-    const int64_t size = size_of(dtype), comps = dtype == SGEMM_EMU_F32 ? 3 : 1, n2 = 2 * F;
-    w.dz = c.take<char>(M * pad_k(n2) * size);
-    w.dzt = c.take<char>(n2 * pad_k(M) * size);
-    w.wt = c.take<uint16_t>(comps * K * pad_k(n2));
+    const int64_t size = size_of(dtype), comps = dtype == SGEMM_EMU_F32 ? 3 : 1, pitch = dz_pitch(F);
+    w.dz = c.take<char>(M * pitch * size);
+    w.dzt = c.take<char>(2 * F * pad_k(M) * size);
+    w.wt = c.take<uint16_t>(comps * K * pitch);
     w.xt = c.take<uint16_t>(comps * K * pad_k(M));
-    w.sums = c.take<float>(gate_tiles(M) * n2);
+    w.sums = c.take<float>(gate_tiles(M) * 2 * F);
     if (dtype == SGEMM_EMU_BF16) {
-        w.part_x = c.take<float>(bf16_gemm_partial_floats(M, K, pad_k(n2), true, num_cus));
-        w.part_w = c.take<float>(bf16_gemm_partial_floats(n2, K, pad_k(M), true, num_cus));
+        w.part_x = c.take<float>(bf16_gemm_partial_floats(M, K, pitch, true, num_cus));
+        w.part_w = c.take<float>(bf16_gemm_partial_floats(2 * F, K, pad_k(M), true, num_cus));
     }
     w.bytes = c.bytes;
     return w;
+}
+
+// W^T with the columns of dZ: F gate columns, zeros to dz_pitch / 2, F up columns, zeros.
+hipError_t lay_out_wt(int dtype, int64_t F, int64_t K, const void *W, int64_t ldw, uint16_t *wt, int num_cus,
+                      hipStream_t s)
+{
+    const int64_t pitch = dz_pitch(F), half = pitch / 2, plane = K * pitch;
+    for (int64_t h = 0; h < 2; ++h) {
+        uint16_t *const P = wt + h * half;
+        hipError_t e;
+        if (dtype == SGEMM_EMU_F32)
+            e = launch_split_transpose(F, K, (const float *)W + h * F * ldw, ldw, P, P + plane, P + 2 * plane, pitch,
+                                       num_cus, s, false, half);
+        else
+            e = launch_transpose_padded(F, K, (const uint16_t *)W + h * F * ldw, ldw, P, half, pitch, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // ---------------------------------------------------------------- adapters
@@ -161,25 +179,28 @@ int check_adapters(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_
     return SGEMM_EMU_OK;
 }
 
+// Few rows read W in one pass; low-rank activations to keep come from the tiles' path.
+bool adapter_few(int64_t M, const float *S) { return M <= kFewRows && S == nullptr; }
+
 struct AdapterWs {
     uint16_t *plan, *x;
-    float *s;
+    float *s, *partials;
     int64_t bytes;
 };
 AdapterWs adapter_ws(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, const void *W,
-                     int64_t ldw, const void *plan, int64_t n, int64_t r, const float *S, void *ws)
+                     int64_t ldw, const void *plan, int64_t n, int64_t r, const float *S, int num_cus, void *ws)
 {
     Carve c(ws);
     AdapterWs w{};
     if (M == 0 || N == 0) return w;
     if (n > 0 && r > 0 && S == nullptr) w.s = c.take<float>(M * rank_pad(r));
-    if (!(M <= kFewRows || K == 0)) {
-        if (dtype == SGEMM_EMU_F32) {
-            if (plan == nullptr) w.plan = c.take<uint16_t>(3 * N * pad_k(K));
-        } else {
-            if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(N * pad_k(K));
-            if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
-        }
+    if (adapter_few(M, S)) {
+        w.partials = c.take<float>(few_rows_partial_floats(dtype, M, N, K, -1, num_cus));
+    } else if (dtype == SGEMM_EMU_F32) {
+        if (plan == nullptr) w.plan = c.take<uint16_t>(3 * N * pad_k(K));
+    } else {
+        if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(N * pad_k(K));
+        if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
     }
     w.bytes = c.bytes;
     return w;
@@ -190,7 +211,7 @@ struct AdapterBackWs {
     float *p;                  // M x pad16(r)
     uint16_t *dy;              // dY laid out
     int32_t *offs, *rows;
-    float *part_down, *part_up;
+    float *partials;
     int64_t bytes;
 };
 AdapterBackWs adapter_back_ws(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r, int num_cus, void *ws)
@@ -205,8 +226,7 @@ AdapterBackWs adapter_back_ws(int dtype, int64_t M, int64_t N, int64_t K, int64_
         w.p = c.take<float>(M * rank_pad(r));
         w.offs = c.take<int32_t>(n + 1);
         w.rows = c.take<int32_t>(M);
-        w.part_down = c.take<float>(lowrank_grad_floats(M, K, n, r, num_cus));
-        w.part_up = c.take<float>(lowrank_grad_floats(M, N, n, r, num_cus));
+        w.partials = c.take<float>(lowrank_grad_floats(dtype, M, K, N, n, r, num_cus));
     }
     w.bytes = c.bytes;
     return w;
@@ -248,7 +268,7 @@ int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, 
             LAUNCH(launch_split_padded(rows, cols, (const float *)W, ldw, P, s));
         }
     } else if (transposed) {
-        LAUNCH(launch_transpose_padded(rows, cols, (const uint16_t *)W, ldw, P, s));
+        LAUNCH(launch_transpose_padded(rows, cols, (const uint16_t *)W, ldw, P, pad_k(rows), pad_k(rows), s));
     } else {
         LAUNCH(launch_copy_padded(rows, cols, (const uint16_t *)W, ldw, P, s));
     }
@@ -259,25 +279,26 @@ int64_t sgemm_emu_gated_linear_workspace(int dtype, int64_t M, int64_t F, int64_
                                          const void *W, int64_t ldw, const void *plan, const void *Z)
 {
     CHECK(check_gated(dtype, M, F, K, SGEMM_EMU_GATE_SILU));
-    return gated_ws(dtype, M, F, K, X, ldx, W, ldw, plan, Z, nullptr).bytes;
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    return gated_ws(dtype, M, F, K, X, ldx, W, ldw, plan, Z, num_cus, nullptr).bytes;
 }
 
 int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *W,
-                           int64_t ldw, const void *plan, const void *bias, int gate, void *H, int64_t ldh, void *Z,
-                           int64_t ldz, void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream)
+                           int64_t ldw, const void *plan, const void *bias, int gate, void *H, int64_t ldh, float *Z,
+                           void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream)
 {
     CHECK(check_gated(dtype, M, F, K, gate));
     CHECK(check_operand(dtype, M, K, X, ldx));
     CHECK(check_operand(dtype, 2 * F, K, W, ldw));
     CHECK(check_vector(2 * F, bias, size_of(dtype), true));
     CHECK(check_operand(dtype, M, F, H, ldh));
-    CHECK(check_operand(dtype, M, 2 * F, Z, ldz, true));
-    if ((uintptr_t)plan % 16 != 0) return SGEMM_EMU_EINVAL;
-    const GatedWs w = gated_ws(dtype, M, F, K, X, ldx, W, ldw, plan, Z, ws);
-    CHECK(check_ws(ws, ws_bytes, w.bytes));
+    if ((uintptr_t)plan % 16 != 0 || (uintptr_t)Z % 16 != 0) return SGEMM_EMU_EINVAL;
     if (M == 0 || F == 0) return SGEMM_EMU_OK;
     int num_cus = 0;
     CHECK(current_cus(&num_cus));
+    const GatedWs w = gated_ws(dtype, M, F, K, X, ldx, W, ldw, plan, Z, num_cus, ws);
+    CHECK(check_ws(ws, ws_bytes, w.bytes));
     hipStream_t s = (hipStream_t)stream;
     if (gated_few(M, K, Z)) {
         FewRows a{};
@@ -285,16 +306,17 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
         a.X = X; a.ldx = ldx; a.W = W; a.ldw = ldw;
         a.bias = bias; a.gate = gate;
         a.Y = H; a.ldy = ldh;
+        a.partials = w.z;
         LAUNCH(launch_few_rows(dtype, a, num_cus, s));
         return SGEMM_EMU_OK;
     }
     if (dtype == SGEMM_EMU_F32) {
         if (w.plan != nullptr) LAUNCH(launch_split_padded(2 * F, K, (const float *)W, ldw, w.plan, s));
-        float *z = w.z != nullptr ? w.z : (float *)Z;
-        const int64_t ld = w.z != nullptr ? 2 * F : ldz;
         CHECK(product_f32(M, 2 * F, K, (const float *)X, ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
-                          (const float *)bias, z, ld, num_cus, s));
-        LAUNCH(launch_gate(M, F, z, ld, gate, (float *)H, ldh, s));
+                          (const float *)bias, w.z, 2 * F, num_cus, s));
+        LAUNCH(launch_gate(M, F, w.z, 2 * F, F, gate, (float *)H, ldh, s));
+        if (Z != nullptr)
+            LAUNCH(launch_copy_z(M, F, w.z, Z, s));
         return SGEMM_EMU_OK;
     }
     Bf16Gemm g{};
@@ -314,7 +336,7 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
     g.bias = (const uint16_t *)bias;
     g.C = (uint16_t *)H; g.ldc = ldh;
     g.gate = gate;
-    g.Z = (uint16_t *)Z; g.ldz = ldz;
+    g.Z = Z; g.ldz = z_pitch(F);
     LAUNCH(launch_bf16_gemm(g, num_cus, s));
     return SGEMM_EMU_OK;
 }
@@ -328,14 +350,14 @@ int64_t sgemm_emu_gated_linear_backward_workspace(int dtype, int64_t M, int64_t 
 }
 
 int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx,
-                                    const void *W, int64_t ldw, const void *Z, int64_t ldz, int gate, const void *dH,
+                                    const void *W, int64_t ldw, const float *Z, int gate, const void *dH,
                                     int64_t lddh, void *dX, int64_t lddx, void *dW, int64_t lddw, void *dbias,
                                     void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream)
 {
     CHECK(check_gated(dtype, M, F, K, gate));
     CHECK(check_operand(dtype, M, K, X, ldx, dW == nullptr));
     CHECK(check_operand(dtype, 2 * F, K, W, ldw, dX == nullptr));
-    CHECK(check_operand(dtype, M, 2 * F, Z, ldz));
+    CHECK(check_vector(M > 0 ? F : 0, Z, 16, false));
     CHECK(check_operand(dtype, M, F, dH, lddh));
     CHECK(check_operand(dtype, M, K, dX, lddx, true));
     CHECK(check_operand(dtype, 2 * F, K, dW, lddw, true));
@@ -345,20 +367,20 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
     const GatedBackWs w = gated_back_ws(dtype, M, F, K, num_cus, ws);
     CHECK(check_ws(ws, ws_bytes, w.bytes));
     hipStream_t s = (hipStream_t)stream;
-    const int64_t n2 = 2 * F, n2p = pad_k(n2), mp = pad_k(M);
+    const int64_t n2 = 2 * F, pitch = dz_pitch(F), mp = pad_k(M);
     if (M > 0 && F > 0)
-        LAUNCH(launch_gate_backward(dtype, M, F, Z, ldz, dH, lddh, gate, dX != nullptr ? w.dz : nullptr, n2p,
+        LAUNCH(launch_gate_backward(dtype, M, F, Z, dH, lddh, gate, dX != nullptr ? w.dz : nullptr,
                                     dW != nullptr ? w.dzt : nullptr, dbias != nullptr ? w.sums : nullptr, s));
     if (dbias != nullptr && F > 0) LAUNCH(launch_sum_tiles(dtype, gate_tiles(M), n2, w.sums, dbias, s));
     if (dX != nullptr && M > 0 && K > 0) {
-        if (n2 > 0) CHECK(sgemm_emu_plan_weight(dtype, n2, K, W, ldw, 1, w.wt, stream));
+        if (F > 0) LAUNCH(lay_out_wt(dtype, F, K, W, ldw, w.wt, num_cus, s));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(product_f32(M, K, n2, (const float *)w.dz, n2p, w.wt, nullptr, (float *)dX, lddx, num_cus, s));
+            CHECK(product_f32(M, K, pitch, (const float *)w.dz, pitch, w.wt, nullptr, (float *)dX, lddx, num_cus, s));
         } else {
             Bf16Gemm g{};
-            g.M = M; g.N = K; g.K = n2p;
-            g.A = (const uint16_t *)w.dz; g.lda = n2p;
-            g.B = w.wt; g.ldb = n2p;
+            g.M = M; g.N = K; g.K = pitch;
+            g.A = (const uint16_t *)w.dz; g.lda = pitch;
+            g.B = w.wt; g.ldb = pitch;
             g.C = (uint16_t *)dX; g.ldc = lddx;
             g.gate = -1;
             g.partials = w.part_x;
@@ -388,7 +410,9 @@ int64_t sgemm_emu_adapter_linear_workspace(int dtype, int64_t M, int64_t N, int6
                                            const float *S)
 {
     CHECK(check_adapters(dtype, M, N, K, n, r));
-    return adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, S, nullptr).bytes;
+    int num_cus = 0;
+    CHECK(current_cus(&num_cus));
+    return adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, S, num_cus, nullptr).bytes;
 }
 
 int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, const void *W,
@@ -410,34 +434,35 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
         if ((uintptr_t)S % 16 != 0) return SGEMM_EMU_EINVAL;
     }
     if ((uintptr_t)plan % 16 != 0) return SGEMM_EMU_EINVAL;
-    const AdapterWs w = adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, S, ws);
-    CHECK(check_ws(ws, ws_bytes, w.bytes));
     if (M == 0 || (N == 0 && (!low || S == nullptr))) return SGEMM_EMU_OK;
     int num_cus = 0;
     CHECK(current_cus(&num_cus));
+    const AdapterWs w = adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, S, num_cus, ws);
+    CHECK(check_ws(ws, ws_bytes, w.bytes));
     hipStream_t s = (hipStream_t)stream;
     const Adapters ad{ids, n, r, down, up, scale};
-    if (low) {
-        if (S == nullptr) S = w.s;
-        LAUNCH(launch_shrink(dtype, M, K, X, ldx, ad, S, num_cus, s));
-        if (N == 0) return SGEMM_EMU_OK;
-    }
-    if (M <= kFewRows || K == 0) {
+    if (adapter_few(M, S)) {
         FewRows a{};
         a.M = M; a.N = N; a.K = K;
         a.X = X; a.ldx = ldx; a.W = W; a.ldw = ldw;
         a.bias = bias; a.gate = -1;
         a.Y = Y; a.ldy = ldy;
         a.ad = low ? &ad : nullptr;
-        a.S = low ? S : nullptr;
+        a.S = w.s;
+        a.partials = w.partials;
         LAUNCH(launch_few_rows(dtype, a, num_cus, s));
         return SGEMM_EMU_OK;
+    }
+    if (low) {
+        if (S == nullptr) S = w.s;
+        LAUNCH(launch_shrink(dtype, M, K, X, ldx, ad, S, num_cus, s));
+        if (N == 0) return SGEMM_EMU_OK;
     }
     if (dtype == SGEMM_EMU_F32) {
         if (w.plan != nullptr) LAUNCH(launch_split_padded(N, K, (const float *)W, ldw, w.plan, s));
         CHECK(product_f32(M, N, K, (const float *)X, ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
                           (const float *)bias, (float *)Y, ldy, num_cus, s));
-        if (low) LAUNCH(launch_expand(dtype, M, N, S, ad, Y, ldy, num_cus, s));
+        if (low) LAUNCH(launch_expand(M, N, S, ad, (float *)Y, ldy, s));
         return SGEMM_EMU_OK;
     }
     Bf16Gemm g{};
@@ -460,7 +485,7 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
     if (low) {
         g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
         g.up = (const uint16_t *)up;
-        g.S = S;
+        g.S = (const uint16_t *)S;
     }
     LAUNCH(launch_bf16_gemm(g, num_cus, s));
     return SGEMM_EMU_OK;
@@ -515,7 +540,7 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
         if (dtype == SGEMM_EMU_F32) {
             CHECK(product_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, nullptr, (float *)dX, lddx,
                               num_cus, s));
-            if (low) LAUNCH(launch_expand(dtype, M, K, w.p, back, dX, lddx, num_cus, s));
+            if (low) LAUNCH(launch_expand(M, K, w.p, back, (float *)dX, lddx, s));
         } else {
             Bf16Gemm g{};
             g.M = M; g.N = K; g.K = bf16_k(N);
@@ -530,19 +555,23 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
             if (low) {
                 g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
                 g.up = (const uint16_t *)w.down_t;
-                g.S = w.p;
+                g.S = (const uint16_t *)w.p;
             }
             LAUNCH(launch_bf16_gemm(g, num_cus, s));
         }
     }
     if (need_down || need_up) {
         LAUNCH(launch_group(M, ids, n, w.offs, w.rows, s));
-        if (need_down)
-            LAUNCH(launch_lowrank_grad(dtype, M, K, n, r, w.p, X, ldx, w.offs, w.rows, false, d_down, w.part_down,
-                                       num_cus, s));
-        if (need_up)
-            LAUNCH(launch_lowrank_grad(dtype, M, N, n, r, S, dY, lddy, w.offs, w.rows, true, d_up, w.part_up, num_cus,
-                                       s));
+        LowrankGrads q{};
+        q.M = M; q.K = K; q.N = N; q.n = n; q.r = r;
+        q.P = w.p; q.S = S;
+        q.X = X; q.ldx = ldx;
+        q.dY = dY; q.lddy = lddy;
+        q.offs = w.offs; q.rows = w.rows;
+        q.down = need_down ? d_down : nullptr;
+        q.up = need_up ? d_up : nullptr;
+        q.partials = w.partials;
+        LAUNCH(launch_lowrank_grad(dtype, q, num_cus, s));
     }
     return SGEMM_EMU_OK;
 }

@@ -26,14 +26,13 @@ def _forward(x, xld, weight, wld, bias, gate, plan, keep):
     dt = ops.DTYPES[x.dtype]
     (M, K), F = x.shape, weight.shape[0] // 2
     h = torch.empty((M, F), dtype=x.dtype, device=x.device)
-    z = torch.empty((M, 2 * F), dtype=x.dtype, device=x.device) if keep else None
+    z = torch.empty((M, 2 * (-(-F // 8) * 8)), dtype=torch.float32, device=x.device) if keep else None
     fwd = None if plan is None else addr(plan.forward)
-    xp, wp, zp, ws, nws = addr(x), addr(weight), addr(z), None, 0
-    if M > ops.FEW_ROWS or keep or K == 0:
-        ws, nws = scratch(ok(L.sgemm_emu_gated_linear_workspace(dt, M, F, K, xp, xld, wp, wld, fwd, zp),
+    xp, wp, zp = addr(x), addr(weight), addr(z)
+    ws, nws = scratch(ok(L.sgemm_emu_gated_linear_workspace(dt, M, F, K, xp, xld, wp, wld, fwd, zp),
                              "sgemm_emu_gated_linear_workspace"), x.device)
     ok(L.sgemm_emu_gated_linear(dt, M, F, K, xp, xld, wp, wld, fwd, addr(bias), gate, addr(h), max(F, 1), zp,
-                                max(2 * F, 1), addr(ws), nws, current_stream()), "sgemm_emu_gated_linear")
+                                addr(ws), nws, current_stream()), "sgemm_emu_gated_linear")
     return h, z
 
 
@@ -62,7 +61,7 @@ class _GatedFn(torch.autograd.Function):
         db = torch.empty((2 * F,), dtype=x.dtype, device=x.device) if need_b and ctx.has_bias else None
         ws, nws = scratch(ok(L.sgemm_emu_gated_linear_backward_workspace(dt, M, F, K),
                              "sgemm_emu_gated_linear_backward_workspace"), x.device)
-        ok(L.sgemm_emu_gated_linear_backward(dt, M, F, K, addr(x), xld, addr(weight), wld, addr(z), max(2 * F, 1),
+        ok(L.sgemm_emu_gated_linear_backward(dt, M, F, K, addr(x), xld, addr(weight), wld, addr(z),
                                              ctx.gate, addr(dh), dhld, addr(dx), max(K, 1), addr(dw), max(K, 1),
                                              addr(db), addr(ws), nws, current_stream()),
            "sgemm_emu_gated_linear_backward")

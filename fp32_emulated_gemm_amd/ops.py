@@ -43,10 +43,10 @@ def ops_lib():
         L.sgemm_emu_plan_bytes.argtypes = [ci, i64, i64, ci]
         L.sgemm_emu_plan_weight.argtypes = [ci, i64, i64, vp, i64, ci, vp, vp]
         L.sgemm_emu_gated_linear_workspace.argtypes = dims3 + [vp, i64, vp, i64, vp, vp]
-        L.sgemm_emu_gated_linear.argtypes = dims3 + [vp, i64, vp, i64, vp, vp, ci, vp, i64, vp, i64, vp, i64, vp]
+        L.sgemm_emu_gated_linear.argtypes = dims3 + [vp, i64, vp, i64, vp, vp, ci, vp, i64, vp, vp, i64, vp]
         L.sgemm_emu_gated_linear_backward_workspace.argtypes = dims3
-        L.sgemm_emu_gated_linear_backward.argtypes = dims3 + [vp, i64, vp, i64, vp, i64, ci, vp, i64, vp, i64, vp,
-                                                              i64, vp, vp, i64, vp]
+        L.sgemm_emu_gated_linear_backward.argtypes = dims3 + [vp, i64, vp, i64, vp, ci, vp, i64, vp, i64, vp, i64,
+                                                              vp, vp, i64, vp]
         L.sgemm_emu_adapter_linear_workspace.argtypes = dims3 + [vp, i64, vp, i64, vp, i64, i64, vp]
         L.sgemm_emu_adapter_linear.argtypes = dims3 + [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64,
                                                        vp, vp, i64, vp]

@@ -70,14 +70,16 @@ int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, 
  *   plan: W's plan (transposed = 0), or NULL: calls of at most
  *   sgemm_emu_few_rows() rows read W itself, and so do bfloat16 calls whose W is
  *   16-byte aligned with K and ldw multiples of 8; other calls lay W out in ws.
- *   Z: NULL, or M x 2F (ldz >= 2F) of the call's type: the pre-activations,
- *   as sgemm_emu_gated_linear_backward takes them.
+ *   Z: NULL, or M rows of 2 pad8(F) floats (pad8: rounded up to a multiple of 8),
+ *   16-byte aligned: the pre-activations, in 32 bits whatever the call's type,
+ *   the gate's from column 0 and the up projection's from column pad8(F), as
+ *   sgemm_emu_gated_linear_backward takes them (the other columns are not set).
  */
 int64_t sgemm_emu_gated_linear_workspace(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx,
                                          const void *W, int64_t ldw, const void *plan, const void *Z);
 int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *W,
-                           int64_t ldw, const void *plan, const void *bias, int gate, void *H, int64_t ldh, void *Z,
-                           int64_t ldz, void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream);
+                           int64_t ldw, const void *plan, const void *bias, int gate, void *H, int64_t ldh, float *Z,
+                           void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream);
 
 /*
  * sgemm_emu_gated_linear_backward -- from dH (M x F) and the forward's X, W, Z:
@@ -89,8 +91,8 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
  */
 int64_t sgemm_emu_gated_linear_backward_workspace(int dtype, int64_t M, int64_t F, int64_t K);
 int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx,
-                                    const void *W, int64_t ldw, const void *Z, int64_t ldz, int gate, const void *dH,
-                                    int64_t lddh, void *dX, int64_t lddx, void *dW, int64_t lddw, void *dbias,
+                                    const void *W, int64_t ldw, const float *Z, int gate, const void *dH, int64_t lddh,
+                                    void *dX, int64_t lddx, void *dW, int64_t lddw, void *dbias,
                                     void *ws, int64_t ws_bytes, sgemm_emu_stream_t stream);
 
 /*
@@ -100,9 +102,10 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
  *   contiguous, of the call's type; scale: n floats or NULL (1); ids: M int32 in
  *   any order; Y: M x N.  n = 0 or r = 0: no adapters (down, up, ids unused).
  *   plan: W's plan (transposed = 0) or NULL, as for sgemm_emu_gated_linear.
- *   S: NULL, or M x pad16(r) floats (r rounded up to a multiple of 16, 16-byte
- *   aligned): scale[i] down_i X[t], zeros past r and for rows without an
- *   adapter, as sgemm_emu_adapter_linear_backward takes it.
+ *   S: NULL, or 4 M pad16(r) bytes (r rounded up to a multiple of 16), 16-byte
+ *   aligned: the low-rank activations scale[i] down_i X[t], as
+ *   sgemm_emu_adapter_linear_backward takes them (floats for FP32; for bfloat16 a
+ *   row's pad16(r) high and pad16(r) low BF16 parts, 16 significant bits).
  *   Inf and NaN in one adapter's weights reach only the rows that use it.
  */
 int64_t sgemm_emu_adapter_linear_workspace(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
