@@ -25,7 +25,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsgemm_emu.so")
 DEBUG_LIB = os.path.join(HERE, "libsgemm_emu_serial_lds.so")
-SOURCES = ["api.hip", "gemm.hip", "split.hip", "ieee.hip", "ops_api.hip", "bf16_gemm.hip", "lowrank.hip", "layouts.hip"]
+SOURCES = ["api.hip", "gemm.hip", "gemm_fused.hip", "split.hip", "ieee.hip", "ops_api.hip", "bf16_gemm.hip", "lowrank.hip", "layouts.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero", "-mcode-object-version=5",

@@ -636,27 +636,21 @@ namespace sgemm_emu_dev {
 int current_cus(int *num_cus) { return current_device(num_cus); }
 
 // The N x K planes path of gemm_common for planes padded with zeros to a K
-// that is a multiple of 64 (16-byte aligned rows): 64 x 64 tiles or stream-K by
-// the same rules, A split into workspace planes for wide N, and a K tail that
-// the kernel masks in A.
-int gemm_padded_planes(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes,
-                       const float *bias, float *C, int64_t ldc, hipStream_t stream)
+// that is a multiple of 64 (16-byte aligned rows; args.B0..B2, args.K the
+// unpadded K): 64 x 64 tiles or stream-K by the same rules, A split into
+// workspace planes for wide N, and a K tail that the kernel masks in A.
+int gemm_padded_planes(const GemmArgs &args, const PlaneLaunchers &launch, hipStream_t stream)
 {
     int num_cus = 0, dev = 0, rc;
     if ((rc = current_device(&num_cus, &dev)) != SGEMM_EMU_OK) return rc;
-    const int64_t kpad = (K + 63) / 64 * 64;
-    GemmArgs g{};
-    g.M = M; g.N = N; g.K = K; g.ka = K;
-    g.A = A; g.lda = lda;
-    g.B0 = planes; g.B1 = planes + N * kpad; g.B2 = planes + 2 * N * kpad; g.ldb = kpad;
-    g.C = C; g.ldc = ldc;
-    g.bias = bias;
-    g.act = SGEMM_EMU_ACT_NONE;
+    GemmArgs g = args;
+    const int64_t M = g.M, N = g.N, K = g.K, kpad = (K + 63) / 64 * 64;
+    g.ka = K;
+    g.ldb = kpad;
     g.num_cus = num_cus;
     g.splits = 1;
     const int skg = gemm_streamk_grid(M, N, kpad, num_cus);
-    if (skg == 0 && gemm_tile64_pays(M, N, K, num_cus, false))
-        return launched(launch_gemm_tile64(g, 5, B_PLANES_NK, stream));
+    if (skg == 0 && gemm_tile64_pays(M, N, K, num_cus, false)) return launched(launch.tile64(g, stream));
 #ifdef SGEMM_EMU_SERIAL_LDS
     const bool presplit_a = false;
 #else
@@ -672,11 +666,11 @@ int gemm_padded_planes(int64_t M, int64_t N, int64_t K, const float *A, int64_t 
     hipError_t e = hipSuccess;
     if (ws != nullptr && presplit_a) {
         uint16_t *Q0 = (uint16_t *)ws, *Q1 = (uint16_t *)(ws + aplane), *Q2 = (uint16_t *)(ws + 2 * aplane);
-        e = launch_split(M, K, A, lda, Q0, Q1, Q2, K, num_cus, stream, false);
+        e = launch_split(M, K, g.A, g.lda, Q0, Q1, Q2, K, num_cus, stream, false);
         if (e == hipSuccess) {
             g.A0 = Q0; g.A1 = Q1; g.A2 = Q2; g.lda = K;
             g.done = lease.event();
-            e = launch_gemm_planes(g, 5, stream);
+            e = launch.planes(g, stream);
         }
         lease.release(e == hipSuccess && g.done != nullptr);
         return launched(e);
@@ -689,8 +683,8 @@ int gemm_padded_planes(int64_t M, int64_t N, int64_t K, const float *A, int64_t 
     }
     g.K = kpad;
     g.done = lease.event();
-    e = launch_gemm(g, 5, B_PLANES_NK, stream, false);
-    lease.release(e == hipSuccess && g.done != nullptr && launch_done_attached(g, B_PLANES_NK));
+    e = launch.dma(g, stream);
+    lease.release(e == hipSuccess && g.done != nullptr);
     return launched(e);
 }
 

@@ -1,0 +1,120 @@
+// gemm_fused.hip -- the BF16x9 kernels with the operators' epilogues: the gated
+// product and the adapters' low-rank part run on a tile's recombined FP32 values
+// before they are stored, which spares a pass over the product.
+//
+// Nine products and the truncating split only.  The plain launchers here are
+// those of gemm.hip with the same argument form.
+#include "gemm_kernels.hpp"
+#include "ops.hpp"
+
+namespace sgemm_emu_dev {
+
+namespace {
+
+using C128 = Cfg8S;
+
+template <class C>
+GemmArgs tiled(const GemmArgs &args)
+{
+    GemmArgs g = args;
+    g.tiles_m = (int)((g.M + C::BM - 1) / C::BM);
+    g.tiles_n = (int)((g.N + C::BN - 1) / C::BN);
+    g.group_m = group_rows(g.tiles_n, g.num_cus);
+    return g;
+}
+
+// One workgroup per CU, a multiple of 8 so that each stays on one XCD.
+dim3 persistent_grid(const GemmArgs &g)
+{
+    const int64_t units = (int64_t)g.tiles_m * g.tiles_n, slots = g.num_cus > 8 ? g.num_cus & ~7 : 8;
+    return dim3((unsigned)(units < slots ? units : slots));
+}
+
+template <class C, int EPI, bool AVEC>
+void tile64_vec(const GemmArgs &g, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n)), block(C::NT);
+    // planes with padded rows: 128-bit loads wherever every 8 elements lie below or above K
+    if (g.K % 8 == 0)
+        hipLaunchKernelGGL((gemm_bf16x9_kernel<C, 5, AVEC, B_PLANES_NK, 1, false, EPI>), grid, block, 0, stream, g);
+    else
+        hipLaunchKernelGGL((gemm_bf16x9_kernel<C, 5, AVEC, B_PLANES_NK, 0, false, EPI>), grid, block, 0, stream, g);
+}
+
+template <int EPI>
+hipError_t tile64(const GemmArgs &args, hipStream_t stream)
+{
+    const GemmArgs g = tiled<Cfg64S>(args);
+    if (aligned(g.A, 16) && g.lda % 4 == 0 && g.K % 4 == 0) tile64_vec<Cfg64S, EPI, true>(g, stream);
+    else tile64_vec<Cfg64S, EPI, false>(g, stream);
+    return hipGetLastError();
+}
+
+template <int EPI>
+hipError_t planes(const GemmArgs &args, hipStream_t stream)
+{
+    const GemmArgs g = tiled<C128>(args);
+    launch_last(gemm_bf16x9_planes_kernel<C128, 5, EPI>, persistent_grid(g), dim3(C128::NT), stream, g);
+    return hipGetLastError();
+}
+
+template <int EPI, bool AVEC, bool KTAIL>
+void dma_vec(const GemmArgs &g, hipStream_t stream)
+{
+    const dim3 block(C128::NT);
+#ifdef SGEMM_EMU_SERIAL_LDS
+    launch_last(gemm_bf16x9_serial_kernel<C128, 5, AVEC, false, KTAIL, EPI>,
+                dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), block, stream, g);
+#else
+    if (g.sk_grid > 0) {
+        GemmArgs s = g;
+        s.sk_domains = (int)streamk_domains((int64_t)g.tiles_m * g.tiles_n, g.K / (2 * BK), g.sk_grid);
+        s.group_m = kStreamkGroupRows;
+        launch_last(gemm_bf16x9_streamk_kernel<C128, 5, AVEC, false, KTAIL, EPI>, dim3((unsigned)g.sk_grid), block,
+                    stream, s);
+        return;
+    }
+    launch_last(gemm_bf16x9_dma_kernel<C128, 5, AVEC, false, KTAIL, EPI>, persistent_grid(g), block, stream, g);
+#endif
+}
+
+template <int EPI>
+hipError_t dma(const GemmArgs &args, hipStream_t stream)
+{
+    const GemmArgs g = tiled<C128>(args);
+    const bool avec = aligned(g.A, 16) && g.lda % 4 == 0 && g.ka % 4 == 0, tail = g.ka != g.K;
+    if (avec && tail) dma_vec<EPI, true, true>(g, stream);
+    else if (avec) dma_vec<EPI, true, false>(g, stream);
+    else if (tail) dma_vec<EPI, false, true>(g, stream);
+    else dma_vec<EPI, false, false>(g, stream);
+    return hipGetLastError();
+}
+
+hipError_t plain_tile64(const GemmArgs &g, hipStream_t stream)
+{
+    return launch_gemm_tile64(g, 5, B_PLANES_NK, stream);
+}
+hipError_t plain_planes(const GemmArgs &g, hipStream_t stream) { return launch_gemm_planes(g, 5, stream); }
+hipError_t plain_dma(const GemmArgs &g, hipStream_t stream) { return launch_gemm(g, 5, B_PLANES_NK, stream); }
+
+}  // namespace
+
+const PlaneLaunchers &plain_launchers()
+{
+    static const PlaneLaunchers l = {plain_tile64, plain_planes, plain_dma};
+    return l;
+}
+
+const PlaneLaunchers &gated_launchers()
+{
+    static const PlaneLaunchers l = {tile64<EPI_GATED>, planes<EPI_GATED>, dma<EPI_GATED>};
+    return l;
+}
+
+const PlaneLaunchers &adapter_launchers()
+{
+    static const PlaneLaunchers l = {tile64<EPI_ADAPTER>, planes<EPI_ADAPTER>, dma<EPI_ADAPTER>};
+    return l;
+}
+
+}  // namespace sgemm_emu_dev

@@ -15,6 +15,16 @@ enum BSource {
     B_PLANES_NK = 2    // three BF16 planes, N x K row-major (B transposed, k contiguous)
 };
 
+// Fused epilogues of the FP32 products (gemm_fused.hip).
+struct GemmEpilogue {
+    int gate;                // gated: the gate; C is H (M x N / 2)
+    float *Z;                // gated: pre-activations to keep (rows of ldz floats, up from ldz / 2), or null
+    int64_t ldz;
+    const int32_t *ids;      // adapters: rows' ids, n adapters of rank r (S: M x rp, up: n x N x r)
+    int64_t n, r, rp;
+    const float *up, *S;
+};
+
 struct GemmArgs {
     int64_t M, N, K;
     int64_t ka;              // K of A (== K, or less when the B planes are zero-padded to K)
@@ -44,6 +54,7 @@ struct GemmArgs {
     uint32_t sk_epoch;       // stream-K: this launch's flag value (never 0)
     int sk_grid;             // stream-K: workgroups G (0: no stream-K)
     int sk_domains;          // stream-K: 1, or 8 (one block of tiles per XCD); set by the launcher
+    GemmEpilogue epi;        // fused epilogues only
 };
 
 // rne: round each split stage to nearest even instead of truncating (ablation).
@@ -83,6 +94,11 @@ hipError_t launch_gemm_planes(const GemmArgs &args, int nbands, hipStream_t stre
 // floats) and a nonzero args.sk_epoch that differs from the flags' values.
 int gemm_streamk_grid(int64_t M, int64_t N, int64_t K, int num_cus);
 
+// Domains of a stream-K grid of G workgroups over T tiles of ppt K pairs, and
+// tile-rows per group of the tile order.
+int64_t streamk_domains(int64_t T, int64_t ppt, int64_t G);
+int group_rows(int tiles_n, int num_cus);
+
 // Most K pieces any tile is cut into by a stream-K grid of `grid` workgroups.
 int gemm_streamk_pieces(int64_t M, int64_t N, int64_t K, int grid);
 
@@ -119,6 +135,14 @@ NativePlan native_plan(int64_t M, int64_t N, int64_t K, int num_cus, bool vec);
 // True when the native kernel loads A and B 128 bits at a time.
 bool native_vec(const float *A, int64_t lda, const float *B, int64_t ldb, int64_t K, int64_t N);
 hipError_t launch_native(const GemmArgs &args, const NativePlan &plan, hipStream_t stream);
+
+// The kernels behind gemm_padded_planes (api.hip): 64 x 64 tiles, both operands
+// as planes, and the LDS-DMA kernel with or without stream-K.
+struct PlaneLaunchers {
+    hipError_t (*tile64)(const GemmArgs &args, hipStream_t stream);
+    hipError_t (*planes)(const GemmArgs &args, hipStream_t stream);
+    hipError_t (*dma)(const GemmArgs &args, hipStream_t stream);
+};
 
 // C := act(0 + bias[j]) (K == 0); without bias and activation C := 0.
 // Recompute, as plain FP32 dot products, every output of C = A B whose row of

@@ -19,12 +19,12 @@ unsigned blocks_for(int64_t items, int64_t per_block, int64_t most)
 
 // One thread splits 8 consecutive elements of a padded row.
 __global__ __launch_bounds__(256) void split_padded_kernel(int64_t rows, int64_t cols, int64_t kp, const float *X,
-                                                           int64_t ldx, uint16_t *P)
+                                                           int64_t ldx, uint16_t *P, bool interleave)
 {
     const int64_t groups = kp / 8, plane = rows * kp;
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < rows * groups; q += (int64_t)gridDim.x * 256) {
         const int64_t row = q / groups, c = (q - row * groups) * 8;
-        const float *src = X + row * ldx + c;
+        const float *src = X + (interleave ? (row & 1) * (rows >> 1) + (row >> 1) : row) * ldx + c;
         float x[8];
         if (c + 8 <= cols && ((uintptr_t)src % 16) == 0) {
             const f32x4_t a = reinterpret_cast<const f32x4_t *>(src)[0], b = reinterpret_cast<const f32x4_t *>(src)[1];
@@ -89,14 +89,22 @@ __global__ __launch_bounds__(256) void transpose_kernel(int64_t rows, int64_t co
 
 // ---------------------------------------------------------------- gate
 
+// The product with an empty K is its bias.
 template <int GATE>
-__global__ __launch_bounds__(256) void gate_kernel(int64_t M, int64_t F, const float *Z, int64_t ldz, int64_t up,
-                                                   float *H, int64_t ldh)
+__global__ __launch_bounds__(256) void gate_bias_kernel(int64_t M, int64_t F, const float *bias, float *H, int64_t ldh,
+                                                        float *Z, int64_t zup)
 {
     const int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (f >= F) return;
-    for (int64_t m = blockIdx.y; m < M; m += gridDim.y)
-        H[m * ldh + f] = gate_act<GATE>(Z[m * ldz + f]) * Z[m * ldz + up + f];
+    const float g = bias != nullptr ? bias[f] : 0.0f, u = bias != nullptr ? bias[F + f] : 0.0f;
+    const float h = gate_act<GATE>(g) * u;
+    for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+        H[m * ldh + f] = h;
+        if (Z != nullptr) {
+            Z[m * 2 * zup + f] = g;
+            Z[m * 2 * zup + zup + f] = u;
+        }
+    }
 }
 
 // 64 rows x 64 outputs per workgroup; a thread takes four consecutive outputs
@@ -239,12 +247,12 @@ hipError_t gate_backward_t(int64_t M, int64_t F, const float *Z, const T *dH, in
 
 }  // namespace
 
-hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64_t ldx, uint16_t *P,
+hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64_t ldx, uint16_t *P, bool interleave,
                                hipStream_t stream)
 {
     const int64_t kp = pad_k(cols);
     hipLaunchKernelGGL(split_padded_kernel, dim3(blocks_for(rows * (kp / 8), 256, 16384)), dim3(256), 0, stream, rows,
-                       cols, kp, X, ldx, P);
+                       cols, kp, X, ldx, P, interleave);
     return hipGetLastError();
 }
 
@@ -278,11 +286,11 @@ hipError_t launch_transpose_bank(int dtype, int64_t n, int64_t rows, int64_t col
     return hipGetLastError();
 }
 
-hipError_t launch_gate(int64_t M, int64_t F, const float *Z, int64_t ldz, int64_t up, int gate, float *H, int64_t ldh,
-                       hipStream_t stream)
+hipError_t launch_gate_bias(int64_t M, int64_t F, const float *bias, int gate, float *H, int64_t ldh, float *Z,
+                            hipStream_t stream)
 {
     const dim3 grid((unsigned)((F + 255) / 256), (unsigned)(M < 16384 ? M : 16384));
-#define LAUNCH(G) hipLaunchKernelGGL((gate_kernel<G>), grid, dim3(256), 0, stream, M, F, Z, ldz, up, H, ldh)
+#define LAUNCH(G) hipLaunchKernelGGL((gate_bias_kernel<G>), grid, dim3(256), 0, stream, M, F, bias, H, ldh, Z, z_pitch(F) / 2)
     switch (gate) {
     case kSilu: LAUNCH(kSilu); break;
     case kGelu: LAUNCH(kGelu); break;
@@ -292,21 +300,6 @@ hipError_t launch_gate(int64_t M, int64_t F, const float *Z, int64_t ldz, int64_
     default: return hipErrorInvalidValue;
     }
 #undef LAUNCH
-    return hipGetLastError();
-}
-
-__global__ __launch_bounds__(256) void copy_z_kernel(int64_t M, int64_t F, const float *Z, int64_t pitch, float *out)
-{
-    const int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (f >= 2 * F) return;
-    for (int64_t m = blockIdx.y; m < M; m += gridDim.y)
-        out[m * pitch + (f < F ? f : pitch / 2 + f - F)] = Z[m * 2 * F + f];
-}
-
-hipError_t launch_copy_z(int64_t M, int64_t F, const float *Z, float *out, hipStream_t stream)
-{
-    hipLaunchKernelGGL(copy_z_kernel, dim3((unsigned)((2 * F + 255) / 256), (unsigned)(M < 16384 ? M : 16384)),
-                       dim3(256), 0, stream, M, F, Z, z_pitch(F), out);
     return hipGetLastError();
 }
 

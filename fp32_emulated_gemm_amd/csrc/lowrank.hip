@@ -537,22 +537,6 @@ hipError_t launch_shrink_t(int64_t M, int64_t K, const T *X, int64_t ldx, const 
     return hipGetLastError();
 }
 
-// ---------------------------------------------------------------- expand (FP32)
-
-__global__ __launch_bounds__(256) void expand_kernel(int64_t M, int64_t N, const float *S, int64_t rp, Adapters ad,
-                                                     float *Y, int64_t ldy)
-{
-    for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
-        const int32_t i = ad.ids[m];
-        const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-        if (!(i >= 0 && i < ad.n) || n >= N) continue;
-        const float *up = (const float *)ad.up + ((int64_t)i * N + n) * ad.r;
-        float d = 0.0f;
-        for (int64_t j = 0; j < ad.r; ++j) d = __builtin_fmaf(S[m * rp + j], up[j], d);
-        Y[m * ldy + n] += d;
-    }
-}
-
 // ---------------------------------------------------------------- grouping rows by adapter
 // Workgroup i lists the rows of adapter i, ascending: it counts the ids below
 // its own (where its rows start) and its own, then writes its rows in order
@@ -813,14 +797,6 @@ hipError_t launch_shrink(int dtype, int64_t M, int64_t K, const void *X, int64_t
 {
     return dtype == kF32 ? launch_shrink_t<float>(M, K, (const float *)X, ldx, ad, S, num_cus, stream)
                          : launch_shrink_t<uint16_t>(M, K, (const uint16_t *)X, ldx, ad, S, num_cus, stream);
-}
-
-hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &ad, float *Y, int64_t ldy,
-                         hipStream_t stream)
-{
-    const dim3 grid((unsigned)((N + 255) / 256), (unsigned)(M < 32768 ? M : 32768));
-    hipLaunchKernelGGL(expand_kernel, grid, dim3(256), 0, stream, M, N, S, rank_pad(ad.r), ad, Y, ldy);
-    return hipGetLastError();
 }
 
 hipError_t launch_group(int64_t M, const int32_t *ids, int64_t n, int32_t *offs, int32_t *rows, hipStream_t stream)

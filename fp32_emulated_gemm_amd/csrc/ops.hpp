@@ -30,10 +30,6 @@ inline int64_t rank_pad(int64_t r) { return round_up(r, 16); }   // row pitch of
 hipError_t launch_shrink(int dtype, int64_t M, int64_t K, const void *X, int64_t ldx, const Adapters &ad, float *S,
                          int num_cus, hipStream_t stream);
 
-// FP32: Y[t] += up[i] S[t] for the rows that have an adapter.
-hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &ad, float *Y, int64_t ldy,
-                         hipStream_t stream);
-
 // offs[0..n]: where each adapter's rows start in rows[]; rows[]: the row
 // numbers that have an adapter, grouped by it, ascending inside a group.
 hipError_t launch_group(int64_t M, const int32_t *ids, int64_t n, int32_t *offs, int32_t *rows, hipStream_t stream);
@@ -107,7 +103,8 @@ hipError_t launch_bf16_gemm(const Bf16Gemm &g, int num_cus, hipStream_t stream);
 // ---------------------------------------------------------------- layouts and elementwise
 // Three BF16 planes of X (rows x cols FP32), rows x pad_k(cols) with zeros past
 // cols; planes at P, P + rows * pad_k(cols), P + 2 rows * pad_k(cols).
-hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64_t ldx, uint16_t *P,
+// interleave: plane rows 2 f, 2 f + 1 are X's rows f, rows / 2 + f.
+hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64_t ldx, uint16_t *P, bool interleave,
                                hipStream_t stream);
 // bfloat16 rows x cols -> rows x pad_k(cols), zeros past cols.
 hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,
@@ -123,12 +120,10 @@ hipError_t launch_transpose_bank(int dtype, int64_t n, int64_t rows, int64_t col
 // gate's from column 0, the up projection's from column z_pitch(F) / 2.
 inline int64_t z_pitch(int64_t F) { return 2 * round_up(F, 8); }
 
-// H = act(gate) * up of Z's halves, `up` columns apart, float32.
-hipError_t launch_gate(int64_t M, int64_t F, const float *Z, int64_t ldz, int64_t up, int gate, float *H, int64_t ldh,
-                       hipStream_t stream);
 
-// Z (M x 2F) -> rows of z_pitch(F).
-hipError_t launch_copy_z(int64_t M, int64_t F, const float *Z, float *out, hipStream_t stream);
+// K == 0: H = act(bias) * bias of the halves (bias null: zeros), and Z where kept.
+hipError_t launch_gate_bias(int64_t M, int64_t F, const float *bias, int gate, float *H, int64_t ldh, float *Z,
+                            hipStream_t stream);
 
 // From Z and dH: dZ (rows of dz_pitch(F): gate from 0, up from dz_pitch / 2,
 // zeros between and after), its transpose (2F x pad_k(M), zeros past M), and the
@@ -140,11 +135,13 @@ hipError_t launch_gate_backward(int dtype, int64_t M, int64_t F, const float *Z,
 // out[c] = sum over t of sums[t][c], t ascending.
 hipError_t launch_sum_tiles(int dtype, int64_t tiles, int64_t cols, const float *sums, void *out, hipStream_t stream);
 
-// ---------------------------------------------------------------- FP32 products (api.hip)
-// C = A B^T (+ bias) with FP32 A (M x K, lda) and B as zero-padded planes
-// (launch_split_padded of an N x K matrix): nine products.
-int gemm_padded_planes(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes,
-                       const float *bias, float *C, int64_t ldc, hipStream_t stream);
+// ---------------------------------------------------------------- FP32 products (api.hip, gemm_fused.hip)
+// C = A B^T with FP32 A (M x K, lda) and B as zero-padded planes
+// (launch_split_padded of an N x K matrix), nine products, by `launch`'s kernels.
+int gemm_padded_planes(const GemmArgs &args, const PlaneLaunchers &launch, hipStream_t stream);
+const PlaneLaunchers &plain_launchers();     // bias
+const PlaneLaunchers &gated_launchers();     // bias, gate (args.epi; B's columns alternate gate, up)
+const PlaneLaunchers &adapter_launchers();   // bias, adapters (args.epi)
 // The current device's CU count if it is a gfx950 (SGEMM_EMU_EARCH otherwise).
 int current_cus(int *num_cus);
 

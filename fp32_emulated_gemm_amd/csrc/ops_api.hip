@@ -79,16 +79,41 @@ bool direct(const void *p, int64_t ld, int64_t K) { return K % 8 == 0 && ld % 8 
 // The K that a bfloat16 product runs over: operands are padded copies unless K is a multiple of 8.
 int64_t bf16_k(int64_t K) { return K % 8 == 0 ? K : pad_k(K); }
 
-// C = A B^T + bias, FP32 through nine products.
-int product_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes,
-                const float *bias, float *C, int64_t ldc, int num_cus, hipStream_t stream)
+// The arguments of an FP32 product C = A B^T + bias (B as padded planes, K > 0).
+GemmArgs product_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes,
+                     const float *bias, float *C, int64_t ldc)
+{
+    const int64_t plane = N * pad_k(K);
+    GemmArgs g{};
+    g.M = M; g.N = N; g.K = K;
+    g.A = A; g.lda = lda;
+    g.B0 = planes; g.B1 = planes + plane; g.B2 = planes + 2 * plane;
+    g.C = C; g.ldc = ldc;
+    g.bias = bias;
+    g.act = SGEMM_EMU_ACT_NONE;
+    return g;
+}
+
+// A product without a fused epilogue; an empty K leaves zeros.
+int plain_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes, float *C,
+              int64_t ldc, int num_cus, hipStream_t stream)
 {
     if (M == 0 || N == 0) return SGEMM_EMU_OK;
     if (K == 0) {
-        LAUNCH(launch_zero(M, N, C, ldc, bias, SGEMM_EMU_ACT_NONE, num_cus, stream));
+        LAUNCH(launch_zero(M, N, C, ldc, nullptr, SGEMM_EMU_ACT_NONE, num_cus, stream));
         return SGEMM_EMU_OK;
     }
-    return gemm_padded_planes(M, N, K, A, lda, planes, bias, C, ldc, stream);
+    return gemm_padded_planes(product_f32(M, N, K, A, lda, planes, nullptr, C, ldc), plain_launchers(), stream);
+}
+
+GemmEpilogue adapter_epilogue(const Adapters &ad, const float *S)
+{
+    GemmEpilogue e{};
+    e.ids = ad.ids;
+    e.n = ad.n; e.r = ad.r; e.rp = rank_pad(ad.r);
+    e.up = (const float *)ad.up;
+    e.S = S;
+    return e;
 }
 
 // ---------------------------------------------------------------- gated projection
@@ -105,7 +130,7 @@ bool gated_few(int64_t M, int64_t K, const void *Z) { return M <= kFewRows && Z 
 
 struct GatedWs {
     uint16_t *plan, *x;   // W and X laid out
-    float *z;             // FP32 pre-activations, or few rows' K slices
+    float *partials;      // few rows' K slices
     int64_t bytes;
 };
 GatedWs gated_ws(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int64_t ldx, const void *W, int64_t ldw,
@@ -115,10 +140,9 @@ GatedWs gated_ws(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int6
     GatedWs w{};
     if (M == 0 || F == 0) return w;
     if (gated_few(M, K, Z)) {
-        w.z = c.take<float>(few_rows_partial_floats(dtype, M, F, K, SGEMM_EMU_GATE_SILU, num_cus));
+        w.partials = c.take<float>(few_rows_partial_floats(dtype, M, F, K, SGEMM_EMU_GATE_SILU, num_cus));
     } else if (dtype == SGEMM_EMU_F32) {
         if (plan == nullptr) w.plan = c.take<uint16_t>(3 * 2 * F * pad_k(K));
-        w.z = c.take<float>(M * 2 * F);
     } else {
         if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(2 * F * pad_k(K));
         if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
@@ -238,18 +262,21 @@ extern "C" {
 
 int sgemm_emu_few_rows(void) { return (int)kFewRows; }
 
-int64_t sgemm_emu_plan_bytes(int dtype, int64_t rows, int64_t cols, int transposed)
+int64_t sgemm_emu_plan_bytes(int dtype, int64_t rows, int64_t cols, int layout)
 {
-    if (!dtype_ok(dtype) || !extent_ok(rows) || !extent_ok(cols) || (transposed != 0 && transposed != 1))
-        return SGEMM_EMU_EINVAL;
+    if (!dtype_ok(dtype) || !extent_ok(rows) || !extent_ok(cols)) return SGEMM_EMU_EINVAL;
+    if (layout < SGEMM_EMU_PLAN_ROWS || layout > SGEMM_EMU_PLAN_GATED) return SGEMM_EMU_EINVAL;
+    if (layout == SGEMM_EMU_PLAN_GATED && rows % 2 != 0) return SGEMM_EMU_EINVAL;
+    const bool transposed = layout == SGEMM_EMU_PLAN_TRANSPOSED;
     const int64_t comps = dtype == SGEMM_EMU_F32 ? 3 : 1;
     return 2 * comps * (transposed ? cols * pad_k(rows) : rows * pad_k(cols));
 }
 
-int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, int64_t ldw, int transposed,
+int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, int64_t ldw, int layout,
                           void *plan, sgemm_emu_stream_t stream)
 {
-    const int64_t bytes = sgemm_emu_plan_bytes(dtype, rows, cols, transposed);
+    const int64_t bytes = sgemm_emu_plan_bytes(dtype, rows, cols, layout);
+    const bool transposed = layout == SGEMM_EMU_PLAN_TRANSPOSED;
     if (bytes < 0) return (int)bytes;
     CHECK(check_operand(dtype, rows, cols, W, ldw));
     if (bytes > 0 && plan == nullptr) return SGEMM_EMU_ENULL;
@@ -265,7 +292,7 @@ int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, 
             LAUNCH(launch_split_transpose(rows, cols, (const float *)W, ldw, P, P + plane, P + 2 * plane, rp, num_cus,
                                           s, false, rp));
         } else {
-            LAUNCH(launch_split_padded(rows, cols, (const float *)W, ldw, P, s));
+            LAUNCH(launch_split_padded(rows, cols, (const float *)W, ldw, P, layout == SGEMM_EMU_PLAN_GATED, s));
         }
     } else if (transposed) {
         LAUNCH(launch_transpose_padded(rows, cols, (const uint16_t *)W, ldw, P, pad_k(rows), pad_k(rows), s));
@@ -306,18 +333,23 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
         a.X = X; a.ldx = ldx; a.W = W; a.ldw = ldw;
         a.bias = bias; a.gate = gate;
         a.Y = H; a.ldy = ldh;
-        a.partials = w.z;
+        a.partials = w.partials;
         LAUNCH(launch_few_rows(dtype, a, num_cus, s));
         return SGEMM_EMU_OK;
     }
     if (dtype == SGEMM_EMU_F32) {
-        if (w.plan != nullptr) LAUNCH(launch_split_padded(2 * F, K, (const float *)W, ldw, w.plan, s));
-        CHECK(product_f32(M, 2 * F, K, (const float *)X, ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
-                          (const float *)bias, w.z, 2 * F, num_cus, s));
-        LAUNCH(launch_gate(M, F, w.z, 2 * F, F, gate, (float *)H, ldh, s));
-        if (Z != nullptr)
-            LAUNCH(launch_copy_z(M, F, w.z, Z, s));
-        return SGEMM_EMU_OK;
+        if (K == 0) {
+            LAUNCH(launch_gate_bias(M, F, (const float *)bias, gate, (float *)H, ldh, Z, s));
+            return SGEMM_EMU_OK;
+        }
+        if (w.plan != nullptr) LAUNCH(launch_split_padded(2 * F, K, (const float *)W, ldw, w.plan, true, s));
+        GemmArgs g = product_f32(M, 2 * F, K, (const float *)X, ldx,
+                                 w.plan != nullptr ? w.plan : (const uint16_t *)plan, (const float *)bias, (float *)H,
+                                 ldh);
+        g.epi.gate = gate;
+        g.epi.Z = Z;
+        g.epi.ldz = z_pitch(F);
+        return gemm_padded_planes(g, gated_launchers(), s);
     }
     Bf16Gemm g{};
     g.M = M; g.N = 2 * F; g.K = bf16_k(K);
@@ -375,7 +407,7 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
     if (dX != nullptr && M > 0 && K > 0) {
         if (F > 0) LAUNCH(lay_out_wt(dtype, F, K, W, ldw, w.wt, num_cus, s));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(product_f32(M, K, pitch, (const float *)w.dz, pitch, w.wt, nullptr, (float *)dX, lddx, num_cus, s));
+            CHECK(plain_f32(M, K, pitch, (const float *)w.dz, pitch, w.wt, (float *)dX, lddx, num_cus, s));
         } else {
             Bf16Gemm g{};
             g.M = M; g.N = K; g.K = pitch;
@@ -388,9 +420,9 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
         }
     }
     if (dW != nullptr && F > 0 && K > 0) {
-        if (M > 0) CHECK(sgemm_emu_plan_weight(dtype, M, K, X, ldx, 1, w.xt, stream));
+        if (M > 0) CHECK(sgemm_emu_plan_weight(dtype, M, K, X, ldx, SGEMM_EMU_PLAN_TRANSPOSED, w.xt, stream));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(product_f32(n2, K, M, (const float *)w.dzt, mp, w.xt, nullptr, (float *)dW, lddw, num_cus, s));
+            CHECK(plain_f32(n2, K, M, (const float *)w.dzt, mp, w.xt, (float *)dW, lddw, num_cus, s));
         } else {
             Bf16Gemm g{};
             g.M = n2; g.N = K; g.K = mp;
@@ -459,11 +491,16 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
         if (N == 0) return SGEMM_EMU_OK;
     }
     if (dtype == SGEMM_EMU_F32) {
-        if (w.plan != nullptr) LAUNCH(launch_split_padded(N, K, (const float *)W, ldw, w.plan, s));
-        CHECK(product_f32(M, N, K, (const float *)X, ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
-                          (const float *)bias, (float *)Y, ldy, num_cus, s));
-        if (low) LAUNCH(launch_expand(M, N, S, ad, (float *)Y, ldy, s));
-        return SGEMM_EMU_OK;
+        if (K == 0) {
+            // S is zero too: Y is the bias
+            LAUNCH(launch_zero(M, N, (float *)Y, ldy, (const float *)bias, SGEMM_EMU_ACT_NONE, num_cus, s));
+            return SGEMM_EMU_OK;
+        }
+        if (w.plan != nullptr) LAUNCH(launch_split_padded(N, K, (const float *)W, ldw, w.plan, false, s));
+        GemmArgs g = product_f32(M, N, K, (const float *)X, ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
+                                 (const float *)bias, (float *)Y, ldy);
+        if (low) g.epi = adapter_epilogue(ad, S);
+        return gemm_padded_planes(g, low ? adapter_launchers() : plain_launchers(), s);
     }
     Bf16Gemm g{};
     g.M = M; g.N = N; g.K = bf16_k(K);
@@ -538,9 +575,15 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
     if (need_dx) {
         if (low) LAUNCH(launch_transpose_bank(dtype, n, r, K, down, w.down_t, s));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(product_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, nullptr, (float *)dX, lddx,
-                              num_cus, s));
-            if (low) LAUNCH(launch_expand(M, K, w.p, back, (float *)dX, lddx, s));
+            if (low && N > 0) {
+                GemmArgs g = product_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, nullptr,
+                                         (float *)dX, lddx);
+                g.epi = adapter_epilogue(back, w.p);
+                CHECK(gemm_padded_planes(g, adapter_launchers(), s));
+            } else {
+                CHECK(plain_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, (float *)dX, lddx, num_cus,
+                                s));
+            }
         } else {
             Bf16Gemm g{};
             g.M = M; g.N = K; g.K = bf16_k(N);

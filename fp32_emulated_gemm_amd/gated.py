@@ -15,9 +15,9 @@ from .linear import Linear
 from .ops import GATES, WeightPlan, addr, check_tensor, current_stream, ok, ops_lib, rows_of, scratch
 
 
-def plan_weight(weight, backward=False):
+def plan_weight(weight):
     """The layout of a fixed weight for gated_linear's `plan` (see ops.WeightPlan)."""
-    return WeightPlan(weight, backward=backward)
+    return WeightPlan(weight, gated=True)
 
 
 def _forward(x, xld, weight, wld, bias, gate, plan, keep):

@@ -18,6 +18,9 @@ SGEMM_EMU_GATE_GELU = 1        # exact (erf) form
 SGEMM_EMU_GATE_GELU_TANH = 2
 SGEMM_EMU_GATE_SIGMOID = 3
 SGEMM_EMU_GATE_RELU = 4
+SGEMM_EMU_PLAN_ROWS = 0
+SGEMM_EMU_PLAN_TRANSPOSED = 1
+SGEMM_EMU_PLAN_GATED = 2
 
 DTYPES = {torch.float32: SGEMM_EMU_F32, torch.bfloat16: SGEMM_EMU_BF16}
 GATES = {"silu": SGEMM_EMU_GATE_SILU, "gelu": SGEMM_EMU_GATE_GELU, "gelu_tanh": SGEMM_EMU_GATE_GELU_TANH,
@@ -116,7 +119,7 @@ class WeightPlan:
 
     __slots__ = ("dtype", "shape", "device", "forward", "backward")
 
-    def __init__(self, weight, forward=True, backward=False):
+    def __init__(self, weight, gated=False, forward=True, backward=False):
         w = weight.detach()
         if w.dtype not in DTYPES:
             raise TypeError(f"weight: expected dtype float32 or bfloat16, got {w.dtype}")
@@ -125,16 +128,17 @@ class WeightPlan:
         self.dtype, self.shape, self.device = w.dtype, tuple(w.shape), w.device
         # a bfloat16 weight with 16-byte aligned rows needs no layout for the forward product
         lies = w.dtype == torch.bfloat16 and w.shape[1] % 8 == 0 and ld % 8 == 0 and w.data_ptr() % 16 == 0
-        self.forward = self._lay_out(w, ld, 0) if forward and not lies else None
-        self.backward = self._lay_out(w, ld, 1) if backward else None
+        rows = SGEMM_EMU_PLAN_GATED if gated else SGEMM_EMU_PLAN_ROWS
+        self.forward = self._lay_out(w, ld, rows) if forward and not lies else None
+        self.backward = self._lay_out(w, ld, SGEMM_EMU_PLAN_TRANSPOSED) if backward else None
 
     @staticmethod
-    def _lay_out(w, ld, transposed):
+    def _lay_out(w, ld, layout):
         L, dt = ops_lib(), DTYPES[w.dtype]
         rows, cols = w.shape
-        nbytes = ok(L.sgemm_emu_plan_bytes(dt, rows, cols, transposed), "sgemm_emu_plan_bytes")
+        nbytes = ok(L.sgemm_emu_plan_bytes(dt, rows, cols, layout), "sgemm_emu_plan_bytes")
         plan = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=w.device)
-        ok(L.sgemm_emu_plan_weight(dt, rows, cols, addr(w), ld, transposed, plan.data_ptr(), current_stream()),
+        ok(L.sgemm_emu_plan_weight(dt, rows, cols, addr(w), ld, layout, plan.data_ptr(), current_stream()),
            "sgemm_emu_plan_weight")
         return plan
 

@@ -52,22 +52,29 @@ enum sgemm_emu_gate {
     SGEMM_EMU_GATE_RELU = 4
 };
 
+/* How a weight is laid out: its rows, the rows of its transpose, or (an even
+   number of) rows whose first half are gate rows and second half up rows. */
+enum sgemm_emu_plan_layout {
+    SGEMM_EMU_PLAN_ROWS = 0,       /* sgemm_emu_adapter_linear's W */
+    SGEMM_EMU_PLAN_TRANSPOSED = 1, /* W^T, for sgemm_emu_adapter_linear_backward */
+    SGEMM_EMU_PLAN_GATED = 2       /* sgemm_emu_gated_linear's W */
+};
+
 /*
  * sgemm_emu_plan_weight -- lays the rows x cols weight W out for the products
- * below: W itself (transposed = 0), or W^T (transposed = 1) for the input
- * gradient.  FP32: three BF16 planes; bfloat16: one.  Rows of
- * pad(k) = k rounded up to a multiple of 64 elements, zeros past k.
- * sgemm_emu_plan_bytes gives the size (negative on invalid arguments).
+ * below.  FP32: three BF16 planes; bfloat16: one.  Rows of pad(k) = k rounded up
+ * to a multiple of 64 elements, zeros past k.  sgemm_emu_plan_bytes gives the
+ * size (negative on invalid arguments).
  */
-int64_t sgemm_emu_plan_bytes(int dtype, int64_t rows, int64_t cols, int transposed);
-int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, int64_t ldw, int transposed,
+int64_t sgemm_emu_plan_bytes(int dtype, int64_t rows, int64_t cols, int layout);
+int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, int64_t ldw, int layout,
                           void *plan, sgemm_emu_stream_t stream);
 
 /*
  * sgemm_emu_gated_linear -- H = act(Z[:, :F]) * Z[:, F:], Z = X W^T + bias.
  *   X: M x K (ldx >= K); W: 2F x K (ldw >= K), the gate's F rows, then the up
  *   projection's F rows; bias: 2F values or NULL; H: M x F (ldh >= F).
- *   plan: W's plan (transposed = 0), or NULL: calls of at most
+ *   plan: W's plan (SGEMM_EMU_PLAN_GATED), or NULL: calls of at most
  *   sgemm_emu_few_rows() rows read W itself, and so do bfloat16 calls whose W is
  *   16-byte aligned with K and ldw multiples of 8; other calls lay W out in ws.
  *   Z: NULL, or M rows of 2 pad8(F) floats (pad8: rounded up to a multiple of 8),
@@ -101,7 +108,7 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
  *   X: M x K; W: N x K; bias: N values or NULL; down: n x r x K and up: n x N x r,
  *   contiguous, of the call's type; scale: n floats or NULL (1); ids: M int32 in
  *   any order; Y: M x N.  n = 0 or r = 0: no adapters (down, up, ids unused).
- *   plan: W's plan (transposed = 0) or NULL, as for sgemm_emu_gated_linear.
+ *   plan: W's plan (SGEMM_EMU_PLAN_ROWS) or NULL, as for sgemm_emu_gated_linear.
  *   S: NULL, or 4 M pad16(r) bytes (r rounded up to a multiple of 16), 16-byte
  *   aligned: the low-rank activations scale[i] down_i X[t], as
  *   sgemm_emu_adapter_linear_backward takes them (floats for FP32; for bfloat16 a
@@ -122,7 +129,7 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
  *   d_down_i = sum over the adapter's rows of P[t] X[t]^T  (n x r x K),
  *   d_up_i = sum over the adapter's rows of dY[t] S[t]^T   (n x N x r);
  *   adapters without rows get zeros.  dX, d_down, d_up may be NULL (not
- *   computed).  W^T enters through its plan (transposed = 1, required for dX).
+ *   computed).  W^T enters through its plan (SGEMM_EMU_PLAN_TRANSPOSED, required for dX).
  *   S: the forward's.  Sums are added in a fixed order: deterministic.
  */
 int64_t sgemm_emu_adapter_linear_backward_workspace(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r);
