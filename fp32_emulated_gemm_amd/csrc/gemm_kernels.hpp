@@ -574,25 +574,44 @@ __device__ __forceinline__ int acc_row(int r, int lane) { return 8 * (r >> 2) + 
 // gate values for its neighbour's lower eight rows' up values (one DPP move per
 // pair), so each lane evaluates eight outputs: even lanes rows r, odd lanes rows
 // r + 8 of the registers.
-template <int GATE>
-__device__ __forceinline__ void emit_gated(const f32x16_t &v, const GemmArgs &g, rsrc_t rc, uint32_t row0,
-                                           int64_t col, int lane)
+//
+// value(r) gives register r with the bias added.
+template <class C, int GATE, class V>
+__device__ __forceinline__ void emit_gated(V value, const GemmArgs &g, int64_t m0, int64_t n0, int i, int j, int wm,
+                                           int wn, int lane)
 {
     const bool odd = (lane & 1) != 0;
-    const uint32_t ldc4 = (uint32_t)g.ldc * 4u;
-    const uint32_t lane_off = (uint32_t)(col >> 1) * 4u + (row0 + 4u * (uint32_t)(lane >> 5) + (odd ? 16u : 0u)) * ldc4;
+    const int64_t col = n0 + wn * C::WTN + j * 32 + (lane & 31), rows = lmin((int64_t)C::BM, g.M - m0);
+    const uint32_t row0 = (uint32_t)(wm * C::WTM + i * 32 + 4 * (lane >> 5));
+    const uint32_t ldc4 = (uint32_t)g.ldc * 4u, ldz4 = (uint32_t)g.epi.ldz * 4u;
+    const rsrc_t rc = make_rsrc(g.C + m0 * g.ldc, ((rows - 1) * g.ldc + (g.N >> 1)) * 4);
+    const rsrc_t rz = make_rsrc(g.epi.Z + m0 * g.epi.ldz, g.epi.Z != nullptr ? rows * g.epi.ldz * 4 : 0);
+    // opaque to the optimiser, which would keep every row's offset live through the whole kernel
+    uint32_t hoff = (uint32_t)(col >> 1) * 4u + (row0 + (odd ? 16u : 0u)) * ldc4;
+    uint32_t zoff = (uint32_t)((col & 1) * (g.epi.ldz >> 1) + (col >> 1)) * 4u + row0 * ldz4;
+    asm volatile("" : "+v"(hoff), "+v"(zoff));
+    float h[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-        const float give = odd ? v[r] : v[r + 8];
+        const float lo = value(r), hi = value(r + 8), give = odd ? lo : hi;
         // quad_perm [1, 0, 3, 2]: the neighbour's value
         const float got = __uint_as_float(
             (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(give), 0xB1, 0xF, 0xF, true));
-        const float gate = odd ? got : v[r], up = odd ? v[r + 8] : got;
-        const float h = gate_act<GATE>(gate) * up;
-        if (col < g.N)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h), rc,
-                                                  (int)(lane_off + (uint32_t)(8 * (r >> 2) + (r & 3)) * ldc4), 0,
+        h[r] = gate_act<GATE>(odd ? got : lo) * (odd ? hi : got);
+    }
+    if (col < g.N) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h[r]), rc,
+                                                  (int)(hoff + (uint32_t)(8 * (r >> 2) + (r & 3)) * ldc4), 0,
                                                   kStreamingStore);
+        if (g.epi.Z != nullptr) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(value(r)), rz,
+                                                      (int)(zoff + (uint32_t)(8 * (r >> 2) + (r & 3)) * ldz4), 0,
+                                                      kStreamingStore);
+        }
     }
 }
 
@@ -637,40 +656,40 @@ __device__ __forceinline__ void add_adapters(f32x16_t &v, const GemmArgs &g, int
     }
 }
 
-// Emit block (i, j) of the wave's part of a tile: its 16 values per lane with
-// the bias added.
-template <class C, int EPI, int GATE>
-__device__ __forceinline__ void emit_block(f32x16_t v, const GemmArgs &g, int64_t m0, int64_t n0, int i, int j, int wm,
+template <class C>
+__device__ __forceinline__ void emit_adapter(f32x16_t v, const GemmArgs &g, int64_t m0, int64_t n0, int i, int j,
+                                             int wm, int wn, int lane)
+{
+    const int64_t rows = lmin((int64_t)C::BM, g.M - m0);
+    const int64_t col = n0 + wn * C::WTN + j * 32 + (lane & 31);
+    const int row0 = wm * C::WTM + i * 32;
+    add_adapters(v, g, m0 + row0, col, lane);
+    const rsrc_t rc = make_rsrc(g.C + m0 * g.ldc, ((rows - 1) * g.ldc + g.N) * 4);
+    const uint32_t ldc4 = (uint32_t)g.ldc * 4u;
+    uint32_t off = (uint32_t)col * 4u + (uint32_t)(row0 + 4 * (lane >> 5)) * ldc4;
+    asm volatile("" : "+v"(off));
+    if (col < g.N) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[r]), rc,
+                                                  (int)(off + (uint32_t)(8 * (r >> 2) + (r & 3)) * ldc4), 0,
+                                                  kStreamingStore);
+    }
+}
+
+// Emit block (i, j) of the wave's part of a tile from value(r), its register r
+// with the bias added.
+template <class C, int EPI, int GATE, class V>
+__device__ __forceinline__ void emit_block(V value, const GemmArgs &g, int64_t m0, int64_t n0, int i, int j, int wm,
                                            int wn, int lane)
 {
-    const int64_t rows = lmin((int64_t)C::BM, g.M - m0), width = EPI == EPI_GATED ? g.N >> 1 : g.N;
-    const int64_t col = n0 + wn * C::WTN + j * 32 + (lane & 31);
-    const uint32_t row0 = (uint32_t)(wm * C::WTM + i * 32);
-    const rsrc_t rc = make_rsrc(g.C + m0 * g.ldc, ((rows - 1) * g.ldc + width) * 4);
     if constexpr (EPI == EPI_GATED) {
-        if (g.epi.Z != nullptr) {
-            const int64_t ldz = g.epi.ldz;
-            const rsrc_t rz = make_rsrc(g.epi.Z + m0 * ldz, rows * ldz * 4);
-            const uint32_t off = (uint32_t)((col & 1) * (ldz >> 1) + (col >> 1)) * 4u;
-            if (col < g.N) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[r]), rz,
-                                                          (int)(off + (row0 + acc_row(r, lane)) * (uint32_t)ldz * 4u),
-                                                          0, kStreamingStore);
-            }
-        }
-        emit_gated<GATE>(v, g, rc, row0, col, lane);
+        emit_gated<C, GATE>(value, g, m0, n0, i, j, wm, wn, lane);
     } else {
-        add_adapters(v, g, m0 + row0, col, lane);
-        const uint32_t ldc4 = (uint32_t)g.ldc * 4u;
-        if (col < g.N) {
+        f32x16_t v;
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[r]), rc,
-                                                      (int)((uint32_t)col * 4u + (row0 + acc_row(r, lane)) * ldc4), 0,
-                                                      kStreamingStore);
-        }
+        for (int r = 0; r < 16; ++r) v[r] = value(r);
+        emit_adapter<C>(v, g, m0, n0, i, j, wm, wn, lane);
     }
 }
 
@@ -684,12 +703,9 @@ __device__ __forceinline__ void store_c_fused(const Acc<C, NB> &acc, const float
 #pragma unroll
     for (int j = 0; j < C::NI; ++j)
 #pragma unroll
-        for (int i = 0; i < C::MI; ++i) {
-            f32x16_t v;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) v[r] = recombine<C, NB>(acc, i, j, r) + bv[j];
-            emit_block<C, EPI, GATE>(v, g, m0, n0, i, j, wm, wn, lane);
-        }
+        for (int i = 0; i < C::MI; ++i)
+            emit_block<C, EPI, GATE>([&](int r) { return recombine<C, NB>(acc, i, j, r) + bv[j]; }, g, m0, n0, i, j, wm,
+                                     wn, lane);
 }
 
 // Calls f with the gate as a compile-time constant.
@@ -1424,15 +1440,13 @@ __device__ __forceinline__ void sk_finish(const Acc<C, NB> &acc, const float (&b
 #pragma unroll
         for (int j = 0; j < C::NI; ++j)
 #pragma unroll
-            for (int i = 0; i < C::MI; ++i) {
-                f32x16_t v;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    v[r] = (w0 < w ? sum[i][j][r] + own[i][j][r] : own[i][j][r]) + bv[j];
-                    if (!ok) v[r] = __builtin_nanf("");
-                }
-                emit_block<C, EPI, GATE>(v, g, m0, n0, i, j, wm, wn, lane);
-            }
+            for (int i = 0; i < C::MI; ++i)
+                emit_block<C, EPI, GATE>(
+                    [&](int r) {
+                        const float x = (w0 < w ? sum[i][j][r] + own[i][j][r] : own[i][j][r]) + bv[j];
+                        return ok ? x : __builtin_nanf("");
+                    },
+                    g, m0, n0, i, j, wm, wn, lane);
         return;
     }
     const int64_t rows = lmin((int64_t)C::BM, g.M - m0);

@@ -35,20 +35,42 @@ struct Elem<uint16_t> {
     static __device__ __forceinline__ uint16_t store(float v) { return f2bf(v); }
 };
 
-__device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + __expf(-z)); }
-
-// act(z) of a gate.
-template <int GATE>
-__device__ __forceinline__ float gate_act(float z)
+// 1 / (1 + exp(-z)) on the hardware's exp2 and reciprocal (1 ulp each): the
+// rounding of z log2(e) leaves |z| 2^-24 or so of relative error.
+__device__ __forceinline__ float sigmoidf(float z)
 {
-    if constexpr (GATE == kSilu) return z * sigmoidf(z);
-    else if constexpr (GATE == kGelu) return gelu_erf(z);
-    else if constexpr (GATE == kGeluTanh) return z * sigmoidf(1.5957691216057308f * z * (1.0f + 0.044715f * z * z));
-    else if constexpr (GATE == kSigmoid) return sigmoidf(z);
-    else return z > 0.0f ? z : (z == z ? 0.0f : z);
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
 }
 
-// act(z) and act'(z).
+// The normal distribution's upper tail 0.5 erfc(|z| / sqrt(2)) and exp(-z^2 / 2).
+// erfc(x) = exp(-x^2) t Q(t) with t = 1 / (1 + x / 2) and Q a polynomial fitted
+// to erfcx(x) / t (relative error 5e-8 over x <= 14).  exp(-z^2 / 2) = 2^n 2^f
+// with f formed by FMAs from the exact square and a two-part log2(e), so the
+// relative error does not grow with z.  No branches: the compiler's erfcf costs
+// twice the time in the backward pass and in the GEMMs' epilogues.
+__device__ __forceinline__ float normal_tail(float z, float &e)
+{
+    const float a = fminf(__builtin_fabsf(z), 20.0f);             // 2^-288: zero from there on
+    const float h = a * a, l = __builtin_fmaf(a, a, -h);
+    const float n = __builtin_rintf(h * -0.72134752f);
+    float f = __builtin_fmaf(h, -0.72134752f, -n);
+    f = __builtin_fmaf(h, -9.62981517e-09f, f);
+    f = __builtin_fmaf(l, -0.72134752f, f);
+    e = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.35355339f, 1.0f));
+    float q = -0.0593863646f;
+    q = __builtin_fmaf(q, t, 0.286123563f);
+    q = __builtin_fmaf(q, t, -0.490405697f);
+    q = __builtin_fmaf(q, t, 0.281732714f);
+    q = __builtin_fmaf(q, t, -0.0291482948f);
+    q = __builtin_fmaf(q, t, 0.203752499f);
+    q = __builtin_fmaf(q, t, 0.242835103f);
+    q = __builtin_fmaf(q, t, 0.282412103f);
+    q = __builtin_fmaf(q, t, 0.282084331f);
+    return 0.5f * e * (t * q);
+}
+
+// act(z) and act'(z) of a gate.
 template <int GATE>
 __device__ __forceinline__ void gate_act_grad(float z, float &a, float &d)
 {
@@ -57,9 +79,10 @@ __device__ __forceinline__ void gate_act_grad(float z, float &a, float &d)
         a = z * s;
         d = s * (1.0f + z * (1.0f - s));
     } else if constexpr (GATE == kGelu) {
-        const float cdf = 0.5f * erfcf(z * -0.70710678118654752f);
+        float e;
+        const float tail = normal_tail(z, e), cdf = z < 0.0f ? tail : 1.0f - tail;
         a = z * cdf;
-        d = cdf + z * (0.3989422804014327f * __expf(-0.5f * z * z));
+        d = cdf + z * (0.3989422804014327f * e);
     } else if constexpr (GATE == kGeluTanh) {
         // 0.5 (1 + tanh(v)) = sigmoid(2 v)
         const float s = sigmoidf(1.5957691216057308f * z * (1.0f + 0.044715f * z * z));
@@ -70,9 +93,18 @@ __device__ __forceinline__ void gate_act_grad(float z, float &a, float &d)
         a = s;
         d = s * (1.0f - s);
     } else {
-        a = gate_act<kRelu>(z);
+        a = z > 0.0f ? z : (z == z ? 0.0f : z);
         d = z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
     }
+}
+
+// act(z) alone.
+template <int GATE>
+__device__ __forceinline__ float gate_act(float z)
+{
+    float a, d;
+    gate_act_grad<GATE>(z, a, d);
+    return a;
 }
 
 // The tail of a float's significand after rounding to BF16, as BF16: v is
