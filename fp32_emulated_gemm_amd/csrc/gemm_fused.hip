@@ -1,6 +1,6 @@
-// gemm_fused.hip -- the BF16x9 kernels with the operators' epilogues: the gated
-// product and the adapters' low-rank part run on a tile's recombined FP32 values
-// before they are stored, which spares a pass over the product.
+// gemm_fused.hip -- the BF16x9 kernels with the gated product in the epilogue: it
+// runs on a tile's recombined FP32 values before they are stored, which spares a
+// pass over the product.
 //
 // Nine products and the truncating split only.  The plain launchers here are
 // those of gemm.hip with the same argument form.
@@ -108,12 +108,6 @@ const PlaneLaunchers &plain_launchers()
 const PlaneLaunchers &gated_launchers()
 {
     static const PlaneLaunchers l = {tile64<EPI_GATED>, planes<EPI_GATED>, dma<EPI_GATED>};
-    return l;
-}
-
-const PlaneLaunchers &adapter_launchers()
-{
-    static const PlaneLaunchers l = {tile64<EPI_ADAPTER>, planes<EPI_ADAPTER>, dma<EPI_ADAPTER>};
     return l;
 }
 

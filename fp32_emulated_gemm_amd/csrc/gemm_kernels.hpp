@@ -57,8 +57,8 @@
 namespace sgemm_emu_dev {
 
 // What a kernel's epilogue does with a tile: store it (bias, activation), or the
-// operators' fused ones.
-enum { EPI_STORE = 0, EPI_GATED = 1, EPI_ADAPTER = 2 };
+// gated product.
+enum { EPI_STORE = 0, EPI_GATED = 1 };
 
 // Launch the last kernel of a call.  With g.done set (a call that used the
 // stream's workspace block), the event is tied to that kernel's completion, so
@@ -564,10 +564,7 @@ __device__ __forceinline__ void store_c_act(const Acc<C, NB> &acc, const float (
     }
 }
 
-// ---------------------------------------------------------------- fused epilogues
-
-// Row of accumulator register r of a 32 x 32 block in lane `lane`.
-__device__ __forceinline__ int acc_row(int r, int lane) { return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); }
+// ---------------------------------------------------------------- gated epilogue
 
 // Gated block: B's columns alternate gate, up, so an output's two values lie in
 // neighbouring lanes of one register.  An even lane gives its upper eight rows'
@@ -615,97 +612,19 @@ __device__ __forceinline__ void emit_gated(V value, const GemmArgs &g, int64_t m
     }
 }
 
-// Adapter block: v[row] += up[i] . S[row] on the FP32 matrix instruction for the
-// rows of each adapter i that occurs in the block's 32 rows (in order of their
-// first row).  A lane's four consecutive ranks are the k of four instructions.
-// A row keeps its old value unless it belongs to the adapter, so Inf and NaN in
-// one adapter's weights never reach another's rows.
-__device__ __forceinline__ void add_adapters(f32x16_t &v, const GemmArgs &g, int64_t m_block, int64_t col, int lane)
-{
-    const GemmEpilogue &e = g.epi;
-    const int64_t m = m_block + (lane & 31);
-    int32_t id = m < g.M ? e.ids[m] : -1;
-    if (id >= e.n) id = -1;
-    uint32_t todo = (uint32_t)__ballot(id >= 0);
-    const float *srow = e.S + lmin(m, g.M - 1) * e.rp + 4 * (lane >> 5);
-    const float *urow = e.up + lmin(col, g.N - 1) * e.r + 4 * (lane >> 5);
-    const bool vec = e.r % 4 == 0 && ((uintptr_t)e.up % 16) == 0;
-    typedef float f32x4 __attribute__((ext_vector_type(4)));
-    while (todo != 0) {
-        const int32_t me = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-        const uint32_t own = (uint32_t)__ballot(id == me);
-        todo &= ~own;
-        f32x16_t t = v;
-        for (int64_t q = 0; q < e.rp; q += 8) {
-            const f32x4 s = *reinterpret_cast<const f32x4 *>(srow + q);
-            const float *p = urow + (int64_t)me * g.N * e.r + q;
-            const int64_t k = q + 4 * (lane >> 5);
-            f32x4 u = {0, 0, 0, 0};
-            if (vec) {
-                if (k < e.r) u = *reinterpret_cast<const f32x4 *>(p);
-            } else {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (k + x < e.r) u[x] = p[x];
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) t = __builtin_amdgcn_mfma_f32_32x32x2f32(s[x], u[x], t, 0, 0, 0);
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = (own >> acc_row(r, lane)) & 1 ? t[r] : v[r];
-    }
-}
-
-template <class C>
-__device__ __forceinline__ void emit_adapter(f32x16_t v, const GemmArgs &g, int64_t m0, int64_t n0, int i, int j,
-                                             int wm, int wn, int lane)
-{
-    const int64_t rows = lmin((int64_t)C::BM, g.M - m0);
-    const int64_t col = n0 + wn * C::WTN + j * 32 + (lane & 31);
-    const int row0 = wm * C::WTM + i * 32;
-    add_adapters(v, g, m0 + row0, col, lane);
-    const rsrc_t rc = make_rsrc(g.C + m0 * g.ldc, ((rows - 1) * g.ldc + g.N) * 4);
-    const uint32_t ldc4 = (uint32_t)g.ldc * 4u;
-    uint32_t off = (uint32_t)col * 4u + (uint32_t)(row0 + 4 * (lane >> 5)) * ldc4;
-    asm volatile("" : "+v"(off));
-    if (col < g.N) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[r]), rc,
-                                                  (int)(off + (uint32_t)(8 * (r >> 2) + (r & 3)) * ldc4), 0,
-                                                  kStreamingStore);
-    }
-}
-
-// Emit block (i, j) of the wave's part of a tile from value(r), its register r
-// with the bias added.
-template <class C, int EPI, int GATE, class V>
-__device__ __forceinline__ void emit_block(V value, const GemmArgs &g, int64_t m0, int64_t n0, int i, int j, int wm,
-                                           int wn, int lane)
-{
-    if constexpr (EPI == EPI_GATED) {
-        emit_gated<C, GATE>(value, g, m0, n0, i, j, wm, wn, lane);
-    } else {
-        f32x16_t v;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = value(r);
-        emit_adapter<C>(v, g, m0, n0, i, j, wm, wn, lane);
-    }
-}
-
 template <class C, int NB>
 __device__ __forceinline__ float recombine(const Acc<C, NB> &acc, int i, int j, int r);
 
-template <class C, int NB, int EPI, int GATE>
-__device__ __forceinline__ void store_c_fused(const Acc<C, NB> &acc, const float (&bv)[C::NI], const GemmArgs &g,
+template <class C, int NB, int GATE>
+__device__ __forceinline__ void store_c_gated(const Acc<C, NB> &acc, const float (&bv)[C::NI], const GemmArgs &g,
                                               int64_t m0, int64_t n0, int wm, int wn, int lane)
 {
 #pragma unroll
     for (int j = 0; j < C::NI; ++j)
 #pragma unroll
         for (int i = 0; i < C::MI; ++i)
-            emit_block<C, EPI, GATE>([&](int r) { return recombine<C, NB>(acc, i, j, r) + bv[j]; }, g, m0, n0, i, j, wm,
-                                     wn, lane);
+            emit_gated<C, GATE>([&](int r) { return recombine<C, NB>(acc, i, j, r) + bv[j]; }, g, m0, n0, i, j, wm, wn,
+                                lane);
 }
 
 // Calls f with the gate as a compile-time constant.
@@ -727,9 +646,8 @@ __device__ __forceinline__ void store_c(const Acc<C, NB> &acc, const float (&bv)
 {
     if constexpr (EPI == EPI_GATED)
         with_gate(g.epi.gate, [&](auto gate) {
-            store_c_fused<C, NB, EPI, decltype(gate)::value>(acc, bv, g, m0, n0, wm, wn, lane);
+            store_c_gated<C, NB, decltype(gate)::value>(acc, bv, g, m0, n0, wm, wn, lane);
         });
-    else if constexpr (EPI == EPI_ADAPTER) store_c_fused<C, NB, EPI, 0>(acc, bv, g, m0, n0, wm, wn, lane);
     else if (g.act == 1) store_c_act<C, NB, 1>(acc, bv, g, m0, n0, wm, wn, lane);
     else store_c_act<C, NB, 0>(acc, bv, g, m0, n0, wm, wn, lane);
 }
@@ -1441,7 +1359,7 @@ __device__ __forceinline__ void sk_finish(const Acc<C, NB> &acc, const float (&b
         for (int j = 0; j < C::NI; ++j)
 #pragma unroll
             for (int i = 0; i < C::MI; ++i)
-                emit_block<C, EPI, GATE>(
+                emit_gated<C, GATE>(
                     [&](int r) {
                         const float x = (w0 < w ? sum[i][j][r] + own[i][j][r] : own[i][j][r]) + bv[j];
                         return ok ? x : __builtin_nanf("");
@@ -1483,7 +1401,6 @@ __device__ __forceinline__ void sk_finish_any(const Acc<C, NB> &acc, const float
         with_gate(g.epi.gate, [&](auto gate) {
             sk_finish<C, NB, 0, EPI, decltype(gate)::value>(acc, bv, g, m0, n0, w0, w, D, wm, wn, lane);
         });
-    else if constexpr (EPI == EPI_ADAPTER) sk_finish<C, NB, 0, EPI, 0>(acc, bv, g, m0, n0, w0, w, D, wm, wn, lane);
     else if (g.act == 1) sk_finish<C, NB, 1, EPI, 0>(acc, bv, g, m0, n0, w0, w, D, wm, wn, lane);
     else sk_finish<C, NB, 0, EPI, 0>(acc, bv, g, m0, n0, w0, w, D, wm, wn, lane);
 }

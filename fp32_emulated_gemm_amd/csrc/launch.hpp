@@ -15,14 +15,11 @@ enum BSource {
     B_PLANES_NK = 2    // three BF16 planes, N x K row-major (B transposed, k contiguous)
 };
 
-// Fused epilogues of the FP32 products (gemm_fused.hip).
+// The gated epilogue of the FP32 products (gemm_fused.hip): C is H (M x N / 2).
 struct GemmEpilogue {
-    int gate;                // gated: the gate; C is H (M x N / 2)
-    float *Z;                // gated: pre-activations to keep (rows of ldz floats, up from ldz / 2), or null
+    int gate;
+    float *Z;                // pre-activations to keep (rows of ldz floats, up from ldz / 2), or null
     int64_t ldz;
-    const int32_t *ids;      // adapters: rows' ids, n adapters of rank r (S: M x rp, up: n x N x r)
-    int64_t n, r, rp;
-    const float *up, *S;
 };
 
 struct GemmArgs {
@@ -54,7 +51,7 @@ struct GemmArgs {
     uint32_t sk_epoch;       // stream-K: this launch's flag value (never 0)
     int sk_grid;             // stream-K: workgroups G (0: no stream-K)
     int sk_domains;          // stream-K: 1, or 8 (one block of tiles per XCD); set by the launcher
-    GemmEpilogue epi;        // fused epilogues only
+    GemmEpilogue epi;        // gated epilogue only
 };
 
 // rne: round each split stage to nearest even instead of truncating (ablation).

@@ -537,6 +537,79 @@ hipError_t launch_shrink_t(int64_t M, int64_t K, const T *X, int64_t ldx, const 
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------- expand (FP32)
+// Y[t] += up[i] S[t].  A wave takes 32 rows x 64 columns: its part of Y is the
+// accumulator of FP32 MFMAs over the rank, for one adapter of its rows after
+// another (in order of their first row); a row keeps its old value unless it
+// belongs to the adapter, so Inf and NaN in one adapter's weights never reach
+// another's rows.  One pass over Y in the shadow of many waves: inside the
+// BF16x9 kernels' epilogue, which has no registers to spare, the same work took
+// 9 us (6144 x 1024 x 256) to 40 us (6144 x 256 x 1024) more than the product.
+__global__ __launch_bounds__(256) void expand_kernel(int64_t M, int64_t N, const float *S, int64_t rp, Adapters ad,
+                                                     float *Y, int64_t ldy)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const int64_t m0 = ((int64_t)blockIdx.x * 2 + (wave >> 1)) * 32, n0 = ((int64_t)blockIdx.y * 2 + (wave & 1)) * 64;
+    if (m0 >= M || n0 >= N) return;
+    const int64_t m = m0 + (lane & 31);
+    int32_t id = m < M ? ad.ids[m] : -1;
+    if (id >= ad.n) id = -1;
+    uint32_t todo = (uint32_t)__ballot(id >= 0);
+    if (todo == 0) return;
+    const float *srow = S + lmin(m, M - 1) * rp + 4 * half;
+    int64_t col[2];
+    float *y[2];
+    f32x16_t acc[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        col[j] = n0 + j * 32 + (lane & 31);
+        y[j] = Y + (m0 + 4 * half) * ldy + col[j];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = 8 * (r >> 2) + (r & 3);
+            acc[j][r] = m0 + 4 * half + row < M && col[j] < N ? y[j][row * ldy] : 0.0f;
+        }
+    }
+    const bool vec = ad.r % 4 == 0 && ((uintptr_t)ad.up % 16) == 0;
+    while (todo != 0) {
+        const int32_t me = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+        const uint32_t own = (uint32_t)__ballot(id == me) >> (4 * half);
+        todo &= ~(uint32_t)__ballot(id == me);
+        const float *bank = (const float *)ad.up + (int64_t)me * N * ad.r + 4 * half;
+        f32x16_t t[2] = {acc[0], acc[1]};
+        for (int64_t q = 0; q < ad.r; q += 8) {
+            // a lane's four consecutive ranks are the k of four instructions
+            const f32x4_t s = *reinterpret_cast<const f32x4_t *>(srow + q);
+            const int64_t k = q + 4 * half;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float *p = bank + lmin(col[j], N - 1) * ad.r + q;
+                f32x4_t u = {0, 0, 0, 0};
+                if (vec) {
+                    if (k < ad.r) u = *reinterpret_cast<const f32x4_t *>(p);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (k + e < ad.r) u[e] = p[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[j] = __builtin_amdgcn_mfma_f32_32x32x2f32(s[e], u[e], t[j], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[j][r] = (own >> (8 * (r >> 2) + (r & 3))) & 1 ? t[j][r] : acc[j][r];
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = 8 * (r >> 2) + (r & 3);
+            if (m0 + 4 * half + row < M && col[j] < N) y[j][row * ldy] = acc[j][r];
+        }
+}
+
 // ---------------------------------------------------------------- grouping rows by adapter
 // Workgroup i lists the rows of adapter i, ascending: it counts the ids below
 // its own (where its rows start) and its own, then writes its rows in order
@@ -797,6 +870,14 @@ hipError_t launch_shrink(int dtype, int64_t M, int64_t K, const void *X, int64_t
 {
     return dtype == kF32 ? launch_shrink_t<float>(M, K, (const float *)X, ldx, ad, S, num_cus, stream)
                          : launch_shrink_t<uint16_t>(M, K, (const uint16_t *)X, ldx, ad, S, num_cus, stream);
+}
+
+hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &ad, float *Y, int64_t ldy,
+                         hipStream_t stream)
+{
+    const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((N + 127) / 128));
+    hipLaunchKernelGGL(expand_kernel, grid, dim3(256), 0, stream, M, N, S, rank_pad(ad.r), ad, Y, ldy);
+    return hipGetLastError();
 }
 
 hipError_t launch_group(int64_t M, const int32_t *ids, int64_t n, int32_t *offs, int32_t *rows, hipStream_t stream)

@@ -30,6 +30,10 @@ inline int64_t rank_pad(int64_t r) { return round_up(r, 16); }   // row pitch of
 hipError_t launch_shrink(int dtype, int64_t M, int64_t K, const void *X, int64_t ldx, const Adapters &ad, float *S,
                          int num_cus, hipStream_t stream);
 
+// FP32: Y[t] += up[i] S[t] for the rows that have an adapter.
+hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &ad, float *Y, int64_t ldy,
+                         hipStream_t stream);
+
 // offs[0..n]: where each adapter's rows start in rows[]; rows[]: the row
 // numbers that have an adapter, grouped by it, ascending inside a group.
 hipError_t launch_group(int64_t M, const int32_t *ids, int64_t n, int32_t *offs, int32_t *rows, hipStream_t stream);
@@ -141,7 +145,6 @@ hipError_t launch_sum_tiles(int dtype, int64_t tiles, int64_t cols, const float 
 int gemm_padded_planes(const GemmArgs &args, const PlaneLaunchers &launch, hipStream_t stream);
 const PlaneLaunchers &plain_launchers();     // bias
 const PlaneLaunchers &gated_launchers();     // bias, gate (args.epi; B's columns alternate gate, up)
-const PlaneLaunchers &adapter_launchers();   // bias, adapters (args.epi)
 // The current device's CU count if it is a gfx950 (SGEMM_EMU_EARCH otherwise).
 int current_cus(int *num_cus);
 

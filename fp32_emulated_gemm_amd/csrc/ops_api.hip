@@ -106,16 +106,6 @@ int plain_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, cons
     return gemm_padded_planes(product_f32(M, N, K, A, lda, planes, nullptr, C, ldc), plain_launchers(), stream);
 }
 
-GemmEpilogue adapter_epilogue(const Adapters &ad, const float *S)
-{
-    GemmEpilogue e{};
-    e.ids = ad.ids;
-    e.n = ad.n; e.r = ad.r; e.rp = rank_pad(ad.r);
-    e.up = (const float *)ad.up;
-    e.S = S;
-    return e;
-}
-
 // ---------------------------------------------------------------- gated projection
 
 int check_gated(int dtype, int64_t M, int64_t F, int64_t K, int gate)
@@ -497,10 +487,12 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
             return SGEMM_EMU_OK;
         }
         if (w.plan != nullptr) LAUNCH(launch_split_padded(N, K, (const float *)W, ldw, w.plan, false, s));
-        GemmArgs g = product_f32(M, N, K, (const float *)X, ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
-                                 (const float *)bias, (float *)Y, ldy);
-        if (low) g.epi = adapter_epilogue(ad, S);
-        return gemm_padded_planes(g, low ? adapter_launchers() : plain_launchers(), s);
+        CHECK(gemm_padded_planes(product_f32(M, N, K, (const float *)X, ldx,
+                                             w.plan != nullptr ? w.plan : (const uint16_t *)plan, (const float *)bias,
+                                             (float *)Y, ldy),
+                                 plain_launchers(), s));
+        if (low) LAUNCH(launch_expand(M, N, S, ad, (float *)Y, ldy, s));
+        return SGEMM_EMU_OK;
     }
     Bf16Gemm g{};
     g.M = M; g.N = N; g.K = bf16_k(K);
@@ -575,15 +567,8 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
     if (need_dx) {
         if (low) LAUNCH(launch_transpose_bank(dtype, n, r, K, down, w.down_t, s));
         if (dtype == SGEMM_EMU_F32) {
-            if (low && N > 0) {
-                GemmArgs g = product_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, nullptr,
-                                         (float *)dX, lddx);
-                g.epi = adapter_epilogue(back, w.p);
-                CHECK(gemm_padded_planes(g, adapter_launchers(), s));
-            } else {
-                CHECK(plain_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, (float *)dX, lddx, num_cus,
-                                s));
-            }
+            CHECK(plain_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, (float *)dX, lddx, num_cus, s));
+            if (low && N > 0) LAUNCH(launch_expand(M, K, w.p, back, (float *)dX, lddx, s));
         } else {
             Bf16Gemm g{};
             g.M = M; g.N = K; g.K = bf16_k(N);
