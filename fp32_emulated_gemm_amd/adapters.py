@@ -29,10 +29,10 @@ def _forward(x, xld, weight, wld, a, b, ids, scale, bias, plan, keep):
     low = n > 0 and r > 0
     s = torch.empty((M, -(-r // 16) * 16), dtype=torch.float32, device=x.device) if low and keep else None
     fwd = None if plan is None else addr(plan.forward)
-    xp, wp, sp = addr(x), addr(weight), addr(s)
-    ws, nws = scratch(ok(L.sgemm_emu_adapter_linear_workspace(dt, M, N, K, xp, xld, wp, wld, fwd, n, r, sp),
+    xp, wp, bp, sp = addr(x), addr(weight), addr(b), addr(s)
+    ws, nws = scratch(ok(L.sgemm_emu_adapter_linear_workspace(dt, M, N, K, xp, xld, wp, wld, fwd, n, r, bp, sp),
                              "sgemm_emu_adapter_linear_workspace"), x.device)
-    ok(L.sgemm_emu_adapter_linear(dt, M, N, K, xp, xld, wp, wld, fwd, addr(bias), n, r, addr(a), addr(b), addr(scale),
+    ok(L.sgemm_emu_adapter_linear(dt, M, N, K, xp, xld, wp, wld, fwd, addr(bias), n, r, addr(a), bp, addr(scale),
                                   addr(ids), addr(y), max(N, 1), sp, addr(ws), nws, current_stream()),
        "sgemm_emu_adapter_linear")
     return y, s

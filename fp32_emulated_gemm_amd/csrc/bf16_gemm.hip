@@ -4,21 +4,25 @@
 // A bfloat16 value is its own first component: one product takes the place of
 // the nine of the FP32 emulation, accumulated in FP32 and rounded once.
 //
-// One workgroup per BM x BN output tile.  K advances in steps of 32; both
-// operands' tiles of a step (64-byte rows, the 16-byte slot of k group kg of
-// row r at slot kg ^ ((r >> 2) & 3), which keeps the 128-bit fragment reads of
-// 16 consecutive rows on distinct banks) are copied global -> LDS by buffer
-// loads with LDS destination, three steps ahead, into a ring of four buffers.
-// One LDS-only barrier per step: the copies of step kt + 3 overwrite the buffer
-// of step kt - 1, whose last fragments every wave read before the barrier of
-// step kt - 1.  After a step's barrier the next step's first fragments are
-// read while the step's last MFMAs run.
+// One workgroup per BM x BN output tile.  K advances in steps of 64, two MFMA
+// slices; both operands' tiles of a step (128-byte rows, so that a copy takes
+// whole cache lines; the 16-byte slot of k group kg of row r at slot
+// kg ^ ((r >> 1) & 7), which keeps the 128-bit fragment reads of 16 rows on
+// distinct banks) are copied global -> LDS by buffer loads with LDS destination
+// into a ring of buffers.  A step enters with its first slice's fragments in
+// registers: it reads the second slice's under the first slice's MFMAs, passes
+// one LDS-only barrier, behind which its buffer is free for the copies of the
+// step a ring ahead, and reads the next step's first slice under its second
+// slice's MFMAs.
+// v_mfma_f32_16x16x32_bf16 rather than 32x32x16: an accumulator is read and
+// written once per 32 products instead of 16, and this load runs at the chip's
+// power limit.
 //
 // The MFMAs take B's rows as their first operand, so a lane's accumulator
 // registers run along N for one row of C (its column in the MFMA's result):
 // gate and up rows of a gated product are dealt to the tile in alternating
 // blocks of 16, which puts act(gate) and up of one output into one lane, and
-// the adapters' part of the epilogue selects its rows per lane.
+// the adapters' part selects its rows per lane.
 // The result goes through LDS (the ring's space) and leaves in 128-bit stores.
 #include "ops_device.hpp"
 #include "ops.hpp"
@@ -29,26 +33,26 @@ namespace {
 
 enum { EPI_PLAIN = 0, EPI_GATED = 1, EPI_ADAPTER = 2, EPI_PARTIAL = 3 };
 
-constexpr int KS = 32;                       // K step
-constexpr int RING = 4;
+constexpr int KS = 64;                       // K step
 
-template <int WAVES_M_, int WAVES_N_, int TM_, int TN_>
+template <int WAVES_M_, int WAVES_N_, int TM_, int TN_, int RING_, int PER_CU_>
 struct Tile {
+    static constexpr int RING = RING_, PER_CU = PER_CU_;           // ring buffers, workgroups per CU
     static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WAVES = WAVES_M * WAVES_N, NT = 64 * WAVES;
     static constexpr int TM = TM_, TN = TN_;                       // one wave's part
     static constexpr int BM = WAVES_M * TM, BN = WAVES_N * TN;
-    static constexpr int MI = TM / 32, NI = TN / 32;
-    static constexpr int A_COPIES = BM / 16 / WAVES, B_COPIES = BN / 16 / WAVES;   // 16-row copies per wave and step
+    static constexpr int MI = TM / 16, NI = TN / 16;
+    static constexpr int A_COPIES = BM / 8 / WAVES, B_COPIES = BN / 8 / WAVES;   // 8-row copies per wave and step
     static constexpr int STAGE = (BM + BN) * KS;                   // BF16 elements of one ring buffer
     static constexpr int PITCH = TN + 8;                           // epilogue rows: an odd number of 16-byte slots
     static constexpr int EPI_WAVE = TM * PITCH;
     static constexpr int LDS = RING * STAGE > WAVES * EPI_WAVE ? RING * STAGE : WAVES * EPI_WAVE;
-    static_assert(BM % (16 * WAVES) == 0 && BN % (16 * WAVES) == 0, "tile rows split into 16-row copies");
+    static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "tile rows split into 8-row copies");
 };
 
-using Tile256 = Tile<2, 4, 128, 64>;         // 8 waves, one workgroup per CU
-using Tile128 = Tile<2, 2, 64, 64>;          // 4 waves, two workgroups per CU
-using Tile64 = Tile<2, 2, 32, 32>;           // 4 waves
+using Tile256 = Tile<2, 4, 128, 64, 2, 1>;        // 8 waves
+using Tile128 = Tile<2, 2, 64, 64, 2, 2>;         // 4 waves
+using Tile64 = Tile<2, 2, 32, 32, 4, 2>;          // 4 waves
 
 constexpr uint32_t OUT_OF_RANGE = 0xFFFFFFF0u;   // past every descriptor: reads zeros
 
@@ -70,106 +74,155 @@ struct Frag {
     bf16x8_t a[T::MI], b[T::NI];
 };
 
+// 16-byte slot of k group kg (8 elements) of tile row `row`.
+__device__ __forceinline__ int kslot(int row, int kg) { return kg ^ ((row >> 1) & 7); }
+
+// Fragments of a slice of 32 k: lane l holds k 8 (l >> 4) .. + 7 of row l & 15 of each block.
 template <class T>
 __device__ __forceinline__ void read_frag(Frag<T> &f, const uint16_t *buf, int slice, int wm, int wn, int lane)
 {
-    const int kg = slice * 2 + (lane >> 5);
+    const int kg = slice * 4 + (lane >> 4);
 #pragma unroll
     for (int j = 0; j < T::NI; ++j) {
-        const int row = wn * T::TN + j * 32 + (lane & 31);
-        f.b[j] = ld_frag(buf + T::BM * KS + row * KS + bslot(row, kg) * 8);
+        const int row = wn * T::TN + j * 16 + (lane & 15);
+        f.b[j] = ld_frag(buf + T::BM * KS + row * KS + kslot(row, kg) * 8);
     }
 #pragma unroll
     for (int i = 0; i < T::MI; ++i) {
-        const int row = wm * T::TM + i * 32 + (lane & 31);
-        f.a[i] = ld_frag(buf + row * KS + bslot(row, kg) * 8);
+        const int row = wm * T::TM + i * 16 + (lane & 15);
+        f.a[i] = ld_frag(buf + row * KS + kslot(row, kg) * 8);
     }
 }
 
-template <class T, int FIRST, int LAST>
-__device__ __forceinline__ void mfma_part(f32x16_t (&acc)[T::NI][T::MI], const Frag<T> &f)
+// Waits until at most N of this wave's copies are outstanding and its fragment
+// reads are done, then for the other waves.  Builtins, so that the compiler knows
+// the reads have arrived and adds no waits of its own.
+template <int N>
+__device__ __forceinline__ void step_barrier()
 {
-    int n = 0;
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Schedules N reads (and N2 copies) one behind each of the first of NM MFMAs:
+// issued together they would hold the MFMAs back; left to the compiler, they sink
+// to the end and the next barrier waits for them.
+template <int NM, int N, int KIND, int N2 = 0, int KIND2 = 0>
+__device__ __forceinline__ void spread()
+{
+    constexpr int PER = (N + N2 + NM - 1) / NM;
+#pragma unroll
+    for (int q = 0; q < (N + PER - 1) / PER; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(KIND, PER, 0);
+    }
+    if constexpr (N2 > 0) {
+#pragma unroll
+        for (int q = 0; q < (N2 + PER - 1) / PER; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(KIND2, PER, 0);
+        }
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void mfma_slice(f32x4_t (&acc)[T::NI][T::MI], const Frag<T> &f)
+{
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-        for (int j = 0; j < T::NI; ++j) {
-            if (n >= FIRST && n < LAST)
-                acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[j][i], 0, 0, 0);
-            ++n;
-        }
+        for (int j = 0; j < T::NI; ++j)
+            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[i], acc[j][i], 0, 0, 0);
 }
 
-// Add the adapters' part: acc[n][m] += up[i][n][:] . S[m][:] for the rows m of
-// adapter i, one adapter of the wave's rows after another (in order of their
-// first row).  S comes in two BF16 parts (16 significant bits; the rest lies
-// 2^-8 below the output's own rounding), up is exact.  A lane keeps its old
-// value unless its row belongs to the adapter: zero times Inf or NaN in one
-// adapter's weights never reaches another's rows.
+// The accumulators' start: the adapters' part, up[i][n][:] . S[m][:] for the
+// rows m of adapter i, zeros for rows without one.  S comes in two BF16 parts (16
+// significant bits; the rest lies 2^-8 below the output's own rounding), up is
+// exact: 16 ranks' high and low parts are the 32 k of one MFMA.
+// A wave whose rows share one adapter (the inside of a request) multiplies them
+// all at once.  Elsewhere each block of 16 rows takes its adapters one after
+// another (in order of their first row), and a lane keeps the products of its
+// own row's: zero times Inf or NaN in one adapter's weights never reaches
+// another's rows.
 template <class T>
-__device__ __forceinline__ void add_adapters(f32x16_t (&acc)[T::NI][T::MI], const Bf16Gemm &g, int64_t m0w,
-                                             int64_t n0w, int lane)
+__device__ __forceinline__ void start_adapters(f32x4_t (&acc)[T::NI][T::MI], const Bf16Gemm &g, int64_t m0w,
+                                               int64_t n0w, int lane)
 {
     int id[T::MI];
-    const uint16_t *srow[T::MI], *urow[T::NI];
-    uint32_t todo[T::MI];
 #pragma unroll
     for (int i = 0; i < T::MI; ++i) {
-        const int64_t m = m0w + i * 32 + (lane & 31);
-        srow[i] = g.S + lmin(m, g.M - 1) * 2 * g.rp + 8 * (lane >> 5);
-        const int v = m < g.M ? g.ids[m] : -1;
+        // rows past M count as the last one: they are dropped
+        const int v = g.ids[lmin(m0w + i * 16 + (lane & 15), g.M - 1)];
         id[i] = v >= 0 && v < g.n ? v : -1;
-        todo[i] = (uint32_t)__ballot(id[i] >= 0);
     }
+    // Rows and ranks past the matrices read zeros: their offsets lie past the
+    // descriptors.
+    const int r8 = 8 * ((lane >> 4) & 1);                        // first rank of this lane
+    const uint32_t srow = (uint32_t)(((lane & 15) * 2 + (lane >> 5)) * g.rp + r8) * 2u;   // high or low part
+    const uint32_t urow = (uint32_t)((lane & 15) * g.r + r8) * 2u;
+    const uint32_t sblock = (uint32_t)g.rp * 64u, ublock = (uint32_t)g.r * 32u;           // bytes of 16 rows
+    const rsrc_t rs = make_rsrc(g.S + m0w * 2 * g.rp, (g.M - m0w) * 2 * g.rp * 2);
+    auto bank = [&](int me) { return make_rsrc(g.up + ((int64_t)me * g.N + n0w) * g.r, (g.N - n0w) * g.r * 2); };
+    auto load_up = [&](u32x4_t (&up)[T::NI], rsrc_t ru, int64_t rc) {
 #pragma unroll
-    for (int j = 0; j < T::NI; ++j)
-        urow[j] = g.up + lmin(n0w + j * 32 + (lane & 31), g.N - 1) * g.r + 8 * (lane >> 5);
-    const bool vec = g.r % 8 == 0 && ((uintptr_t)g.up % 16) == 0;
-    for (;;) {
-        int me = -1;
+        for (int j = 0; j < T::NI; ++j)
+            up[j] = bload_u32x4(ru, rc + r8 < g.r ? urow + j * ublock + (uint32_t)rc * 2u : OUT_OF_RANGE, 0);
+    };
+    const int first = __builtin_amdgcn_readfirstlane(id[0]);
+    bool same = true;
 #pragma unroll
-        for (int i = T::MI - 1; i >= 0; --i)
-            if (todo[i] != 0) me = __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo[i]));
-        if (me < 0) break;
-        bool own[T::MI];
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i) {
-            own[i] = id[i] == me;
-            todo[i] &= ~(uint32_t)__ballot(own[i]);
-        }
-        const int64_t bank = (int64_t)me * g.N * g.r;
+    for (int i = 0; i < T::MI; ++i) same = same && id[i] == first;
+    if (__all(same)) {
+        if (first < 0) return;
+        const rsrc_t ru = bank(first);
         for (int64_t rc = 0; rc < g.rp; rc += 16) {
-            u32x4_t up[T::NI], hi[T::MI], lo[T::MI];
+            u32x4_t up[T::NI], sv[T::MI];
+            load_up(up, ru, rc);
 #pragma unroll
-            for (int j = 0; j < T::NI; ++j) {
-                const uint16_t *p = urow[j] + bank + rc;
-                const int64_t r0 = rc + 8 * (lane >> 5);
-                up[j] = u32x4_t{0, 0, 0, 0};
-                if (vec) {
-                    if (r0 < g.r) up[j] = *reinterpret_cast<const u32x4_t *>(p);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (r0 + e < g.r) up[j][e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < T::MI; ++i) {
-                hi[i] = *reinterpret_cast<const u32x4_t *>(srow[i] + rc);
-                lo[i] = *reinterpret_cast<const u32x4_t *>(srow[i] + g.rp + rc);
-            }
+            for (int i = 0; i < T::MI; ++i) sv[i] = bload_u32x4(rs, srow + i * sblock + (uint32_t)rc * 2u, 0);
 #pragma unroll
             for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-                for (int j = 0; j < T::NI; ++j) {
-                    const bf16x8_t u = __builtin_bit_cast(bf16x8_t, up[j]);
-                    f32x16_t t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u, __builtin_bit_cast(bf16x8_t, lo[i]),
-                                                                         acc[j][i], 0, 0, 0);
-                    t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u, __builtin_bit_cast(bf16x8_t, hi[i]), t, 0, 0, 0);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) acc[j][i][q] = own[i] ? t[q] : acc[j][i][q];
-                }
+                for (int j = 0; j < T::NI; ++j)
+                    acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8_t, up[j]), __builtin_bit_cast(bf16x8_t, sv[i]), acc[j][i], 0, 0, 0);
         }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i) {
+        f32x4_t mine[T::NI];
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) mine[j] = f32x4_t{};
+        uint32_t todo = (uint32_t)__ballot(id[i] >= 0) & 0xFFFFu;
+        while (todo != 0) {
+            const int me = __builtin_amdgcn_readlane(id[i], __builtin_ctz(todo));
+            todo &= ~(uint32_t)__ballot(id[i] == me);
+            const rsrc_t ru = bank(me);
+            f32x4_t t[T::NI];
+#pragma unroll
+            for (int j = 0; j < T::NI; ++j) t[j] = f32x4_t{};
+            for (int64_t rc = 0; rc < g.rp; rc += 16) {
+                u32x4_t up[T::NI];
+                load_up(up, ru, rc);
+                const u32x4_t sv = bload_u32x4(rs, srow + i * sblock + (uint32_t)rc * 2u, 0);
+#pragma unroll
+                for (int j = 0; j < T::NI; ++j)
+                    t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, up[j]),
+                                                                   __builtin_bit_cast(bf16x8_t, sv), t[j], 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < T::NI; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mine[j][q] = id[i] == me ? t[j][q] : mine[j][q];
+        }
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) acc[j][i] = mine[j];
     }
 }
 
@@ -189,11 +242,9 @@ __device__ __forceinline__ void flush_block(const uint16_t *buf, uint16_t *out, 
             if (m0w + row < M) *reinterpret_cast<u32x4_t *>(out + (m0w + row) * ld + c0 + c) = v;
         }
     } else {
-        constexpr int ROWS = 64 / W;
-        const int c = lane % W;
 #pragma unroll 8
-        for (int p = 0; p < T::TM / ROWS; ++p) {
-            const int row = p * ROWS + lane / W;
+        for (int e = lane; e < T::TM * W; e += 64) {
+            const int row = e / W, c = e % W;
             const uint16_t v = buf[row * T::PITCH + c];
             if (m0w + row < M && c0 + c < cols) out[(m0w + row) * ld + c0 + c] = v;
         }
@@ -215,7 +266,7 @@ __device__ __forceinline__ void put4(uint16_t *buf, int row, int col, float v0, 
     *reinterpret_cast<u32x2 *>(buf + row * T::PITCH + col) = u32x2{pack2(v0, v1), pack2(v2, v3)};
 }
 
-template <class T, int EPI, int GATE>
+template <class T, int EPI, int GATE, bool KTAIL>
 __device__ __forceinline__ void gemm_tile(const Bf16Gemm &g, uint16_t *lds)
 {
     typedef __attribute__((address_space(3))) void lds_void_t;
@@ -228,184 +279,171 @@ __device__ __forceinline__ void gemm_tile(const Bf16Gemm &g, uint16_t *lds)
     const int64_t kb = (int64_t)blockIdx.y * g.k_per_split, ke = lmin(kb + g.k_per_split, g.K);
     const int nk = (int)((ke - kb + KS - 1) / KS);
 
-    // Copies: lane -> (row, 16-byte slot) of a 16-row block.  The rows' offsets
-    // are relative to a per-copy base; k past the end reads zeros.
-    const int srow = lane >> 2;
+    // Copies: lane -> (row, 16-byte slot) of an 8-row block.  A lane's offset from
+    // its block's first row is fixed; k advances in the scalar offset, so a copy
+    // costs no vector arithmetic.  Copies past the last step repeat it (nobody
+    // reads them), so every access lies inside the operand; in the last step of a
+    // K that is not a multiple of KS the lanes past K read zeros.
+    const int srow = lane >> 3;
     rsrc_t ra[T::A_COPIES], rb[T::B_COPIES];
-    uint32_t aoff[T::A_COPIES], boff[T::B_COPIES];
-    int akg[T::A_COPIES], bkg[T::B_COPIES];
+    uint32_t aoff[T::A_COPIES], boff[T::B_COPIES], aend[T::A_COPIES], bend[T::B_COPIES];
+    const int64_t klast = (ke - kb) - (int64_t)(nk - 1) * KS;        // k of the last step
 #pragma unroll
     for (int d = 0; d < T::A_COPIES; ++d) {
-        const int r = (wave * T::A_COPIES + d) * 16;
+        const int r = (wave * T::A_COPIES + d) * 8, kg = kslot(r + srow, lane & 7) * 8;
         const int64_t first = lmin(m0 + r, g.M - 1), mine = lmin(m0 + r + srow, g.M - 1);
-        ra[d] = make_rsrc(g.A + first * g.lda, 0xFFFFFFF0ll);
-        akg[d] = bslot(r + srow, lane & 3) * 8;
-        aoff[d] = (uint32_t)((mine - first) * g.lda * 2);
+        ra[d] = make_rsrc(g.A + first * g.lda + kb, 0xFFFFFFF0ll);
+        aoff[d] = (uint32_t)(((mine - first) * g.lda + kg) * 2);
+        aend[d] = kg < klast ? aoff[d] : OUT_OF_RANGE;
     }
 #pragma unroll
     for (int d = 0; d < T::B_COPIES; ++d) {
-        const int r = (wave * T::B_COPIES + d) * 16;
+        const int r = (wave * T::B_COPIES + d) * 8, kg = kslot(r + srow, lane & 7) * 8;
         const int64_t first = b_row<EPI>(g, n0, r), mine = b_row<EPI>(g, n0, r + srow);
-        rb[d] = make_rsrc(g.B + first * g.ldb, 0xFFFFFFF0ll);
-        bkg[d] = bslot(r + srow, lane & 3) * 8;
-        boff[d] = (uint32_t)((mine - first) * g.ldb * 2);
+        rb[d] = make_rsrc(g.B + first * g.ldb + kb, 0xFFFFFFF0ll);
+        boff[d] = (uint32_t)(((mine - first) * g.ldb + kg) * 2);
+        bend[d] = kg < klast ? boff[d] : OUT_OF_RANGE;
     }
     auto stage = [&](int kt) {
-        uint16_t *const buf = lds + (kt & (RING - 1)) * T::STAGE;
-        const int64_t k0 = kb + (int64_t)kt * KS;
+        uint16_t *const buf = lds + (kt % T::RING) * T::STAGE;
+        const bool end = KTAIL && kt >= nk - 1;
+        const int soff = (kt < nk ? kt : nk - 1) * (KS * 2);
 #pragma unroll
-        for (int d = 0; d < T::A_COPIES; ++d) {
-            const int64_t k = k0 + akg[d];
-            const uint32_t off = k < ke ? aoff[d] + (uint32_t)(k * 2) : OUT_OF_RANGE;
+        for (int d = 0; d < T::A_COPIES; ++d)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                ra[d], (lds_void_t *)(buf + (wave * T::A_COPIES + d) * 16 * KS), 16, (int)off, 0, 0, 0);
-        }
+                ra[d], (lds_void_t *)(buf + (wave * T::A_COPIES + d) * 8 * KS), 16, (int)(end ? aend[d] : aoff[d]),
+                soff, 0, 0);
 #pragma unroll
-        for (int d = 0; d < T::B_COPIES; ++d) {
-            const int64_t k = k0 + bkg[d];
-            const uint32_t off = k < ke ? boff[d] + (uint32_t)(k * 2) : OUT_OF_RANGE;
+        for (int d = 0; d < T::B_COPIES; ++d)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rb[d], (lds_void_t *)(buf + T::BM * KS + (wave * T::B_COPIES + d) * 16 * KS), 16, (int)off, 0, 0, 0);
-        }
+                rb[d], (lds_void_t *)(buf + T::BM * KS + (wave * T::B_COPIES + d) * 8 * KS), 16,
+                (int)(end ? bend[d] : boff[d]), soff, 0, 0);
     };
 
-    f32x16_t acc[T::NI][T::MI];
+    f32x4_t acc[T::NI][T::MI];
 #pragma unroll
     for (int j = 0; j < T::NI; ++j)
 #pragma unroll
-        for (int i = 0; i < T::MI; ++i) acc[j][i] = f32x16_t{};
+        for (int i = 0; i < T::MI; ++i) acc[j][i] = f32x4_t{};
 
-    constexpr int COPIES = T::A_COPIES + T::B_COPIES, NM = T::MI * T::NI, TAIL = NM / 2;
-    Frag<T> f0, f1;
-    stage(0);
-    stage(1);
-    stage(2);
-    wait_vmem_at_most<2 * COPIES>();
-    lds_barrier();
-    read_frag<T>(f0, lds, 0, wm, wn, lane);
-    for (int kt = 0; kt < nk; ++kt) {
-        const uint16_t *const buf = lds + (kt & (RING - 1)) * T::STAGE;
-        stage(kt + 3);
-        read_frag<T>(f1, buf, 1, wm, wn, lane);
-        mfma_part<T, 0, NM>(acc, f0);
-        mfma_part<T, 0, NM - TAIL>(acc, f1);
-        wait_vmem_at_most<2 * COPIES>();     // step kt + 1 has landed; kt + 2 and kt + 3 may be in flight
+    // acc[j][i][q]: row m0w + 16 i + (lane & 15), column n0w + 16 j + 4 (lane >> 4) + q
+    const int64_t m0w = m0 + wm * T::TM, n0w = n0 + wn * T::TN;
+    constexpr int COPIES = T::A_COPIES + T::B_COPIES;
+    if (nk > 0) {
+#pragma unroll
+        for (int q = 0; q < T::RING; ++q) stage(q);
+    }
+    // The adapters' part first, while the copies are under way: behind the loop it
+    // would take the registers that the loop needs.
+    if constexpr (EPI == EPI_ADAPTER) start_adapters<T>(acc, g, m0w, n0w, lane);
+    if (nk > 0) {
+        Frag<T> f0, f1;
+        wait_vmem_at_most<(T::RING - 1) * COPIES>();
         lds_barrier();
-        read_frag<T>(f0, lds + ((kt + 1) & (RING - 1)) * T::STAGE, 0, wm, wn, lane);
-        mfma_part<T, NM - TAIL, NM>(acc, f1);
+        read_frag<T>(f0, lds, 0, wm, wn, lane);
+        for (int kt = 0; kt < nk; ++kt) {
+            const uint16_t *const buf = lds + (kt % T::RING) * T::STAGE, *const next = lds + ((kt + 1) % T::RING) * T::STAGE;
+            constexpr int NM = T::MI * T::NI, NR = T::MI + T::NI;
+            read_frag<T>(f1, buf, 1, wm, wn, lane);
+            mfma_slice<T>(acc, f0);
+            spread<NM, NR, 0x100>();
+            step_barrier<(T::RING - 2) * COPIES>();   // step kt + 1 has landed, buf's readers are done
+            read_frag<T>(f0, next, 0, wm, wn, lane);
+            stage(kt + T::RING);
+            mfma_slice<T>(acc, f1);
+            spread<NM, NR, 0x100, COPIES, 0x020>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
     wait_vmem_at_most<0>();                  // no copy may land in the epilogue's space
     lds_barrier();
 
-    const int64_t m0w = m0 + wm * T::TM, n0w = n0 + wn * T::TN;
-    const int mlane = lane & 31, half = lane >> 5;
+    const int mlane = lane & 15, quad = 4 * (lane >> 4);
     if constexpr (EPI == EPI_PARTIAL) {
         float *const part = g.partials + (int64_t)blockIdx.y * g.M * g.N;
         const bool vec = g.N % 4 == 0;
 #pragma unroll
         for (int i = 0; i < T::MI; ++i) {
-            const int64_t m = m0w + i * 32 + mlane;
+            const int64_t m = m0w + i * 16 + mlane;
             if (m >= g.M) continue;
 #pragma unroll
-            for (int j = 0; j < T::NI; ++j)
+            for (int j = 0; j < T::NI; ++j) {
+                const int64_t n = n0w + j * 16 + quad;
+                float *const p = part + m * g.N + n;
+                if (vec && n + 4 <= g.N) {
+                    *reinterpret_cast<f32x4_t *>(p) = acc[j][i];
+                } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t n = n0w + j * 32 + 8 * q + 4 * half;
-                    float *const p = part + m * g.N + n;
-                    const f32x4_t v = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2],
-                                       acc[j][i][4 * q + 3]};
-                    if (vec && n + 4 <= g.N) {
-                        *reinterpret_cast<f32x4_t *>(p) = v;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (n + e < g.N) p[e] = v[e];
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < g.N) p[e] = acc[j][i][e];
                 }
+            }
         }
         return;
     }
-    if constexpr (EPI == EPI_ADAPTER) add_adapters<T>(acc, g, m0w, n0w, lane);
-
     uint16_t *const out = lds + wave * T::EPI_WAVE;
     if constexpr (EPI == EPI_GATED) {
+        // blocks 2 p are gate rows, 2 p + 1 the up rows of the same 16 outputs
         const int64_t F = g.N >> 1, f0w = n0w >> 1;
-        if (g.bias != nullptr) {
 #pragma unroll
-            for (int j = 0; j < T::NI; ++j)
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int n = 8 * (q >> 2) + 4 * half + (q & 3);             // row of the 32-row block
-                    const int64_t f = lmin(f0w + j * 16 + (n & 15), F - 1);
-                    const float b = bf2f(g.bias[n < 16 ? f : F + f]);
-#pragma unroll
-                    for (int i = 0; i < T::MI; ++i) acc[j][i][q] += b;
-                }
-        }
-        constexpr int W = T::TN / 2;
-        if (g.Z != nullptr) {
-            // pre-activations stay in 32 bits: a lane's four are 16 bytes of a row
-#pragma unroll
-            for (int i = 0; i < T::MI; ++i) {
-                const int64_t m = m0w + i * 32 + mlane;
-                if (m >= g.M) continue;
-#pragma unroll
-                for (int j = 0; j < T::NI; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int64_t f = f0w + j * 16 + 8 * (q & 1) + 4 * half;
-                        // rows are padded to a multiple of 8, so four always fit
-                        if (f < F)
-                            *reinterpret_cast<f32x4_t *>(g.Z + m * g.ldz + (q >> 1) * (g.ldz / 2) + f) =
-                                f32x4_t{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2],
-                                        acc[j][i][4 * q + 3]};
-                    }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-            for (int j = 0; j < T::NI; ++j)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float h[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = gate_act<GATE>(acc[j][i][4 * q + e]) * acc[j][i][8 + 4 * q + e];
-                    put4<T>(out, i * 32 + mlane, j * 16 + 8 * q + 4 * half, h[0], h[1], h[2], h[3]);
-                }
-        wave_fence();
-        flush_block<T, W>(out, g.C, g.ldc, g.M, F, m0w, f0w, lane);
-    } else {
-        if (g.bias != nullptr) {
-#pragma unroll
-            for (int j = 0; j < T::NI; ++j)
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const float b = bf2f(g.bias[lmin(n0w + j * 32 + 8 * (q >> 2) + 4 * half + (q & 3), g.N - 1)]);
-#pragma unroll
-                    for (int i = 0; i < T::MI; ++i) acc[j][i][q] += b;
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-            for (int j = 0; j < T::NI; ++j)
+        for (int p = 0; p < T::NI / 2; ++p) {
+            float bg[4] = {0, 0, 0, 0}, bu[4] = {0, 0, 0, 0};
+            if (g.bias != nullptr) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const f32x16_t &v = acc[j][i];
-                    put4<T>(out, i * 32 + mlane, j * 32 + 8 * q + 4 * half, v[4 * q], v[4 * q + 1], v[4 * q + 2],
-                            v[4 * q + 3]);
+                    const int64_t f = lmin(f0w + p * 16 + quad + q, F - 1);
+                    bg[q] = bf2f(g.bias[f]);
+                    bu[q] = bf2f(g.bias[F + f]);
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < T::MI; ++i) {
+                f32x4_t zg, zu;
+                float h[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    zg[q] = acc[2 * p][i][q] + bg[q];
+                    zu[q] = acc[2 * p + 1][i][q] + bu[q];
+                    h[q] = gate_act<GATE>(zg[q]) * zu[q];
+                }
+                put4<T>(out, i * 16 + mlane, p * 16 + quad, h[0], h[1], h[2], h[3]);
+                if (g.Z != nullptr) {
+                    // pre-activations stay in 32 bits: a lane's four are 16 bytes of a row,
+                    // whose padding to a multiple of 8 always takes them
+                    const int64_t m = m0w + i * 16 + mlane, f = f0w + p * 16 + quad;
+                    if (m < g.M && f < F) {
+                        float *const z = g.Z + m * g.ldz + f;
+                        *reinterpret_cast<f32x4_t *>(z) = zg;
+                        *reinterpret_cast<f32x4_t *>(z + g.ldz / 2) = zu;
+                    }
+                }
+            }
+        }
+        wave_fence();
+        flush_block<T, T::TN / 2>(out, g.C, g.ldc, g.M, F, m0w, f0w, lane);
+    } else {
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) {
+            float b[4] = {0, 0, 0, 0};
+            if (g.bias != nullptr) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) b[q] = bf2f(g.bias[lmin(n0w + j * 16 + quad + q, g.N - 1)]);
+            }
+#pragma unroll
+            for (int i = 0; i < T::MI; ++i)
+                put4<T>(out, i * 16 + mlane, j * 16 + quad, acc[j][i][0] + b[0], acc[j][i][1] + b[1],
+                        acc[j][i][2] + b[2], acc[j][i][3] + b[3]);
+        }
         wave_fence();
         flush_block<T, T::TN>(out, g.C, g.ldc, g.M, g.N, m0w, n0w, lane);
     }
 }
 
-template <class T, int EPI, int GATE>
-__global__ __launch_bounds__(T::NT, T::BM == 256 ? 1 : 2) void bf16_gemm_kernel(Bf16Gemm g)
+template <class T, int EPI, int GATE, bool KTAIL>
+__global__ __launch_bounds__(T::NT, T::PER_CU) void bf16_gemm_kernel(Bf16Gemm g)
 {
     __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS];
-    gemm_tile<T, EPI, GATE>(g, lds);
+    gemm_tile<T, EPI, GATE, KTAIL>(g, lds);
 }
 
 // C = bf16(sum of the K slices' products, in slice order, + bias).
@@ -429,7 +467,9 @@ void launch_tile(Bf16Gemm g, hipStream_t stream)
     g.tiles_n = (int)((g.N + T::BN - 1) / T::BN);
     g.group_m = g.tiles_m < 8 ? g.tiles_m : 8;
     const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n), (unsigned)g.splits);
-    hipLaunchKernelGGL((bf16_gemm_kernel<T, EPI, GATE>), grid, dim3(T::NT), 0, stream, g);
+    // K slices begin at multiples of KS, so only the last can end inside a step
+    if (g.K % KS == 0) hipLaunchKernelGGL((bf16_gemm_kernel<T, EPI, GATE, false>), grid, dim3(T::NT), 0, stream, g);
+    else hipLaunchKernelGGL((bf16_gemm_kernel<T, EPI, GATE, true>), grid, dim3(T::NT), 0, stream, g);
 }
 
 template <class T>
@@ -489,6 +529,7 @@ hipError_t launch_bf16_gemm(const Bf16Gemm &args, int num_cus, hipStream_t strea
         g.A = g.B = nullptr;
         g.lda = g.ldb = 8;
     }
+    if (g.ids != nullptr && (g.r % 8 != 0 || !aligned(g.up, 16))) return hipErrorInvalidValue;
     if (g.K % 8 != 0 || g.lda % 8 != 0 || g.ldb % 8 != 0 || !aligned(g.A, 16) || !aligned(g.B, 16))
         return hipErrorInvalidValue;
     const bool plain = g.gate < 0 && g.ids == nullptr;

@@ -256,10 +256,9 @@ hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64
     return hipGetLastError();
 }
 
-hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,
+hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P, int64_t kp,
                               hipStream_t stream)
 {
-    const int64_t kp = pad_k(cols);
     hipLaunchKernelGGL(copy_padded_kernel, dim3(blocks_for(rows * (kp / 8), 256, 16384)), dim3(256), 0, stream, rows,
                        cols, kp, X, ldx, P);
     return hipGetLastError();

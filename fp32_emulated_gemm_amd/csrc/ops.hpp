@@ -92,7 +92,7 @@ struct Bf16Gemm {
     float *Z;                // with a gate: pre-activations (see z_pitch), or null
     int64_t ldz;
     const int32_t *ids;      // adapters (or null): rows' ids, up (n x N x r)
-    int64_t n, r, rp;
+    int64_t n, r, rp;        // r (up's row pitch) a multiple of 8, up 16-byte aligned, zeros past the rank
     const uint16_t *up;
     const uint16_t *S;       // M x 2 rp: high parts, low parts
     float *partials;         // K slices: splits x M x N floats
@@ -110,8 +110,8 @@ hipError_t launch_bf16_gemm(const Bf16Gemm &g, int num_cus, hipStream_t stream);
 // interleave: plane rows 2 f, 2 f + 1 are X's rows f, rows / 2 + f.
 hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64_t ldx, uint16_t *P, bool interleave,
                                hipStream_t stream);
-// bfloat16 rows x cols -> rows x pad_k(cols), zeros past cols.
-hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,
+// bfloat16 rows x cols -> rows of `pitch` (a multiple of 8), zeros past cols.
+hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P, int64_t pitch,
                               hipStream_t stream);
 // bfloat16 rows x cols -> cols x out_rows with pitch ldp, zeros past rows.
 hipError_t launch_transpose_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,

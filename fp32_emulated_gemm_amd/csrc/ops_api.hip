@@ -196,13 +196,17 @@ int check_adapters(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_
 // Few rows read W in one pass; low-rank activations to keep come from the tiles' path.
 bool adapter_few(int64_t M, const float *S) { return M <= kFewRows && S == nullptr; }
 
+// A bfloat16 bank of up factors whose rows the GEMM reads as they lie.
+bool bank_lies(int64_t r, const void *up) { return r % 8 == 0 && aligned(up, 16); }
+
 struct AdapterWs {
-    uint16_t *plan, *x;
+    uint16_t *plan, *x, *up;
     float *s, *partials;
     int64_t bytes;
 };
 AdapterWs adapter_ws(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, const void *W,
-                     int64_t ldw, const void *plan, int64_t n, int64_t r, const float *S, int num_cus, void *ws)
+                     int64_t ldw, const void *plan, int64_t n, int64_t r, const void *up, const float *S, int num_cus,
+                     void *ws)
 {
     Carve c(ws);
     AdapterWs w{};
@@ -215,6 +219,7 @@ AdapterWs adapter_ws(int dtype, int64_t M, int64_t N, int64_t K, const void *X, 
     } else {
         if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(N * pad_k(K));
         if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
+        if (n > 0 && r > 0 && !bank_lies(r, up)) w.up = c.take<uint16_t>(n * N * rank_pad(r));
     }
     w.bytes = c.bytes;
     return w;
@@ -223,7 +228,7 @@ AdapterWs adapter_ws(int dtype, int64_t M, int64_t N, int64_t K, const void *X, 
 struct AdapterBackWs {
     void *up_t, *down_t;       // n x r x N, n x K x r
     float *p;                  // M x pad16(r)
-    uint16_t *dy;              // dY laid out
+    uint16_t *dy, *down_p;     // dY laid out, down_t's rows padded
     int32_t *offs, *rows;
     float *partials;
     int64_t bytes;
@@ -237,6 +242,7 @@ AdapterBackWs adapter_back_ws(int dtype, int64_t M, int64_t N, int64_t K, int64_
     if (n > 0 && r > 0) {
         w.up_t = c.take<char>(n * r * N * size);
         w.down_t = c.take<char>(n * r * K * size);
+        if (dtype == SGEMM_EMU_BF16 && r % 8 != 0) w.down_p = c.take<uint16_t>(n * K * rank_pad(r));
         w.p = c.take<float>(M * rank_pad(r));
         w.offs = c.take<int32_t>(n + 1);
         w.rows = c.take<int32_t>(M);
@@ -287,7 +293,7 @@ int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, 
     } else if (transposed) {
         LAUNCH(launch_transpose_padded(rows, cols, (const uint16_t *)W, ldw, P, pad_k(rows), pad_k(rows), s));
     } else {
-        LAUNCH(launch_copy_padded(rows, cols, (const uint16_t *)W, ldw, P, s));
+        LAUNCH(launch_copy_padded(rows, cols, (const uint16_t *)W, ldw, P, pad_k(cols), s));
     }
     return SGEMM_EMU_OK;
 }
@@ -345,14 +351,14 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
     g.M = M; g.N = 2 * F; g.K = bf16_k(K);
     g.A = (const uint16_t *)X; g.lda = ldx;
     if (w.x != nullptr) {
-        LAUNCH(launch_copy_padded(M, K, (const uint16_t *)X, ldx, w.x, s));
+        LAUNCH(launch_copy_padded(M, K, (const uint16_t *)X, ldx, w.x, pad_k(K), s));
         g.A = w.x; g.lda = pad_k(K);
     }
     g.B = (const uint16_t *)W; g.ldb = ldw;
     if (plan != nullptr) {
         g.B = (const uint16_t *)plan; g.ldb = pad_k(K);
     } else if (w.plan != nullptr) {
-        LAUNCH(launch_copy_padded(2 * F, K, (const uint16_t *)W, ldw, w.plan, s));
+        LAUNCH(launch_copy_padded(2 * F, K, (const uint16_t *)W, ldw, w.plan, pad_k(K), s));
         g.B = w.plan; g.ldb = pad_k(K);
     }
     g.bias = (const uint16_t *)bias;
@@ -429,12 +435,12 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
 
 int64_t sgemm_emu_adapter_linear_workspace(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
                                            const void *W, int64_t ldw, const void *plan, int64_t n, int64_t r,
-                                           const float *S)
+                                           const void *up, const float *S)
 {
     CHECK(check_adapters(dtype, M, N, K, n, r));
     int num_cus = 0;
     CHECK(current_cus(&num_cus));
-    return adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, S, num_cus, nullptr).bytes;
+    return adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, up, S, num_cus, nullptr).bytes;
 }
 
 int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, const void *W,
@@ -459,7 +465,7 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
     if (M == 0 || (N == 0 && (!low || S == nullptr))) return SGEMM_EMU_OK;
     int num_cus = 0;
     CHECK(current_cus(&num_cus));
-    const AdapterWs w = adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, S, num_cus, ws);
+    const AdapterWs w = adapter_ws(dtype, M, N, K, X, ldx, W, ldw, plan, n, r, up, S, num_cus, ws);
     CHECK(check_ws(ws, ws_bytes, w.bytes));
     hipStream_t s = (hipStream_t)stream;
     const Adapters ad{ids, n, r, down, up, scale};
@@ -498,14 +504,14 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
     g.M = M; g.N = N; g.K = bf16_k(K);
     g.A = (const uint16_t *)X; g.lda = ldx;
     if (w.x != nullptr) {
-        LAUNCH(launch_copy_padded(M, K, (const uint16_t *)X, ldx, w.x, s));
+        LAUNCH(launch_copy_padded(M, K, (const uint16_t *)X, ldx, w.x, pad_k(K), s));
         g.A = w.x; g.lda = pad_k(K);
     }
     g.B = (const uint16_t *)W; g.ldb = ldw;
     if (plan != nullptr) {
         g.B = (const uint16_t *)plan; g.ldb = pad_k(K);
     } else if (w.plan != nullptr) {
-        LAUNCH(launch_copy_padded(N, K, (const uint16_t *)W, ldw, w.plan, s));
+        LAUNCH(launch_copy_padded(N, K, (const uint16_t *)W, ldw, w.plan, pad_k(K), s));
         g.B = w.plan; g.ldb = pad_k(K);
     }
     g.bias = (const uint16_t *)bias;
@@ -514,6 +520,11 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
     if (low) {
         g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
         g.up = (const uint16_t *)up;
+        if (!bank_lies(r, up)) {
+            LAUNCH(launch_copy_padded(n * N, r, (const uint16_t *)up, r, w.up, rank_pad(r), s));
+            g.r = rank_pad(r);
+            g.up = w.up;
+        }
         g.S = (const uint16_t *)S;
     }
     LAUNCH(launch_bf16_gemm(g, num_cus, s));
@@ -574,7 +585,7 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
             g.M = M; g.N = K; g.K = bf16_k(N);
             g.A = (const uint16_t *)dY; g.lda = lddy;
             if (!direct(dY, lddy, N)) {
-                if (N > 0) LAUNCH(launch_copy_padded(M, N, (const uint16_t *)dY, lddy, w.dy, s));
+                if (N > 0) LAUNCH(launch_copy_padded(M, N, (const uint16_t *)dY, lddy, w.dy, pad_k(N), s));
                 g.A = w.dy; g.lda = pad_k(N);
             }
             g.B = (const uint16_t *)plan_t; g.ldb = pad_k(N);
@@ -583,6 +594,11 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
             if (low) {
                 g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
                 g.up = (const uint16_t *)w.down_t;
+                if (r % 8 != 0) {
+                    LAUNCH(launch_copy_padded(n * K, r, (const uint16_t *)w.down_t, r, w.down_p, rank_pad(r), s));
+                    g.r = rank_pad(r);
+                    g.up = w.down_p;
+                }
                 g.S = (const uint16_t *)w.p;
             }
             LAUNCH(launch_bf16_gemm(g, num_cus, s));

@@ -50,7 +50,7 @@ def ops_lib():
         L.sgemm_emu_gated_linear_backward_workspace.argtypes = dims3
         L.sgemm_emu_gated_linear_backward.argtypes = dims3 + [vp, i64, vp, i64, vp, ci, vp, i64, vp, i64, vp, i64,
                                                               vp, vp, i64, vp]
-        L.sgemm_emu_adapter_linear_workspace.argtypes = dims3 + [vp, i64, vp, i64, vp, i64, i64, vp]
+        L.sgemm_emu_adapter_linear_workspace.argtypes = dims3 + [vp, i64, vp, i64, vp, i64, i64, vp, vp]
         L.sgemm_emu_adapter_linear.argtypes = dims3 + [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, i64,
                                                        vp, vp, i64, vp]
         L.sgemm_emu_adapter_linear_backward_workspace.argtypes = dims3 + [i64, i64]

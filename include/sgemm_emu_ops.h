@@ -117,7 +117,7 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
  */
 int64_t sgemm_emu_adapter_linear_workspace(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
                                            const void *W, int64_t ldw, const void *plan, int64_t n, int64_t r,
-                                           const float *S);
+                                           const void *up, const float *S);
 int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, const void *W,
                              int64_t ldw, const void *plan, const void *bias, int64_t n, int64_t r, const void *down,
                              const void *up, const float *scale, const int32_t *ids, void *Y, int64_t ldy, float *S,
