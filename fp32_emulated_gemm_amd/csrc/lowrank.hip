@@ -1,11 +1,16 @@
 // lowrank.hip -- few-row products and the low-rank parts of the adapters.
 //
 // dot_tile, shared by the few-row products and the shrink: a workgroup's eight
-// waves split K; each reads rows of both operands straight into the fragments
-// of a 16 x 16 MFMA (128 bits of consecutive k per lane, four lanes of a row in
-// one 64-byte segment), and the waves' sums are added through LDS in wave
-// order.  There is no reuse to stage: with few rows of X the weight passes
-// once, and the time is its bytes' and the latency of the loads.
+// waves split K, and their sums are added through LDS in wave order.  With few
+// rows of X the weight passes once, and the time is its bytes' and the latency
+// of the loads.
+//   * Aligned operands go through LDS: steps of 512 bytes of every row are copied
+//     by buffer loads with LDS destination (two whole row pieces per
+//     instruction) into a ring, and each wave multiplies its 64-byte slice of the
+//     rows.  Loaded straight into the MFMA's fragments (16 rows x 64 bytes per
+//     instruction), a CU takes in about 20 bytes per ns whatever the loads in
+//     flight: 81 us for the shrink of 8192 x 4096 bfloat16 to rank 64.
+//   * Other operands are loaded element by element into the fragments.
 // FP32 operands take the FP32 matrix instruction (FP32 products, FP32 sums): a
 // lane's four consecutive k are the k of four instructions, the same for both
 // operands, so their order inside a step does not matter.
@@ -34,64 +39,110 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c)
     }
 }
 
-// B blocks of 16 rows of an operand: each block's descriptor and this lane's row
-// offset in it (row l & 15), or OUT_OF_RANGE for a row that reads zeros.
+// B blocks of 16 rows of an operand: each block's descriptor and the offset of
+// this lane's row in it, or OUT_OF_RANGE for a row that reads zeros.
 template <int B>
 struct Rows {
     rsrc_t r[B];
     uint32_t off[B];
 };
 
-// VEC elements of a row from k on, zeros from ke on.  ALIGNED: rows are 16-byte
-// aligned and every K bound is a multiple of VEC, so a load is whole or empty.
-template <class T, bool ALIGNED>
+// The row of a block that a lane loads.
+template <bool ALIGNED>
+__device__ __forceinline__ int lane_row(int wave, int lane)
+{
+    return ALIGNED ? 2 * wave + (lane >> 5) : lane & 15;
+}
+
+// VEC elements of a row from k on, zeros from ke on, element by element.
+template <class T>
 __device__ __forceinline__ u32x4_t load_k(rsrc_t r, uint32_t row, int64_t k, int64_t ke)
 {
     constexpr int V = Elem<T>::VEC;
     const uint32_t off = row + (uint32_t)(k * (int64_t)sizeof(T));
     const bool none = row == OUT_OF_RANGE;
-    if constexpr (ALIGNED) {
-        return bload_u32x4(r, none || k >= ke ? OUT_OF_RANGE : off, 0);
-    } else {
-        u32x4_t v = {0, 0, 0, 0};
+    u32x4_t v = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const uint32_t o = none || k + e >= ke ? OUT_OF_RANGE : off + e * (uint32_t)sizeof(T);
-            if constexpr (sizeof(T) == 4) v[e] = bload_u32(r, o, 0);
-            else v[e >> 1] |= bload_u16(r, o, 0) << (16 * (e & 1));
-        }
-        return v;
+    for (int e = 0; e < V; ++e) {
+        const uint32_t o = none || k + e >= ke ? OUT_OF_RANGE : off + e * (uint32_t)sizeof(T);
+        if constexpr (sizeof(T) == 4) v[e] = bload_u32(r, o, 0);
+        else v[e >> 1] |= bload_u16(r, o, 0) << (16 * (e & 1));
     }
+    return v;
 }
 
+constexpr int STEP_BYTES = 512;                  // of a row, per step
+template <int NB, int MB>
+struct Ring {
+    static constexpr int BLOCKS = NB + MB, STAGE = BLOCKS * 16 * STEP_BYTES;   // bytes
+    static constexpr int STAGES = BLOCKS <= 3 ? 4 : BLOCKS <= 6 ? 3 : 2;
+    static constexpr int SUMS = WAVES * NB * MB * 1024;
+    static constexpr int BYTES = STAGES * STAGE > SUMS ? STAGES * STAGE : SUMS;
+};
+
 // acc[nb][mb] += rows of W times rows of X over this wave's share of [kb, ke).
-// Two neighbouring steps of a row are one wave's, so it reads 128 bytes of
-// each.  DEPTH steps' loads are in flight while a step multiplies.
-template <class T, int NB, int MB, bool AW, bool AX>
+template <class T, int NB, int MB, bool ALIGNED>
 __device__ __forceinline__ void dot_tile(f32x4_t (&acc)[NB][MB], const Rows<NB> &w, const Rows<MB> &x, int64_t kb,
-                                         int64_t ke, int wave, int lane)
+                                         int64_t ke, float *lds, int wave, int lane)
 {
-    constexpr int V = Elem<T>::VEC, STEP = 4 * V, DEPTH = !AW || !AX ? 2 : NB + MB <= 3 ? 8 : 4;
-    u32x4_t fw[DEPTH][NB], fx[DEPTH][MB];
-    // step i of this wave starts at k = kb + first(i)
-    auto first = [&](int64_t i) { return ((i >> 1) * (2 * WAVES) + wave * 2 + (i & 1)) * STEP; };
-    auto load = [&](int d, int64_t i) {
-        const int64_t k = kb + first(i) + (lane >> 4) * V;
+    typedef __attribute__((address_space(3))) void lds_void_t;
+    constexpr int V = Elem<T>::VEC;
+    if constexpr (ALIGNED) {
+        // 16-byte slot s of row r of a block lies at slot s ^ r, so the fragment
+        // reads of 16 rows are on distinct banks
+        typedef Ring<NB, MB> R;
+        constexpr int KC = STEP_BYTES / (int)sizeof(T);
+        const int row = lane_row<true>(wave, lane), k_lane = ((lane & 31) ^ row) * V;
+        const int n = (int)((ke - kb + KC - 1) / KC);
+        auto stage = [&](int t) {
+            char *const buf = (char *)lds + (t % R::STAGES) * R::STAGE;
+            const int64_t k = kb + (int64_t)t * KC + k_lane;
+            const bool in = k < ke;              // rows end at multiples of 16 bytes
+            const uint32_t koff = (uint32_t)(k * (int64_t)sizeof(T));
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) fw[d][nb] = load_k<T, AW>(w.r[nb], w.off[nb], k, ke);
+            for (int b = 0; b < R::BLOCKS; ++b) {
+                const uint32_t off = b < NB ? w.off[b < NB ? b : 0] : x.off[b < NB ? 0 : b - NB];
+                const rsrc_t r = b < NB ? w.r[b < NB ? b : 0] : x.r[b < NB ? 0 : b - NB];
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t *)(buf + b * 16 * STEP_BYTES + wave * 1024), 16,
+                                                         (int)(in && off != OUT_OF_RANGE ? off + koff : OUT_OF_RANGE),
+                                                         0, 0, 0);
+            }
+        };
+        __syncthreads();                         // the ring's space may still be read by its last user
+        const int slot = ((wave * 4 + (lane >> 4)) ^ (lane & 15)) * 16 + (lane & 15) * STEP_BYTES;
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) fx[d][mb] = load_k<T, AX>(x.r[mb], x.off[mb], k, ke);
-    };
+        for (int t = 0; t < R::STAGES - 1; ++t) stage(t);
+        for (int t = 0; t < n; ++t) {
+            wait_vmem_at_most<(R::STAGES - 2) * R::BLOCKS>();   // step t has landed
+            lds_barrier();                                      // everybody's, and step t - 1 is read
+            stage(t + R::STAGES - 1);
+            const char *const buf = (const char *)lds + (t % R::STAGES) * R::STAGE + slot;
+            u32x4_t fw[NB], fx[MB];
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(d, d);
-    for (int64_t i = 0; kb + first(i) < ke; i += DEPTH) {
+            for (int nb = 0; nb < NB; ++nb) fw[nb] = *reinterpret_cast<const u32x4_t *>(buf + nb * 16 * STEP_BYTES);
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
+            for (int mb = 0; mb < MB; ++mb)
+                fx[mb] = *reinterpret_cast<const u32x4_t *>(buf + (NB + mb) * 16 * STEP_BYTES);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = mfma16<T>(fw[d][nb], fx[d][mb], acc[nb][mb]);
-            load(d, i + DEPTH + d);
+                for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = mfma16<T>(fw[nb], fx[mb], acc[nb][mb]);
+        }
+        wait_vmem_at_most<0>();                  // no copy may land in what comes next
+        lds_barrier();
+    } else {
+        constexpr int STEP = 4 * V;
+        for (int64_t k0 = kb + wave * STEP; k0 < ke; k0 += WAVES * STEP) {
+            const int64_t k = k0 + (lane >> 4) * V;
+            u32x4_t fw[NB], fx[MB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) fw[nb] = load_k<T>(w.r[nb], w.off[nb], k, ke);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) fx[mb] = load_k<T>(x.r[mb], x.off[mb], k, ke);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = mfma16<T>(fw[nb], fx[mb], acc[nb][mb]);
         }
     }
 }
@@ -126,17 +177,17 @@ __device__ __forceinline__ float get_sum(const float *lds, int n, int m)
     return v;
 }
 
-// Blocks b of rows r0 + 16 b + (l & 15) of an operand of `rows` rows; rows past
-// it re-read the last one (their results are dropped).
+// Blocks b of rows r0 + 16 b + `row` of an operand of `rows` rows; rows past it
+// re-read the last one (their results are dropped).
 template <class T, int B>
-__device__ __forceinline__ Rows<B> rows_at(const T *p, int64_t ld, int64_t r0, int64_t rows, int lane)
+__device__ __forceinline__ Rows<B> rows_at(const T *p, int64_t ld, int64_t r0, int64_t rows, int row)
 {
     Rows<B> q;
     const rsrc_t r = make_rsrc(p + r0 * ld, 0xFFFFFFF0ll);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
         q.r[b] = r;
-        q.off[b] = (uint32_t)((lmin(r0 + b * 16 + (lane & 15), rows - 1) - r0) * ld * (int64_t)sizeof(T));
+        q.off[b] = (uint32_t)((lmin(r0 + b * 16 + row, rows - 1) - r0) * ld * (int64_t)sizeof(T));
     }
     return q;
 }
@@ -144,24 +195,25 @@ __device__ __forceinline__ Rows<B> rows_at(const T *p, int64_t ld, int64_t r0, i
 // ---------------------------------------------------------------- gated, one pass
 // NB / 2 blocks of 16 gate rows, then the NB / 2 blocks of up rows of the same
 // outputs; the whole K in one workgroup.
-template <class T, int NB, int MB, int GATE, bool AW, bool AX>
+template <class T, int NB, int MB, int GATE, bool ALIGNED>
 __global__ __launch_bounds__(NT) void few_gated_kernel(FewRows a)
 {
-    __shared__ __attribute__((aligned(16))) float lds[WAVES * NB * MB * 256];
+    __shared__ __attribute__((aligned(16))) float lds[Ring<NB, MB>::BYTES / 4];
     constexpr int OUT = NB / 2 * 16;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * OUT, F = a.N;
-    Rows<NB> w = rows_at<T, NB>((const T *)a.W, a.ldw, n0, F, lane);
+    const int row = lane_row<ALIGNED>(wave, lane);
+    Rows<NB> w = rows_at<T, NB>((const T *)a.W, a.ldw, n0, F, row);
     const rsrc_t up = make_rsrc((const T *)a.W + (F + n0) * a.ldw, 0xFFFFFFF0ll);
 #pragma unroll
     for (int b = 0; b < NB / 2; ++b) {
         w.r[NB / 2 + b] = up;
         w.off[NB / 2 + b] = w.off[b];
     }
-    const Rows<MB> x = rows_at<T, MB>((const T *)a.X, a.ldx, 0, a.M, lane);
+    const Rows<MB> x = rows_at<T, MB>((const T *)a.X, a.ldx, 0, a.M, row);
     f32x4_t acc[NB][MB];
     clear<NB, MB>(acc);
-    dot_tile<T, NB, MB, AW, AX>(acc, w, x, 0, a.K, wave, lane);
+    dot_tile<T, NB, MB, ALIGNED>(acc, w, x, 0, a.K, lds, wave, lane);
     put_sums<NB, MB>(lds, acc, wave, lane);
     __syncthreads();
     const T *bias = (const T *)a.bias;
@@ -199,7 +251,7 @@ struct Tokens {
 
 // One workgroup per row of a 16-row tile: the first row of an adapter multiplies
 // the tile's rows of that adapter, the others end.
-template <class T, bool AX, bool AD>
+template <class T, bool ALIGNED>
 __device__ __forceinline__ void shrink_row(const Tokens<T> &a, int block, float *lds, int wave, int lane)
 {
     const int64_t m0 = (int64_t)(block >> 4) * 16;
@@ -218,45 +270,47 @@ __device__ __forceinline__ void shrink_row(const Tokens<T> &a, int block, float 
     }
     const uint32_t own = (uint32_t)(__ballot(id == me) & 0xFFFFu);
     if ((own & ((1u << mine) - 1u)) != 0) return;                    // an earlier row computes it
-    Rows<1> x = rows_at<T, 1>(a.X, a.ldx, m0, a.M, lane);
-    if (!((own >> (lane & 15)) & 1u)) x.off[0] = OUT_OF_RANGE;
+    const int row = lane_row<ALIGNED>(wave, lane);
+    Rows<1> x = rows_at<T, 1>(a.X, a.ldx, m0, a.M, row);
+    if (!((own >> row) & 1u)) x.off[0] = OUT_OF_RANGE;
     const T *down = (const T *)a.ad.down + (int64_t)me * a.ad.r * a.K;
     const float scale = a.ad.scale != nullptr ? a.ad.scale[me] : 1.0f;
     for (int64_t r0 = 0; r0 < a.rp; r0 += 16) {
-        const Rows<1> w = rows_at<T, 1>(down, a.K, r0, a.ad.r, lane);
+        const Rows<1> w = rows_at<T, 1>(down, a.K, r0, a.ad.r, row);
         f32x4_t acc[1][1];
         clear<1, 1>(acc);
-        dot_tile<T, 1, 1, AD, AX>(acc, w, x, 0, a.K, wave, lane);
+        dot_tile<T, 1, 1, ALIGNED>(acc, w, x, 0, a.K, lds, wave, lane);
         put_sums<1, 1>(lds, acc, wave, lane);
         __syncthreads();
         if (threadIdx.x < 256) {
-            const int n = threadIdx.x & 15, row = threadIdx.x >> 4;
-            if ((own >> row) & 1u)
-                a.S[(m0 + row) * a.rp + r0 + n] = r0 + n < a.ad.r ? scale * get_sum<1, 1>(lds, n, row) : 0.0f;
+            const int n = threadIdx.x & 15, t = threadIdx.x >> 4;
+            if ((own >> t) & 1u)
+                a.S[(m0 + t) * a.rp + r0 + n] = r0 + n < a.ad.r ? scale * get_sum<1, 1>(lds, n, t) : 0.0f;
         }
         __syncthreads();
     }
 }
 
-template <class T, int MB, bool AW, bool AX, bool AD>
+template <class T, int MB, bool ALIGNED>
 __global__ __launch_bounds__(NT) void tokens_kernel(Tokens<T> a)
 {
     constexpr int NB = 2;
-    __shared__ __attribute__((aligned(16))) float lds[WAVES * NB * MB * 256];
+    __shared__ __attribute__((aligned(16))) float lds[Ring<NB, MB>::BYTES / 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int block = (int)blockIdx.x;
     if (block < a.shrink_blocks) {
-        shrink_row<T, AX, AD>(a, block, lds, wave, lane);
+        shrink_row<T, ALIGNED>(a, block, lds, wave, lane);
         return;
     }
     block -= a.shrink_blocks;
     const int64_t n0 = (int64_t)(block % a.n_blocks) * (16 * NB), slice = block / a.n_blocks;
     const int64_t kb = slice * a.k_per_slice, ke = lmin(kb + a.k_per_slice, a.K);
-    const Rows<NB> w = rows_at<T, NB>(a.W, a.ldw, n0, a.N, lane);
-    const Rows<MB> x = rows_at<T, MB>(a.X, a.ldx, 0, a.M, lane);
+    const int row = lane_row<ALIGNED>(wave, lane);
+    const Rows<NB> w = rows_at<T, NB>(a.W, a.ldw, n0, a.N, row);
+    const Rows<MB> x = rows_at<T, MB>(a.X, a.ldx, 0, a.M, row);
     f32x4_t acc[NB][MB];
     clear<NB, MB>(acc);
-    dot_tile<T, NB, MB, AW, AX>(acc, w, x, kb, ke, wave, lane);
+    dot_tile<T, NB, MB, ALIGNED>(acc, w, x, kb, ke, lds, wave, lane);
     put_sums<NB, MB>(lds, acc, wave, lane);
     __syncthreads();
     float *const part = a.partials + slice * a.M * a.N;
@@ -364,10 +418,10 @@ template <class T, int MB>
 void launch_tokens_mb(const Tokens<T> &t, int slices, hipStream_t stream)
 {
     const dim3 grid((unsigned)(t.shrink_blocks + t.n_blocks * slices)), block(NT);
-    const bool aw = rows_aligned<T>(t.W, t.ldw, t.K), ax = rows_aligned<T>(t.X, t.ldx, t.K);
-    const bool ad = rows_aligned<T>(t.ad.down, t.K, t.K);
-    if (aw && ax && ad) hipLaunchKernelGGL((tokens_kernel<T, MB, true, true, true>), grid, block, 0, stream, t);
-    else hipLaunchKernelGGL((tokens_kernel<T, MB, false, false, false>), grid, block, 0, stream, t);
+    if (rows_aligned<T>(t.W, t.ldw, t.K) && rows_aligned<T>(t.X, t.ldx, t.K) && rows_aligned<T>(t.ad.down, t.K, t.K))
+        hipLaunchKernelGGL((tokens_kernel<T, MB, true>), grid, block, 0, stream, t);
+    else
+        hipLaunchKernelGGL((tokens_kernel<T, MB, false>), grid, block, 0, stream, t);
 }
 
 template <class T>
@@ -383,9 +437,10 @@ void launch_few_gated_al(const FewRows &a, hipStream_t stream)
 {
     constexpr int OUT = NB / 2 * 16;
     const dim3 grid((unsigned)((a.N + OUT - 1) / OUT)), block(NT);
-    const bool aw = rows_aligned<T>(a.W, a.ldw, a.K), ax = rows_aligned<T>(a.X, a.ldx, a.K);
-    if (aw && ax) hipLaunchKernelGGL((few_gated_kernel<T, NB, MB, GATE, true, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((few_gated_kernel<T, NB, MB, GATE, false, false>), grid, block, 0, stream, a);
+    if (rows_aligned<T>(a.W, a.ldw, a.K) && rows_aligned<T>(a.X, a.ldx, a.K))
+        hipLaunchKernelGGL((few_gated_kernel<T, NB, MB, GATE, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((few_gated_kernel<T, NB, MB, GATE, false>), grid, block, 0, stream, a);
 }
 
 template <class T, int GATE>
@@ -469,7 +524,7 @@ template <class T, int NB, int MB, bool AL>
 __global__ __launch_bounds__(NT) void shrink_kernel(int64_t M, int64_t K, const T *X, int64_t ldx, Adapters ad,
                                                     float *S, int64_t rp)
 {
-    __shared__ __attribute__((aligned(16))) float lds[WAVES * NB * MB * 256];
+    __shared__ __attribute__((aligned(16))) float lds[Ring<NB, MB>::BYTES / 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr int ROWS = 16 * MB;
     const int64_t m0 = (int64_t)blockIdx.x * ROWS;
@@ -478,7 +533,8 @@ __global__ __launch_bounds__(NT) void shrink_kernel(int64_t M, int64_t K, const 
         id = ad.ids[m0 + lane];
         if (id >= ad.n) id = -1;
     }
-    const Rows<MB> x = rows_at<T, MB>(X, ldx, m0, M, lane);
+    const int row = lane_row<AL>(wave, lane);
+    const Rows<MB> x = rows_at<T, MB>(X, ldx, m0, M, row);
     uint64_t todo = __ballot(id >= 0);
     const uint64_t none = __ballot(id < 0 && lane < ROWS && m0 + lane < M);
     if (none != 0)
@@ -491,10 +547,10 @@ __global__ __launch_bounds__(NT) void shrink_kernel(int64_t M, int64_t K, const 
         const T *down = (const T *)ad.down + (int64_t)me * ad.r * K;
         const float scale = ad.scale != nullptr ? ad.scale[me] : 1.0f;
         for (int64_t r0 = 0; r0 < rp; r0 += 16 * NB) {
-            const Rows<NB> w = rows_at<T, NB>(down, K, r0, ad.r, lane);
+            const Rows<NB> w = rows_at<T, NB>(down, K, r0, ad.r, row);
             f32x4_t acc[NB][MB];
             clear<NB, MB>(acc);
-            dot_tile<T, NB, MB, AL, AL>(acc, w, x, 0, K, wave, lane);
+            dot_tile<T, NB, MB, AL>(acc, w, x, 0, K, lds, wave, lane);
             put_sums<NB, MB>(lds, acc, wave, lane);
             __syncthreads();
             for (int o = threadIdx.x; o < 16 * NB * ROWS; o += NT) {
