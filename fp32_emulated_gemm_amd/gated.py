@@ -12,7 +12,7 @@ import torch
 
 from . import ops
 from .linear import Linear
-from .ops import GATES, WeightPlan, addr, check_tensor, current_stream, ok, ops_lib, rows_of, scratch
+from .ops import DTYPES, GATES, WeightPlan, addr, check_tensor, few_bytes, ok, ops_lib, rows_of, scratch, stream_of
 
 
 def plan_weight(weight):
@@ -23,16 +23,23 @@ def plan_weight(weight):
 def _forward(x, xld, weight, wld, bias, gate, plan, keep):
     """H and, with `keep`, the pre-activations Z."""
     L = ops_lib()
-    dt = ops.DTYPES[x.dtype]
+    dt = DTYPES[x.dtype]
     (M, K), F = x.shape, weight.shape[0] // 2
-    h = torch.empty((M, F), dtype=x.dtype, device=x.device)
-    z = torch.empty((M, 2 * (-(-F // 8) * 8)), dtype=torch.float32, device=x.device) if keep else None
+    h = x.new_empty((M, F))
+    z = x.new_empty((M, 2 * (-(-F // 8) * 8)), dtype=torch.float32) if keep else None
     fwd = None if plan is None else addr(plan.forward)
     xp, wp, zp = addr(x), addr(weight), addr(z)
-    ws, nws = scratch(ok(L.sgemm_emu_gated_linear_workspace(dt, M, F, K, xp, xld, wp, wld, fwd, zp),
-                             "sgemm_emu_gated_linear_workspace"), x.device)
+
+    def query():
+        return L.sgemm_emu_gated_linear_workspace(dt, M, F, K, xp, xld, wp, wld, fwd, zp)
+
+    if M <= ops.FEW_ROWS and K and not keep:
+        nws = few_bytes((dt, M, F, K, x.device), query)
+    else:
+        nws = ok(query(), "sgemm_emu_gated_linear_workspace")
+    ws = scratch(nws, x)
     ok(L.sgemm_emu_gated_linear(dt, M, F, K, xp, xld, wp, wld, fwd, addr(bias), gate, addr(h), max(F, 1), zp,
-                                addr(ws), nws, current_stream()), "sgemm_emu_gated_linear")
+                                addr(ws), nws, stream_of(x.get_device())), "sgemm_emu_gated_linear")
     return h, z
 
 
@@ -53,19 +60,46 @@ class _GatedFn(torch.autograd.Function):
         x, weight, z = ctx.saved_tensors
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
         L = ops_lib()
-        dt = ops.DTYPES[x.dtype]
+        dt = DTYPES[x.dtype]
         (M, K), F = x.shape, weight.shape[0] // 2
         (x, xld), (weight, wld), (dh, dhld) = rows_of(x), rows_of(weight), rows_of(dh)
-        dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if need_x else None
-        dw = torch.empty((2 * F, K), dtype=x.dtype, device=x.device) if need_w else None
-        db = torch.empty((2 * F,), dtype=x.dtype, device=x.device) if need_b and ctx.has_bias else None
-        ws, nws = scratch(ok(L.sgemm_emu_gated_linear_backward_workspace(dt, M, F, K),
-                             "sgemm_emu_gated_linear_backward_workspace"), x.device)
+        dx = x.new_empty((M, K)) if need_x else None
+        dw = x.new_empty((2 * F, K)) if need_w else None
+        db = x.new_empty((2 * F,)) if need_b and ctx.has_bias else None
+        nws = ok(L.sgemm_emu_gated_linear_backward_workspace(dt, M, F, K), "sgemm_emu_gated_linear_backward_workspace")
+        ws = scratch(nws, x)
         ok(L.sgemm_emu_gated_linear_backward(dt, M, F, K, addr(x), xld, addr(weight), wld, addr(z),
                                              ctx.gate, addr(dh), dhld, addr(dx), max(K, 1), addr(dw), max(K, 1),
-                                             addr(db), addr(ws), nws, current_stream()),
+                                             addr(db), addr(ws), nws, stream_of(x.get_device())),
            "sgemm_emu_gated_linear_backward")
         return dx, dw, db, None, None
+
+
+def _check(x, weight, bias):
+    """Raises for the first argument that does not fit."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"x: expected a torch tensor, got {type(x).__name__}")
+    dt = x.dtype
+    if dt not in DTYPES:
+        raise TypeError(f"x: expected dtype float32 or bfloat16, got {dt}")
+    if x.dim() < 1:
+        raise ValueError("x: expected at least one dimension")
+    check_tensor(x, "x", dt, x.shape)
+    check_tensor(weight, "weight", dt, (None, x.shape[-1]))
+    if weight.shape[0] % 2 != 0:
+        raise ValueError(f"weight: expected an even number of rows (gate, then up), got {weight.shape[0]}")
+    if bias is not None:
+        check_tensor(bias, "bias", dt, (weight.shape[0],))
+
+
+def _fits(x, weight, bias):
+    """Whether every argument fits: _check's conditions in one expression, for the calls where the
+    host's time counts."""
+    dt, d = x.dtype, torch.cuda.current_device()
+    rows, K = weight.shape
+    return (dt in DTYPES and weight.dtype is dt and x.shape[-1] == K and rows % 2 == 0
+            and x.get_device() == d == weight.get_device()
+            and (bias is None or (bias.dtype is dt and bias.shape == (rows,) and bias.get_device() == d)))
 
 
 def gated_linear(x, weight, bias=None, gate="silu", plan=None):
@@ -73,31 +107,27 @@ def gated_linear(x, weight, bias=None, gate="silu", plan=None):
     all float32 or all bfloat16 on the current HIP device.  gate: "silu", "gelu" (exact), "gelu_tanh",
     "sigmoid" or "relu".  `plan` (plan_weight(weight)) spares laying out a weight that does not change.
     Differentiable in x, weight and bias."""
-    if gate not in GATES:
+    act = GATES.get(gate)
+    if act is None:
         raise ValueError(f"unknown gate {gate!r} (one of {', '.join(GATES)})")
-    if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
-        raise TypeError("gated_linear expects torch tensors")
-    if x.dtype not in ops.DTYPES:
-        raise TypeError(f"x: expected dtype float32 or bfloat16, got {x.dtype}")
-    if x.dim() < 1:
-        raise ValueError("x: expected at least one dimension")
-    check_tensor(weight, "weight", x.dtype, (None, x.shape[-1]))
-    if weight.shape[0] % 2 != 0:
-        raise ValueError(f"weight: expected an even number of rows (gate, then up), got {weight.shape[0]}")
-    x2d = x if x.dim() == 2 else x.reshape(-1, x.shape[-1]) if x.shape[-1] else x.new_empty(x.shape[:-1].numel(), 0)
-    check_tensor(x2d, "x", x.dtype, (None, None))
-    if bias is not None:
-        check_tensor(bias, "bias", x.dtype, (weight.shape[0],))
+    try:
+        fits = _fits(x, weight, bias)
+    except (AttributeError, IndexError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        _check(x, weight, bias)
+    dims, K, rows = x.dim(), x.shape[-1], weight.shape[0]
+    x2d = x if dims == 2 else x.reshape(-1, K) if K else x.new_empty(x.shape[:-1].numel(), 0)
     if plan is not None:
         plan.check(weight)
     ops_lib()
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad
                                     or (bias is not None and bias.requires_grad)):
-        h = _GatedFn.apply(x2d, weight, bias, GATES[gate], plan)
+        h = _GatedFn.apply(x2d, weight, bias, act, plan)
     else:
         (xr, xld), (wr, wld) = rows_of(x2d), rows_of(weight)
-        h, _ = _forward(xr, xld, wr, wld, None if bias is None else bias.contiguous(), GATES[gate], plan, False)
-    return h if x.dim() == 2 else h.reshape(*x.shape[:-1], weight.shape[0] // 2)
+        h, _ = _forward(xr, xld, wr, wld, None if bias is None else bias.contiguous(), act, plan, False)
+    return h if dims == 2 else h.reshape(*x.shape[:-1], rows // 2)
 
 
 class GatedLinear(torch.nn.Module):

@@ -77,12 +77,13 @@ def check_tensor(t, name, dtype, shape):
     """A tensor of `dtype` and `shape` (None: any extent) on the current HIP device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+    have = t.shape
+    if len(have) != len(shape) or any([w is not None and s != w for s, w in zip(have, shape)]):
         raise ValueError(f"{name}: expected shape {tuple('any' if w is None else w for w in shape)}, "
-                         f"got {tuple(t.shape)}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+                         f"got {tuple(have)}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name}: expected a tensor on the current HIP device, got {t.device}")
 
 
@@ -90,18 +91,28 @@ def rows_of(t):
     """A 2-D tensor whose rows lie one after another with unit stride along columns (itself, or a
     contiguous copy of a transposed, expanded or overlapping one), and its leading dimension."""
     rows, cols = t.shape
-    ld = t.stride(0)
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and ld < cols):
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
         t = t.contiguous()
         ld = cols
-    return t, max(ld, cols, 1)
+    return t, ld if ld >= cols and ld > 0 else max(cols, 1)
 
 
-def scratch(nbytes, device):
-    """Workspace of a call and its size: torch's allocator keeps it in the stream's order."""
-    if nbytes == 0:
-        return None, 0
-    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+def scratch(nbytes, like):
+    """Workspace of a call on `like`'s device: torch's allocator keeps it in the stream's order."""
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+
+
+# Workspace bytes of a call on few rows by its dimensions (which alone decide them there), so that
+# the calls where latency counts ask once.
+_FEW_BYTES = {}
+
+
+def few_bytes(key, query):
+    n = _FEW_BYTES.get(key)
+    if n is None:
+        n = _FEW_BYTES[key] = ok(query(), "workspace query")
+    return n
 
 
 def addr(t):
@@ -110,6 +121,15 @@ def addr(t):
 
 def current_stream():
     return torch.cuda.current_stream().cuda_stream
+
+
+# torch.cuda.current_stream() builds a Stream object (2 us); torch's own accessor gives the handle alone.
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def stream_of(device_index):
+    """The handle of torch's current stream on a device."""
+    return _RAW_STREAM(device_index) if _RAW_STREAM is not None else current_stream()
 
 
 class WeightPlan:
