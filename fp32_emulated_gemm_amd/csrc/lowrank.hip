@@ -111,11 +111,10 @@ __device__ __forceinline__ void dot_tile(f32x4_t (&acc)[NB][MB], const Rows<NB> 
         __syncthreads();                         // the ring's space may still be read by its last user
         const int slot = ((wave * 4 + (lane >> 4)) ^ (lane & 15)) * 16 + (lane & 15) * STEP_BYTES;
 #pragma unroll
-        for (int t = 0; t < R::STAGES - 1; ++t) stage(t);
+        for (int t = 0; t < R::STAGES; ++t) stage(t);
         for (int t = 0; t < n; ++t) {
-            wait_vmem_at_most<(R::STAGES - 2) * R::BLOCKS>();   // step t has landed
-            lds_barrier();                                      // everybody's, and step t - 1 is read
-            stage(t + R::STAGES - 1);
+            wait_vmem_at_most<(R::STAGES - 1) * R::BLOCKS>();   // step t has landed,
+            lds_barrier();                                      // everybody's
             const char *const buf = (const char *)lds + (t % R::STAGES) * R::STAGE + slot;
             u32x4_t fw[NB], fx[MB];
 #pragma unroll
@@ -123,6 +122,8 @@ __device__ __forceinline__ void dot_tile(f32x4_t (&acc)[NB][MB], const Rows<NB> 
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
                 fx[mb] = *reinterpret_cast<const u32x4_t *>(buf + (NB + mb) * 16 * STEP_BYTES);
+            lds_barrier();                                      // everybody has read it: all buffers in flight again
+            stage(t + R::STAGES);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -461,6 +462,9 @@ void launch_few_gated(const FewRows &a, int num_cus, hipStream_t stream)
     } else if (a.M <= 32) {
         if (wide) launch_few_gated_al<T, 4, 2, GATE>(a, stream);
         else launch_few_gated_al<T, 2, 2, GATE>(a, stream);
+    } else if (a.M <= 48) {
+        if (wide) launch_few_gated_al<T, 4, 3, GATE>(a, stream);
+        else launch_few_gated_al<T, 2, 3, GATE>(a, stream);
     } else {
         if (wide) launch_few_gated_al<T, 4, 4, GATE>(a, stream);
         else launch_few_gated_al<T, 2, 4, GATE>(a, stream);
