@@ -742,11 +742,15 @@ struct DmaLayout {
     static_assert(C::BN == 128 && B_ROWS_PER_WAVE % 16 == 0, "plane tile rows split into 16-row copies");
 };
 
-// Vector-memory operations one thread issues per K step of the DMA pipeline.
-template <class C, bool AVEC>
+// The least number of vector-memory operations one thread issues per K step of
+// the DMA pipeline: the waits for the step before count on no more.  The eight
+// element loads of an unaligned A chunk count as two, because the compiler may
+// merge neighbouring ones into 128-bit loads (a bound of eight let the next
+// step's B copies still be in flight behind the barrier).
+template <class C>
 constexpr int dma_vmem_per_step()
 {
-    return 3 * DmaLayout<C>::B_COPIES + C::A_CHUNKS * (AVEC ? 2 : 8);
+    return 3 * DmaLayout<C>::B_COPIES + C::A_CHUNKS * 2;
 }
 
 // Copy one K step (BK columns) of a 128-row tile of three BF16 planes with k
@@ -971,7 +975,7 @@ __device__ __forceinline__ void dma_step(Acc<C, NB> &acc, Frags<C> &f0, Frags<C>
     // The next step's B tile must have landed before the barrier; only the
     // copies and A loads issued at the top of this step may still be in
     // flight (vector-memory operations complete in order).
-    wait_vmem_at_most<dma_vmem_per_step<C, AVEC>()>();
+    wait_vmem_at_most<dma_vmem_per_step<C>()>();
     lds_barrier();
     read_frags_dma<C>(f0, abuf_next, bbuf_next, 0, wm, wn, lane);
     mfma_slice_part<C, NB, NM - TAIL, NM>(acc, f1);
@@ -1051,7 +1055,7 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_dma_kernel(GemmArgs g)
     load_a_stage<C, AVEC>(a_next, cur.a_off, g, cur.m0, cur.kb + BK);
     if (store_a_stage<C, RNE, KTAIL>(a_cur, a_lds, a_base, g.ka - cur.kb))
         restage_a_special<C, AVEC, RNE, KTAIL>(cur.a_off, a_lds, g, cur.m0, cur.kb, a_base);
-    wait_vmem_at_most<dma_vmem_per_step<C, AVEC>()>();
+    wait_vmem_at_most<dma_vmem_per_step<C>()>();
     lds_barrier();
     read_frags_dma<C>(f0, a_base, b_base, 0, wm, wn, lane);
 
@@ -1450,7 +1454,7 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_streamk_kernel(GemmArgs 
     load_a_stage<C, AVEC>(a_next, cur.s.a_off, g, cur.s.m0, cur.s.kb + BK);
     if (store_a_stage<C, RNE, KTAIL>(a_cur, a_lds, a_base, g.ka - cur.s.kb))
         restage_a_special<C, AVEC, RNE, KTAIL>(cur.s.a_off, a_lds, g, cur.s.m0, cur.s.kb, a_base);
-    wait_vmem_at_most<dma_vmem_per_step<C, AVEC>()>();
+    wait_vmem_at_most<dma_vmem_per_step<C>()>();
     lds_barrier();
     read_frags_dma<C>(f0, a_base, b_base, 0, wm, wn, lane);
 
