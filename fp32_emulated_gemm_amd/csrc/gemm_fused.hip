@@ -30,63 +30,43 @@ dim3 persistent_grid(const GemmArgs &g)
     return dim3((unsigned)(units < slots ? units : slots));
 }
 
-template <class C, int EPI, bool AVEC>
-void tile64_vec(const GemmArgs &g, hipStream_t stream)
-{
-    const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n)), block(C::NT);
-    // planes with padded rows: 128-bit loads wherever every 8 elements lie below or above K
-    if (g.K % 8 == 0)
-        hipLaunchKernelGGL((gemm_bf16x9_kernel<C, 5, AVEC, B_PLANES_NK, 1, false, EPI>), grid, block, 0, stream, g);
-    else
-        hipLaunchKernelGGL((gemm_bf16x9_kernel<C, 5, AVEC, B_PLANES_NK, 0, false, EPI>), grid, block, 0, stream, g);
-}
-
-template <int EPI>
-hipError_t tile64(const GemmArgs &args, hipStream_t stream)
+// A's rows lie in 16-byte pieces and K is a multiple of 64 (callers copy others
+// to padded rows), so only the kernels without element loads or masks are built.
+hipError_t gated_tile64(const GemmArgs &args, hipStream_t stream)
 {
     const GemmArgs g = tiled<Cfg64S>(args);
-    if (aligned(g.A, 16) && g.lda % 4 == 0 && g.K % 4 == 0) tile64_vec<Cfg64S, EPI, true>(g, stream);
-    else tile64_vec<Cfg64S, EPI, false>(g, stream);
+    hipLaunchKernelGGL((gemm_bf16x9_kernel<Cfg64S, 5, true, B_PLANES_NK, 1, false, EPI_GATED>),
+                       dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), dim3(Cfg64S::NT), 0, stream, g);
     return hipGetLastError();
 }
 
-template <int EPI>
-hipError_t planes(const GemmArgs &args, hipStream_t stream)
+hipError_t gated_planes(const GemmArgs &args, hipStream_t stream)
 {
     const GemmArgs g = tiled<C128>(args);
-    launch_last(gemm_bf16x9_planes_kernel<C128, 5, EPI>, persistent_grid(g), dim3(C128::NT), stream, g);
+    launch_last(gemm_bf16x9_planes_kernel<C128, 5, EPI_GATED>, persistent_grid(g), dim3(C128::NT), stream, g);
     return hipGetLastError();
 }
 
-template <int EPI, bool AVEC, bool KTAIL>
-void dma_vec(const GemmArgs &g, hipStream_t stream)
+hipError_t gated_dma(const GemmArgs &args, hipStream_t stream)
 {
+    const GemmArgs g = tiled<C128>(args);
     const dim3 block(C128::NT);
+    if (!aligned(g.A, 16) || g.lda % 4 != 0 || g.ka != g.K) return hipErrorInvalidValue;
 #ifdef SGEMM_EMU_SERIAL_LDS
-    launch_last(gemm_bf16x9_serial_kernel<C128, 5, AVEC, false, KTAIL, EPI>,
+    launch_last(gemm_bf16x9_serial_kernel<C128, 5, true, false, false, EPI_GATED>,
                 dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), block, stream, g);
 #else
     if (g.sk_grid > 0) {
         GemmArgs s = g;
         s.sk_domains = (int)streamk_domains((int64_t)g.tiles_m * g.tiles_n, g.K / (2 * BK), g.sk_grid);
         s.group_m = kStreamkGroupRows;
-        launch_last(gemm_bf16x9_streamk_kernel<C128, 5, AVEC, false, KTAIL, EPI>, dim3((unsigned)g.sk_grid), block,
-                    stream, s);
-        return;
+        launch_last(gemm_bf16x9_streamk_kernel<C128, 5, true, false, false, EPI_GATED>, dim3((unsigned)g.sk_grid),
+                    block, stream, s);
+    } else {
+        launch_last(gemm_bf16x9_dma_kernel<C128, 5, true, false, false, EPI_GATED>, persistent_grid(g), block, stream,
+                    g);
     }
-    launch_last(gemm_bf16x9_dma_kernel<C128, 5, AVEC, false, KTAIL, EPI>, persistent_grid(g), block, stream, g);
 #endif
-}
-
-template <int EPI>
-hipError_t dma(const GemmArgs &args, hipStream_t stream)
-{
-    const GemmArgs g = tiled<C128>(args);
-    const bool avec = aligned(g.A, 16) && g.lda % 4 == 0 && g.ka % 4 == 0, tail = g.ka != g.K;
-    if (avec && tail) dma_vec<EPI, true, true>(g, stream);
-    else if (avec) dma_vec<EPI, true, false>(g, stream);
-    else if (tail) dma_vec<EPI, false, true>(g, stream);
-    else dma_vec<EPI, false, false>(g, stream);
     return hipGetLastError();
 }
 
@@ -107,7 +87,7 @@ const PlaneLaunchers &plain_launchers()
 
 const PlaneLaunchers &gated_launchers()
 {
-    static const PlaneLaunchers l = {tile64<EPI_GATED>, planes<EPI_GATED>, dma<EPI_GATED>};
+    static const PlaneLaunchers l = {gated_tile64, gated_planes, gated_dma};
     return l;
 }
 

@@ -43,20 +43,26 @@ __global__ __launch_bounds__(256) void split_padded_kernel(int64_t rows, int64_t
     }
 }
 
-__global__ __launch_bounds__(256) void copy_padded_kernel(int64_t rows, int64_t cols, int64_t kp, const uint16_t *X,
-                                                          int64_t ldx, uint16_t *P)
+// 16 bytes of a row per thread.
+template <class T>
+__global__ __launch_bounds__(256) void copy_padded_kernel(int64_t rows, int64_t cols, int64_t kp, const T *X,
+                                                          int64_t ldx, T *P)
 {
-    const int64_t groups = kp / 8;
+    constexpr int V = 16 / sizeof(T);
+    const int64_t groups = kp / V;
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < rows * groups; q += (int64_t)gridDim.x * 256) {
-        const int64_t row = q / groups, c = (q - row * groups) * 8;
-        const uint16_t *src = X + row * ldx + c;
+        const int64_t row = q / groups, c = (q - row * groups) * V;
+        const T *src = X + row * ldx + c;
         u32x4_t v = {0, 0, 0, 0};
-        if (c + 8 <= cols && ((uintptr_t)src % 16) == 0) {
+        if (c + V <= cols && ((uintptr_t)src % 16) == 0) {
             v = *reinterpret_cast<const u32x4_t *>(src);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < cols) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+            for (int e = 0; e < V; ++e)
+                if (c + e < cols) {
+                    if constexpr (sizeof(T) == 2) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+                    else v[e] = src[e];
+                }
         }
         *reinterpret_cast<u32x4_t *>(P + row * kp + c) = v;
     }
@@ -256,11 +262,15 @@ hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64
     return hipGetLastError();
 }
 
-hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P, int64_t kp,
+hipError_t launch_copy_padded(int dtype, int64_t rows, int64_t cols, const void *X, int64_t ldx, void *P, int64_t kp,
                               hipStream_t stream)
 {
-    hipLaunchKernelGGL(copy_padded_kernel, dim3(blocks_for(rows * (kp / 8), 256, 16384)), dim3(256), 0, stream, rows,
-                       cols, kp, X, ldx, P);
+    if (dtype == kF32)
+        hipLaunchKernelGGL((copy_padded_kernel<uint32_t>), dim3(blocks_for(rows * (kp / 4), 256, 16384)), dim3(256), 0,
+                           stream, rows, cols, kp, (const uint32_t *)X, ldx, (uint32_t *)P);
+    else
+        hipLaunchKernelGGL((copy_padded_kernel<uint16_t>), dim3(blocks_for(rows * (kp / 8), 256, 16384)), dim3(256), 0,
+                           stream, rows, cols, kp, (const uint16_t *)X, ldx, (uint16_t *)P);
     return hipGetLastError();
 }
 

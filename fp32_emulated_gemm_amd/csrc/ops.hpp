@@ -110,9 +110,9 @@ hipError_t launch_bf16_gemm(const Bf16Gemm &g, int num_cus, hipStream_t stream);
 // interleave: plane rows 2 f, 2 f + 1 are X's rows f, rows / 2 + f.
 hipError_t launch_split_padded(int64_t rows, int64_t cols, const float *X, int64_t ldx, uint16_t *P, bool interleave,
                                hipStream_t stream);
-// bfloat16 rows x cols -> rows of `pitch` (a multiple of 8), zeros past cols.
-hipError_t launch_copy_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P, int64_t pitch,
-                              hipStream_t stream);
+// rows x cols -> rows of `pitch` (a multiple of 8), zeros past cols.
+hipError_t launch_copy_padded(int dtype, int64_t rows, int64_t cols, const void *X, int64_t ldx, void *P,
+                              int64_t pitch, hipStream_t stream);
 // bfloat16 rows x cols -> cols x out_rows with pitch ldp, zeros past rows.
 hipError_t launch_transpose_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,
                                    int64_t out_rows, int64_t ldp, hipStream_t stream);

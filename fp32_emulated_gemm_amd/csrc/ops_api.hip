@@ -74,8 +74,20 @@ int check_ws(const void *ws, int64_t ws_bytes, int64_t need)
     return SGEMM_EMU_OK;
 }
 
-// bfloat16 operands that the GEMM reads as they lie.
-bool direct(const void *p, int64_t ld, int64_t K) { return K % 8 == 0 && ld % 8 == 0 && aligned(p, 16); }
+// Operands whose rows the GEMM reads as they lie, in 16-byte loads.  The FP32
+// kernels also take others, element by element, but then run out of registers:
+// 3328 x 371 x 2 5744 gated took 2030 us where the copy makes it 264.
+bool direct(int dtype, const void *p, int64_t ld, int64_t K)
+{
+    const int64_t v = 16 / size_of(dtype);
+    return K % v == 0 && ld % v == 0 && aligned(p, 16);
+}
+// The gated FP32 kernels take K in multiples of the padding only: the masks of a
+// ragged K cost registers that their epilogue needs.
+bool gated_direct(int dtype, const void *p, int64_t ld, int64_t K)
+{
+    return direct(dtype, p, ld, K) && (dtype == SGEMM_EMU_BF16 || K % kPadK == 0);
+}
 // The K that a bfloat16 product runs over: operands are padded copies unless K is a multiple of 8.
 int64_t bf16_k(int64_t K) { return K % 8 == 0 ? K : pad_k(K); }
 
@@ -119,7 +131,8 @@ int check_gated(int dtype, int64_t M, int64_t F, int64_t K, int gate)
 bool gated_few(int64_t M, int64_t K, const void *Z) { return M <= kFewRows && Z == nullptr && K > 0; }
 
 struct GatedWs {
-    uint16_t *plan, *x;   // W and X laid out
+    uint16_t *plan;       // W laid out
+    void *x;              // X in padded rows
     float *partials;      // few rows' K slices
     int64_t bytes;
 };
@@ -133,9 +146,10 @@ GatedWs gated_ws(int dtype, int64_t M, int64_t F, int64_t K, const void *X, int6
         w.partials = c.take<float>(few_rows_partial_floats(dtype, M, F, K, SGEMM_EMU_GATE_SILU, num_cus));
     } else if (dtype == SGEMM_EMU_F32) {
         if (plan == nullptr) w.plan = c.take<uint16_t>(3 * 2 * F * pad_k(K));
+        if (!gated_direct(dtype, X, ldx, K)) w.x = c.take<float>(M * pad_k(K));
     } else {
-        if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(2 * F * pad_k(K));
-        if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
+        if (plan == nullptr && !direct(dtype, W, ldw, K)) w.plan = c.take<uint16_t>(2 * F * pad_k(K));
+        if (!gated_direct(dtype, X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
     }
     w.bytes = c.bytes;
     return w;
@@ -200,7 +214,8 @@ bool adapter_few(int64_t M, const float *S) { return M <= kFewRows && S == nullp
 bool bank_lies(int64_t r, const void *up) { return r % 8 == 0 && aligned(up, 16); }
 
 struct AdapterWs {
-    uint16_t *plan, *x, *up;
+    uint16_t *plan, *up;
+    void *x;
     float *s, *partials;
     int64_t bytes;
 };
@@ -216,9 +231,10 @@ AdapterWs adapter_ws(int dtype, int64_t M, int64_t N, int64_t K, const void *X, 
         w.partials = c.take<float>(few_rows_partial_floats(dtype, M, N, K, -1, num_cus));
     } else if (dtype == SGEMM_EMU_F32) {
         if (plan == nullptr) w.plan = c.take<uint16_t>(3 * N * pad_k(K));
+        if (!direct(dtype, X, ldx, K)) w.x = c.take<float>(M * pad_k(K));
     } else {
-        if (plan == nullptr && !direct(W, ldw, K)) w.plan = c.take<uint16_t>(N * pad_k(K));
-        if (!direct(X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
+        if (plan == nullptr && !direct(dtype, W, ldw, K)) w.plan = c.take<uint16_t>(N * pad_k(K));
+        if (!direct(dtype, X, ldx, K)) w.x = c.take<uint16_t>(M * pad_k(K));
         if (n > 0 && r > 0 && !bank_lies(r, up)) w.up = c.take<uint16_t>(n * N * rank_pad(r));
     }
     w.bytes = c.bytes;
@@ -228,7 +244,8 @@ AdapterWs adapter_ws(int dtype, int64_t M, int64_t N, int64_t K, const void *X, 
 struct AdapterBackWs {
     void *up_t, *down_t;       // n x r x N, n x K x r
     float *p;                  // M x pad16(r)
-    uint16_t *dy, *down_p;     // dY laid out, down_t's rows padded
+    void *dy;                  // dY in padded rows
+    uint16_t *down_p;          // down_t's rows padded
     int32_t *offs, *rows;
     float *partials;
     int64_t bytes;
@@ -238,7 +255,7 @@ AdapterBackWs adapter_back_ws(int dtype, int64_t M, int64_t N, int64_t K, int64_
     Carve c(ws);
     AdapterBackWs w{};
     const int64_t size = size_of(dtype);
-    if (dtype == SGEMM_EMU_BF16) w.dy = c.take<uint16_t>(M * pad_k(N));
+    w.dy = c.take<char>(M * pad_k(N) * size);
     if (n > 0 && r > 0) {
         w.up_t = c.take<char>(n * r * N * size);
         w.down_t = c.take<char>(n * r * K * size);
@@ -293,7 +310,7 @@ int sgemm_emu_plan_weight(int dtype, int64_t rows, int64_t cols, const void *W, 
     } else if (transposed) {
         LAUNCH(launch_transpose_padded(rows, cols, (const uint16_t *)W, ldw, P, pad_k(rows), pad_k(rows), s));
     } else {
-        LAUNCH(launch_copy_padded(rows, cols, (const uint16_t *)W, ldw, P, pad_k(cols), s));
+        LAUNCH(launch_copy_padded(dtype, rows, cols, W, ldw, P, pad_k(cols), s));
     }
     return SGEMM_EMU_OK;
 }
@@ -339,7 +356,9 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
             return SGEMM_EMU_OK;
         }
         if (w.plan != nullptr) LAUNCH(launch_split_padded(2 * F, K, (const float *)W, ldw, w.plan, true, s));
-        GemmArgs g = product_f32(M, 2 * F, K, (const float *)X, ldx,
+        if (w.x != nullptr) LAUNCH(launch_copy_padded(dtype, M, K, X, ldx, w.x, pad_k(K), s));
+        GemmArgs g = product_f32(M, 2 * F, pad_k(K), w.x != nullptr ? (const float *)w.x : (const float *)X,
+                                 w.x != nullptr ? pad_k(K) : ldx,
                                  w.plan != nullptr ? w.plan : (const uint16_t *)plan, (const float *)bias, (float *)H,
                                  ldh);
         g.epi.gate = gate;
@@ -351,14 +370,14 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
     g.M = M; g.N = 2 * F; g.K = bf16_k(K);
     g.A = (const uint16_t *)X; g.lda = ldx;
     if (w.x != nullptr) {
-        LAUNCH(launch_copy_padded(M, K, (const uint16_t *)X, ldx, w.x, pad_k(K), s));
-        g.A = w.x; g.lda = pad_k(K);
+        LAUNCH(launch_copy_padded(dtype, M, K, X, ldx, w.x, pad_k(K), s));
+        g.A = (const uint16_t *)w.x; g.lda = pad_k(K);
     }
     g.B = (const uint16_t *)W; g.ldb = ldw;
     if (plan != nullptr) {
         g.B = (const uint16_t *)plan; g.ldb = pad_k(K);
     } else if (w.plan != nullptr) {
-        LAUNCH(launch_copy_padded(2 * F, K, (const uint16_t *)W, ldw, w.plan, pad_k(K), s));
+        LAUNCH(launch_copy_padded(dtype, 2 * F, K, W, ldw, w.plan, pad_k(K), s));
         g.B = w.plan; g.ldb = pad_k(K);
     }
     g.bias = (const uint16_t *)bias;
@@ -418,7 +437,7 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
     if (dW != nullptr && F > 0 && K > 0) {
         if (M > 0) CHECK(sgemm_emu_plan_weight(dtype, M, K, X, ldx, SGEMM_EMU_PLAN_TRANSPOSED, w.xt, stream));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(plain_f32(n2, K, M, (const float *)w.dzt, mp, w.xt, (float *)dW, lddw, num_cus, s));
+            CHECK(plain_f32(n2, K, mp, (const float *)w.dzt, mp, w.xt, (float *)dW, lddw, num_cus, s));
         } else {
             Bf16Gemm g{};
             g.M = n2; g.N = K; g.K = mp;
@@ -493,7 +512,10 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
             return SGEMM_EMU_OK;
         }
         if (w.plan != nullptr) LAUNCH(launch_split_padded(N, K, (const float *)W, ldw, w.plan, false, s));
-        CHECK(gemm_padded_planes(product_f32(M, N, K, (const float *)X, ldx,
+        if (w.x != nullptr) LAUNCH(launch_copy_padded(dtype, M, K, X, ldx, w.x, pad_k(K), s));
+        CHECK(gemm_padded_planes(product_f32(M, N, w.x != nullptr ? pad_k(K) : K,
+                                             w.x != nullptr ? (const float *)w.x : (const float *)X,
+                                             w.x != nullptr ? pad_k(K) : ldx,
                                              w.plan != nullptr ? w.plan : (const uint16_t *)plan, (const float *)bias,
                                              (float *)Y, ldy),
                                  plain_launchers(), s));
@@ -504,14 +526,14 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
     g.M = M; g.N = N; g.K = bf16_k(K);
     g.A = (const uint16_t *)X; g.lda = ldx;
     if (w.x != nullptr) {
-        LAUNCH(launch_copy_padded(M, K, (const uint16_t *)X, ldx, w.x, pad_k(K), s));
-        g.A = w.x; g.lda = pad_k(K);
+        LAUNCH(launch_copy_padded(dtype, M, K, X, ldx, w.x, pad_k(K), s));
+        g.A = (const uint16_t *)w.x; g.lda = pad_k(K);
     }
     g.B = (const uint16_t *)W; g.ldb = ldw;
     if (plan != nullptr) {
         g.B = (const uint16_t *)plan; g.ldb = pad_k(K);
     } else if (w.plan != nullptr) {
-        LAUNCH(launch_copy_padded(N, K, (const uint16_t *)W, ldw, w.plan, pad_k(K), s));
+        LAUNCH(launch_copy_padded(dtype, N, K, W, ldw, w.plan, pad_k(K), s));
         g.B = w.plan; g.ldb = pad_k(K);
     }
     g.bias = (const uint16_t *)bias;
@@ -521,7 +543,7 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
         g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
         g.up = (const uint16_t *)up;
         if (!bank_lies(r, up)) {
-            LAUNCH(launch_copy_padded(n * N, r, (const uint16_t *)up, r, w.up, rank_pad(r), s));
+            LAUNCH(launch_copy_padded(dtype, n * N, r, up, r, w.up, rank_pad(r), s));
             g.r = rank_pad(r);
             g.up = w.up;
         }
@@ -577,17 +599,17 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
     }
     if (need_dx) {
         if (low) LAUNCH(launch_transpose_bank(dtype, n, r, K, down, w.down_t, s));
+        const bool lies = direct(dtype, dY, lddy, N);
+        if (!lies && N > 0) LAUNCH(launch_copy_padded(dtype, M, N, dY, lddy, w.dy, pad_k(N), s));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(plain_f32(M, K, N, (const float *)dY, lddy, (const uint16_t *)plan_t, (float *)dX, lddx, num_cus, s));
+            CHECK(plain_f32(M, K, lies ? N : pad_k(N), lies ? (const float *)dY : (const float *)w.dy,
+                            lies ? lddy : pad_k(N), (const uint16_t *)plan_t, (float *)dX, lddx, num_cus, s));
             if (low && N > 0) LAUNCH(launch_expand(M, K, w.p, back, (float *)dX, lddx, s));
         } else {
             Bf16Gemm g{};
             g.M = M; g.N = K; g.K = bf16_k(N);
             g.A = (const uint16_t *)dY; g.lda = lddy;
-            if (!direct(dY, lddy, N)) {
-                if (N > 0) LAUNCH(launch_copy_padded(M, N, (const uint16_t *)dY, lddy, w.dy, pad_k(N), s));
-                g.A = w.dy; g.lda = pad_k(N);
-            }
+            if (!lies) { g.A = (const uint16_t *)w.dy; g.lda = pad_k(N); }
             g.B = (const uint16_t *)plan_t; g.ldb = pad_k(N);
             g.C = (uint16_t *)dX; g.ldc = lddx;
             g.gate = -1;
@@ -595,7 +617,7 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
                 g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
                 g.up = (const uint16_t *)w.down_t;
                 if (r % 8 != 0) {
-                    LAUNCH(launch_copy_padded(n * K, r, (const uint16_t *)w.down_t, r, w.down_p, rank_pad(r), s));
+                    LAUNCH(launch_copy_padded(dtype, n * K, r, w.down_t, r, w.down_p, rank_pad(r), s));
                     g.r = rank_pad(r);
                     g.up = w.down_p;
                 }
