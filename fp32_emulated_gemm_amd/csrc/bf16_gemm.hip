@@ -168,10 +168,18 @@ __device__ __forceinline__ void start_adapters(f32x4_t (&acc)[T::NI][T::MI], con
     const uint32_t sblock = (uint32_t)g.rp * 64u, ublock = (uint32_t)g.r * 32u;           // bytes of 16 rows
     const rsrc_t rs = make_rsrc(g.S + m0w * 2 * g.rp, (g.M - m0w) * 2 * g.rp * 2);
     auto bank = [&](int me) { return make_rsrc(g.up + ((int64_t)me * g.N + n0w) * g.r, (g.N - n0w) * g.r * 2); };
+    // Eight ranks from rc + r8 on; those past the rank belong to the next row of
+    // up, and S's zeros would not take an Inf or NaN of it away.
     auto load_up = [&](u32x4_t (&up)[T::NI], rsrc_t ru, int64_t rc) {
+        const int64_t left = g.r - (rc + r8);
 #pragma unroll
-        for (int j = 0; j < T::NI; ++j)
-            up[j] = bload_u32x4(ru, rc + r8 < g.r ? urow + j * ublock + (uint32_t)rc * 2u : OUT_OF_RANGE, 0);
+        for (int j = 0; j < T::NI; ++j) {
+            up[j] = bload_u32x4(ru, left > 0 ? urow + j * ublock + (uint32_t)rc * 2u : OUT_OF_RANGE, 0);
+            if ((g.r & 7) != 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) up[j][e] = 2 * e < left ? up[j][e] : 0u;
+            }
+        }
     };
     const int first = __builtin_amdgcn_readfirstlane(id[0]);
     bool same = true;
@@ -227,28 +235,29 @@ __device__ __forceinline__ void start_adapters(f32x4_t (&acc)[T::NI][T::MI], con
 }
 
 // One wave's TM x W block of BF16 results in LDS (rows of PITCH elements) ->
-// rows m0w.., columns c0.. of a matrix of `cols` columns: 128-bit stores where
-// the matrix allows them, else a row's elements by consecutive lanes.
+// rows m0w.., columns c0.. of a matrix of `cols` columns, in 128-bit stores
+// whatever the rows' alignment (the hardware takes any), the last columns one by
+// one.
 template <class T, int W>
 __device__ __forceinline__ void flush_block(const uint16_t *buf, uint16_t *out, int64_t ld, int64_t M, int64_t cols,
                                             int64_t m0w, int64_t c0, int lane)
 {
-    if (((uintptr_t)out % 16) == 0 && ld % 8 == 0 && c0 + W <= cols) {
-        constexpr int PER_ROW = W / 8, ROWS = 64 / PER_ROW;        // lanes per row, rows per pass
+    constexpr int PER_ROW = W / 8, ROWS = 64 / PER_ROW;            // lanes per row, rows per pass
+    const int c = (lane % PER_ROW) * 8;
+    const int64_t left = cols - (c0 + c);                          // columns from this lane's first on
+    const uint16_t *src = buf + lane / PER_ROW * T::PITCH + c;
+    uint16_t *dst = out + (m0w + lane / PER_ROW) * ld + c0 + c;
+    const int rows = (int)lmin(M - m0w, T::TM) - lane / PER_ROW;
 #pragma unroll 4
-        for (int p = 0; p < T::TM / ROWS; ++p) {
-            const int row = p * ROWS + lane / PER_ROW, c = (lane % PER_ROW) * 8;
-            const u32x4_t v = *reinterpret_cast<const u32x4_t *>(buf + row * T::PITCH + c);
-            if (m0w + row < M) *reinterpret_cast<u32x4_t *>(out + (m0w + row) * ld + c0 + c) = v;
-        }
-    } else {
-#pragma unroll 8
-        for (int e = lane; e < T::TM * W; e += 64) {
-            const int row = e / W, c = e % W;
-            const uint16_t v = buf[row * T::PITCH + c];
-            if (m0w + row < M && c0 + c < cols) out[(m0w + row) * ld + c0 + c] = v;
-        }
+    for (int p = 0; p < T::TM; p += ROWS, src += ROWS * T::PITCH, dst += ROWS * ld) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(src);
+        if (p < rows && left >= 8) *reinterpret_cast<u32x4_any *>(dst) = v;
     }
+    if (left <= 0 || left >= 8) return;
+    src -= T::TM * T::PITCH;
+    dst -= T::TM * ld;
+    for (int p = 0; p < rows; p += ROWS, src += ROWS * T::PITCH, dst += ROWS * ld)
+        for (int e = 0; e < left; ++e) dst[e] = src[e];
 }
 
 // LDS accesses of one wave complete in order; this keeps the compiler from
@@ -529,7 +538,7 @@ hipError_t launch_bf16_gemm(const Bf16Gemm &args, int num_cus, hipStream_t strea
         g.A = g.B = nullptr;
         g.lda = g.ldb = 8;
     }
-    if (g.ids != nullptr && (g.r % 8 != 0 || !aligned(g.up, 16))) return hipErrorInvalidValue;
+    if (g.ids != nullptr && (g.r % 2 != 0 || !aligned(g.up, 4))) return hipErrorInvalidValue;
     if (g.K % 8 != 0 || g.lda % 8 != 0 || g.ldb % 8 != 0 || !aligned(g.A, 16) || !aligned(g.B, 16))
         return hipErrorInvalidValue;
     const bool plain = g.gate < 0 && g.ids == nullptr;

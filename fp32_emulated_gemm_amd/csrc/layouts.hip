@@ -3,6 +3,8 @@
 //
 // Everything here is one pass over its data, bound by memory; the transposes
 // go through LDS tiles so that both sides are read and written in rows.
+#include <type_traits>
+
 #include "ops_device.hpp"
 #include "split_device.hpp"
 #include "ops.hpp"
@@ -54,8 +56,8 @@ __global__ __launch_bounds__(256) void copy_padded_kernel(int64_t rows, int64_t 
         const int64_t row = q / groups, c = (q - row * groups) * V;
         const T *src = X + row * ldx + c;
         u32x4_t v = {0, 0, 0, 0};
-        if (c + V <= cols && ((uintptr_t)src % 16) == 0) {
-            v = *reinterpret_cast<const u32x4_t *>(src);
+        if (c + V <= cols) {
+            v = *reinterpret_cast<const u32x4_any *>(src);
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e)
@@ -68,6 +70,21 @@ __global__ __launch_bounds__(256) void copy_padded_kernel(int64_t rows, int64_t 
     }
 }
 
+// Four elements and the access that takes them at any element's address.
+template <class T>
+struct Four {
+    T v[4];
+    typedef std::conditional_t<sizeof(T) == 4, u32x4_any, u32x2_any> access_t;
+    static __device__ __forceinline__ Four load(const T *p)
+    {
+        return __builtin_bit_cast(Four, *reinterpret_cast<const access_t *>(p));
+    }
+    __device__ __forceinline__ void store(T *p) const
+    {
+        *reinterpret_cast<access_t *>(p) = __builtin_bit_cast(access_t, *this);
+    }
+};
+
 // 64 x 64 tiles through LDS: src rows x cols (batch b at b * src_step) -> dst
 // cols x out_rows with pitch ldo, zeros in rows rows..out_rows.
 template <class T>
@@ -75,21 +92,42 @@ __global__ __launch_bounds__(256) void transpose_kernel(int64_t rows, int64_t co
                                                         int64_t lds_, int64_t src_step, T *dst, int64_t ldo,
                                                         int64_t dst_step)
 {
+    // four elements per access, rows in dwords an odd number apart
     __shared__ T tile[64][64 + 4 / sizeof(T)];
     const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
     src += (int64_t)blockIdx.z * src_step;
     dst += (int64_t)blockIdx.z * dst_step;
-    const int lo = threadIdx.x & 63, hi = threadIdx.x >> 6;
+    const int q = (threadIdx.x & 15) * 4, hi = threadIdx.x >> 4;
+    Four<T> v[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int r = hi + 4 * i;
-        tile[r][lo] = r0 + r < rows && c0 + lo < cols ? src[(r0 + r) * lds_ + c0 + lo] : (T)0;
+    for (int i = 0; i < 4; ++i) {
+        const int r = hi + 16 * i;
+        const T *const p = src + (r0 + r) * lds_ + c0 + q;
+        if (r0 + r < rows && c0 + q + 4 <= cols) {
+            v[i] = Four<T>::load(p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i].v[e] = r0 + r < rows && c0 + q + e < cols ? p[e] : (T)0;
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tile[hi + 16 * i][q + e] = v[i].v[e];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int c = hi + 4 * i;
-        if (c0 + c < cols && r0 + lo < out_rows) dst[(c0 + c) * ldo + r0 + lo] = tile[lo][c];
+    for (int i = 0; i < 4; ++i) {
+        const int c = hi + 16 * i;
+        if (c0 + c >= cols) continue;
+        T *const p = dst + (c0 + c) * ldo + r0 + q;
+        const Four<T> t = {{tile[q][c], tile[q + 1][c], tile[q + 2][c], tile[q + 3][c]}};
+        if (r0 + q + 4 <= out_rows) {
+            t.store(p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (r0 + q + e < out_rows) p[e] = t.v[e];
+        }
     }
 }
 
@@ -118,7 +156,7 @@ __global__ __launch_bounds__(256) void gate_bias_kernel(int64_t M, int64_t F, co
 // transpose and the column sums, which take the unrounded values.
 template <class T, int GATE>
 __global__ __launch_bounds__(256) void gate_backward_kernel(int64_t M, int64_t F, const float *Z, const T *dH,
-                                                            int64_t lddh, bool vec_h, T *dZ, T *dZt, float *sums)
+                                                            int64_t lddh, T *dZ, T *dZt, float *sums)
 {
     __shared__ float tile[2][64][65];
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -137,13 +175,13 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(int64_t M, int64_t F
             zg[i] = *reinterpret_cast<const f32x4_t *>(Z + m * 2 * zup + f);
             zu[i] = *reinterpret_cast<const f32x4_t *>(Z + m * 2 * zup + zup + f);
             const T *p = dH + m * lddh + f;
-            if (vec_h && f + 4 <= F) {
+            if (f + 4 <= F) {
                 if constexpr (sizeof(T) == 4) {
-                    const f32x4_t x = *reinterpret_cast<const f32x4_t *>(p);
+                    const u32x4_t x = *reinterpret_cast<const u32x4_any *>(p);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dh[i][e] = x[e];
+                    for (int e = 0; e < 4; ++e) dh[i][e] = __uint_as_float(x[e]);
                 } else {
-                    const u32x2 x = *reinterpret_cast<const u32x2 *>(p);
+                    const u32x2 x = *reinterpret_cast<const u32x2_any *>(p);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) dh[i][e] = bf2f((uint16_t)(x[e >> 1] >> (16 * (e & 1))));
                 }
@@ -235,10 +273,8 @@ hipError_t gate_backward_t(int64_t M, int64_t F, const float *Z, const T *dH, in
                            float *sums, hipStream_t stream)
 {
     const dim3 grid((unsigned)gate_tiles(M), (unsigned)((F + 63) / 64));
-    const bool vec_h = lddh % 4 == 0 && aligned(dH, 4 * sizeof(T));
 #define LAUNCH(G)                                                                                                 \
-    hipLaunchKernelGGL((gate_backward_kernel<T, G>), grid, dim3(256), 0, stream, M, F, Z, dH, lddh, vec_h, dZ, dZt, \
-                       sums)
+    hipLaunchKernelGGL((gate_backward_kernel<T, G>), grid, dim3(256), 0, stream, M, F, Z, dH, lddh, dZ, dZt, sums)
     switch (gate) {
     case kSilu: LAUNCH(kSilu); break;
     case kGelu: LAUNCH(kGelu); break;

@@ -92,7 +92,7 @@ struct Bf16Gemm {
     float *Z;                // with a gate: pre-activations (see z_pitch), or null
     int64_t ldz;
     const int32_t *ids;      // adapters (or null): rows' ids, up (n x N x r)
-    int64_t n, r, rp;        // r (up's row pitch) a multiple of 8, up 16-byte aligned, zeros past the rank
+    int64_t n, r, rp;        // r (up's row pitch) even, up 4-byte aligned
     const uint16_t *up;
     const uint16_t *S;       // M x 2 rp: high parts, low parts
     float *partials;         // K slices: splits x M x N floats

@@ -210,8 +210,8 @@ int check_adapters(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_
 // Few rows read W in one pass; low-rank activations to keep come from the tiles' path.
 bool adapter_few(int64_t M, const float *S) { return M <= kFewRows && S == nullptr; }
 
-// A bfloat16 bank of up factors whose rows the GEMM reads as they lie.
-bool bank_lies(int64_t r, const void *up) { return r % 8 == 0 && aligned(up, 16); }
+// A bfloat16 bank of up factors whose rows the GEMM reads as they lie (whole dwords).
+bool bank_lies(int64_t r, const void *up) { return r % 2 == 0 && aligned(up, 4); }
 
 struct AdapterWs {
     uint16_t *plan, *up;
@@ -259,7 +259,7 @@ AdapterBackWs adapter_back_ws(int dtype, int64_t M, int64_t N, int64_t K, int64_
     if (n > 0 && r > 0) {
         w.up_t = c.take<char>(n * r * N * size);
         w.down_t = c.take<char>(n * r * K * size);
-        if (dtype == SGEMM_EMU_BF16 && r % 8 != 0) w.down_p = c.take<uint16_t>(n * K * rank_pad(r));
+        if (dtype == SGEMM_EMU_BF16 && r % 2 != 0) w.down_p = c.take<uint16_t>(n * K * rank_pad(r));
         w.p = c.take<float>(M * rank_pad(r));
         w.offs = c.take<int32_t>(n + 1);
         w.rows = c.take<int32_t>(M);
@@ -616,7 +616,7 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
             if (low) {
                 g.ids = ids; g.n = n; g.r = r; g.rp = rank_pad(r);
                 g.up = (const uint16_t *)w.down_t;
-                if (r % 8 != 0) {
+                if (r % 2 != 0) {
                     LAUNCH(launch_copy_padded(dtype, n * K, r, w.down_t, r, w.down_p, rank_pad(r), s));
                     g.r = rank_pad(r);
                     g.up = w.down_p;

@@ -5,6 +5,11 @@
 
 namespace sgemm_emu_dev {
 
+// 16 and 8 bytes at any address of an element: the hardware takes unaligned
+// vector accesses, at the cost of a line more where one is crossed.
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+
 enum { kF32 = 0, kBF16 = 1 };                                      // sgemm_emu_dtype
 enum { kSilu = 0, kGelu = 1, kGeluTanh = 2, kSigmoid = 3, kRelu = 4, kGates = 5 };   // sgemm_emu_gate
 
