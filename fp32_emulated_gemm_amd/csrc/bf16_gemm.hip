@@ -52,6 +52,7 @@ struct Tile {
 
 using Tile256 = Tile<2, 4, 128, 64, 2, 1>;        // 8 waves
 using Tile128 = Tile<2, 2, 64, 64, 2, 2>;         // 4 waves
+using Tile128Deep = Tile<2, 4, 64, 32, 4, 1>;     // 8 waves: a CU of its own, its loads further ahead
 using Tile64 = Tile<2, 2, 32, 32, 4, 2>;          // 4 waves
 
 constexpr uint32_t OUT_OF_RANGE = 0xFFFFFFF0u;   // past every descriptor: reads zeros
@@ -284,7 +285,7 @@ __device__ __forceinline__ void gemm_tile(const Bf16Gemm &g, uint16_t *lds)
 
     int tm, tn;
     tile_of_index((int)blockIdx.x, (int)gridDim.x, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
-    const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
+    const int64_t m0 = g.m_base + (int64_t)tm * T::BM, n0 = g.n_base + (int64_t)tn * T::BN;
     const int64_t kb = (int64_t)blockIdx.y * g.k_per_split, ke = lmin(kb + g.k_per_split, g.K);
     const int nk = (int)((ke - kb + KS - 1) / KS);
 
@@ -468,12 +469,22 @@ __global__ __launch_bounds__(256) void bf16_sum_slices_kernel(Bf16Gemm g)
     }
 }
 
+// ---------------------------------------------------------------- tiles
+
+// The part of a product that one launch covers: tiles from row m_base, column
+// n_base (multiples of the tile) to row m_end, column n_end.
+struct Part {
+    int64_t m_base, n_base, m_end, n_end;
+};
+
 template <class T, int EPI, int GATE>
-void launch_tile(Bf16Gemm g, hipStream_t stream)
+void launch_tile(Bf16Gemm g, const Part &p, hipStream_t stream)
 {
-    g.tiles_m = (int)((g.M + T::BM - 1) / T::BM);
+    g.m_base = p.m_base;
+    g.n_base = p.n_base;
+    g.tiles_m = (int)((p.m_end - p.m_base + T::BM - 1) / T::BM);
     // a gated tile holds BN / 2 outputs of F = N / 2
-    g.tiles_n = (int)((g.N + T::BN - 1) / T::BN);
+    g.tiles_n = (int)((p.n_end - p.n_base + T::BN - 1) / T::BN);
     g.group_m = g.tiles_m < 8 ? g.tiles_m : 8;
     const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n), (unsigned)g.splits);
     // K slices begin at multiples of KS, so only the last can end inside a step
@@ -482,43 +493,116 @@ void launch_tile(Bf16Gemm g, hipStream_t stream)
 }
 
 template <class T>
-hipError_t launch_epi(const Bf16Gemm &g, hipStream_t stream)
+hipError_t launch_epi(const Bf16Gemm &g, const Part &p, hipStream_t stream)
 {
     if (g.splits > 1) {
-        launch_tile<T, EPI_PARTIAL, 0>(g, stream);
+        launch_tile<T, EPI_PARTIAL, 0>(g, p, stream);
         const dim3 grid((unsigned)((g.N + 255) / 256), (unsigned)(g.M < 16384 ? g.M : 16384));
         hipLaunchKernelGGL(bf16_sum_slices_kernel, grid, dim3(256), 0, stream, g);
         return hipGetLastError();
     }
     switch (g.gate) {
-    case kSilu: launch_tile<T, EPI_GATED, kSilu>(g, stream); break;
-    case kGelu: launch_tile<T, EPI_GATED, kGelu>(g, stream); break;
-    case kGeluTanh: launch_tile<T, EPI_GATED, kGeluTanh>(g, stream); break;
-    case kSigmoid: launch_tile<T, EPI_GATED, kSigmoid>(g, stream); break;
-    case kRelu: launch_tile<T, EPI_GATED, kRelu>(g, stream); break;
+    case kSilu: launch_tile<T, EPI_GATED, kSilu>(g, p, stream); break;
+    case kGelu: launch_tile<T, EPI_GATED, kGelu>(g, p, stream); break;
+    case kGeluTanh: launch_tile<T, EPI_GATED, kGeluTanh>(g, p, stream); break;
+    case kSigmoid: launch_tile<T, EPI_GATED, kSigmoid>(g, p, stream); break;
+    case kRelu: launch_tile<T, EPI_GATED, kRelu>(g, p, stream); break;
     default:
-        if (g.ids != nullptr) launch_tile<T, EPI_ADAPTER, 0>(g, stream);
-        else launch_tile<T, EPI_PLAIN, 0>(g, stream);
+        if (g.ids != nullptr) launch_tile<T, EPI_ADAPTER, 0>(g, p, stream);
+        else launch_tile<T, EPI_PLAIN, 0>(g, p, stream);
     }
     return hipGetLastError();
 }
 
-struct TilePlan {
-    int tile;
-    int splits;
-};
+enum { TILE_64, TILE_128_DEEP, TILE_128, TILE_256, TILES };
+
+hipError_t launch_part(int tile, const Bf16Gemm &g, const Part &p, hipStream_t stream)
+{
+    switch (tile) {
+    case TILE_256: return launch_epi<Tile256>(g, p, stream);
+    case TILE_128: return launch_epi<Tile128>(g, p, stream);
+    case TILE_128_DEEP: return launch_epi<Tile128Deep>(g, p, stream);
+    default: return launch_epi<Tile64>(g, p, stream);
+    }
+}
 
 int64_t tiles_of(int64_t M, int64_t N, int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); }
 
-// The tile and the K slices of a product.
+// Expected time of `rounds` of tiles over K, in tenths of a us: per K step of 64
+// and per round, as measured on 256 CUs (128 .. 10922 x 288 .. 10240 x 256 ..
+// 8192).  A round is one workgroup per CU, or two for TILE_64 and TILE_128; 64 x 64
+// tiles with a CU each take 0.22 us a step.
+//   1024 x 4096 x 4096: 64: 51 us, 128 deep: 34, 128: 47, 256: 74
+//   2048 x 4096 x 4096:     97             67       60       81
+//   8192 x 2048 x 8192:    358            245      219      183
+//    512 x 4096 x 4096:     26             30       44       73
+int64_t tile_cost(int tile, int64_t M, int64_t N, int64_t K, int64_t splits, int num_cus)
+{
+    static const struct { int size, per_cu, step, fixed; } t[TILES] = {
+        {64, 2, 38, 20}, {128, 1, 43, 35}, {128, 2, 82, 50}, {256, 1, 138, 100}};
+    const int64_t steps = (K + KS * splits - 1) / (KS * splits), tiles = tiles_of(M, N, t[tile].size) * splits;
+    const int64_t slots = (int64_t)num_cus * t[tile].per_cu;
+    const int64_t step = tile == TILE_64 && tiles <= num_cus ? 22 : t[tile].step;
+    return (tiles + slots - 1) / slots * (steps * step + t[tile].fixed * 10) / 10;
+}
+
+int best_tile(int64_t M, int64_t N, int64_t K, int64_t splits, int num_cus, int64_t *cost)
+{
+    int best = TILE_64;
+    *cost = tile_cost(TILE_64, M, N, K, splits, num_cus);
+    for (int t = TILE_64 + 1; t < TILES; ++t) {
+        const int64_t c = tile_cost(t, M, N, K, splits, num_cus);
+        if (c < *cost) { *cost = c; best = t; }
+    }
+    return best;
+}
+
+// How a product is run: one tile, over K slices where there are few tiles; or
+// whole rounds of 256 x 256 tiles and the rows (or columns) left over as a second
+// launch of smaller tiles, which spares a last round that few tiles fill
+// (10922 x 2048 x 8192: 317 us as 344 tiles, 283 as 256 and 352 small ones).
+struct TilePlan {
+    int tile;
+    int64_t splits;
+    Part main;
+    int tail_tile;           // -1: none
+    Part tail;
+};
+
 TilePlan tile_plan(int64_t M, int64_t N, int64_t K, bool plain, int num_cus)
 {
-    TilePlan p{64, 1};
-    if (tiles_of(M, N, 256) * 4 >= num_cus * 3) p.tile = 256;
-    else if (tiles_of(M, N, 128) >= num_cus || plain) p.tile = 128;
-    if (plain && p.tile == 128) {
-        const int64_t t = tiles_of(M, N, 128);
-        while (p.splits < 16 && t * (p.splits + 1) <= 2 * (int64_t)num_cus && K / (p.splits + 1) >= 512) ++p.splits;
+    const Part whole{0, 0, M, N};
+    TilePlan p{0, 1, whole, -1, whole};
+    int64_t cost = 0;
+    p.tile = best_tile(M, N, K, 1, num_cus, &cost);
+    const int64_t tm = (M + 255) / 256, tn = (N + 255) / 256, rounds = tm * tn / num_cus;
+    if (rounds > 0) {
+        for (int along_n = 0; along_n < 2; ++along_n) {
+            const int64_t lines = rounds * num_cus / (along_n ? tm : tn), at = 256 * lines;
+            if (lines == 0 || at >= (along_n ? N : M)) continue;
+            const Part a = along_n ? Part{0, 0, M, at} : Part{0, 0, at, N},
+                       b = along_n ? Part{0, at, M, N} : Part{at, 0, M, N};
+            int64_t rest = 0;
+            const int t = best_tile(b.m_end - b.m_base, b.n_end - b.n_base, K, 1, num_cus, &rest);
+            const int64_t c = tile_cost(TILE_256, a.m_end, a.n_end, K, 1, num_cus) + rest + 30;
+            if (c < cost) {
+                cost = c;
+                p.tile = TILE_256;
+                p.main = a;
+                p.tail_tile = t;
+                p.tail = b;
+            }
+        }
+    }
+    // the slices' sums pass through memory twice, at about 4 TB/s
+    for (int64_t s = 2; plain && s <= 16 && K / s >= 512; ++s) {
+        int64_t c = 0;
+        const int t = best_tile(M, N, K, s, num_cus, &c);
+        c += 50 + (8 * s + 2) * M * N / 400000;
+        if (c < cost) {
+            cost = c;
+            p = TilePlan{t, s, whole, -1, whole};
+        }
     }
     return p;
 }
@@ -534,6 +618,7 @@ int64_t bf16_gemm_partial_floats(int64_t M, int64_t N, int64_t K, bool plain, in
 hipError_t launch_bf16_gemm(const Bf16Gemm &args, int num_cus, hipStream_t stream)
 {
     Bf16Gemm g = args;
+    if (g.M == 0 || g.N == 0) return hipSuccess;
     if (g.K == 0) {                          // nothing is read: every copy is past the end of K
         g.A = g.B = nullptr;
         g.lda = g.ldb = 8;
@@ -542,13 +627,11 @@ hipError_t launch_bf16_gemm(const Bf16Gemm &args, int num_cus, hipStream_t strea
     if (g.K % 8 != 0 || g.lda % 8 != 0 || g.ldb % 8 != 0 || !aligned(g.A, 16) || !aligned(g.B, 16))
         return hipErrorInvalidValue;
     const bool plain = g.gate < 0 && g.ids == nullptr;
-    TilePlan p = tile_plan(g.M, g.N, g.K, plain, num_cus);
-    if (g.partials == nullptr) p.splits = 1;
-    g.splits = p.splits;
+    const TilePlan p = tile_plan(g.M, g.N, g.K, plain && g.partials != nullptr, num_cus);
+    g.splits = (int)p.splits;
     g.k_per_split = round_up((g.K + p.splits - 1) / p.splits, KS);
-    if (p.tile == 256) return launch_epi<Tile256>(g, stream);
-    if (p.tile == 128) return launch_epi<Tile128>(g, stream);
-    return launch_epi<Tile64>(g, stream);
+    const hipError_t e = launch_part(p.tile, g, p.main, stream);
+    return e != hipSuccess || p.tail_tile < 0 ? e : launch_part(p.tail_tile, g, p.tail, stream);
 }
 
 }  // namespace sgemm_emu_dev

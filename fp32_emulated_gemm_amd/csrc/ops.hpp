@@ -98,6 +98,7 @@ struct Bf16Gemm {
     float *partials;         // K slices: splits x M x N floats
     int splits;
     int64_t k_per_split;
+    int64_t m_base, n_base;  // the launch's first row and column
     int tiles_m, tiles_n, group_m;
 };
 // Floats of `partials` the product takes (0: one pass over K).
