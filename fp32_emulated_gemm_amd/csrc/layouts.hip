@@ -85,18 +85,14 @@ struct Four {
     }
 };
 
-// 64 x 64 tiles through LDS: src rows x cols (batch b at b * src_step) -> dst
-// cols x out_rows with pitch ldo, zeros in rows rows..out_rows.
+// A 64 x 64 tile through LDS, by 256 threads: rows r0.., columns c0.. of src (rows x
+// cols) -> dst (cols x out_rows with pitch ldo), zeros in rows rows..out_rows.
 template <class T>
-__global__ __launch_bounds__(256) void transpose_kernel(int64_t rows, int64_t cols, int64_t out_rows, const T *src,
-                                                        int64_t lds_, int64_t src_step, T *dst, int64_t ldo,
-                                                        int64_t dst_step)
+__device__ __forceinline__ void transpose_tile(int64_t rows, int64_t cols, int64_t out_rows, const T *src,
+                                               int64_t lds_, T *dst, int64_t ldo, int64_t r0, int64_t c0)
 {
     // four elements per access, rows in dwords an odd number apart
     __shared__ T tile[64][64 + 4 / sizeof(T)];
-    const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-    src += (int64_t)blockIdx.z * src_step;
-    dst += (int64_t)blockIdx.z * dst_step;
     const int q = (threadIdx.x & 15) * 4, hi = threadIdx.x >> 4;
     Four<T> v[4];
 #pragma unroll
@@ -128,6 +124,87 @@ __global__ __launch_bounds__(256) void transpose_kernel(int64_t rows, int64_t co
             for (int e = 0; e < 4; ++e)
                 if (r0 + q + e < out_rows) p[e] = t.v[e];
         }
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void transpose_kernel(int64_t rows, int64_t cols, int64_t out_rows, const T *src,
+                                                        int64_t lds_, T *dst, int64_t ldo)
+{
+    transpose_tile<T>(rows, cols, out_rows, src, lds_, dst, ldo, (int64_t)blockIdx.x * 64, (int64_t)blockIdx.y * 64);
+}
+
+// ---------------------------------------------------------------- before the adapters' backward
+
+// Lists the rows of adapter `me`, ascending, by 256 threads: a thread takes a run of
+// ids, counts those below its own (where its rows start) and its own, and, with
+// the counts of the threads before it, writes its rows.  No atomics: the order,
+// and with it the gradients' order of additions, is fixed.
+__device__ __forceinline__ void group_rows_of(int32_t me, int64_t M, const int32_t *ids, int64_t n, int32_t *offs,
+                                              int32_t *rows)
+{
+    __shared__ int32_t less_sum[4], own_sum[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t run = ((M + 255) / 256 + 3) / 4 * 4, begin = run * threadIdx.x, end = lmin(begin + run, M);
+    auto each = [&](auto f) {
+#pragma unroll 4
+        for (int64_t t = begin; t < end; t += 4) {
+            const u32x4_t v = t + 4 <= end ? (u32x4_t)*reinterpret_cast<const u32x4_any *>(ids + t)
+                                           : u32x4_t{(uint32_t)ids[t], t + 1 < end ? (uint32_t)ids[t + 1] : ~0u,
+                                                     t + 2 < end ? (uint32_t)ids[t + 2] : ~0u, ~0u};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f(t + e, (int32_t)v[e]);
+        }
+    };
+    int32_t less = 0, own = 0;
+    each([&](int64_t, int32_t v) {
+        less += v >= 0 && v < me;
+        own += v == me;
+    });
+    int32_t before = own;                        // of this wave's threads up to this one
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        less += __shfl_xor(less, s);
+        const int32_t v = __shfl_up(before, s);
+        before += lane >= s ? v : 0;
+    }
+    if (lane == 63) { less_sum[wave] = less; own_sum[wave] = before; }
+    __syncthreads();
+    const int32_t first = less_sum[0] + less_sum[1] + less_sum[2] + less_sum[3];
+    if (threadIdx.x == 0) {
+        offs[me] = first;
+        if (me == n - 1) offs[n] = first + own_sum[0] + own_sum[1] + own_sum[2] + own_sum[3];
+    }
+    if (own == 0) return;
+    int32_t at = first + before - own;
+    for (int w = 0; w < wave; ++w) at += own_sum[w];
+    each([&](int64_t t, int32_t v) {
+        if (v == me) rows[at++] = (int32_t)t;
+    });
+}
+
+// The adapters' factors transposed and their rows grouped, in one launch: each of
+// the three alone is a few us of latency.
+template <class T>
+__global__ __launch_bounds__(256) void prepare_kernel(AdapterPrepare q)
+{
+    int64_t b = blockIdx.x;
+    if (b < q.groups) {
+        group_rows_of((int32_t)b, q.M, q.ids, q.n, q.offs, q.rows);
+        return;
+    }
+    b -= q.groups;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const AdapterPrepare::Bank &m = q.bank[k];
+        const int64_t tr = (m.rows + 63) / 64, tc = (m.cols + 63) / 64, tiles = m.dst != nullptr ? q.n * tr * tc : 0;
+        if (b < tiles) {
+            const int64_t i = b / (tr * tc), t = b - i * (tr * tc), step = i * m.rows * m.cols;
+            transpose_tile<T>(m.rows, m.cols, m.rows, (const T *)m.src + step, m.cols, (T *)m.dst + step, m.rows,
+                              t % tr * 64, t / tr * 64);
+            return;
+        }
+        b -= tiles;
     }
 }
 
@@ -314,20 +391,22 @@ hipError_t launch_transpose_padded(int64_t rows, int64_t cols, const uint16_t *X
                                    int64_t out_rows, int64_t ldp, hipStream_t stream)
 {
     hipLaunchKernelGGL((transpose_kernel<uint16_t>), dim3((unsigned)((out_rows + 63) / 64), (unsigned)((cols + 63) / 64)),
-                       dim3(256), 0, stream, rows, cols, out_rows, X, ldx, (int64_t)0, P, ldp, (int64_t)0);
+                       dim3(256), 0, stream, rows, cols, out_rows, X, ldx, P, ldp);
     return hipGetLastError();
 }
 
-hipError_t launch_transpose_bank(int dtype, int64_t n, int64_t rows, int64_t cols, const void *src, void *dst,
-                                 hipStream_t stream)
+hipError_t launch_adapter_prepare(int dtype, AdapterPrepare q, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((rows + 63) / 64), (unsigned)((cols + 63) / 64), (unsigned)n);
+    q.groups = q.offs != nullptr ? q.n : 0;
+    int64_t blocks = q.groups;
+    for (const AdapterPrepare::Bank &m : q.bank)
+        if (m.dst != nullptr) blocks += q.n * ((m.rows + 63) / 64) * ((m.cols + 63) / 64);
+    if (blocks == 0) return hipSuccess;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
     if (dtype == kF32)
-        hipLaunchKernelGGL((transpose_kernel<float>), grid, dim3(256), 0, stream, rows, cols, rows, (const float *)src,
-                           cols, rows * cols, (float *)dst, rows, rows * cols);
+        hipLaunchKernelGGL((prepare_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, stream, q);
     else
-        hipLaunchKernelGGL((transpose_kernel<uint16_t>), grid, dim3(256), 0, stream, rows, cols, rows,
-                           (const uint16_t *)src, cols, rows * cols, (uint16_t *)dst, rows, rows * cols);
+        hipLaunchKernelGGL((prepare_kernel<uint16_t>), dim3((unsigned)blocks), dim3(256), 0, stream, q);
     return hipGetLastError();
 }
 

@@ -670,59 +670,10 @@ __global__ __launch_bounds__(256) void expand_kernel(int64_t M, int64_t N, const
         }
 }
 
-// ---------------------------------------------------------------- grouping rows by adapter
-// Workgroup i lists the rows of adapter i, ascending: it counts the ids below
-// its own (where its rows start) and its own, then writes its rows in order
-// (ballots and a prefix over the waves).  No atomics: the order, and with it
-// the gradients' order of additions, is fixed.
-constexpr int GROUP_NT = 1024;
-__global__ __launch_bounds__(GROUP_NT) void group_kernel(int64_t M, const int32_t *ids, int64_t n, int32_t *offs,
-                                                         int32_t *rows)
-{
-    __shared__ int32_t less_sum[GROUP_NT / 64], own_sum[GROUP_NT / 64], found[GROUP_NT / 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int32_t me = (int32_t)blockIdx.x;
-    int32_t less = 0, own = 0;
-    for (int64_t t = tid; t < M; t += GROUP_NT) {
-        const int32_t v = ids[t];
-        less += v >= 0 && v < me;
-        own += v == me;
-    }
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        less += __shfl_xor(less, s);
-        own += __shfl_xor(own, s);
-    }
-    if (lane == 0) { less_sum[wave] = less; own_sum[wave] = own; }
-    __syncthreads();
-    int32_t at = 0, mine = 0;
-    for (int w = 0; w < GROUP_NT / 64; ++w) { at += less_sum[w]; mine += own_sum[w]; }
-    if (tid == 0) {
-        offs[me] = at;
-        if (me == n - 1) offs[n] = at + mine;
-    }
-    if (mine == 0) return;
-    for (int64_t base = 0; base < M; base += GROUP_NT) {
-        const int64_t t = base + tid;
-        const bool hit = t < M && ids[t] == me;
-        const uint64_t mask = __ballot(hit);
-        if (lane == 0) found[wave] = __popcll(mask);
-        __syncthreads();
-        int32_t before = 0, all = 0;
-        for (int w = 0; w < GROUP_NT / 64; ++w) {
-            before += w < wave ? found[w] : 0;
-            all += found[w];
-        }
-        if (hit) rows[at + before + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)t;
-        at += all;
-        __syncthreads();
-    }
-}
-
 // ---------------------------------------------------------------- gradients of the low-rank factors
 // G[i] = sum over adapter i's rows t of L[t] (x) R[t] (r x C), for one or two
 // jobs (the two factors) in one launch.  The rows, grouped by adapter
-// (group_kernel), are cut into chunks of CH; workgroup (column block, chunk)
+// (prepare_kernel, layouts.hip), are cut into chunks of CH; workgroup (column block, chunk)
 // sums the pieces of the adapters that its chunk meets, each into slot
 // chunk + i of the partials (chunks and adapters both ascend along the list, so
 // a piece's slot is its own), and a second kernel adds each adapter's slots in
@@ -738,7 +689,7 @@ struct GradJob {
     T *G;
     float *partials;
     int blocks;               // column blocks
-    bool vec, transposed;
+    bool transposed;
 };
 template <class T>
 struct GradJobs {
@@ -766,7 +717,7 @@ __global__ __launch_bounds__(64 * GRAD_WAVES) void lowrank_grad_kernel(GradJobs<
         if (a.offs[mid] <= first) lo = mid;
         else hi = mid - 1;
     }
-    const bool vec = g.vec && c + V <= C;
+    const bool vec = c + V <= C;
     for (int64_t i = lo; i < a.n && a.offs[i] < end; ++i) {
         const int64_t pb = a.offs[i] > first ? a.offs[i] : first, pe = lmin(a.offs[i + 1], end);
         if (pb >= pe) continue;
@@ -795,7 +746,7 @@ __global__ __launch_bounds__(64 * GRAD_WAVES) void lowrank_grad_kernel(GradJobs<
                 }
                 const T *src = g.R + t[u] * g.ldr + c;
                 if (vec) {
-                    const u32x4_t v = *reinterpret_cast<const u32x4_t *>(src);
+                    const u32x4_t v = *reinterpret_cast<const u32x4_any *>(src);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         if constexpr (sizeof(T) == 4) x[u][e] = __uint_as_float(v[e]);
@@ -883,7 +834,6 @@ hipError_t launch_lowrank_grad_t(const LowrankGrads &q, int num_cus, hipStream_t
         g.L = L; g.R = (const T *)R; g.ldr = ldr; g.C = C;
         g.G = (T *)G; g.partials = partials;
         g.blocks = (int)((C + 16 * V - 1) / (16 * V));
-        g.vec = ldr % V == 0 && aligned(R, 16);
         g.transposed = transposed;
         blocks += g.blocks;
         if (C > most) most = C;
@@ -937,12 +887,6 @@ hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &a
 {
     const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((N + 127) / 128));
     hipLaunchKernelGGL(expand_kernel, grid, dim3(256), 0, stream, M, N, S, rank_pad(ad.r), ad, Y, ldy);
-    return hipGetLastError();
-}
-
-hipError_t launch_group(int64_t M, const int32_t *ids, int64_t n, int32_t *offs, int32_t *rows, hipStream_t stream)
-{
-    hipLaunchKernelGGL(group_kernel, dim3((unsigned)n), dim3(GROUP_NT), 0, stream, M, ids, n, offs, rows);
     return hipGetLastError();
 }
 

@@ -34,9 +34,22 @@ hipError_t launch_shrink(int dtype, int64_t M, int64_t K, const void *X, int64_t
 hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &ad, float *Y, int64_t ldy,
                          hipStream_t stream);
 
-// offs[0..n]: where each adapter's rows start in rows[]; rows[]: the row
-// numbers that have an adapter, grouped by it, ascending inside a group.
-hipError_t launch_group(int64_t M, const int32_t *ids, int64_t n, int32_t *offs, int32_t *rows, hipStream_t stream);
+// What the adapters' backward needs first, in one launch: up to two banks
+// transposed (n x rows x cols -> n x cols x rows, contiguous), and the rows
+// grouped: offs[0..n] tells where each adapter's rows start in rows[], the row
+// numbers that have an adapter, ascending inside a group.
+struct AdapterPrepare {
+    struct Bank {
+        int64_t rows, cols;
+        const void *src;
+        void *dst;            // null: not wanted
+    } bank[2];
+    int64_t n, M;
+    const int32_t *ids;
+    int32_t *offs, *rows;     // null: not wanted
+    int64_t groups;           // set by the launch
+};
+hipError_t launch_adapter_prepare(int dtype, AdapterPrepare q, hipStream_t stream);
 
 // down[i] = sum over the adapter's rows of P[t] (x) X[t] (n x r x K), up[i] = sum
 // of dY[t] (x) S[t] (n x N x r); either may be null.  P, S as launch_shrink writes
@@ -117,10 +130,6 @@ hipError_t launch_copy_padded(int dtype, int64_t rows, int64_t cols, const void 
 // bfloat16 rows x cols -> cols x out_rows with pitch ldp, zeros past rows.
 hipError_t launch_transpose_padded(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, uint16_t *P,
                                    int64_t out_rows, int64_t ldp, hipStream_t stream);
-// src n x rows x cols -> dst n x cols x rows (contiguous).
-hipError_t launch_transpose_bank(int dtype, int64_t n, int64_t rows, int64_t cols, const void *src, void *dst,
-                                 hipStream_t stream);
-
 // Pre-activations Z are floats whatever the call's type: rows of z_pitch(F), the
 // gate's from column 0, the up projection's from column z_pitch(F) / 2.
 inline int64_t z_pitch(int64_t F) { return 2 * round_up(F, 8); }

@@ -593,12 +593,18 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
     const Adapters back{ids, n, r, w.up_t, w.down_t, scale};
     const bool need_dx = dX != nullptr && M > 0 && K > 0, need_down = low && d_down != nullptr && K > 0,
                need_up = low && d_up != nullptr && N > 0;
-    if (low && M > 0 && (need_dx || need_down)) {
-        if (N > 0) LAUNCH(launch_transpose_bank(dtype, n, N, r, up, w.up_t, s));
-        LAUNCH(launch_shrink(dtype, M, N, dY, lddy, back, w.p, num_cus, s));
+    if (low) {
+        const bool need_p = M > 0 && (need_dx || need_down), need_rows = need_down || need_up;
+        AdapterPrepare q{};
+        q.bank[0] = {N, r, up, need_p ? w.up_t : nullptr};
+        q.bank[1] = {r, K, down, need_dx ? w.down_t : nullptr};
+        q.n = n; q.M = M; q.ids = ids;
+        q.offs = need_rows ? w.offs : nullptr;
+        q.rows = w.rows;
+        LAUNCH(launch_adapter_prepare(dtype, q, s));
+        if (need_p) LAUNCH(launch_shrink(dtype, M, N, dY, lddy, back, w.p, num_cus, s));
     }
     if (need_dx) {
-        if (low) LAUNCH(launch_transpose_bank(dtype, n, r, K, down, w.down_t, s));
         const bool lies = direct(dtype, dY, lddy, N);
         if (!lies && N > 0) LAUNCH(launch_copy_padded(dtype, M, N, dY, lddy, w.dy, pad_k(N), s));
         if (dtype == SGEMM_EMU_F32) {
@@ -627,7 +633,6 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
         }
     }
     if (need_down || need_up) {
-        LAUNCH(launch_group(M, ids, n, w.offs, w.rows, s));
         LowrankGrads q{};
         q.M = M; q.K = K; q.N = N; q.n = n; q.r = r;
         q.P = w.p; q.S = S;
