@@ -32,30 +32,40 @@ dim3 persistent_grid(const GemmArgs &g)
 
 // A's rows lie in 16-byte pieces and K is a multiple of 64 (callers copy others
 // to padded rows), so only the kernels without element loads or masks are built.
-hipError_t gated_tile64(const GemmArgs &args, hipStream_t stream)
+template <int EPI>
+hipError_t fused_tile64(const GemmArgs &args, hipStream_t stream)
 {
     const GemmArgs g = tiled<Cfg64S>(args);
-    hipLaunchKernelGGL((gemm_bf16x9_kernel<Cfg64S, 5, true, B_PLANES_NK, 1, false, EPI_GATED>),
+    hipLaunchKernelGGL((gemm_bf16x9_kernel<Cfg64S, 5, true, B_PLANES_NK, 1, false, EPI>),
                        dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), dim3(Cfg64S::NT), 0, stream, g);
     return hipGetLastError();
 }
 
-hipError_t gated_planes(const GemmArgs &args, hipStream_t stream)
+template <int EPI>
+hipError_t fused_planes(const GemmArgs &args, hipStream_t stream)
 {
     const GemmArgs g = tiled<C128>(args);
-    launch_last(gemm_bf16x9_planes_kernel<C128, 5, EPI_GATED>, persistent_grid(g), dim3(C128::NT), stream, g);
+    launch_last(gemm_bf16x9_planes_kernel<C128, 5, EPI>, persistent_grid(g), dim3(C128::NT), stream, g);
     return hipGetLastError();
 }
 
-hipError_t gated_dma(const GemmArgs &args, hipStream_t stream)
+template <int EPI>
+hipError_t fused_dma(const GemmArgs &args, hipStream_t stream)
 {
     const GemmArgs g = tiled<C128>(args);
     const dim3 block(C128::NT);
     if (!aligned(g.A, 16) || g.lda % 4 != 0 || g.ka != g.K) return hipErrorInvalidValue;
 #ifdef SGEMM_EMU_SERIAL_LDS
-    launch_last(gemm_bf16x9_serial_kernel<C128, 5, true, false, false, EPI_GATED>,
+    launch_last(gemm_bf16x9_serial_kernel<C128, 5, true, false, false, EPI>,
                 dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), block, stream, g);
 #else
+    if (g.sk_grid > 0 && EPI == EPI_ADAPTER) {
+        // Stream-K's epilogue holds whole partial tiles in registers: with the
+        // adapters' start it spilled, 53 us for 6144 x 256 x 1024 against 49 as the
+        // product and a pass over C, and 136 against 114 for 3136 x 336 x 3592.
+        const hipError_t e = launch_gemm(args, 5, B_PLANES_NK, stream);
+        return e != hipSuccess ? e : launch_expand(g.M, g.N, g.epi, g.C, g.ldc, stream);
+    }
     if (g.sk_grid > 0) {
         GemmArgs s = g;
         s.sk_domains = (int)streamk_domains((int64_t)g.tiles_m * g.tiles_n, g.K / (2 * BK), g.sk_grid);
@@ -63,7 +73,7 @@ hipError_t gated_dma(const GemmArgs &args, hipStream_t stream)
         launch_last(gemm_bf16x9_streamk_kernel<C128, 5, true, false, false, EPI_GATED>, dim3((unsigned)g.sk_grid),
                     block, stream, s);
     } else {
-        launch_last(gemm_bf16x9_dma_kernel<C128, 5, true, false, false, EPI_GATED>, persistent_grid(g), block, stream,
+        launch_last(gemm_bf16x9_dma_kernel<C128, 5, true, false, false, EPI>, persistent_grid(g), block, stream,
                     g);
     }
 #endif
@@ -87,7 +97,13 @@ const PlaneLaunchers &plain_launchers()
 
 const PlaneLaunchers &gated_launchers()
 {
-    static const PlaneLaunchers l = {gated_tile64, gated_planes, gated_dma};
+    static const PlaneLaunchers l = {fused_tile64<EPI_GATED>, fused_planes<EPI_GATED>, fused_dma<EPI_GATED>};
+    return l;
+}
+
+const PlaneLaunchers &adapter_launchers()
+{
+    static const PlaneLaunchers l = {fused_tile64<EPI_ADAPTER>, fused_planes<EPI_ADAPTER>, fused_dma<EPI_ADAPTER>};
     return l;
 }
 

@@ -56,9 +56,9 @@
 
 namespace sgemm_emu_dev {
 
-// What a kernel's epilogue does with a tile: store it (bias, activation), or the
-// gated product.
-enum { EPI_STORE = 0, EPI_GATED = 1 };
+// What a kernel does with a tile: store it (bias, activation), the gated product,
+// or store it with the adapters' part in the accumulators from the start.
+enum { EPI_STORE = 0, EPI_GATED = 1, EPI_ADAPTER = 2 };
 
 // Launch the last kernel of a call.  With g.done set (a call that used the
 // stream's workspace block), the event is tied to that kernel's completion, so
@@ -652,6 +652,68 @@ __device__ __forceinline__ void store_c(const Acc<C, NB> &acc, const float (&bv)
     else store_c_act<C, NB, 0>(acc, bv, g, m0, n0, wm, wn, lane);
 }
 
+// ---------------------------------------------------------------- adapters' part
+
+// Band 0 of the accumulators starts as up[i] S[t], by FP32 products and sums, for
+// the rows t of adapter i and zero for rows without one: one pass less over C
+// than a kernel of its own behind the product (12 us of 6144 x 1024), and behind
+// the main loop it would need registers that the epilogue has not.  A block of
+// 32 rows takes its adapters one after another (in order of their first row) and
+// a row keeps the products of its own: zero times Inf or NaN in one adapter's
+// weights never reaches another's rows.
+template <class C, int NB>
+__device__ __forceinline__ void start_adapters(Acc<C, NB> &acc, const GemmArgs &g, int64_t m0, int64_t n0, int wm,
+                                               int wn, int lane)
+{
+    const GemmEpilogue &a = g.epi;
+    const int half = lane >> 5;
+    const bool vec = a.r % 4 == 0 && ((uintptr_t)a.up % 16) == 0;
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) {
+        const int64_t m = m0 + wm * C::WTM + i * 32 + (lane & 31);
+        int32_t id = m < g.M ? a.ids[m] : -1;
+        if (id >= a.n) id = -1;
+        const float *const srow = a.S + lmin(m, g.M - 1) * a.rp + 4 * half;
+        uint32_t todo = (uint32_t)__ballot(id >= 0);
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j) acc.v[i][j][0] = f32x16_t{};
+        while (todo != 0) {
+            const int32_t me = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+            const uint32_t same = (uint32_t)__ballot(id == me), own = same >> (4 * half);
+            todo &= ~same;
+            const float *const bank = a.up + (int64_t)me * g.N * a.r + 4 * half;
+            f32x16_t t[C::NI];
+#pragma unroll
+            for (int j = 0; j < C::NI; ++j) t[j] = f32x16_t{};
+            for (int64_t q = 0; q < a.r; q += 8) {
+                // a lane's four consecutive ranks are the k of four instructions
+                const f32x4_t s = *reinterpret_cast<const f32x4_t *>(srow + q);
+                const int64_t k = q + 4 * half;
+#pragma unroll
+                for (int j = 0; j < C::NI; ++j) {
+                    const int64_t col = n0 + wn * C::WTN + j * 32 + (lane & 31);
+                    const float *p = bank + lmin(col, g.N - 1) * a.r + q;
+                    f32x4_t u = {0, 0, 0, 0};
+                    if (vec) {
+                        if (k < a.r) u = *reinterpret_cast<const f32x4_t *>(p);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (k + e < a.r) u[e] = p[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[j] = __builtin_amdgcn_mfma_f32_32x32x2f32(s[e], u[e], t[j], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < C::NI; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc.v[i][j][0][r] = (own >> (8 * (r >> 2) + (r & 3))) & 1 ? t[j][r] : acc.v[i][j][0][r];
+        }
+    }
+}
+
 template <class C, int NB, bool AVEC, int BSRC, int BVEC, bool RNE, int EPI = EPI_STORE>
 __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_kernel(GemmArgs g)
 {
@@ -675,6 +737,7 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_kernel(GemmArgs g)
         for (int j = 0; j < C::NI; ++j)
 #pragma unroll
             for (int s = 0; s < NB; ++s) acc.v[i][j][s] = f32x16_t{};
+    if constexpr (EPI == EPI_ADAPTER) start_adapters<C, NB>(acc, g, m0, n0, wm, wn, lane);
 
     const int64_t nk = (g.K + BK - 1) / BK;
 
@@ -996,6 +1059,15 @@ __device__ __forceinline__ void clear_acc(Acc<C, NB> &acc)
                 acc.v[i][j][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(z, z, f32x16_t{}, 0, 0, 0);
 }
 
+// The accumulators of the tile at (m0, n0).
+template <class C, int NB, int EPI>
+__device__ __forceinline__ void begin_acc(Acc<C, NB> &acc, const GemmArgs &g, int64_t m0, int64_t n0, int wm, int wn,
+                                          int lane)
+{
+    clear_acc<C, NB>(acc);
+    if constexpr (EPI == EPI_ADAPTER) start_adapters<C, NB>(acc, g, m0, n0, wm, wn, lane);
+}
+
 // Work unit v (a tile) -> its origin; its K range starts at 0.
 template <class C>
 __device__ __forceinline__ void unit_src(StepSrc<C> &u, int v, int T, const GemmArgs &g)
@@ -1042,8 +1114,6 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_dma_kernel(GemmArgs g)
     unit_src<C>(cur, v, T, g);
 
     Acc<C, NB> acc;
-    clear_acc<C, NB>(acc);
-
     float a_next[C::A_CHUNKS][8], a_cur[C::A_CHUNKS][8];
     Frags<C> f0, f1;
 
@@ -1058,6 +1128,7 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_dma_kernel(GemmArgs g)
     wait_vmem_at_most<dma_vmem_per_step<C>()>();
     lds_barrier();
     read_frags_dma<C>(f0, a_base, b_base, 0, wm, wn, lane);
+    begin_acc<C, NB, EPI>(acc, g, cur.m0, cur.n0, wm, wn, lane);
 
     int bs = 0;                                  // B ring slot of the current step
     for (;;) {
@@ -1100,9 +1171,9 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_dma_kernel(GemmArgs g)
 
         store_c<C, NB, EPI>(acc, bias, g, cur.m0, cur.n0, wm, wn, lane);
         if (!has_next) break;
-        clear_acc<C, NB>(acc);
         v = (int)vn;
         cur = nxt;
+        begin_acc<C, NB, EPI>(acc, g, cur.m0, cur.n0, wm, wn, lane);
     }
     wait_vmem_at_most<0>();      // drain the copies issued past the end of K
 }
@@ -1133,7 +1204,7 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_serial_kernel(GemmArgs g
     StepSrc<C> cur;
     unit_src<C>(cur, (int)blockIdx.x, T, g);
     Acc<C, NB> acc;
-    clear_acc<C, NB>(acc);
+    begin_acc<C, NB, EPI>(acc, g, cur.m0, cur.n0, wm, wn, lane);
     Frags<C> f;
     for (int64_t k0 = 0; k0 < g.K; k0 += BK) {
         dma_b_stage<C>(g, cur.n0, k0, bbuf, wave, lane);
@@ -1358,7 +1429,7 @@ __device__ __forceinline__ void sk_finish(const Acc<C, NB> &acc, const float (&b
 #pragma unroll
                 for (int r = 0; r < 16; ++r) sum[i][j][r] = u == w0 ? p[i][j][r] : sum[i][j][r] + p[i][j][r];
     }
-    if constexpr (EPI != EPI_STORE) {
+    if constexpr (EPI == EPI_GATED) {
 #pragma unroll
         for (int j = 0; j < C::NI; ++j)
 #pragma unroll
@@ -1571,7 +1642,6 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_planes_kernel(GemmArgs g
     };
 
     Acc<C, NB> acc;
-    clear_acc<C, NB>(acc);
     Frags<C> f0, f1;
 
     // Prologue: steps 0 and 1 in flight, step 0 landed, its first fragments read.
@@ -1580,6 +1650,7 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_planes_kernel(GemmArgs g
     wait_vmem_at_most<NV>();
     lds_barrier();
     read_frags_planes<C>(f0, a_base, b_base, 0, wm, wn, lane);
+    begin_acc<C, NB, EPI>(acc, g, cur.m0, cur.n0, wm, wn, lane);
 
     int bs = 0;                                  // ring slot of the current step
     for (;;) {
@@ -1607,9 +1678,9 @@ __global__ __launch_bounds__(C::NT, 1) void gemm_bf16x9_planes_kernel(GemmArgs g
         }
         store_c<C, NB, EPI>(acc, bias, g, cur.m0, cur.n0, wm, wn, lane);
         if (!has_next) break;
-        clear_acc<C, NB>(acc);
         v = (int)vn;
         cur = nxt;
+        begin_acc<C, NB, EPI>(acc, g, cur.m0, cur.n0, wm, wn, lane);
     }
     wait_vmem_at_most<0>();      // drain the copies issued past the end of K
 }

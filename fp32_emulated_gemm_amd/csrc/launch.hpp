@@ -15,11 +15,15 @@ enum BSource {
     B_PLANES_NK = 2    // three BF16 planes, N x K row-major (B transposed, k contiguous)
 };
 
-// The gated epilogue of the FP32 products (gemm_fused.hip): C is H (M x N / 2).
+// What the fused FP32 products (gemm_fused.hip) do beside the product.  Gated: C is
+// H (M x N / 2).  Adapters: C += up[i] S[t] for the rows t with ids[t] = i.
 struct GemmEpilogue {
     int gate;
     float *Z;                // pre-activations to keep (rows of ldz floats, up from ldz / 2), or null
     int64_t ldz;
+    const int32_t *ids;
+    int64_t n, r, rp;        // up n x N x r, S rows of rp floats (zeros past r)
+    const float *up, *S;
 };
 
 struct GemmArgs {

@@ -31,8 +31,7 @@ hipError_t launch_shrink(int dtype, int64_t M, int64_t K, const void *X, int64_t
                          int num_cus, hipStream_t stream);
 
 // FP32: Y[t] += up[i] S[t] for the rows that have an adapter.
-hipError_t launch_expand(int64_t M, int64_t N, const float *S, const Adapters &ad, float *Y, int64_t ldy,
-                         hipStream_t stream);
+hipError_t launch_expand(int64_t M, int64_t N, const GemmEpilogue &ad, float *Y, int64_t ldy, hipStream_t stream);
 
 // What the adapters' backward needs first, in one launch: up to two banks
 // transposed (n x rows x cols -> n x cols x rows, contiguous), and the rows
@@ -155,6 +154,7 @@ hipError_t launch_sum_tiles(int dtype, int64_t tiles, int64_t cols, const float 
 int gemm_padded_planes(const GemmArgs &args, const PlaneLaunchers &launch, hipStream_t stream);
 const PlaneLaunchers &plain_launchers();     // bias
 const PlaneLaunchers &gated_launchers();     // bias, gate (args.epi; B's columns alternate gate, up)
+const PlaneLaunchers &adapter_launchers();   // bias, adapters (args.epi)
 // The current device's CU count if it is a gfx950 (SGEMM_EMU_EARCH otherwise).
 int current_cus(int *num_cus);
 

@@ -83,7 +83,7 @@ bool direct(int dtype, const void *p, int64_t ld, int64_t K)
     return K % v == 0 && ld % v == 0 && aligned(p, 16);
 }
 // The gated FP32 kernels take K in multiples of the padding only: the masks of a
-// ragged K cost registers that their epilogue needs.
+// ragged K cost registers that they need.
 bool gated_direct(int dtype, const void *p, int64_t ld, int64_t K)
 {
     return direct(dtype, p, ld, K) && (dtype == SGEMM_EMU_BF16 || K % kPadK == 0);
@@ -116,6 +116,25 @@ int plain_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, cons
         return SGEMM_EMU_OK;
     }
     return gemm_padded_planes(product_f32(M, N, K, A, lda, planes, nullptr, C, ldc), plain_launchers(), stream);
+}
+
+// The product with the adapters' part (or none).  A ragged K whose rows lie takes
+// the plain kernels and a pass over C: a padded copy of A for the fused ones cost
+// as much or more (3136 x 336 x 3592: 128 us against 114).
+int adapted_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes,
+                const float *bias, const Adapters *ad, const float *S, float *C, int64_t ldc, hipStream_t stream)
+{
+    GemmArgs g = product_f32(M, N, K, A, lda, planes, bias, C, ldc);
+    if (ad == nullptr) return gemm_padded_planes(g, plain_launchers(), stream);
+    g.epi.gate = -1;
+    g.epi.ids = ad->ids;
+    g.epi.n = ad->n; g.epi.r = ad->r; g.epi.rp = rank_pad(ad->r);
+    g.epi.up = (const float *)ad->up;
+    g.epi.S = S;
+    if (K % kPadK == 0) return gemm_padded_planes(g, adapter_launchers(), stream);
+    CHECK(gemm_padded_planes(g, plain_launchers(), stream));
+    LAUNCH(launch_expand(M, N, g.epi, C, ldc, stream));
+    return SGEMM_EMU_OK;
 }
 
 // ---------------------------------------------------------------- gated projection
@@ -513,14 +532,9 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
         }
         if (w.plan != nullptr) LAUNCH(launch_split_padded(N, K, (const float *)W, ldw, w.plan, false, s));
         if (w.x != nullptr) LAUNCH(launch_copy_padded(dtype, M, K, X, ldx, w.x, pad_k(K), s));
-        CHECK(gemm_padded_planes(product_f32(M, N, w.x != nullptr ? pad_k(K) : K,
-                                             w.x != nullptr ? (const float *)w.x : (const float *)X,
-                                             w.x != nullptr ? pad_k(K) : ldx,
-                                             w.plan != nullptr ? w.plan : (const uint16_t *)plan, (const float *)bias,
-                                             (float *)Y, ldy),
-                                 plain_launchers(), s));
-        if (low) LAUNCH(launch_expand(M, N, S, ad, (float *)Y, ldy, s));
-        return SGEMM_EMU_OK;
+        return adapted_f32(M, N, w.x != nullptr ? pad_k(K) : K, w.x != nullptr ? (const float *)w.x : (const float *)X,
+                           w.x != nullptr ? pad_k(K) : ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
+                           (const float *)bias, low ? &ad : nullptr, S, (float *)Y, ldy, s);
     }
     Bf16Gemm g{};
     g.M = M; g.N = N; g.K = bf16_k(K);
@@ -608,9 +622,12 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
         const bool lies = direct(dtype, dY, lddy, N);
         if (!lies && N > 0) LAUNCH(launch_copy_padded(dtype, M, N, dY, lddy, w.dy, pad_k(N), s));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(plain_f32(M, K, lies ? N : pad_k(N), lies ? (const float *)dY : (const float *)w.dy,
-                            lies ? lddy : pad_k(N), (const uint16_t *)plan_t, (float *)dX, lddx, num_cus, s));
-            if (low && N > 0) LAUNCH(launch_expand(M, K, w.p, back, (float *)dX, lddx, s));
+            if (N == 0)
+                LAUNCH(launch_zero(M, K, (float *)dX, lddx, nullptr, SGEMM_EMU_ACT_NONE, num_cus, s));
+            else
+                CHECK(adapted_f32(M, K, lies ? N : pad_k(N), lies ? (const float *)dY : (const float *)w.dy,
+                                  lies ? lddy : pad_k(N), (const uint16_t *)plan_t, nullptr, low ? &back : nullptr,
+                                  w.p, (float *)dX, lddx, s));
         } else {
             Bf16Gemm g{};
             g.M = M; g.N = K; g.K = bf16_k(N);
