@@ -128,7 +128,7 @@ def adapter_linear(x, weight, a, b, ids, scale=None, bias=None, plan=None):
         scale = torch.full(a.shape[:1], float(scale), dtype=torch.float32, device=a.device)
     try:
         fits = _fits(x, weight, a, b, ids, scale, bias)
-    except (AttributeError, IndexError, TypeError, ValueError):
+    except (AttributeError, IndexError, TypeError, ValueError, RuntimeError):   # RuntimeError: no device
         fits = False
     if not fits:
         _check(x, weight, a, b, ids, scale, bias)

@@ -221,9 +221,8 @@ hipError_t lay_out_wt(int dtype, int64_t F, int64_t K, const void *W, int64_t ld
 int check_adapters(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r)
 {
     if (!dtype_ok(dtype) || !extent_ok(M) || !extent_ok(N) || !extent_ok(K) || !extent_ok(r)) return SGEMM_EMU_EINVAL;
-    if (n < 0 || n > kMaxAdapters) return SGEMM_EMU_EINVAL;
-    if (n > 0 && r > 0 && ((K > 0 && r > kMaxBytes / n / K) || (N > 0 && r > kMaxBytes / n / N))) return SGEMM_EMU_EINVAL;
-    return SGEMM_EMU_OK;
+    // the banks' bytes then stay below 2^63
+    return n < 0 || n > kMaxAdapters ? SGEMM_EMU_EINVAL : SGEMM_EMU_OK;
 }
 
 // Few rows read W in one pass; low-rank activations to keep come from the tiles' path.

@@ -112,7 +112,7 @@ def gated_linear(x, weight, bias=None, gate="silu", plan=None):
         raise ValueError(f"unknown gate {gate!r} (one of {', '.join(GATES)})")
     try:
         fits = _fits(x, weight, bias)
-    except (AttributeError, IndexError, TypeError, ValueError):
+    except (AttributeError, IndexError, TypeError, ValueError, RuntimeError):   # RuntimeError: no device
         fits = False
     if not fits:
         _check(x, weight, bias)
