@@ -4,13 +4,13 @@
 // waves split K, and their sums are added through LDS in wave order.  With few
 // rows of X the weight passes once, and the time is its bytes' and the latency
 // of the loads.
-//   * Aligned operands go through LDS: steps of 512 bytes of every row are copied
+//   * Operands whose rows start at whole dwords go through LDS: steps of 512 bytes of every row are copied
 //     by buffer loads with LDS destination (two whole row pieces per
 //     instruction) into a ring, and each wave multiplies its 64-byte slice of the
 //     rows.  Loaded straight into the MFMA's fragments (16 rows x 64 bytes per
 //     instruction), a CU takes in about 20 bytes per ns whatever the loads in
 //     flight: 81 us for the shrink of 8192 x 4096 bfloat16 to rank 64.
-//   * Other operands are loaded element by element into the fragments.
+//   * Others (bfloat16 with odd rows) are loaded straight into the fragments.
 // FP32 operands take the FP32 matrix instruction (FP32 products, FP32 sums): a
 // lane's four consecutive k are the k of four instructions, the same for both
 // operands, so their order inside a step does not matter.
@@ -39,35 +39,33 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c)
     }
 }
 
-// B blocks of 16 rows of an operand: each block's descriptor and the offset of
-// this lane's row in it, or OUT_OF_RANGE for a row that reads zeros.
+// B blocks of 16 rows of an operand: where each block starts, and the offsets of
+// this lane's row in it as the copies take it and as the fragments do, or
+// OUT_OF_RANGE for a row that reads zeros.
 template <int B>
 struct Rows {
-    rsrc_t r[B];
-    uint32_t off[B];
+    const char *p[B];
+    uint32_t off[B], frag[B];
 };
 
-// The row of a block that a lane loads.
-template <bool ALIGNED>
-__device__ __forceinline__ int lane_row(int wave, int lane)
-{
-    return ALIGNED ? 2 * wave + (lane >> 5) : lane & 15;
-}
+// The row of a block that a lane copies.
+__device__ __forceinline__ int copy_row(int wave, int lane) { return 2 * wave + (lane >> 5); }
 
-// VEC elements of a row from k on, zeros from ke on, element by element.
+// VEC elements of a row from k on, zeros from ke on, at any element's address.
 template <class T>
-__device__ __forceinline__ u32x4_t load_k(rsrc_t r, uint32_t row, int64_t k, int64_t ke)
+__device__ __forceinline__ u32x4_t load_k(const char *p, uint32_t row, int64_t k, int64_t ke)
 {
     constexpr int V = Elem<T>::VEC;
-    const uint32_t off = row + (uint32_t)(k * (int64_t)sizeof(T));
-    const bool none = row == OUT_OF_RANGE;
+    const T *const src = (const T *)(p + row) + k;
     u32x4_t v = {0, 0, 0, 0};
+    if (row == OUT_OF_RANGE || k >= ke) return v;
+    if (k + V <= ke) return *reinterpret_cast<const u32x4_any *>(src);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const uint32_t o = none || k + e >= ke ? OUT_OF_RANGE : off + e * (uint32_t)sizeof(T);
-        if constexpr (sizeof(T) == 4) v[e] = bload_u32(r, o, 0);
-        else v[e >> 1] |= bload_u16(r, o, 0) << (16 * (e & 1));
-    }
+    for (int e = 0; e < V; ++e)
+        if (k + e < ke) {
+            if constexpr (sizeof(T) == 4) v[e] = __float_as_uint(src[e]);
+            else v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+        }
     return v;
 }
 
@@ -92,17 +90,17 @@ __device__ __forceinline__ void dot_tile(f32x4_t (&acc)[NB][MB], const Rows<NB> 
         // reads of 16 rows are on distinct banks
         typedef Ring<NB, MB> R;
         constexpr int KC = STEP_BYTES / (int)sizeof(T);
-        const int row = lane_row<true>(wave, lane), k_lane = ((lane & 31) ^ row) * V;
+        const int row = copy_row(wave, lane), k_lane = ((lane & 31) ^ row) * V;
         const int n = (int)((ke - kb + KC - 1) / KC);
         auto stage = [&](int t) {
             char *const buf = (char *)lds + (t % R::STAGES) * R::STAGE;
             const int64_t k = kb + (int64_t)t * KC + k_lane;
-            const bool in = k < ke;              // rows end at multiples of 16 bytes
+            const bool in = k + V <= ke;         // whole pieces only
             const uint32_t koff = (uint32_t)(k * (int64_t)sizeof(T));
 #pragma unroll
             for (int b = 0; b < R::BLOCKS; ++b) {
                 const uint32_t off = b < NB ? w.off[b < NB ? b : 0] : x.off[b < NB ? 0 : b - NB];
-                const rsrc_t r = b < NB ? w.r[b < NB ? b : 0] : x.r[b < NB ? 0 : b - NB];
+                const rsrc_t r = make_rsrc(b < NB ? w.p[b < NB ? b : 0] : x.p[b < NB ? 0 : b - NB], 0xFFFFFFF0ll);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t *)(buf + b * 16 * STEP_BYTES + wave * 1024), 16,
                                                          (int)(in && off != OUT_OF_RANGE ? off + koff : OUT_OF_RANGE),
                                                          0, 0, 0);
@@ -112,6 +110,19 @@ __device__ __forceinline__ void dot_tile(f32x4_t (&acc)[NB][MB], const Rows<NB> 
         const int slot = ((wave * 4 + (lane >> 4)) ^ (lane & 15)) * 16 + (lane & 15) * STEP_BYTES;
 #pragma unroll
         for (int t = 0; t < R::STAGES; ++t) stage(t);
+        const int64_t whole = ke - (ke - kb) % V;
+        if (whole < ke && wave == 0) {           // the elements behind the last whole piece
+            const int64_t k = whole + (lane >> 4) * V;
+            u32x4_t fw[NB], fx[MB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) fw[nb] = load_k<T>(w.p[nb], w.frag[nb], k, ke);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) fx[mb] = load_k<T>(x.p[mb], x.frag[mb], k, ke);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) acc[nb][mb] = mfma16<T>(fw[nb], fx[mb], acc[nb][mb]);
+        }
         for (int t = 0; t < n; ++t) {
             wait_vmem_at_most<(R::STAGES - 1) * R::BLOCKS>();   // step t has landed,
             lds_barrier();                                      // everybody's
@@ -137,9 +148,9 @@ __device__ __forceinline__ void dot_tile(f32x4_t (&acc)[NB][MB], const Rows<NB> 
             const int64_t k = k0 + (lane >> 4) * V;
             u32x4_t fw[NB], fx[MB];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) fw[nb] = load_k<T>(w.r[nb], w.off[nb], k, ke);
+            for (int nb = 0; nb < NB; ++nb) fw[nb] = load_k<T>(w.p[nb], w.frag[nb], k, ke);
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) fx[mb] = load_k<T>(x.r[mb], x.off[mb], k, ke);
+            for (int mb = 0; mb < MB; ++mb) fx[mb] = load_k<T>(x.p[mb], x.frag[mb], k, ke);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -178,17 +189,20 @@ __device__ __forceinline__ float get_sum(const float *lds, int n, int m)
     return v;
 }
 
-// Blocks b of rows r0 + 16 b + `row` of an operand of `rows` rows; rows past it
-// re-read the last one (their results are dropped).
+// Blocks b of rows r0 + 16 b .. of an operand of `rows` rows; rows past it re-read
+// the last one (their results are dropped).
 template <class T, int B>
-__device__ __forceinline__ Rows<B> rows_at(const T *p, int64_t ld, int64_t r0, int64_t rows, int row)
+__device__ __forceinline__ Rows<B> rows_at(const T *p, int64_t ld, int64_t r0, int64_t rows, int wave, int lane)
 {
     Rows<B> q;
-    const rsrc_t r = make_rsrc(p + r0 * ld, 0xFFFFFFF0ll);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-        q.r[b] = r;
-        q.off[b] = (uint32_t)((lmin(r0 + b * 16 + row, rows - 1) - r0) * ld * (int64_t)sizeof(T));
+        auto at = [&](int row) {
+            return (uint32_t)((lmin(r0 + b * 16 + row, rows - 1) - r0) * ld * (int64_t)sizeof(T));
+        };
+        q.p[b] = (const char *)(p + r0 * ld);
+        q.off[b] = at(copy_row(wave, lane));
+        q.frag[b] = at(lane & 15);
     }
     return q;
 }
@@ -203,15 +217,14 @@ __global__ __launch_bounds__(NT) void few_gated_kernel(FewRows a)
     constexpr int OUT = NB / 2 * 16;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * OUT, F = a.N;
-    const int row = lane_row<ALIGNED>(wave, lane);
-    Rows<NB> w = rows_at<T, NB>((const T *)a.W, a.ldw, n0, F, row);
-    const rsrc_t up = make_rsrc((const T *)a.W + (F + n0) * a.ldw, 0xFFFFFFF0ll);
+    Rows<NB> w = rows_at<T, NB>((const T *)a.W, a.ldw, n0, F, wave, lane);
 #pragma unroll
     for (int b = 0; b < NB / 2; ++b) {
-        w.r[NB / 2 + b] = up;
+        w.p[NB / 2 + b] = (const char *)((const T *)a.W + (F + n0) * a.ldw);
         w.off[NB / 2 + b] = w.off[b];
+        w.frag[NB / 2 + b] = w.frag[b];
     }
-    const Rows<MB> x = rows_at<T, MB>((const T *)a.X, a.ldx, 0, a.M, row);
+    const Rows<MB> x = rows_at<T, MB>((const T *)a.X, a.ldx, 0, a.M, wave, lane);
     f32x4_t acc[NB][MB];
     clear<NB, MB>(acc);
     dot_tile<T, NB, MB, ALIGNED>(acc, w, x, 0, a.K, lds, wave, lane);
@@ -271,13 +284,13 @@ __device__ __forceinline__ void shrink_row(const Tokens<T> &a, int block, float 
     }
     const uint32_t own = (uint32_t)(__ballot(id == me) & 0xFFFFu);
     if ((own & ((1u << mine) - 1u)) != 0) return;                    // an earlier row computes it
-    const int row = lane_row<ALIGNED>(wave, lane);
-    Rows<1> x = rows_at<T, 1>(a.X, a.ldx, m0, a.M, row);
-    if (!((own >> row) & 1u)) x.off[0] = OUT_OF_RANGE;
+    Rows<1> x = rows_at<T, 1>(a.X, a.ldx, m0, a.M, wave, lane);
+    if (!((own >> copy_row(wave, lane)) & 1u)) x.off[0] = OUT_OF_RANGE;
+    if (!((own >> (lane & 15)) & 1u)) x.frag[0] = OUT_OF_RANGE;
     const T *down = (const T *)a.ad.down + (int64_t)me * a.ad.r * a.K;
     const float scale = a.ad.scale != nullptr ? a.ad.scale[me] : 1.0f;
     for (int64_t r0 = 0; r0 < a.rp; r0 += 16) {
-        const Rows<1> w = rows_at<T, 1>(down, a.K, r0, a.ad.r, row);
+        const Rows<1> w = rows_at<T, 1>(down, a.K, r0, a.ad.r, wave, lane);
         f32x4_t acc[1][1];
         clear<1, 1>(acc);
         dot_tile<T, 1, 1, ALIGNED>(acc, w, x, 0, a.K, lds, wave, lane);
@@ -306,9 +319,8 @@ __global__ __launch_bounds__(NT) void tokens_kernel(Tokens<T> a)
     block -= a.shrink_blocks;
     const int64_t n0 = (int64_t)(block % a.n_blocks) * (16 * NB), slice = block / a.n_blocks;
     const int64_t kb = slice * a.k_per_slice, ke = lmin(kb + a.k_per_slice, a.K);
-    const int row = lane_row<ALIGNED>(wave, lane);
-    const Rows<NB> w = rows_at<T, NB>(a.W, a.ldw, n0, a.N, row);
-    const Rows<MB> x = rows_at<T, MB>(a.X, a.ldx, 0, a.M, row);
+    const Rows<NB> w = rows_at<T, NB>(a.W, a.ldw, n0, a.N, wave, lane);
+    const Rows<MB> x = rows_at<T, MB>(a.X, a.ldx, 0, a.M, wave, lane);
     f32x4_t acc[NB][MB];
     clear<NB, MB>(acc);
     dot_tile<T, NB, MB, ALIGNED>(acc, w, x, kb, ke, lds, wave, lane);
@@ -379,10 +391,11 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(Tokens<T> a, int slic
     H[m * ldh + f] = Elem<T>::store(gate_act<GATE>(g) * u);
 }
 
+// Rows that the copies to LDS take: they start at whole dwords.
 template <class T>
-bool rows_aligned(const void *p, int64_t ld, int64_t K)
+bool rows_copied(const void *p, int64_t ld)
 {
-    return K % Elem<T>::VEC == 0 && ld % Elem<T>::VEC == 0 && aligned(p, 16);
+    return ld * (int64_t)sizeof(T) % 4 == 0 && aligned(p, 4);
 }
 
 // K slices of a few-row product over n_blocks blocks of 32 weight rows: about
@@ -419,7 +432,7 @@ template <class T, int MB>
 void launch_tokens_mb(const Tokens<T> &t, int slices, hipStream_t stream)
 {
     const dim3 grid((unsigned)(t.shrink_blocks + t.n_blocks * slices)), block(NT);
-    if (rows_aligned<T>(t.W, t.ldw, t.K) && rows_aligned<T>(t.X, t.ldx, t.K) && rows_aligned<T>(t.ad.down, t.K, t.K))
+    if (rows_copied<T>(t.W, t.ldw) && rows_copied<T>(t.X, t.ldx) && (t.shrink_blocks == 0 || rows_copied<T>(t.ad.down, t.K)))
         hipLaunchKernelGGL((tokens_kernel<T, MB, true>), grid, block, 0, stream, t);
     else
         hipLaunchKernelGGL((tokens_kernel<T, MB, false>), grid, block, 0, stream, t);
@@ -438,7 +451,7 @@ void launch_few_gated_al(const FewRows &a, hipStream_t stream)
 {
     constexpr int OUT = NB / 2 * 16;
     const dim3 grid((unsigned)((a.N + OUT - 1) / OUT)), block(NT);
-    if (rows_aligned<T>(a.W, a.ldw, a.K) && rows_aligned<T>(a.X, a.ldx, a.K))
+    if (rows_copied<T>(a.W, a.ldw) && rows_copied<T>(a.X, a.ldx))
         hipLaunchKernelGGL((few_gated_kernel<T, NB, MB, GATE, true>), grid, block, 0, stream, a);
     else
         hipLaunchKernelGGL((few_gated_kernel<T, NB, MB, GATE, false>), grid, block, 0, stream, a);
@@ -537,8 +550,7 @@ __global__ __launch_bounds__(NT) void shrink_kernel(int64_t M, int64_t K, const 
         id = ad.ids[m0 + lane];
         if (id >= ad.n) id = -1;
     }
-    const int row = lane_row<AL>(wave, lane);
-    const Rows<MB> x = rows_at<T, MB>(X, ldx, m0, M, row);
+    const Rows<MB> x = rows_at<T, MB>(X, ldx, m0, M, wave, lane);
     uint64_t todo = __ballot(id >= 0);
     const uint64_t none = __ballot(id < 0 && lane < ROWS && m0 + lane < M);
     if (none != 0)
@@ -551,7 +563,7 @@ __global__ __launch_bounds__(NT) void shrink_kernel(int64_t M, int64_t K, const 
         const T *down = (const T *)ad.down + (int64_t)me * ad.r * K;
         const float scale = ad.scale != nullptr ? ad.scale[me] : 1.0f;
         for (int64_t r0 = 0; r0 < rp; r0 += 16 * NB) {
-            const Rows<NB> w = rows_at<T, NB>(down, K, r0, ad.r, row);
+            const Rows<NB> w = rows_at<T, NB>(down, K, r0, ad.r, wave, lane);
             f32x4_t acc[NB][MB];
             clear<NB, MB>(acc);
             dot_tile<T, NB, MB, AL>(acc, w, x, 0, K, lds, wave, lane);
@@ -571,7 +583,7 @@ template <class T, int NB, int MB>
 void launch_shrink_mb(int64_t M, int64_t K, const T *X, int64_t ldx, const Adapters &ad, float *S, hipStream_t stream)
 {
     const dim3 grid((unsigned)((M + 16 * MB - 1) / (16 * MB)));
-    if (rows_aligned<T>(X, ldx, K) && aligned(ad.down, 16))
+    if (rows_copied<T>(X, ldx) && rows_copied<T>(ad.down, K))
         hipLaunchKernelGGL((shrink_kernel<T, NB, MB, true>), grid, dim3(NT), 0, stream, M, K, X, ldx, ad, S,
                            rank_pad(ad.r));
     else
