@@ -595,7 +595,16 @@ template <class T, int NB>
 void launch_shrink_nb(int64_t M, int64_t K, const T *X, int64_t ldx, const Adapters &ad, float *S, int num_cus,
                       hipStream_t stream)
 {
-    if (M <= (int64_t)32 * num_cus) launch_shrink_mb<T, NB, 1>(M, K, X, ldx, ad, S, stream);
+    // 16 rows per workgroup while that leaves at most two for a CU, else 32: with 32,
+    // 8192 x 4096 bfloat16 to rank 16 took 24 us instead of 20.  From rank 33 on the
+    // copies of `down` decide, NB + MB blocks of rows for each workgroup that a CU
+    // runs: 37 us against 43 for rank 64 (float32: 91 against 103).
+    auto taken = [&](int64_t mb) {
+        const int64_t groups = (M + 16 * mb - 1) / (16 * mb);
+        return (groups + num_cus - 1) / num_cus * (NB + mb);
+    };
+    const bool one = NB < 4 ? M <= (int64_t)32 * num_cus : taken(1) <= taken(2);
+    if (one) launch_shrink_mb<T, NB, 1>(M, K, X, ldx, ad, S, stream);
     else launch_shrink_mb<T, NB, 2>(M, K, X, ldx, ad, S, stream);
 }
 
