@@ -32,16 +32,16 @@ MI355X_FP32_VECTOR_TFLOPS = 157.3
 MI355X_HBM_GBS = 8000.0
 METRIC = "BF16x9 SGEMM effective FP32 TFLOP/s (2MNK/t) and % of bf16 MFMA peak"
 HERE = os.path.dirname(os.path.abspath(__file__))
-GEMM_SOURCE = os.path.join(HERE, "fp32_emulated_gemm_amd", "csrc", "gemm.hip")
+GEMM_SOURCE = os.path.join(HERE, "fp32_emulated_gemm_amd", "csrc", "gemm_kernels.hpp")
 
 # HBM traffic of the timed GEMM kernel per launch ([X@W1, H@W2], bytes), from two
 # rocprofv3 --pmc runs of `python3 bench.py --traffic-probe` (FETCH_SIZE, then
 # WRITE_SIZE, KiB per dispatch), each scaled by what the same counter reads for
 # the probe's cold 2 GiB device copy (FETCH_SIZE reads half the copied bytes:
 # x2.0; WRITE_SIZE reads all of them: x1.0).  The figures belong to the kernel
-# source they were taken on; once gemm.hip has changed, roofline.traffic is null.
-GEMM_TRAFFIC = {"gemm_hip_sha256": "75195d81894525a370e411dd08d3e74a307f23e645ba9ed56e41630d4769eaeb",
-                "bytes_per_launch": [2843925792, 3264026398]}
+# source they were taken on; once gemm_kernels.hpp has changed, roofline.traffic is null.
+GEMM_TRAFFIC = {"gemm_kernels_sha256": "a735b47f70183a24203440c5ac83efcfe0888779c0b5f7517b325c882c5972a7",
+                "bytes_per_launch": [2843928053, 3264037753]}
 
 # MFMA activity of the same launches, from one rocprofv3 --pmc run of the same
 # probe (SQ_VALU_MFMA_BUSY_CYCLES SQ_INSTS_MFMA SQ_BUSY_CYCLES GRBM_GUI_ACTIVE).
@@ -50,9 +50,9 @@ GEMM_TRAFFIC = {"gemm_hip_sha256": "75195d81894525a370e411dd08d3e74a307f23e645ba
 # (one 32x32x16 BF16 MFMA keeps it busy 32 cycles).  GRBM_GUI_ACTIVE per XCD
 # divided by the kernel's own time in this run gives the shader clock the chip
 # held under the load; roofline.frac = busy x clock / 2.4 GHz.
-GEMM_MFMA_PMC = {"gemm_hip_sha256": GEMM_TRAFFIC["gemm_hip_sha256"],
-                 "mfma_busy": [0.6544, 0.7188],
-                 "active_cycles_per_xcd": [3815687, 3465315]}
+GEMM_MFMA_PMC = {"gemm_kernels_sha256": GEMM_TRAFFIC["gemm_kernels_sha256"],
+                 "mfma_busy": [0.6610, 0.7240],
+                 "active_cycles_per_xcd": [3777372, 3439794]}
 
 
 def log(msg):
@@ -212,11 +212,11 @@ def main():
     # bytes each GEMM must move at least: A (FP32) + three BF16 planes of B + C (FP32)
     algo_bytes = [4 * M * D + 6 * D * F + 4 * M * F, 4 * M * F + 6 * F * D + 4 * M * D]
     traffic_per_launch = None
-    if GEMM_TRAFFIC["gemm_hip_sha256"] == source_sha256(GEMM_SOURCE):
+    if GEMM_TRAFFIC["gemm_kernels_sha256"] == source_sha256(GEMM_SOURCE):
         traffic_per_launch = GEMM_TRAFFIC["bytes_per_launch"]
     traffic = None if traffic_per_launch is None else sum(traffic_per_launch) / len(traffic_per_launch)
     mfma_busy = sclk = None
-    if GEMM_MFMA_PMC["gemm_hip_sha256"] == source_sha256(GEMM_SOURCE):
+    if GEMM_MFMA_PMC["gemm_kernels_sha256"] == source_sha256(GEMM_SOURCE):
         mfma_busy = GEMM_MFMA_PMC["mfma_busy"]
         sclk = [round(c / (t * 1e-3) / 1e9, 3) for c, t in zip(GEMM_MFMA_PMC["active_cycles_per_xcd"], (g1_ms, g2_ms))]
 
