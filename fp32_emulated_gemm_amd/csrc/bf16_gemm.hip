@@ -24,6 +24,11 @@
 // blocks of 16, which puts act(gate) and up of one output into one lane, and
 // the adapters' part selects its rows per lane.
 // The result goes through LDS (the ring's space) and leaves in 128-bit stores.
+//
+// Bound by the matrix cores at the power limit: 8192 x 4096 -> 2 x 8192 gated 816-830
+// us, 1.34 PFLOP/s (the platform's library 1.34 on the plain product); 8192 x 4096 x
+// 4096 with adapters of rank 16 230 us, 1.19, of which about 13 us are the start and
+// the end of a tile.
 #include "ops_device.hpp"
 #include "ops.hpp"
 

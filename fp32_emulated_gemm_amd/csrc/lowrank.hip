@@ -10,7 +10,8 @@
 //     rows.  Loaded straight into the MFMA's fragments (16 rows x 64 bytes per
 //     instruction), a CU takes in about 20 bytes per ns whatever the loads in
 //     flight: 81 us for the shrink of 8192 x 4096 bfloat16 to rank 64.
-//   * Others (bfloat16 with odd rows) are loaded straight into the fragments.
+//   * Others (bfloat16 with odd rows) are loaded straight into the fragments: 40 us
+//     for 48 x 1271 -> 2 x 8024 gated, 19 us with K = 1270.
 // FP32 operands take the FP32 matrix instruction (FP32 products, FP32 sums): a
 // lane's four consecutive k are the k of four instructions, the same for both
 // operands, so their order inside a step does not matter.
@@ -209,7 +210,10 @@ __device__ __forceinline__ Rows<B> rows_at(const T *p, int64_t ld, int64_t r0, i
 
 // ---------------------------------------------------------------- gated, one pass
 // NB / 2 blocks of 16 gate rows, then the NB / 2 blocks of up rows of the same
-// outputs; the whole K in one workgroup.
+// outputs; the whole K in one workgroup, so that the gate runs on the sums before
+// they leave.  Bound by the weight's bytes: bfloat16 4096 -> 2 x 8192 (134 MB) 34 us
+// for 1 row (3.9 TB/s), 41 for 64, whose X every workgroup copies beside its rows
+// of W; float32 1 x 1024 -> 2 x 4096 (34 MB) 6 us.
 template <class T, int NB, int MB, int GATE, bool ALIGNED>
 __global__ __launch_bounds__(NT) void few_gated_kernel(FewRows a)
 {
@@ -246,7 +250,11 @@ __global__ __launch_bounds__(NT) void few_gated_kernel(FewRows a)
 
 // ---------------------------------------------------------------- K slices
 // partials[slice][m][n] of X W^T, 32 rows of W per workgroup, beside the
-// shrink's workgroups (they come first; nothing here depends on them).
+// shrink's workgroups (they come first; nothing here depends on them).  Sliced
+// because 32 rows a workgroup leave CUs idle otherwise; the gated product with
+// few outputs comes here too.  64 rows of 64 adapters of rank 16 on bfloat16 4096 x
+// 4096 (50 MB): 22 us, and 4 for the finish; 16 rows, float32 1024 x 1024: 7 and 5,
+// the latency of two launches.
 template <class T>
 struct Tokens {
     int64_t M, N, K;
@@ -509,7 +517,8 @@ hipError_t launch_few_rows_t(const FewRows &a, int num_cus, hipStream_t stream)
 // adapters that occur in them, in order of their first row: each pass multiplies
 // all the tile's rows by that adapter's r rows and keeps the rows that belong to
 // it.  Rows of one request are neighbours, so a tile of a prompt holds one or
-// two adapters.  FP32 keeps S as floats; bfloat16 as two BF16 parts (rp high
+// two adapters.  Bound by what a CU takes in, X's rows and `down`'s: bfloat16 8192 x
+// 4096 to rank 16 19 us (X alone at the copy rate 13), to rank 64 37.  FP32 keeps S as floats; bfloat16 as two BF16 parts (rp high
 // parts, then rp low parts per row, 16 significant bits), which is how the GEMM
 // epilogue multiplies it.
 template <class T>
@@ -619,11 +628,11 @@ hipError_t launch_shrink_t(int64_t M, int64_t K, const T *X, int64_t ldx, const 
 }
 
 // ---------------------------------------------------------------- expand (FP32)
-// Y[t] += up[i] S[t], one pass over Y: 12 us of 6144 x 1024, 4.2 TB/s.  A wave takes 32 rows x 64 columns: its part of Y is the
-// accumulator of FP32 MFMAs over the rank, for one adapter of its rows after
-// another (in order of their first row); a row keeps its old value unless it
-// belongs to the adapter, so Inf and NaN in one adapter's weights never reach
-// another's rows.
+// Y[t] += up[i] S[t], one pass over Y: 12 us of 6144 x 1024, 4.2 TB/s.  A wave
+// takes 32 rows x 64 columns: its part of Y is the accumulator of FP32 MFMAs over
+// the rank, for one adapter of its rows after another (in order of their first
+// row); a row keeps its old value unless it belongs to the adapter, so Inf and NaN
+// in one adapter's weights never reach another's rows.
 __global__ __launch_bounds__(256) void expand_kernel(int64_t M, int64_t N, GemmEpilogue ad, float *Y,
                                                      int64_t ldy)
 {
@@ -698,6 +707,11 @@ __global__ __launch_bounds__(256) void expand_kernel(int64_t M, int64_t N, GemmE
 // a piece's slot is its own), and a second kernel adds each adapter's slots in
 // order.  t is the k of an FP32 MFMA, so both operands are read as they lie:
 // rows of R 128 bits per lane, a lane's elements going to as many instructions.
+// 8192 rows, both factors of bfloat16 4096 x 4096 at rank 16 (134 MB): 54 us and 7 for
+// the second kernel, 2.5 TB/s; float32 6144 rows, 256 and 1024 columns: 11 and 6.
+// Tried and slower: the next group's loads issued a step ahead (58 us, 15 in float32);
+// waves side by side along the columns without the sum through LDS (48, but
+// 10 for the second kernel's larger partials; float32 17 and 10).
 constexpr int GRAD_WAVES = 4;
 
 template <class T>
