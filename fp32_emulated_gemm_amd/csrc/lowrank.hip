@@ -74,7 +74,7 @@ constexpr int STEP_BYTES = 512;                  // of a row, per step
 template <int NB, int MB>
 struct Ring {
     static constexpr int BLOCKS = NB + MB, STAGE = BLOCKS * 16 * STEP_BYTES;   // bytes
-    static constexpr int STAGES = BLOCKS <= 3 ? 4 : BLOCKS <= 6 ? 3 : 2;
+    static constexpr int STAGES = BLOCKS <= 2 ? 4 : BLOCKS == 3 || BLOCKS == 6 ? 3 : 2;
     static constexpr int SUMS = WAVES * NB * MB * 1024;
     static constexpr int BYTES = STAGES * STAGE > SUMS ? STAGES * STAGE : SUMS;
 };
@@ -249,9 +249,9 @@ __global__ __launch_bounds__(NT) void few_gated_kernel(FewRows a)
 }
 
 // ---------------------------------------------------------------- K slices
-// partials[slice][m][n] of X W^T, 32 rows of W per workgroup, beside the
+// partials[slice][m][n] of X W^T, 32 or 64 rows of W per workgroup, beside the
 // shrink's workgroups (they come first; nothing here depends on them).  Sliced
-// because 32 rows a workgroup leave CUs idle otherwise; the gated product with
+// because so few rows a workgroup leave CUs idle otherwise; the gated product with
 // few outputs comes here too.  64 rows of 64 adapters of rank 16 on bfloat16 4096 x
 // 4096 (50 MB): 22 us, and 4 for the finish; 16 rows, float32 1024 x 1024: 7 and 5,
 // the latency of two launches.
@@ -316,7 +316,7 @@ __device__ __forceinline__ void shrink_row(const Tokens<T> &a, int block, float 
 template <class T, int MB, bool ALIGNED>
 __global__ __launch_bounds__(NT) void tokens_kernel(Tokens<T> a)
 {
-    constexpr int NB = 2;
+    constexpr int NB = MB > 2 ? 4 : 2;           // token_rows
     __shared__ __attribute__((aligned(16))) float lds[Ring<NB, MB>::BYTES / 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int block = (int)blockIdx.x;
@@ -406,15 +406,23 @@ bool rows_copied(const void *p, int64_t ld)
     return ld * (int64_t)sizeof(T) % 4 == 0 && aligned(p, 4);
 }
 
-// K slices of a few-row product over n_blocks blocks of 32 weight rows: about
-// two workgroups per CU, each with a step or more for every wave.
-int token_slices(int dtype, int64_t N, int64_t K, int num_cus)
+// Rows of W per workgroup of a K-sliced product of M rows, and its K slices beside
+// `others` workgroups of the launch, each with a step or more for every wave.  Up
+// to 32 rows of X two workgroups fit a CU; with more, W and X take as many rows
+// and one workgroup fills its LDS, so the launch should be one round of them
+// (64 rows, 64 adapters of rank 16, bfloat16 4096 x 4096: 19 us; as two rounds of
+// 32 rows of W 25).
+int64_t token_rows(int64_t M) { return M > 32 ? 64 : 32; }
+int token_slices(int dtype, int64_t M, int64_t N, int64_t K, int64_t others, int num_cus)
 {
-    const int64_t blocks = (N + 31) / 32, least = WAVES * (dtype == kF32 ? 16 : 32);
-    int64_t s = 2 * (int64_t)num_cus / (blocks > 0 ? blocks : 1);
+    const int64_t blocks = (N + token_rows(M) - 1) / token_rows(M), least = WAVES * (dtype == kF32 ? 16 : 32);
+    int64_t s = ((M > 32 ? 1 : 2) * (int64_t)num_cus - others) / (blocks > 0 ? blocks : 1);
     if (s > K / least) s = K / least;
     return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
+
+// Workgroups of the shrink beside a few-row product.
+int64_t shrink_rows(const FewRows &a) { return a.ad != nullptr ? round_up(a.M, 16) : 0; }
 
 template <class T>
 Tokens<T> make_tokens(const FewRows &a, int64_t N, int slices)
@@ -426,12 +434,12 @@ Tokens<T> make_tokens(const FewRows &a, int64_t N, int slices)
     t.partials = a.partials;
     // slices begin at whole 128-byte pairs of steps
     t.k_per_slice = round_up((a.K + slices - 1) / slices, 8 * Elem<T>::VEC);
-    t.n_blocks = (int)((N + 31) / 32);
+    t.n_blocks = (int)((N + token_rows(a.M) - 1) / token_rows(a.M));
     if (a.ad != nullptr) {
         t.ad = *a.ad;
         t.S = a.S;
         t.rp = rank_pad(a.ad->r);
-        t.shrink_blocks = (int)((a.M + 15) / 16 * 16);
+        t.shrink_blocks = (int)shrink_rows(a);
     }
     return t;
 }
@@ -469,7 +477,7 @@ template <class T, int GATE>
 void launch_few_gated(const FewRows &a, int num_cus, hipStream_t stream)
 {
     if (a.partials != nullptr) {
-        const int slices = token_slices(sizeof(T) == 4 ? kF32 : kBF16, 2 * a.N, a.K, num_cus);
+        const int slices = token_slices(sizeof(T) == 4 ? kF32 : kBF16, a.M, 2 * a.N, a.K, 0, num_cus);
         const Tokens<T> t = make_tokens<T>(a, 2 * a.N, slices);
         launch_tokens<T>(t, slices, stream);
         hipLaunchKernelGGL((gated_finish_kernel<T, GATE>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256),
@@ -502,7 +510,7 @@ hipError_t launch_few_rows_t(const FewRows &a, int num_cus, hipStream_t stream)
     case kSigmoid: launch_few_gated<T, kSigmoid>(a, num_cus, stream); break;
     case kRelu: launch_few_gated<T, kRelu>(a, num_cus, stream); break;
     default: {
-        const int slices = token_slices(sizeof(T) == 4 ? kF32 : kBF16, a.N, a.K, num_cus);
+        const int slices = token_slices(sizeof(T) == 4 ? kF32 : kBF16, a.M, a.N, a.K, shrink_rows(a), num_cus);
         const Tokens<T> t = make_tokens<T>(a, a.N, slices);
         launch_tokens<T>(t, slices, stream);
         hipLaunchKernelGGL((tokens_finish_kernel<T>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256), 0,
@@ -895,10 +903,11 @@ hipError_t launch_lowrank_grad_t(const LowrankGrads &q, int num_cus, hipStream_t
 
 int64_t few_rows_partial_floats(int dtype, int64_t M, int64_t N, int64_t K, int gate, int num_cus)
 {
-    if (gate < 0) return token_slices(dtype, N, K, num_cus) * M * N;
+    // without adapters there are at least as many slices
+    if (gate < 0) return token_slices(dtype, M, N, K, 0, num_cus) * M * N;
     // a gated product with enough outputs for a workgroup per CU runs in one pass
     if (N >= (int64_t)16 * num_cus) return 0;
-    const int s = token_slices(dtype, 2 * N, K, num_cus);
+    const int s = token_slices(dtype, M, 2 * N, K, 0, num_cus);
     return s > 1 ? s * M * 2 * N : 0;
 }
 
