@@ -253,7 +253,7 @@ __global__ __launch_bounds__(NT) void few_gated_kernel(FewRows a)
 // shrink's workgroups (they come first; nothing here depends on them).  Sliced
 // because so few rows a workgroup leave CUs idle otherwise; the gated product with
 // few outputs comes here too.  64 rows of 64 adapters of rank 16 on bfloat16 4096 x
-// 4096 (50 MB): 22 us, and 4 for the finish; 16 rows, float32 1024 x 1024: 7 and 5,
+// 4096 (50 MB): 15 us, and 4 for the finish; 16 rows, float32 1024 x 1024: 6 and 5,
 // the latency of two launches.
 template <class T>
 struct Tokens {
