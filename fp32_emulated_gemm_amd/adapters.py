@@ -134,7 +134,7 @@ def adapter_linear(x, weight, a, b, ids, scale=None, bias=None, plan=None):
         _check(x, weight, a, b, ids, scale, bias)
     dims, K, N = x.dim(), x.shape[-1], weight.shape[0]
     if plan is not None:
-        plan.check(weight)
+        plan.check(weight, gated=False)
     x2d = x if dims == 2 else x.reshape(-1, K) if K else x.new_empty(x.shape[:-1].numel(), 0)
     if ids.dim() != 1:
         ids = ids.reshape(-1)

@@ -119,7 +119,7 @@ def gated_linear(x, weight, bias=None, gate="silu", plan=None):
     dims, K, rows = x.dim(), x.shape[-1], weight.shape[0]
     x2d = x if dims == 2 else x.reshape(-1, K) if K else x.new_empty(x.shape[:-1].numel(), 0)
     if plan is not None:
-        plan.check(weight)
+        plan.check(weight, gated=True)
     ops_lib()
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad
                                     or (bias is not None and bias.requires_grad)):

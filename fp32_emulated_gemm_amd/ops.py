@@ -135,9 +135,10 @@ def stream_of(device_index):
 class WeightPlan:
     """A weight laid out for the products (sgemm_emu_plan_weight): `forward` holds W (None where a
     bfloat16 weight is read as it lies), `backward` W^T (None unless asked for).  It holds the
-    values of the weight at the time: lay a changed weight out again."""
+    values of the weight at the time: lay a changed weight out again.  `gated`: laid out for
+    gated_linear (gate and up rows alternate), else for adapter_linear."""
 
-    __slots__ = ("dtype", "shape", "device", "forward", "backward")
+    __slots__ = ("dtype", "shape", "device", "gated", "forward", "backward")
 
     def __init__(self, weight, gated=False, forward=True, backward=False):
         w = weight.detach()
@@ -145,7 +146,7 @@ class WeightPlan:
             raise TypeError(f"weight: expected dtype float32 or bfloat16, got {w.dtype}")
         check_tensor(w, "weight", w.dtype, (None, None))
         w, ld = rows_of(w)
-        self.dtype, self.shape, self.device = w.dtype, tuple(w.shape), w.device
+        self.dtype, self.shape, self.device, self.gated = w.dtype, tuple(w.shape), w.device, gated
         # a bfloat16 weight with 16-byte aligned rows needs no layout for the forward product
         lies = w.dtype == torch.bfloat16 and w.shape[1] % 8 == 0 and ld % 8 == 0 and w.data_ptr() % 16 == 0
         rows = SGEMM_EMU_PLAN_GATED if gated else SGEMM_EMU_PLAN_ROWS
@@ -162,7 +163,12 @@ class WeightPlan:
            "sgemm_emu_plan_weight")
         return plan
 
-    def check(self, weight):
+    def check(self, weight, gated):
+        """Raises where this is no layout of such a weight for gated_linear (gated) or adapter_linear.
+        The two differ in the order of W's rows, so one never stands in for the other."""
+        if self.gated != gated:
+            mine, other = ("gated", "adapters") if gated else ("adapters", "gated")
+            raise ValueError(f"plan: laid out by {other}.plan_weight, expected one of {mine}.plan_weight")
         if self.dtype != weight.dtype or self.shape != tuple(weight.shape) or self.device != weight.device:
             raise ValueError(f"plan: laid out for a {self.dtype} weight of shape {self.shape} on {self.device}, got "
                              f"{weight.dtype} {tuple(weight.shape)} on {weight.device}")
