@@ -32,6 +32,8 @@ OPS_EXPORTS = ("sgemm_emu_plan_bytes", "sgemm_emu_plan_weight", "sgemm_emu_gated
                "sgemm_emu_adapter_linear_backward_workspace", "sgemm_emu_adapter_linear_backward",
                "sgemm_emu_few_rows")
 
+MAX_LD = 8388544   # leading dimensions that the library takes
+
 _OPS = None
 FEW_ROWS = None   # sgemm_emu_few_rows(), set when the library is first used
 
@@ -89,13 +91,15 @@ def check_tensor(t, name, dtype, shape):
 
 def rows_of(t):
     """A 2-D tensor whose rows lie one after another with unit stride along columns (itself, or a
-    contiguous copy of a transposed, expanded or overlapping one), and its leading dimension."""
+    contiguous copy of a transposed, expanded or overlapping one, or of one whose rows lie further
+    apart than the library takes), and its leading dimension.  The stride of a single row means
+    nothing."""
     rows, cols = t.shape
     ld, step = t.stride()
-    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+    if (cols > 1 and step != 1) or (rows > 1 and not cols <= ld <= MAX_LD):
         t = t.contiguous()
         ld = cols
-    return t, ld if ld >= cols and ld > 0 else max(cols, 1)
+    return t, ld if rows > 1 and ld > 0 else max(cols, 1)
 
 
 def scratch(nbytes, like):

@@ -1,4 +1,5 @@
-"""Arguments of the operators' tensor functions on the GPU: layouts of a weight."""
+"""Arguments of the operators' tensor functions on the GPU: layouts of a weight, rows far
+apart."""
 import pytest
 import torch
 
@@ -29,3 +30,38 @@ def test_a_plan_of_the_other_operator_is_refused(dtype, M, K):
         y = adapters.adapter_linear(c["x"], c["w"], c["a"], c["b"], ids.cuda(), c["scale"], c["bias"],
                                     plan=adapters.plan_weight(c["w"], backward=backward))
         ref.check(y, ref.adapter(t["x"], t["w"], t["a"], t["b"], ids, t["scale"], t["bias"])["y"], "Y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_last_tokens_of_long_prompts(dtype):
+    """One row, or several, of a buffer whose sequences lie further apart than a leading dimension
+    may: inputs, weights and output gradients alike."""
+    from fp32_emulated_gemm_amd.adapters import adapter_linear
+    from fp32_emulated_gemm_amd.gated import gated_linear
+    K, F, step = 64, 16, 8_388_544 + 64
+    for M in (1, 2, 3):
+        x, w, b, dh = gated_inputs(dtype, M, K, F, True, seed=M)
+        hidden = torch.zeros(M, step // K, K, dtype=x.dtype, device="cuda")
+        xs = hidden[:, -1]
+        xs.copy_(x)
+        grads = torch.zeros(M, step, dtype=x.dtype, device="cuda")[:, 8:8 + F]
+        grads.copy_(dh)
+        want = ref.gated(x, w, b, "silu", dh)
+        ref.check(gated_linear(xs, w.cuda(), b.cuda()), want["h"], "H")
+        leaf = xs.detach().requires_grad_(True)
+        dx, = torch.autograd.grad(gated_linear(leaf, w.cuda(), b.cuda()), (leaf,), grads)
+        ref.check(dx, want["dx"], "dx")
+        t = adapter_inputs(dtype, M, K, F, 2, 4, seed=M)
+        c = {k: _cuda(v) for k, v in t.items()}
+        ids = torch.arange(M, dtype=torch.int32) % 2
+        xs.copy_(t["x"])
+        grads.copy_(t["dy"])
+        want = ref.adapter(t["x"], t["w"], t["a"], t["b"], ids, t["scale"], t["bias"], t["dy"])
+        leaf = xs.detach().requires_grad_(True)
+        y = adapter_linear(leaf, c["w"], c["a"], c["b"], ids.cuda(), c["scale"], c["bias"])
+        ref.check(y.detach(), want["y"], "Y")
+        ref.check(torch.autograd.grad(y, (leaf,), grads)[0], want["dx"], "dx")
+        wide = torch.zeros(F, step, dtype=x.dtype, device="cuda")[:, :K]
+        wide.copy_(t["w"])
+        y = adapter_linear(xs, wide, c["a"], c["b"], ids.cuda(), c["scale"], c["bias"])
+        ref.check(y, want["y"], "Y, rows of W far apart")

@@ -18,3 +18,25 @@ def test_a_plan_stands_for_its_own_operator_only(held):
             plan.check(w, gated=not gated)
         with pytest.raises(ValueError):
             plan.check(w[:4], gated=gated)
+
+
+@pytest.mark.parametrize("rows,cols,stride,copied", [
+    (1, 16, (8_392_704, 1), False),      # the last token of a long prompt: one row, whatever its stride
+    (1, 16, (0, 1), False), (1, 16, (3, 1), False), (1, 1, (1, 5), False), (1, 16, (16, 2), True),
+    (3, 16, (8_392_704, 1), True), (3, 16, (8_388_544, 1), False), (3, 16, (8_388_545, 1), True),
+    (3, 16, (16, 1), False), (3, 16, (24, 1), False), (3, 16, (0, 1), True), (3, 16, (8, 1), True),
+    (3, 16, (1, 3), True), (3, 1, (1, 1), False), (3, 1, (7, 9), False), (0, 16, (16, 1), False),
+    (3, 0, (1, 1), False), (0, 0, (1, 1), False)])
+def test_rows_of_any_stride(rows, cols, stride, copied):
+    """Rows come with a leading dimension that the library takes, and keep their values."""
+    from fp32_emulated_gemm_amd.ops import rows_of
+    need = 1 + sum((n - 1) * s for n, s in zip((rows, cols), stride)) if rows and cols else 0
+    base = torch.arange(need, dtype=torch.int32)
+    t = torch.as_strided(base, (rows, cols), stride)
+    got, ld = rows_of(t)
+    assert (got is not t) == copied
+    assert max(cols, 1) <= ld <= 8_388_544
+    assert got.shape == t.shape and torch.equal(got, t)
+    if rows and cols:
+        again = torch.as_strided(got, (rows, cols), (ld, 1)) if cols > 1 or rows > 1 else got
+        assert torch.equal(again, t)
