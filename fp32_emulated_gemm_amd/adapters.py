@@ -11,7 +11,8 @@ gradients are deterministic.
 import torch
 
 from . import ops
-from .ops import DTYPES, WeightPlan, addr, check_tensor, few_bytes, ok, ops_lib, rows_of, scratch, stream_of
+from .ops import (DTYPES, FixedWeight, WeightPlan, addr, check_tensor, few_bytes, ok, ops_lib, rows_of, scratch,
+                  stream_of)
 
 
 def plan_weight(weight, backward=False):
@@ -153,7 +154,9 @@ def adapter_linear(x, weight, a, b, ids, scale=None, bias=None, plan=None):
 
 class AdapterLinear(torch.nn.Module):
     """A fixed linear layer with `adapters` trainable low-rank adapters of rank `rank`:
-    forward(x, ids).  `up` starts at zero, so a new adapter changes nothing."""
+    forward(x, ids).  `up` starts at zero, so a new adapter changes nothing.  Every call reads the
+    weight as it is; `plan` (plan_weight(m.weight, backward=True)) spares laying it out where the
+    caller knows that it does not change."""
 
     def __init__(self, in_features, out_features, adapters, rank, alpha=None, bias=True, device=None, dtype=None):
         super().__init__()
@@ -169,7 +172,7 @@ class AdapterLinear(torch.nn.Module):
         bound = in_features ** -0.5 if in_features else 0.0
         torch.nn.init.uniform_(self.weight, -bound, bound)
         torch.nn.init.uniform_(self.down, -bound, bound)
-        self._plan = None
+        self._fixed = None
 
     @classmethod
     def from_linear(cls, layer, adapters, rank, alpha=None):
@@ -183,16 +186,14 @@ class AdapterLinear(torch.nn.Module):
         return m.fix_weights()
 
     def fix_weights(self):
-        """Lay the weight out (after it was loaded or changed)."""
-        self._plan = (plan_weight(self.weight, backward=True), self.weight._version)
+        """Take the weight as it is for the fixed one: calls raise once it has changed, until this is
+        called again."""
+        self._fixed = FixedWeight(self.weight)
         return self
 
-    def forward(self, x, ids):
-        plan = None
-        if self._plan is not None:
-            plan, version = self._plan
-            if version != self.weight._version or plan.device != self.weight.device:
-                raise RuntimeError("the weight changed after fix_weights(); call it again")
+    def forward(self, x, ids, plan=None):
+        if self._fixed is not None:
+            self._fixed.check(self.weight)
         return adapter_linear(x, self.weight, self.down, self.up, ids, self.scale, self.bias, plan)
 
     def extra_repr(self):

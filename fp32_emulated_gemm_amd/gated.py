@@ -12,7 +12,8 @@ import torch
 
 from . import ops
 from .linear import Linear
-from .ops import DTYPES, GATES, WeightPlan, addr, check_tensor, few_bytes, ok, ops_lib, rows_of, scratch, stream_of
+from .ops import (DTYPES, GATES, FixedWeight, WeightPlan, addr, check_tensor, few_bytes, ok, ops_lib, rows_of, scratch,
+                  stream_of)
 
 
 def plan_weight(weight):
@@ -132,7 +133,9 @@ def gated_linear(x, weight, bias=None, gate="silu", plan=None):
 
 class GatedLinear(torch.nn.Module):
     """gated_linear as a module: `weight` [2 out_features, in_features] (gate rows, then up rows) and
-    `bias` [2 out_features], trainable.  fix_weights() freezes them and keeps their layout."""
+    `bias` [2 out_features], trainable.  fix_weights() freezes them.  Every call reads the weight as it
+    is; `plan` (plan_weight(m.weight)) spares laying it out where the caller knows that it does not
+    change."""
 
     def __init__(self, in_features, out_features, bias=True, gate="silu", device=None, dtype=None):
         super().__init__()
@@ -141,7 +144,7 @@ class GatedLinear(torch.nn.Module):
         self.in_features, self.out_features, self.gate = in_features, out_features, gate
         self.weight = torch.nn.Parameter(torch.empty((2 * out_features, in_features), device=device, dtype=dtype))
         self.bias = torch.nn.Parameter(torch.zeros(2 * out_features, device=device, dtype=dtype)) if bias else None
-        self._plan = None
+        self._fixed = None
         bound = in_features ** -0.5 if in_features else 0.0
         torch.nn.init.uniform_(self.weight, -bound, bound)
 
@@ -159,18 +162,15 @@ class GatedLinear(torch.nn.Module):
         return m
 
     def fix_weights(self):
-        """Freeze the parameters and lay the weight out once for the calls to come."""
+        """Freeze the parameters: calls raise once the weight has changed, until this is called again."""
         for p in self.parameters():
             p.requires_grad_(False)
-        self._plan = (plan_weight(self.weight), self.weight._version)
+        self._fixed = FixedWeight(self.weight)
         return self
 
-    def forward(self, x):
-        plan = None
-        if self._plan is not None:
-            plan, version = self._plan
-            if version != self.weight._version or plan.device != self.weight.device:
-                raise RuntimeError("the weight changed after fix_weights(); call it again")
+    def forward(self, x, plan=None):
+        if self._fixed is not None:
+            self._fixed.check(self.weight)
         return gated_linear(x, self.weight, self.bias, self.gate, plan)
 
     def extra_repr(self):

@@ -176,3 +176,28 @@ class WeightPlan:
         if self.dtype != weight.dtype or self.shape != tuple(weight.shape) or self.device != weight.device:
             raise ValueError(f"plan: laid out for a {self.dtype} weight of shape {self.shape} on {self.device}, got "
                              f"{weight.dtype} {tuple(weight.shape)} on {weight.device}")
+
+
+class FixedWeight:
+    """Tells whether a module's weight is still the one that was fixed: the same tensor, with no
+    change that torch counts.  A copy of the module (deepcopy, pickle) holds a copy of its weight,
+    which is as fixed as the original was.
+
+    A layout (WeightPlan) is not kept with it: writes through `weight.data` count nowhere, and a
+    layout kept over them would multiply with the old weight."""
+
+    __slots__ = ("weight", "version")
+
+    def __init__(self, weight):
+        self.weight, self.version = weight, weight._version
+
+    def check(self, weight):
+        if weight is not self.weight or weight._version != self.version:
+            raise RuntimeError("the weight changed after fix_weights(); call it again")
+
+    def __getstate__(self):
+        return self.weight, self.weight._version == self.version
+
+    def __setstate__(self, state):
+        self.weight, fixed = state
+        self.version = self.weight._version if fixed else None
