@@ -11,8 +11,8 @@ gradients are deterministic.
 import torch
 
 from . import ops
-from .ops import (DTYPES, FixedWeight, WeightPlan, addr, check_tensor, few_bytes, ok, ops_lib, rows_of, scratch,
-                  stream_of)
+from .ops import (DTYPES, FixedWeight, WeightPlan, addr, check_tensor, few_bytes, forward_mode, ok, ops_lib, rows_of,
+                  scratch, stream_of)
 
 
 def plan_weight(weight, backward=False):
@@ -124,7 +124,8 @@ def adapter_linear(x, weight, a, b, ids, scale=None, bias=None, plan=None):
     """x W^T + bias + scale[i] (x a[i]^T) b[i]^T with i = ids[row], for x[..., K], weight[N, K],
     a[n, r, K], b[n, N, r], bias[N] or None, all float32 or all bfloat16 on the current HIP device;
     ids: int32 of x's leading shape (outside [0, n): no adapter); scale: None (1), a number, or float32
-    [n].  `plan` (plan_weight(weight)) spares laying the weight out.  Differentiable in x, a and b."""
+    [n].  `plan` (plan_weight(weight)) spares laying the weight out.  Differentiable in x, a and b, in reverse
+    mode."""
     if scale is not None and not isinstance(scale, torch.Tensor) and isinstance(a, torch.Tensor):
         scale = torch.full(a.shape[:1], float(scale), dtype=torch.float32, device=a.device)
     try:
@@ -142,9 +143,10 @@ def adapter_linear(x, weight, a, b, ids, scale=None, bias=None, plan=None):
     ops_lib()
     bias = None if bias is None else bias.contiguous()
     scale = None if scale is None else scale.contiguous()
-    if torch.is_grad_enabled() and (x.requires_grad or a.requires_grad or b.requires_grad or weight.requires_grad
-                                    or (scale is not None and scale.requires_grad)
-                                    or (bias is not None and bias.requires_grad)):
+    if forward_mode() or (torch.is_grad_enabled()
+                          and (x.requires_grad or a.requires_grad or b.requires_grad or weight.requires_grad
+                               or (scale is not None and scale.requires_grad)
+                               or (bias is not None and bias.requires_grad))):
         y = _AdapterFn.apply(x2d, weight, a, b, ids, scale, bias, plan)
     else:
         (xr, xld), (wr, wld) = rows_of(x2d), rows_of(weight)

@@ -12,8 +12,8 @@ import torch
 
 from . import ops
 from .linear import Linear
-from .ops import (DTYPES, GATES, FixedWeight, WeightPlan, addr, check_tensor, few_bytes, ok, ops_lib, rows_of, scratch,
-                  stream_of)
+from .ops import (DTYPES, GATES, FixedWeight, WeightPlan, addr, check_tensor, few_bytes, forward_mode, ok, ops_lib,
+                  rows_of, scratch, stream_of)
 
 
 def plan_weight(weight):
@@ -107,7 +107,7 @@ def gated_linear(x, weight, bias=None, gate="silu", plan=None):
     """act(x Wg^T + bg) * (x Wu^T + bu) for x[..., K], weight[2F, K] = [Wg; Wu], bias[2F] or None,
     all float32 or all bfloat16 on the current HIP device.  gate: "silu", "gelu" (exact), "gelu_tanh",
     "sigmoid" or "relu".  `plan` (plan_weight(weight)) spares laying out a weight that does not change.
-    Differentiable in x, weight and bias."""
+    Differentiable in x, weight and bias, in reverse mode."""
     act = GATES.get(gate)
     if act is None:
         raise ValueError(f"unknown gate {gate!r} (one of {', '.join(GATES)})")
@@ -122,8 +122,8 @@ def gated_linear(x, weight, bias=None, gate="silu", plan=None):
     if plan is not None:
         plan.check(weight, gated=True)
     ops_lib()
-    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad
-                                    or (bias is not None and bias.requires_grad)):
+    if forward_mode() or (torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad
+                                                       or (bias is not None and bias.requires_grad))):
         h = _GatedFn.apply(x2d, weight, bias, act, plan)
     else:
         (xr, xld), (wr, wld) = rows_of(x2d), rows_of(weight)

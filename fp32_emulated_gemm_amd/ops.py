@@ -8,6 +8,7 @@ allocate outputs and differentiate are in ``gated`` and ``adapters``.
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from . import SgemmEmuError, lib
 
@@ -100,6 +101,12 @@ def rows_of(t):
         t = t.contiguous()
         ld = cols
     return t, ld if rows > 1 and ld > 0 else max(cols, 1)
+
+
+def forward_mode():
+    """Whether a level of forward-mode differentiation is open: operands may then carry tangents, which
+    only a call through an autograd function sees (and refuses)."""
+    return forward_ad._current_level >= 0
 
 
 def scratch(nbytes, like):

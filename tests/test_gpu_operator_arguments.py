@@ -1,5 +1,5 @@
 """Arguments of the operators' tensor functions on the GPU: layouts of a weight, rows far
-apart."""
+apart, tangents."""
 import pytest
 import torch
 
@@ -65,3 +65,38 @@ def test_last_tokens_of_long_prompts(dtype):
         wide.copy_(t["w"])
         y = adapter_linear(xs, wide, c["a"], c["b"], ids.cuda(), c["scale"], c["bias"])
         ref.check(y, want["y"], "Y, rows of W far apart")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [8, 100])
+@pytest.mark.parametrize("grad", [True, False])
+def test_tangents_are_refused(dtype, M, grad):
+    """Forward-mode derivatives are not provided: an operand with a tangent raises, and none is
+    dropped; without one, a call inside an open level computes as ever."""
+    from torch.autograd import forward_ad
+    from fp32_emulated_gemm_amd.adapters import adapter_linear
+    from fp32_emulated_gemm_amd.gated import gated_linear
+    x, w, b, _ = (_cuda(t) for t in gated_inputs(dtype, M, 64, 24, True))
+    c = {k: _cuda(v) for k, v in adapter_inputs(dtype, M, 64, 48, 3, 4).items()}
+    ids = _ids("mixed", M, 3).cuda()
+    names = ("x", "w", "a", "b", "scale", "bias")
+
+    def adapters(t):
+        return adapter_linear(t["x"], t["w"], t["a"], t["b"], ids, t["scale"], t["bias"])
+
+    with torch.set_grad_enabled(grad):
+        with forward_ad.dual_level():
+            for k in range(3):
+                t = [x, w, b]
+                t[k] = forward_ad.make_dual(t[k], torch.ones_like(t[k]))
+                with pytest.raises(NotImplementedError):
+                    gated_linear(*t)
+            for name in names:
+                t = dict(c)
+                t[name] = forward_ad.make_dual(t[name], torch.ones_like(t[name]))
+                with pytest.raises(NotImplementedError):
+                    adapters(t)
+            h, y = gated_linear(x, w, b), adapters(c)
+        ref.check(h, ref.gated(x.cpu(), w.cpu(), b.cpu(), "silu")["h"], "H")
+        t = {k: v.cpu() for k, v in c.items()}
+        ref.check(y, ref.adapter(t["x"], t["w"], t["a"], t["b"], ids.cpu(), t["scale"], t["bias"])["y"], "Y")
