@@ -112,14 +112,21 @@ __device__ __forceinline__ float gate_act(float z)
     return a;
 }
 
-// The tail of a float's significand after rounding to BF16, as BF16: v is
-// hi + lo to 16 bits or more.
+// A float as two BF16: hi + lo is v to 16 bits or more.  Infinities and NaN stay in
+// hi.  A finite v beyond the largest BF16 (3.3895e38, where hi would round to
+// Inf and hi + lo to NaN) takes that as hi, and a lo cut off rather than rounded,
+// so that the sum stays below 2^128.
 __device__ __forceinline__ void split_hi_lo(float v, uint16_t &hi, uint16_t &lo)
 {
+    constexpr uint32_t INF = 0x7F80, MOST = 0x7F7F;
+    const uint32_t bits = __float_as_uint(v), sign = (bits >> 16) & 0x8000u;
+    const bool finite = (bits & 0x7FFFFFFFu) < 0x7F800000u;
     hi = f2bf(v);
-    const float rest = v - bf2f(hi);
-    // Inf - Inf (an infinite or overflowing v) would turn the sum into NaN
-    lo = rest == rest ? f2bf(rest) : (uint16_t)0;
+    const bool over = finite && (hi & 0x7FFFu) == INF;
+    if (over) hi = (uint16_t)(sign | MOST);
+    const float rest = v - bf2f(hi);             // exact
+    const uint16_t cut = (uint16_t)(__float_as_uint(rest) >> 16), near = f2bf(rest);
+    lo = !finite ? (uint16_t)0 : over ? cut : near;
 }
 
 }  // namespace sgemm_emu_dev
