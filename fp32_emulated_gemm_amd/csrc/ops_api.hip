@@ -141,7 +141,9 @@ int adapted_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, co
 
 int check_gated(int dtype, int64_t M, int64_t F, int64_t K, int gate)
 {
-    if (!dtype_ok(dtype) || !extent_ok(M) || !extent_ok(2 * F) || !extent_ok(K)) return SGEMM_EMU_EINVAL;
+    // F by itself first: 2 F of an F near INT64_MIN wraps to a small number
+    if (!dtype_ok(dtype) || !extent_ok(M) || !extent_ok(F) || !extent_ok(2 * F) || !extent_ok(K))
+        return SGEMM_EMU_EINVAL;
     if (gate < SGEMM_EMU_GATE_SILU || gate > SGEMM_EMU_GATE_RELU) return SGEMM_EMU_EINVAL;
     return SGEMM_EMU_OK;
 }

@@ -1,7 +1,16 @@
 """Checks of the operators' arguments that need no GPU: what the tensor functions
-make of strides, and which layouts of a weight they take."""
+make of strides, which layouts of a weight they take, sizes whose products wrap."""
 import pytest
 import torch
+
+EINVAL = -1
+P = 0x10000   # any nonzero, 256-byte aligned address: never dereferenced on these paths
+
+
+@pytest.fixture(scope="module")
+def L():
+    from fp32_emulated_gemm_amd import ops
+    return ops.ops_lib()
 
 
 @pytest.mark.parametrize("held", [None, "laid out"])
@@ -40,3 +49,11 @@ def test_rows_of_any_stride(rows, cols, stride, copied):
     if rows and cols:
         again = torch.as_strided(got, (rows, cols), (ld, 1)) if cols > 1 or rows > 1 else got
         assert torch.equal(again, t)
+
+
+@pytest.mark.parametrize("F", [-2 ** 63, -2 ** 63 + 1, -2 ** 63 + 1000, -1, 2 ** 62, 2 ** 63 - 1, 2 ** 21])
+def test_a_width_whose_double_wraps_is_refused(L, F):
+    assert L.sgemm_emu_gated_linear_workspace(0, 4, F, 8, P, 8, P, 8, None, None) == EINVAL
+    assert L.sgemm_emu_gated_linear_backward_workspace(0, 4, F, 8) == EINVAL
+    ld = max(F, 1) if F < 2 ** 23 else 2 ** 22
+    assert L.sgemm_emu_gated_linear(0, 4, F, 8, P, 8, P, 8, None, None, 0, P, ld, None, None, 0, None) == EINVAL
