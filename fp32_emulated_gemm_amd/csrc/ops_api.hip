@@ -18,6 +18,7 @@ constexpr int64_t kMaxBytes = INT64_MAX / 8;
 constexpr int64_t kMaxLd = ((int64_t)1 << 32) / (128 * 4) - 64;   // as the GEMM's: 128-row tiles in 32-bit offsets
 constexpr int64_t kMaxExtent = 65535 * 64;                        // grid extents of 64-wide tiles
 constexpr int64_t kMaxAdapters = 65535;
+constexpr int64_t kMaxBankElems = (int64_t)1 << 55;               // n r (K + N)
 
 int64_t size_of(int dtype) { return dtype == SGEMM_EMU_F32 ? 4 : 2; }
 bool dtype_ok(int dtype) { return dtype == SGEMM_EMU_F32 || dtype == SGEMM_EMU_BF16; }
@@ -223,8 +224,11 @@ hipError_t lay_out_wt(int dtype, int64_t F, int64_t K, const void *W, int64_t ld
 int check_adapters(int dtype, int64_t M, int64_t N, int64_t K, int64_t n, int64_t r)
 {
     if (!dtype_ok(dtype) || !extent_ok(M) || !extent_ok(N) || !extent_ok(K) || !extent_ok(r)) return SGEMM_EMU_EINVAL;
-    // the banks' bytes then stay below 2^63
-    return n < 0 || n > kMaxAdapters ? SGEMM_EMU_EINVAL : SGEMM_EMU_OK;
+    if (n < 0 || n > kMaxAdapters) return SGEMM_EMU_EINVAL;
+    // The banks, their copies (ranks padded up to 16 times) and their gradients' partial
+    // sums then take less than 2^62 bytes.
+    if (n > 0 && r > 0 && K + N > 0 && n > kMaxBankElems / (r * (K + N))) return SGEMM_EMU_EINVAL;
+    return SGEMM_EMU_OK;
 }
 
 // Few rows read W in one pass; low-rank activations to keep come from the tiles' path.

@@ -29,7 +29,7 @@
  *              (see sgemm_emu_split_k), and return SGEMM_EMU_ECAPTURE on a
  *              stream being captured into a graph.
  *   limits     leading dimensions up to 8,388,544 elements; M, F, N, K up to
- *              4,194,240; up to 65,535 adapters.
+ *              4,194,240; up to 65,535 adapters, n r (K + N) up to 2^55.
  * Outputs must not overlap inputs (not checked).
  */
 #ifndef SGEMM_EMU_OPS_H

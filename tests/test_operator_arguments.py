@@ -3,7 +3,7 @@ make of strides, which layouts of a weight they take, sizes whose products wrap.
 import pytest
 import torch
 
-EINVAL = -1
+EINVAL, EARCH = -1, -3
 P = 0x10000   # any nonzero, 256-byte aligned address: never dereferenced on these paths
 
 
@@ -57,3 +57,20 @@ def test_a_width_whose_double_wraps_is_refused(L, F):
     assert L.sgemm_emu_gated_linear_backward_workspace(0, 4, F, 8) == EINVAL
     ld = max(F, 1) if F < 2 ** 23 else 2 ** 22
     assert L.sgemm_emu_gated_linear(0, 4, F, 8, P, 8, P, 8, None, None, 0, P, ld, None, None, 0, None) == EINVAL
+
+
+@pytest.mark.parametrize("n,r,N,K,fits", [
+    (65535, 4194240, 4194240, 4194240, False), (65535, 4194240, 4194240, 0, False), (65535, 1 << 20, 1 << 20, 1, False),
+    (65535, 256, 16384, 16384, True), (1, 4194240, 4194240, 4194240, True), (65535, 4194240, 0, 0, True),
+    (0, 4194240, 4194240, 4194240, True)])
+def test_banks_whose_bytes_wrap_are_refused(L, n, r, N, K, fits):
+    """A workspace's size adds up the banks' copies and the partial sums of their gradients."""
+    for dtype in (0, 1):
+        for got in (L.sgemm_emu_adapter_linear_workspace(dtype, 4, N, K, P, max(K, 1), P, max(K, 1), None, n, r, P, None),
+                    L.sgemm_emu_adapter_linear_backward_workspace(dtype, 4, N, K, n, r)):
+            if not fits:
+                assert got == EINVAL
+            elif torch.cuda.is_available():
+                assert 0 <= got < 2 ** 62
+            else:
+                assert got == EARCH
