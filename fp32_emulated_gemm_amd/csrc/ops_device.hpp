@@ -92,7 +92,9 @@ __device__ __forceinline__ void gate_act_grad(float z, float &a, float &d)
         // 0.5 (1 + tanh(v)) = sigmoid(2 v)
         const float s = sigmoidf(1.5957691216057308f * z * (1.0f + 0.044715f * z * z));
         a = z * s;
-        d = s + z * s * (1.0f - s) * (1.5957691216057308f * (1.0f + 0.134145f * z * z));
+        // s is 0 or 1 from |z| = 12 on; the square stops there, before it is Inf and its
+        // product with s (1 - s) = 0 NaN
+        d = s + z * s * (1.0f - s) * (1.5957691216057308f * (1.0f + fminf(0.134145f * z * z, 1e6f)));
     } else if constexpr (GATE == kSigmoid) {
         const float s = sigmoidf(z);
         a = s;
