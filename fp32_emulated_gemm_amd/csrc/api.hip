@@ -21,6 +21,7 @@
 #include "../../include/sgemm_emu.h"
 #include "launch.hpp"
 #include "ops.hpp"
+#include "workspace.hpp"
 
 using namespace sgemm_emu_dev;
 
@@ -160,17 +161,6 @@ int launched(hipError_t e) { return e == hipSuccess ? SGEMM_EMU_OK : SGEMM_EMU_E
 // their kernels.  Nothing is allocated on a stream being captured into a
 // graph (stream_capturing): the callers fall back to paths without workspace
 // or report SGEMM_EMU_ECAPTURE.
-struct StreamWs {
-    bool used = false;
-    uintptr_t key = 0;           // the stream handle
-    void *ptr = nullptr;
-    size_t bytes = 0;
-    hipEvent_t done = nullptr;   // recorded on the stream after the last call that used ptr
-    bool recorded = false;
-    uint64_t tick = 0;           // last use, for eviction
-    uint32_t epoch = 0;          // stream-K flag value of the block's last call (flags start at 0)
-};
-
 constexpr int kStreamSlots = 8;
 
 struct DeviceWs {
@@ -180,28 +170,6 @@ struct DeviceWs {
 };
 
 DeviceWs g_ws[kMaxDevices];
-
-// Lease on a workspace for one call; release() after the call's last launch.
-struct WsLease {
-    std::unique_lock<std::mutex> lock;
-    StreamWs *entry = nullptr;
-    hipStream_t stream = nullptr;
-    uint32_t *flags = nullptr;   // the block's stream-K flags (its first kFlagBytes)
-    uint32_t epoch = 0;          // this call's flag value
-
-    // The event of the held block, for the launch helpers to tie to the call's
-    // last kernel (a separate event record costs the stream a few microseconds).
-    void *event() const { return entry != nullptr ? (void *)entry->done : nullptr; }
-
-    // attached: the call's last kernel already carries the event.
-    void release(bool attached = false)
-    {
-        if (entry != nullptr) entry->recorded = attached || hipEventRecord(entry->done, stream) == hipSuccess;
-        entry = nullptr;
-        if (lock.owns_lock()) lock.unlock();
-    }
-    ~WsLease() { release(); }
-};
 
 // True if `stream` is being captured into a graph (or its state cannot be
 // read, which is treated the same way).
@@ -281,7 +249,9 @@ void *acquire_workspace(int dev, hipStream_t stream, size_t bytes, WsLease &L)
     L.entry = e;
     L.flags = (uint32_t *)e->ptr;
     L.epoch = e->epoch;
-    return (char *)e->ptr + kFlagBytes;
+    L.ptr = (char *)e->ptr + kFlagBytes;
+    L.bytes = e->bytes - kFlagBytes;
+    return L.ptr;
 }
 
 
@@ -635,56 +605,91 @@ namespace sgemm_emu_dev {
 
 int current_cus(int *num_cus) { return current_device(num_cus); }
 
-// The N x K planes path of gemm_common for planes padded with zeros to a K
-// that is a multiple of 64 (16-byte aligned rows; args.B0..B2, args.K the
-// unpadded K): 64 x 64 tiles or stream-K by the same rules, A split into
-// workspace planes for wide N, and a K tail that the kernel masks in A.
-int gemm_padded_planes(const GemmArgs &args, const PlaneLaunchers &launch, hipStream_t stream)
+namespace {
+
+// What gemm_padded_planes does with a product: stream-K workgroups (0: none), 64 x 64
+// tiles, and the workspace of the stream-K slots or of A's planes (one or neither).
+struct PlanePath {
+    int skg;
+    bool tile64;
+    size_t slots, aplane;
+    size_t bytes() const { return slots + 3 * aplane; }
+};
+
+PlanePath plane_path(int64_t M, int64_t N, int64_t K, int num_cus)
+{
+    const int64_t kpad = (K + 63) / 64 * 64;
+    PlanePath p{gemm_streamk_grid(M, N, kpad, num_cus), false, 0, 0};
+    p.tile64 = p.skg == 0 && gemm_tile64_pays(M, N, K, num_cus, false);
+    p.slots = (size_t)p.skg * kSkSlotBytes;
+#ifndef SGEMM_EMU_SERIAL_LDS
+    if (p.skg == 0 && !p.tile64 && kpad == K && M >= kPresplitMinRows && N >= kPresplitAMinCols &&
+        (uint64_t)M * (uint64_t)K <= kPresplitMaxElems)
+        p.aplane = ((size_t)M * (size_t)K * sizeof(uint16_t) + 255) & ~(size_t)255;
+#endif
+    return p;
+}
+
+}  // namespace
+
+int lease_plane_workspace(const PlaneProduct *products, int count, hipStream_t stream, WsLease &lease)
 {
     int num_cus = 0, dev = 0, rc;
     if ((rc = current_device(&num_cus, &dev)) != SGEMM_EMU_OK) return rc;
+    size_t most = 0, least = 0;              // with A's planes, and what cannot be done without
+    for (int i = 0; i < count; ++i) {
+        const PlanePath p = plane_path(products[i].M, products[i].N, products[i].K, num_cus);
+        if (p.bytes() > most) most = p.bytes();
+        if (p.slots > least) least = p.slots;
+    }
+    if (most == 0 || acquire_workspace(dev, stream, most, lease) != nullptr || least == 0) return SGEMM_EMU_OK;
+    if (stream_capturing(stream)) return SGEMM_EMU_ECAPTURE;
+    return least < most && acquire_workspace(dev, stream, least, lease) != nullptr ? SGEMM_EMU_OK : SGEMM_EMU_ENOMEM;
+}
+
+// The N x K planes path of gemm_common for planes padded with zeros to a K
+// that is a multiple of 64 (16-byte aligned rows; args.B0..B2, args.K the
+// unpadded K): 64 x 64 tiles or stream-K by the same rules, A split into
+// workspace planes for wide N (where the lease has room), and a K tail that the
+// kernel masks in A.
+int gemm_padded_planes(const GemmArgs &args, const PlaneLaunchers &launch, WsLease &lease, hipStream_t stream)
+{
+    int num_cus = 0, rc;
+    if ((rc = current_device(&num_cus)) != SGEMM_EMU_OK) return rc;
     GemmArgs g = args;
-    const int64_t M = g.M, N = g.N, K = g.K, kpad = (K + 63) / 64 * 64;
+    const int64_t M = g.M, K = g.K, kpad = (K + 63) / 64 * 64;
     g.ka = K;
     g.ldb = kpad;
     g.num_cus = num_cus;
     g.splits = 1;
-    const int skg = gemm_streamk_grid(M, N, kpad, num_cus);
-    if (skg == 0 && gemm_tile64_pays(M, N, K, num_cus, false)) return launched(launch.tile64(g, stream));
-#ifdef SGEMM_EMU_SERIAL_LDS
-    const bool presplit_a = false;
-#else
-    const bool presplit_a = skg == 0 && kpad == K && M >= kPresplitMinRows && N >= kPresplitAMinCols &&
-                            (uint64_t)M * (uint64_t)K <= kPresplitMaxElems;
-#endif
-    const size_t aplane = presplit_a ? ((size_t)M * (size_t)K * sizeof(uint16_t) + 255) & ~(size_t)255 : 0;
-    const size_t part = skg > 0 ? (size_t)skg * kSkSlotBytes : 0;
-    WsLease lease;
-    char *ws = nullptr;
-    if (aplane + part > 0) ws = (char *)acquire_workspace(dev, stream, 3 * aplane + part, lease);
-    if (ws == nullptr && skg > 0) return stream_capturing(stream) ? SGEMM_EMU_ECAPTURE : SGEMM_EMU_ENOMEM;
+    const PlanePath p = plane_path(M, g.N, K, num_cus);
+    if (p.tile64) return launched(launch.tile64(g, stream));
+    const bool room = lease.entry != nullptr && lease.bytes >= p.bytes();
+    if (p.skg > 0 && !room) return SGEMM_EMU_ENOMEM;
+    if (p.bytes() == 0 || !room) {
+        g.K = kpad;
+        return launched(launch.dma(g, stream));
+    }
+    g.done = lease.event();
     hipError_t e = hipSuccess;
-    if (ws != nullptr && presplit_a) {
-        uint16_t *Q0 = (uint16_t *)ws, *Q1 = (uint16_t *)(ws + aplane), *Q2 = (uint16_t *)(ws + 2 * aplane);
+    if (p.skg > 0) {
+        g.sk_grid = p.skg;
+        g.sk_flags = lease.flags;
+        g.sk_epoch = lease.epoch;
+        g.partials = (float *)lease.ptr;
+        g.K = kpad;
+        e = launch.dma(g, stream);
+        lease.next_epoch();                  // for the call's next product
+    } else {
+        uint16_t *const Q0 = (uint16_t *)lease.ptr, *const Q1 = (uint16_t *)(lease.ptr + p.aplane),
+                 *const Q2 = (uint16_t *)(lease.ptr + 2 * p.aplane);
         e = launch_split(M, K, g.A, g.lda, Q0, Q1, Q2, K, num_cus, stream, false);
         if (e == hipSuccess) {
             g.A0 = Q0; g.A1 = Q1; g.A2 = Q2; g.lda = K;
-            g.done = lease.event();
             e = launch.planes(g, stream);
         }
-        lease.release(e == hipSuccess && g.done != nullptr);
-        return launched(e);
     }
-    if (skg > 0) {
-        g.sk_grid = skg;
-        g.sk_flags = lease.flags;
-        g.sk_epoch = lease.epoch;
-        g.partials = (float *)ws;
-    }
-    g.K = kpad;
-    g.done = lease.event();
-    e = launch.dma(g, stream);
-    lease.release(e == hipSuccess && g.done != nullptr);
+    lease.attached = e == hipSuccess;
     return launched(e);
 }
 

@@ -148,10 +148,8 @@ hipError_t launch_gate_backward(int dtype, int64_t M, int64_t F, const float *Z,
 // out[c] = sum over t of sums[t][c], t ascending.
 hipError_t launch_sum_tiles(int dtype, int64_t tiles, int64_t cols, const float *sums, void *out, hipStream_t stream);
 
-// ---------------------------------------------------------------- FP32 products (api.hip, gemm_fused.hip)
-// C = A B^T with FP32 A (M x K, lda) and B as zero-padded planes
-// (launch_split_padded of an N x K matrix), nine products, by `launch`'s kernels.
-int gemm_padded_planes(const GemmArgs &args, const PlaneLaunchers &launch, hipStream_t stream);
+// ---------------------------------------------------------------- FP32 products (gemm_fused.hip)
+// The kernels of gemm_padded_planes (workspace.hpp).
 const PlaneLaunchers &plain_launchers();     // bias
 const PlaneLaunchers &gated_launchers();     // bias, gate (args.epi; B's columns alternate gate, up)
 const PlaneLaunchers &adapter_launchers();   // bias, adapters (args.epi)

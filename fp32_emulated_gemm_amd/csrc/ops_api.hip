@@ -3,12 +3,15 @@
 //
 // As in api.hip every argument is checked before the first HIP call.  Scratch
 // memory is the caller's: each call lays its buffers out in `ws` with the same
-// code that its *_workspace function sizes them with (Carve).
+// code that its *_workspace function sizes them with (Carve).  What the FP32
+// products take of the stream's own workspace is leased before the first launch
+// (lease_plane_workspace).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "../../include/sgemm_emu_ops.h"
 #include "ops.hpp"
+#include "workspace.hpp"
 
 using namespace sgemm_emu_dev;
 
@@ -109,31 +112,33 @@ GemmArgs product_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t ld
 
 // A product without a fused epilogue; an empty K leaves zeros.
 int plain_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes, float *C,
-              int64_t ldc, int num_cus, hipStream_t stream)
+              int64_t ldc, int num_cus, WsLease &lease, hipStream_t stream)
 {
     if (M == 0 || N == 0) return SGEMM_EMU_OK;
     if (K == 0) {
         LAUNCH(launch_zero(M, N, C, ldc, nullptr, SGEMM_EMU_ACT_NONE, num_cus, stream));
         return SGEMM_EMU_OK;
     }
-    return gemm_padded_planes(product_f32(M, N, K, A, lda, planes, nullptr, C, ldc), plain_launchers(), stream);
+    return gemm_padded_planes(product_f32(M, N, K, A, lda, planes, nullptr, C, ldc), plain_launchers(), lease,
+                              stream);
 }
 
 // The product with the adapters' part (or none).  A ragged K whose rows lie takes
 // the plain kernels and a pass over C: a padded copy of A for the fused ones cost
 // as much or more (3136 x 336 x 3592: 128 us against 114).
 int adapted_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, const uint16_t *planes,
-                const float *bias, const Adapters *ad, const float *S, float *C, int64_t ldc, hipStream_t stream)
+                const float *bias, const Adapters *ad, const float *S, float *C, int64_t ldc, WsLease &lease,
+                hipStream_t stream)
 {
     GemmArgs g = product_f32(M, N, K, A, lda, planes, bias, C, ldc);
-    if (ad == nullptr) return gemm_padded_planes(g, plain_launchers(), stream);
+    if (ad == nullptr) return gemm_padded_planes(g, plain_launchers(), lease, stream);
     g.epi.gate = -1;
     g.epi.ids = ad->ids;
     g.epi.n = ad->n; g.epi.r = ad->r; g.epi.rp = rank_pad(ad->r);
     g.epi.up = (const float *)ad->up;
     g.epi.S = S;
-    if (K % kPadK == 0) return gemm_padded_planes(g, adapter_launchers(), stream);
-    CHECK(gemm_padded_planes(g, plain_launchers(), stream));
+    if (K % kPadK == 0) return gemm_padded_planes(g, adapter_launchers(), lease, stream);
+    CHECK(gemm_padded_planes(g, plain_launchers(), lease, stream));
     LAUNCH(launch_expand(M, N, g.epi, C, ldc, stream));
     return SGEMM_EMU_OK;
 }
@@ -379,6 +384,9 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
             LAUNCH(launch_gate_bias(M, F, (const float *)bias, gate, (float *)H, ldh, Z, s));
             return SGEMM_EMU_OK;
         }
+        const PlaneProduct product{M, 2 * F, pad_k(K)};
+        WsLease lease;
+        CHECK(lease_plane_workspace(&product, 1, s, lease));
         if (w.plan != nullptr) LAUNCH(launch_split_padded(2 * F, K, (const float *)W, ldw, w.plan, true, s));
         if (w.x != nullptr) LAUNCH(launch_copy_padded(dtype, M, K, X, ldx, w.x, pad_k(K), s));
         GemmArgs g = product_f32(M, 2 * F, pad_k(K), w.x != nullptr ? (const float *)w.x : (const float *)X,
@@ -388,7 +396,7 @@ int sgemm_emu_gated_linear(int dtype, int64_t M, int64_t F, int64_t K, const voi
         g.epi.gate = gate;
         g.epi.Z = Z;
         g.epi.ldz = z_pitch(F);
-        return gemm_padded_planes(g, gated_launchers(), s);
+        return gemm_padded_planes(g, gated_launchers(), lease, s);
     }
     Bf16Gemm g{};
     g.M = M; g.N = 2 * F; g.K = bf16_k(K);
@@ -439,6 +447,14 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
     CHECK(check_ws(ws, ws_bytes, w.bytes));
     hipStream_t s = (hipStream_t)stream;
     const int64_t n2 = 2 * F, pitch = dz_pitch(F), mp = pad_k(M);
+    WsLease lease;
+    if (dtype == SGEMM_EMU_F32 && M > 0 && F > 0 && K > 0) {
+        PlaneProduct products[2];
+        int count = 0;
+        if (dX != nullptr) products[count++] = {M, K, pitch};
+        if (dW != nullptr) products[count++] = {n2, K, mp};
+        CHECK(lease_plane_workspace(products, count, s, lease));
+    }
     if (M > 0 && F > 0)
         LAUNCH(launch_gate_backward(dtype, M, F, Z, dH, lddh, gate, dX != nullptr ? w.dz : nullptr,
                                     dW != nullptr ? w.dzt : nullptr, dbias != nullptr ? w.sums : nullptr, s));
@@ -446,7 +462,7 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
     if (dX != nullptr && M > 0 && K > 0) {
         if (F > 0) LAUNCH(lay_out_wt(dtype, F, K, W, ldw, w.wt, num_cus, s));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(plain_f32(M, K, pitch, (const float *)w.dz, pitch, w.wt, (float *)dX, lddx, num_cus, s));
+            CHECK(plain_f32(M, K, pitch, (const float *)w.dz, pitch, w.wt, (float *)dX, lddx, num_cus, lease, s));
         } else {
             Bf16Gemm g{};
             g.M = M; g.N = K; g.K = pitch;
@@ -461,7 +477,7 @@ int sgemm_emu_gated_linear_backward(int dtype, int64_t M, int64_t F, int64_t K, 
     if (dW != nullptr && F > 0 && K > 0) {
         if (M > 0) CHECK(sgemm_emu_plan_weight(dtype, M, K, X, ldx, SGEMM_EMU_PLAN_TRANSPOSED, w.xt, stream));
         if (dtype == SGEMM_EMU_F32) {
-            CHECK(plain_f32(n2, K, mp, (const float *)w.dzt, mp, w.xt, (float *)dW, lddw, num_cus, s));
+            CHECK(plain_f32(n2, K, mp, (const float *)w.dzt, mp, w.xt, (float *)dW, lddw, num_cus, lease, s));
         } else {
             Bf16Gemm g{};
             g.M = n2; g.N = K; g.K = mp;
@@ -524,6 +540,12 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
         LAUNCH(launch_few_rows(dtype, a, num_cus, s));
         return SGEMM_EMU_OK;
     }
+    WsLease lease;
+    const int64_t kx = w.x != nullptr ? pad_k(K) : K;            // the FP32 product's K
+    if (dtype == SGEMM_EMU_F32 && N > 0 && K > 0) {
+        const PlaneProduct product{M, N, kx};
+        CHECK(lease_plane_workspace(&product, 1, s, lease));
+    }
     if (low) {
         if (S == nullptr) S = w.s;
         LAUNCH(launch_shrink(dtype, M, K, X, ldx, ad, S, num_cus, s));
@@ -537,9 +559,9 @@ int sgemm_emu_adapter_linear(int dtype, int64_t M, int64_t N, int64_t K, const v
         }
         if (w.plan != nullptr) LAUNCH(launch_split_padded(N, K, (const float *)W, ldw, w.plan, false, s));
         if (w.x != nullptr) LAUNCH(launch_copy_padded(dtype, M, K, X, ldx, w.x, pad_k(K), s));
-        return adapted_f32(M, N, w.x != nullptr ? pad_k(K) : K, w.x != nullptr ? (const float *)w.x : (const float *)X,
-                           w.x != nullptr ? pad_k(K) : ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
-                           (const float *)bias, low ? &ad : nullptr, S, (float *)Y, ldy, s);
+        return adapted_f32(M, N, kx, w.x != nullptr ? (const float *)w.x : (const float *)X,
+                           w.x != nullptr ? kx : ldx, w.plan != nullptr ? w.plan : (const uint16_t *)plan,
+                           (const float *)bias, low ? &ad : nullptr, S, (float *)Y, ldy, lease, s);
     }
     Bf16Gemm g{};
     g.M = M; g.N = N; g.K = bf16_k(K);
@@ -612,6 +634,12 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
     const Adapters back{ids, n, r, w.up_t, w.down_t, scale};
     const bool need_dx = dX != nullptr && M > 0 && K > 0, need_down = low && d_down != nullptr && K > 0,
                need_up = low && d_up != nullptr && N > 0;
+    const bool lies = direct(dtype, dY, lddy, N);
+    WsLease lease;
+    if (dtype == SGEMM_EMU_F32 && need_dx && N > 0) {
+        const PlaneProduct product{M, K, lies ? N : pad_k(N)};
+        CHECK(lease_plane_workspace(&product, 1, s, lease));
+    }
     if (low) {
         const bool need_p = M > 0 && (need_dx || need_down), need_rows = need_down || need_up;
         AdapterPrepare q{};
@@ -624,7 +652,6 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
         if (need_p) LAUNCH(launch_shrink(dtype, M, N, dY, lddy, back, w.p, num_cus, s));
     }
     if (need_dx) {
-        const bool lies = direct(dtype, dY, lddy, N);
         if (!lies && N > 0) LAUNCH(launch_copy_padded(dtype, M, N, dY, lddy, w.dy, pad_k(N), s));
         if (dtype == SGEMM_EMU_F32) {
             if (N == 0)
@@ -632,7 +659,7 @@ int sgemm_emu_adapter_linear_backward(int dtype, int64_t M, int64_t N, int64_t K
             else
                 CHECK(adapted_f32(M, K, lies ? N : pad_k(N), lies ? (const float *)dY : (const float *)w.dy,
                                   lies ? lddy : pad_k(N), (const uint16_t *)plan_t, nullptr, low ? &back : nullptr,
-                                  w.p, (float *)dX, lddx, s));
+                                  w.p, (float *)dX, lddx, lease, s));
         } else {
             Bf16Gemm g{};
             g.M = M; g.N = K; g.K = bf16_k(N);

@@ -6,7 +6,8 @@
  * Conventions are those of sgemm_emu.h (row-major, device pointers on the
  * current HIP device, int64_t sizes, leading dimensions in elements, work
  * enqueued on `stream`, arguments checked before any HIP call, nothing enqueued
- * on an error status), and:
+ * on an error status other than SGEMM_EMU_ELAUNCH, which a call's later kernels
+ * can give too), and:
  *   dtype      SGEMM_EMU_F32: float tensors; products are the nine BF16
  *              products of sgemm_bf16x9, or FP32 matrix instructions where a
  *              call has few rows.  SGEMM_EMU_BF16: bfloat16 tensors (uint16_t
@@ -26,8 +27,12 @@
  *              Its contents do not matter before or after the call; two calls
  *              that may overlap in time need one each.  FP32 products on small
  *              tile grids additionally use the library's per-stream workspace
- *              (see sgemm_emu_split_k), and return SGEMM_EMU_ECAPTURE on a
- *              stream being captured into a graph.
+ *              for their stream-K partial results (see sgemm_emu_split_k), and
+ *              products of at least 1024 rows and 4096 columns for A's BF16
+ *              planes.  Without memory for the former, a call returns
+ *              SGEMM_EMU_ENOMEM, or SGEMM_EMU_ECAPTURE on a stream being
+ *              captured into a graph; without the latter the kernel splits A
+ *              itself (bitwise the same result).
  *   limits     leading dimensions up to 8,388,544 elements; M, F, N, K up to
  *              4,194,240; up to 65,535 adapters, n r (K + N) up to 2^55.
  * Outputs must not overlap inputs (not checked).
