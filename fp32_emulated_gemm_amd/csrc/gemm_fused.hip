@@ -61,22 +61,21 @@ hipError_t fused_dma(const GemmArgs &args, hipStream_t stream)
     launch_last(gemm_bf16x9_serial_kernel<C128, 5, true, false, false, EPI>,
                 dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), block, stream, g);
 #else
-    if (g.sk_grid > 0 && EPI == EPI_ADAPTER) {
+    if (g.sk_grid == 0) {
+        launch_last(gemm_bf16x9_dma_kernel<C128, 5, true, false, false, EPI>, persistent_grid(g), block, stream,
+                    g);
+    } else if constexpr (EPI == EPI_ADAPTER) {
         // Stream-K's epilogue holds whole partial tiles in registers: with the
         // adapters' start it spilled, 53 us for 6144 x 256 x 1024 against 49 as the
         // product and a pass over C, and 136 against 114 for 3136 x 336 x 3592.
         const hipError_t e = launch_gemm(args, 5, B_PLANES_NK, stream);
         return e != hipSuccess ? e : launch_expand(g.M, g.N, g.epi, g.C, g.ldc, stream);
-    }
-    if (g.sk_grid > 0) {
+    } else {
         GemmArgs s = g;
         s.sk_domains = (int)streamk_domains((int64_t)g.tiles_m * g.tiles_n, g.K / (2 * BK), g.sk_grid);
         s.group_m = kStreamkGroupRows;
-        launch_last(gemm_bf16x9_streamk_kernel<C128, 5, true, false, false, EPI_GATED>, dim3((unsigned)g.sk_grid),
-                    block, stream, s);
-    } else {
-        launch_last(gemm_bf16x9_dma_kernel<C128, 5, true, false, false, EPI>, persistent_grid(g), block, stream,
-                    g);
+        launch_last(gemm_bf16x9_streamk_kernel<C128, 5, true, false, false, EPI>, dim3((unsigned)g.sk_grid), block,
+                    stream, s);
     }
 #endif
     return hipGetLastError();

@@ -55,7 +55,7 @@ struct GemmArgs {
     uint32_t sk_epoch;       // stream-K: this launch's flag value (never 0)
     int sk_grid;             // stream-K: workgroups G (0: no stream-K)
     int sk_domains;          // stream-K: 1, or 8 (one block of tiles per XCD); set by the launcher
-    GemmEpilogue epi;        // gated epilogue only
+    GemmEpilogue epi;        // fused kernels (gemm_fused.hip) only
 };
 
 // rne: round each split stage to nearest even instead of truncating (ablation).
