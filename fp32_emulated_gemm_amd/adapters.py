@@ -187,6 +187,15 @@ class AdapterLinear(torch.nn.Module):
                 m.bias.copy_(layer.bias)
         return m.fix_weights()
 
+    def _apply(self, fn, recurse=True):
+        """Moves and casts as Module does, but the scale, which the kernels take in 32 bits, keeps its
+        type and its value."""
+        scale = self.scale
+        super()._apply(fn, recurse)
+        if self.scale.dtype != scale.dtype:
+            self.scale = scale.to(self.scale.device)
+        return self
+
     def fix_weights(self):
         """Take the weight as it is for the fixed one: calls raise once it has changed, until this is
         called again."""
