@@ -196,15 +196,20 @@ class FixedWeight:
     __slots__ = ("weight", "version")
 
     def __init__(self, weight):
-        self.weight, self.version = weight, weight._version
+        self.weight, self.version = weight, _version(weight)
 
     def check(self, weight):
-        if weight is not self.weight or weight._version != self.version:
+        if weight is not self.weight or _version(weight) != self.version:
             raise RuntimeError("the weight changed after fix_weights(); call it again")
 
     def __getstate__(self):
-        return self.weight, self.weight._version == self.version
+        return self.weight, _version(self.weight) == self.version
 
     def __setstate__(self, state):
         self.weight, fixed = state
-        self.version = self.weight._version if fixed else None
+        self.version = _version(self.weight) if fixed else -1
+
+
+def _version(t):
+    """torch's count of a tensor's changes; None for an inference tensor, whose changes it does not count."""
+    return None if t.is_inference() else t._version

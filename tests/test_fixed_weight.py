@@ -61,3 +61,21 @@ def test_copies_are_as_fixed_as_the_original(which):
     for c in _copies(m):
         with pytest.raises(RuntimeError):
             c._fixed.check(c.weight)
+
+
+def test_modules_made_for_inference():
+    """An inference tensor's changes are not counted; only its replacement is seen."""
+    with torch.inference_mode():
+        for m in _modules():
+            m.fix_weights()
+            m._fixed.check(m.weight)
+            m.weight.mul_(2)
+            m._fixed.check(m.weight)
+            c = copy.deepcopy(m)
+            c._fixed.check(c.weight)
+            m.weight = torch.nn.Parameter(m.weight.clone(), requires_grad=False)
+            with pytest.raises(RuntimeError):
+                m._fixed.check(m.weight)
+        from fp32_emulated_gemm_amd.adapters import AdapterLinear
+        m = AdapterLinear.from_linear(torch.nn.Linear(8, 6), 2, 3)
+        m._fixed.check(m.weight)

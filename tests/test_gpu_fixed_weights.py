@@ -93,3 +93,19 @@ def test_copies_and_a_caller_s_plan(dtype):
         m(x, ids)
     with pytest.raises(RuntimeError):
         copy.deepcopy(m)(x, ids)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [9, 100])
+def test_modules_made_and_run_for_inference(dtype, rows):
+    from fp32_emulated_gemm_amd.adapters import AdapterLinear
+    from fp32_emulated_gemm_amd.gated import GatedLinear
+    torch.manual_seed(7)
+    with torch.inference_mode():
+        x, ids = torch.randn(rows, 72, device="cuda").to(DT[dtype]), _ids("mixed", rows, 3)
+        m = GatedLinear(72, 40, device="cuda", dtype=DT[dtype]).fix_weights()
+        ref.check(m(x), ref.gated(x.cpu(), m.weight.cpu(), m.bias.cpu(), "silu")["h"], "GatedLinear")
+        m = AdapterLinear.from_linear(torch.nn.Linear(72, 40, device="cuda", dtype=DT[dtype]), 3, 4)
+        m.up.normal_()
+        t = [v.cpu() for v in (m.weight, m.down, m.up)]
+        ref.check(m(x, ids.cuda()), ref.adapter(x.cpu(), *t, ids, m.scale.cpu(), m.bias.cpu())["y"], "AdapterLinear")
