@@ -137,7 +137,7 @@ def adapter_linear(x, weight, a, b, ids, scale=None, bias=None, plan=None):
     dims, K, N = x.dim(), x.shape[-1], weight.shape[0]
     if plan is not None:
         plan.check(weight, gated=False)
-    x2d = x if dims == 2 else x.reshape(-1, K) if K else x.new_empty(x.shape[:-1].numel(), 0)
+    x2d = x if dims == 2 else x.reshape(x.shape[:-1].numel(), K)
     if ids.dim() != 1:
         ids = ids.reshape(-1)
     ops_lib()

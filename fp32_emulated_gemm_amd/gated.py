@@ -118,7 +118,7 @@ def gated_linear(x, weight, bias=None, gate="silu", plan=None):
     if not fits:
         _check(x, weight, bias)
     dims, K, rows = x.dim(), x.shape[-1], weight.shape[0]
-    x2d = x if dims == 2 else x.reshape(-1, K) if K else x.new_empty(x.shape[:-1].numel(), 0)
+    x2d = x if dims == 2 else x.reshape(x.shape[:-1].numel(), K)
     if plan is not None:
         plan.check(weight, gated=True)
     ops_lib()

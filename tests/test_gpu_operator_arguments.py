@@ -1,5 +1,5 @@
 """Arguments of the operators' tensor functions on the GPU: layouts of a weight, rows far
-apart, tangents."""
+apart, tangents, empty inputs of more dimensions."""
 import pytest
 import torch
 
@@ -100,3 +100,30 @@ def test_tangents_are_refused(dtype, M, grad):
         ref.check(h, ref.gated(x.cpu(), w.cpu(), b.cpu(), "silu")["h"], "H")
         t = {k: v.cpu() for k, v in c.items()}
         ref.check(y, ref.adapter(t["x"], t["w"], t["a"], t["b"], ids.cpu(), t["scale"], t["bias"])["y"], "Y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lead", [(2, 3), (2, 50), (0, 3), ()])
+@pytest.mark.parametrize("K", [0, 8])
+def test_leading_dimensions_keep_the_graph(dtype, lead, K):
+    """Any number of leading dimensions, empty ones and an empty K among them, has a gradient."""
+    from fp32_emulated_gemm_amd.adapters import adapter_linear
+    from fp32_emulated_gemm_amd.gated import gated_linear
+    M = torch.Size(lead).numel()
+    x, w, b, dh = gated_inputs(dtype, M, K, 6, True)
+    leaf = x.cuda().reshape(*lead, K).requires_grad_(True)
+    h = gated_linear(leaf, w.cuda(), b.cuda())
+    assert h.shape == (*lead, 6)
+    dx, = torch.autograd.grad(h, (leaf,), dh.cuda().reshape(*lead, 6))
+    want = ref.gated(x, w, b, "silu", dh)
+    ref.check(h.detach().reshape(M, 6), want["h"], "H")
+    ref.check(dx.reshape(M, K), want["dx"], "dx")
+    t = adapter_inputs(dtype, M, K, 6, 2, 4)
+    c = {k: _cuda(v) for k, v in t.items()}
+    ids = torch.arange(M, dtype=torch.int32) % 2
+    leaf = c["x"].reshape(*lead, K).requires_grad_(True)
+    y = adapter_linear(leaf, c["w"], c["a"], c["b"], ids.cuda().reshape(lead), c["scale"], c["bias"])
+    dx, = torch.autograd.grad(y, (leaf,), c["dy"].reshape(*lead, 6))
+    want = ref.adapter(t["x"], t["w"], t["a"], t["b"], ids, t["scale"], t["bias"], t["dy"])
+    ref.check(y.detach().reshape(M, 6), want["y"], "Y")
+    ref.check(dx.reshape(M, K), want["dx"], "dx")
