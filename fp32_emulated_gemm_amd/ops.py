@@ -106,7 +106,7 @@ def rows_of(t):
 def forward_mode():
     """Whether a level of forward-mode differentiation is open: operands may then carry tangents, which
     only a call through an autograd function sees (and refuses)."""
-    return forward_ad._current_level >= 0
+    return getattr(forward_ad, "_current_level", 0) >= 0   # torch's own record; without it, as if one were
 
 
 def scratch(nbytes, like):
