@@ -1,0 +1,140 @@
+// expert_gate.hip -- the gate's backward on sorted rows and the bias gradients.
+//
+// One pass over Z and dH: a workgroup takes a tile of 64 rows of one expert and 64
+// outputs, writes dZ and adds its columns; a second launch adds an expert's tiles
+// in order, so the sums are deterministic.  Memory bounds it.
+#include "expert_device.hpp"
+
+namespace sgemm_emu_dev {
+
+namespace {
+
+constexpr int ROWS = 64, COLS = 64, NT = 256;
+
+template <class T>
+__device__ __forceinline__ void load4(float (&f)[4], const T *p, int64_t left)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = e < left ? Elem<T>::load(p + e) : 0.0f;
+}
+
+// Four elements, columns c.. of a row of dZ (whose pitch is a multiple of 32).
+__device__ __forceinline__ void store4(float *p, const float (&f)[4])
+{
+    *reinterpret_cast<f32x4_t *>(p) = f32x4_t{f[0], f[1], f[2], f[3]};
+}
+__device__ __forceinline__ void store4(uint16_t *p, const float (&f)[4])
+{
+    *reinterpret_cast<uint64_t *>(p) = (uint64_t)pack2(f[0], f[1]) | (uint64_t)pack2(f[2], f[3]) << 32;
+}
+
+template <class T, int GATE>
+__global__ __launch_bounds__(NT) void expert_gate_kernel(ExpertGate g)
+{
+    constexpr int PARTS = GATE >= 0 ? 2 : 1;
+    __shared__ float sums[PARTS][16][COLS];
+    const int lane = threadIdx.x & 63, q = (threadIdx.x & 15) * 4, hi = threadIdx.x >> 4;
+    const RowTile t = find_tile<ROWS>(g.offsets, g.n, g.P, (int)g.n, (int)blockIdx.x, lane);
+    if (t.segment < 0) return;
+    const int64_t c = (int64_t)blockIdx.y * COLS + q, left = g.F - c, h = dz_pitch(g.F) / 2, zp = z_pitch(g.F);
+    float sg[4] = {0, 0, 0, 0}, su[4] = {0, 0, 0, 0};
+    for (int i = 0; i < ROWS / 16; ++i) {
+        const int64_t r = t.row + hi + 16 * i;
+        if (r >= t.end) break;
+        float d[4];
+        load4<T>(d, (const T *)g.dH + r * g.lddh + c, left);
+        if constexpr (GATE < 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sg[e] += d[e];
+        } else {
+            float zg[4], zu[4], a[4];
+            load4<float>(zg, g.Z + r * zp + c, left);
+            load4<float>(zu, g.Z + r * zp + zp / 2 + c, left);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float slope;
+                gate_act_grad<GATE>(zg[e], a[e], slope);
+                zg[e] = e < left ? d[e] * zu[e] * slope : 0.0f;
+                zu[e] = e < left ? d[e] * a[e] : 0.0f;
+                sg[e] += zg[e];
+                su[e] += zu[e];
+            }
+            if (g.dZ != nullptr && c < h) {
+                T *const out = (T *)g.dZ + r * 2 * h + c;
+                store4(out, zg);
+                store4(out + h, zu);
+            }
+        }
+    }
+    if (g.sums == nullptr) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sums[0][hi][q + e] = sg[e];
+        if constexpr (PARTS == 2) sums[1][hi][q + e] = su[e];
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < PARTS * COLS; o += NT) {
+        const int part = o / COLS, col = o % COLS;
+        const int64_t f = (int64_t)blockIdx.y * COLS + col;
+        if (f >= g.F) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += sums[part][i][col];
+        g.sums[(int64_t)blockIdx.x * PARTS * g.F + part * g.F + f] = v;
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(NT) void expert_sum_kernel(ExpertGate g, int64_t cols)
+{
+    const int lane = threadIdx.x & 63, e = (int)blockIdx.y;
+    int before = 0;
+    for (int i = lane; i < e; i += 64) before += count_tiles<ROWS>(g.offsets, g.n, g.P, i, (int)g.n);
+    before = __builtin_amdgcn_readfirstlane(wave_sum(before));
+    // offsets that do not ascend may count more tiles than there are
+    const int most = (int)expert_gate_tiles(g.P, g.n), mine = count_tiles<ROWS>(g.offsets, g.n, g.P, e, (int)g.n);
+    const int tiles = imin(mine, most - imin(before, most));
+    const int64_t c = (int64_t)blockIdx.x * NT + threadIdx.x;
+    if (c >= cols) return;
+    float v = 0.0f;
+    for (int t = 0; t < tiles; ++t) v += g.sums[(int64_t)(before + t) * cols + c];
+    ((T *)g.dbias)[(int64_t)e * cols + c] = Elem<T>::store(v);
+}
+
+template <class T, int GATE>
+hipError_t launch(const ExpertGate &g, hipStream_t stream)
+{
+    const int64_t width = GATE >= 0 ? dz_pitch(g.F) / 2 : g.F, tiles = expert_gate_tiles(g.P, g.n);
+    if (tiles > 0 && width > 0)
+        hipLaunchKernelGGL((expert_gate_kernel<T, GATE>), dim3((unsigned)tiles, (unsigned)((width + COLS - 1) / COLS)),
+                           dim3(NT), 0, stream, g);
+    if (g.dbias != nullptr) {
+        const int64_t cols = GATE >= 0 ? 2 * g.F : g.F;
+        if (cols > 0 && g.n > 0)
+            hipLaunchKernelGGL(expert_sum_kernel<T>, dim3((unsigned)((cols + NT - 1) / NT), (unsigned)g.n), dim3(NT), 0,
+                               stream, g, cols);
+    }
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_gate(const ExpertGate &g, hipStream_t stream)
+{
+    switch (g.gate) {
+    case kSilu: return launch<T, kSilu>(g, stream);
+    case kGelu: return launch<T, kGelu>(g, stream);
+    case kGeluTanh: return launch<T, kGeluTanh>(g, stream);
+    case kSigmoid: return launch<T, kSigmoid>(g, stream);
+    case kRelu: return launch<T, kRelu>(g, stream);
+    default: return launch<T, -1>(g, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_expert_gate(int dtype, const ExpertGate &g, hipStream_t stream)
+{
+    return dtype == kF32 ? launch_gate<float>(g, stream) : launch_gate<uint16_t>(g, stream);
+}
+
+}  // namespace sgemm_emu_dev

@@ -10,8 +10,8 @@
 namespace sgemm_emu_dev {
 
 constexpr int64_t kPadK = 64;   // K of a laid-out operand is padded with zeros to a multiple of this
-inline int64_t pad_k(int64_t k) { return (k + kPadK - 1) / kPadK * kPadK; }
-inline int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+constexpr int64_t pad_k(int64_t k) { return (k + kPadK - 1) / kPadK * kPadK; }
+constexpr int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- low-rank adapters
 // Row t of X belongs to adapter ids[t]; an id outside [0, n) means none.
@@ -131,7 +131,7 @@ hipError_t launch_transpose_padded(int64_t rows, int64_t cols, const uint16_t *X
                                    int64_t out_rows, int64_t ldp, hipStream_t stream);
 // Pre-activations Z are floats whatever the call's type: rows of z_pitch(F), the
 // gate's from column 0, the up projection's from column z_pitch(F) / 2.
-inline int64_t z_pitch(int64_t F) { return 2 * round_up(F, 8); }
+constexpr int64_t z_pitch(int64_t F) { return 2 * round_up(F, 8); }
 
 
 // K == 0: H = act(bias) * bias of the halves (bias null: zeros), and Z where kept.
@@ -141,7 +141,7 @@ hipError_t launch_gate_bias(int64_t M, int64_t F, const float *bias, int gate, f
 // From Z and dH: dZ (rows of dz_pitch(F): gate from 0, up from dz_pitch / 2,
 // zeros between and after), its transpose (2F x pad_k(M), zeros past M), and the
 // column sums' partials (gate_tiles(M) x 2F floats); each may be null.
-inline int64_t dz_pitch(int64_t F) { return 2 * round_up(F, 32); }
+constexpr int64_t dz_pitch(int64_t F) { return 2 * round_up(F, 32); }
 inline int64_t gate_tiles(int64_t M) { return (M + 63) / 64; }
 hipError_t launch_gate_backward(int dtype, int64_t M, int64_t F, const float *Z, const void *dH, int64_t lddh,
                                 int gate, void *dZ, void *dZt, float *sums, hipStream_t stream);

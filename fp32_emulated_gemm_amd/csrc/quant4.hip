@@ -1,0 +1,378 @@
+// quant4.hip -- weights of 4 bits: quantised, packed, unpacked, and their products
+// with few rows.
+//
+// A value q of 0..15 stands for (q - zero) scale.  Packed, a tile of 16 rows by 128
+// columns is 1 KB: lane l's 16 bytes hold row l & 15, dword d the columns 32 d + 8
+// (l >> 4) + e, e = 0..7, at bits 4 (e >> 1) + 16 (e & 1).  That is the first operand
+// of four 16x16x32 MFMAs, so a wave loads a tile in one contiguous access.  Tiles of
+// 16 rows follow each other along K.  Behind the values: scales [group][row] in
+// FP32, then zeros [group][row], 16 added, in a byte.
+//
+// A nibble pair becomes two BF16 with a shift and an and-or: 0x4180 is 16, whose
+// last four mantissa bits count ones, so 0x4180 | q << 3 is 16 + q, exactly.  With
+// xs = the sum of x over the group (an MFMA with ones, shared by all rows of W),
+//   sum (q - zero) x = sum (16 + q) x - (16 + zero) xs,
+// formed in FP32 and scaled once a group.  The offset of 16 costs two or three of
+// FP32's 24 bits (128 + q, one shift less, would cost five).  FP32 rows of X come in
+// three BF16 parts; a weight is one, so three products in three bands.
+#include "expert_device.hpp"
+
+namespace sgemm_emu_dev {
+
+namespace {
+
+constexpr int WAVES = 8, NT = 64 * WAVES;
+constexpr int KB = 128;                      // columns of a tile
+
+// ---------------------------------------------------------------- quantise, pack, unpack
+
+// One wave per group and row: 32 to 128 columns.
+template <class T>
+__global__ __launch_bounds__(256) void quantize_kernel(Quant4 w, const T *W, uint8_t *q, float *scale, uint8_t *zero)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t groups = (w.K + w.group - 1) / w.group, total = w.n * w.N * groups;
+    for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < total; u += (int64_t)gridDim.x * 4) {
+        const int64_t row = u / groups, c = (u - row * groups) * w.group;
+        const int64_t left = lmin(w.group, w.K - c);
+        float v[2], lo = 0.0f, hi = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = lane + 64 * i;
+            v[i] = at < left ? Elem<T>::load(W + row * w.K + c + at) : 0.0f;
+            lo = fminf(lo, v[i]);
+            hi = fmaxf(hi, v[i]);
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) {
+            lo = fminf(lo, __shfl_xor(lo, d));
+            hi = fmaxf(hi, __shfl_xor(hi, d));
+        }
+        float s, z = 8.0f;
+        if (zero != nullptr) {
+            s = hi * (1.0f / 15.0f) - lo * (1.0f / 15.0f);       // apart: the difference may pass the largest float
+            z = s > 0.0f ? fminf(fmaxf(__builtin_rintf(-lo / s), 0.0f), 15.0f) : 0.0f;
+        } else {
+            s = fmaxf(hi, -lo) * (1.0f / 7.0f);
+        }
+        const float most = zero != nullptr ? 15.0f - z : 7.0f, least = zero != nullptr ? -z : -7.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = lane + 64 * i;
+            const float t = s > 0.0f ? __builtin_rintf(v[i] / s) : 0.0f;
+            if (at < left) q[row * w.K + c + at] = (uint8_t)(int)(fminf(fmaxf(t, least), most) + z);
+        }
+        if (lane == 0) {
+            scale[u] = s;
+            if (zero != nullptr) zero[u] = (uint8_t)(int)z;
+        }
+    }
+}
+
+struct Packed {
+    const uint32_t *values;
+    const float *scale;
+    const uint8_t *zero;
+};
+
+__host__ __device__ __forceinline__ Packed packed_bank(const Quant4 &w, const void *packed, int64_t bank)
+{
+    const char *const p = (const char *)packed + bank * w.bank_bytes();
+    return Packed{(const uint32_t *)p, (const float *)(p + w.value_bytes()),
+                  (const uint8_t *)(p + w.value_bytes() + w.scale_bytes())};
+}
+
+// One thread per dword of values.
+__global__ __launch_bounds__(256) void pack_values_kernel(Quant4 w, const uint8_t *q, char *packed)
+{
+    const int64_t per = w.value_bytes() / 4, total = w.n * per;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+        const int64_t bank = u / per, at = u - bank * per;
+        const int64_t tile = at >> 8, blocks = w.blocks();
+        const int l = (int)(at >> 2) & 63, d = (int)at & 3;
+        const int64_t row = tile / blocks * 16 + (l & 15), c = tile % blocks * KB + d * 32 + (l >> 4) * 8;
+        uint32_t v = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (row < w.N && c + e < w.K)
+                v |= (uint32_t)(q[(bank * w.N + row) * w.K + c + e] & 15) << (4 * (e >> 1) + 16 * (e & 1));
+        ((uint32_t *)(packed + bank * w.bank_bytes()))[at] = v;
+    }
+}
+
+__global__ __launch_bounds__(256) void pack_scales_kernel(Quant4 w, const float *scale, const uint8_t *zero, char *packed)
+{
+    const int64_t rows = w.rows(), per = w.groups() * rows, total = w.n * per, groups = (w.K + w.group - 1) / w.group;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+        const int64_t bank = u / per, at = u - bank * per, g = at / rows, row = at - g * rows;
+        const bool in = row < w.N && g < groups;
+        const int64_t src = (bank * w.N + row) * groups + g;
+        char *const p = packed + bank * w.bank_bytes() + w.value_bytes();
+        ((float *)p)[at] = in ? scale[src] : 0.0f;
+        if (w.zeros) ((uint8_t *)(p + w.scale_bytes()))[at] = in ? 16 + (zero[src] & 15) : 24;
+    }
+}
+
+// One thread per dword of values: eight columns of a row.
+template <class T>
+__global__ __launch_bounds__(256) void unpack_kernel(Quant4 w, const void *packed, T *W)
+{
+    const int64_t per = w.value_bytes() / 4, total = w.n * per, rows = w.rows();
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+        const int64_t bank = u / per, at = u - bank * per;
+        const Packed p = packed_bank(w, packed, bank);
+        const int64_t tile = at >> 8, blocks = w.blocks();
+        const int l = (int)(at >> 2) & 63, d = (int)at & 3;
+        const int64_t row = tile / blocks * 16 + (l & 15), c = tile % blocks * KB + d * 32 + (l >> 4) * 8;
+        if (row >= w.N) continue;
+        const uint32_t v = p.values[at];
+        const int64_t g = c / w.group * rows + row;
+        const float s = p.scale[g], z = w.zeros ? (float)(p.zero[g] - 16) : 8.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < w.K)
+                W[(bank * w.N + row) * w.K + c + e] =
+                    Elem<T>::store(((float)((v >> (4 * (e >> 1) + 16 * (e & 1))) & 15) - z) * s);
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Eight values 16 + q of a dword as BF16.
+__device__ __forceinline__ bf16x8_t widen(uint32_t w)
+{
+    u32x4_t v;
+    v[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
+    v[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
+    v[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
+    v[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+    return __builtin_bit_cast(bf16x8_t, v);
+}
+
+template <class T>
+struct Xs {
+    static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+};
+
+// GROUP columns share a scale.  A workgroup takes NB tiles of 16 rows of W (with a
+// gate, NB / 2 of the gate's and those of the up projection's same outputs) and 16 MB
+// rows of X at a time; its waves take the blocks of 128 columns in turn.
+template <class T, int NB, int MB, int GROUP, int GATE>
+__global__ __launch_bounds__(NT) void quant4_few_kernel(Quant4 w, Quant4Product g)
+{
+    constexpr int PARTS = Xs<T>::PARTS, STEPS = GROUP / 32, GROUPS = KB / GROUP;
+    constexpr bool GATED = GATE >= 0;
+    constexpr int OUT = GATED ? NB / 2 * 16 : NB * 16;
+    __shared__ __attribute__((aligned(16))) f32x4_t sums[WAVES][NB][MB][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t e = blockIdx.y, F = GATED ? w.N / 2 : w.N, n0 = (int64_t)blockIdx.x * OUT;
+    const int64_t r0 = expert_start(g.offsets, e, g.P), r1 = expert_end(g.offsets, e, w.n, g.P);
+    T *const H = (T *)g.H;
+    if (e >= w.n) {                                        // rows of no expert
+        for (int64_t o = threadIdx.x; o < (r1 - r0) * OUT; o += NT) {
+            const int64_t n = n0 + o % OUT;
+            if (n < F) H[(r0 + o / OUT) * g.ldh + n] = Elem<T>::store(0.0f);
+        }
+        return;
+    }
+    const Packed p = packed_bank(w, g.packed, e);
+    const int64_t blocks = w.blocks(), rows = w.rows();
+    // Rows of W behind each tile: a gate's up rows begin at F, inside a tile where F is
+    // no multiple of 16, so a lane's row is found one by one.
+    int64_t wrow[NB], srow[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int64_t base = GATED ? (b < NB / 2 ? 0 : F) + n0 + (b % (NB / 2)) * 16 : n0 + b * 16;
+        wrow[b] = lmin(base + (lane & 15), rows - 1);
+        srow[b] = base + 4 * (lane >> 4);
+    }
+    const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+    for (int64_t m0 = r0; m0 < r1; m0 += 16 * MB) {
+        f32x4_t acc[NB][MB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m = 0; m < MB; ++m) acc[b][m] = f32x4_t{};
+        for (int64_t kb = wave; kb < blocks; kb += WAVES) {
+            u32x4_t v[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                v[b] = *reinterpret_cast<const u32x4_t *>(
+                    p.values + (((wrow[b] >> 4) * blocks + kb) << 8) + (((lane & 48) | (wrow[b] & 15)) << 2));
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr) {
+                f32x4_t part[PARTS][NB][MB], xs[PARTS][MB];
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) {
+                        xs[q][m] = f32x4_t{};
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) part[q][b][m] = f32x4_t{};
+                    }
+#pragma unroll
+                for (int st = 0; st < STEPS; ++st) {
+                    const int d = gr * STEPS + st;
+                    const int64_t k = kb * KB + d * 32 + 8 * (lane >> 4);
+                    bf16x8_t wf[NB];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) wf[b] = widen(v[b][d]);
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) {
+                        const int64_t row = m0 + m * 16 + (lane & 15);
+                        Eight<T> x;
+                        x.load((const T *)g.X + lmin(row, r1 - 1) * g.ldx + k, row < r1 ? w.K - k : 0);
+                        u32x4_t xp[PARTS];
+                        if constexpr (PARTS == 3) split8_nearest(x, xp);
+                        else xp[0] = x.v[0];
+#pragma unroll
+                        for (int q = 0; q < PARTS; ++q) {
+                            const bf16x8_t xf = __builtin_bit_cast(bf16x8_t, xp[q]);
+                            xs[q][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf, xs[q][m], 0, 0, 0);
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)
+                                part[q][b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[b], xf, part[q][b][m], 0, 0, 0);
+                        }
+                    }
+                }
+                const int64_t at = (kb * GROUPS + gr) * rows;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float s[4], z[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int64_t r = lmin(srow[b] + q, rows - 1);
+                        s[q] = p.scale[at + r];
+                        z[q] = w.zeros ? (float)p.zero[at + r] : 24.0f;
+                    }
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float t = __builtin_fmaf(-z[q], xs[0][m][q], part[0][b][m][q]);
+                            if constexpr (PARTS == 3) {
+                                const float t1 = __builtin_fmaf(-z[q], xs[1][m][q], part[1][b][m][q]);
+                                const float t2 = __builtin_fmaf(-z[q], xs[2][m][q], part[2][b][m][q]);
+                                t += __builtin_fmaf(t2, 0x1p-16f, t1 * 0x1p-8f);
+                            }
+                            acc[b][m][q] = __builtin_fmaf(s[q], t, acc[b][m][q]);
+                        }
+                }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m = 0; m < MB; ++m) sums[wave][b][m][lane] = acc[b][m];
+        __syncthreads();
+        const T *const bias = g.bias != nullptr ? (const T *)g.bias + e * w.N : nullptr;
+        auto total = [&](int b, int n, int m) {            // row n of tile b, row m of X
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WAVES; ++i) v += sums[i][b][m >> 4][(n >> 2) * 16 + (m & 15)][n & 3];
+            return v;
+        };
+        for (int o = threadIdx.x; o < OUT * 16 * MB; o += NT) {
+            const int n = o % OUT, m = o / OUT;
+            if (n0 + n >= F || m0 + m >= r1) continue;
+            float v = total(n >> 4, n & 15, m);
+            if (bias != nullptr) v += Elem<T>::load(bias + n0 + n);
+            if constexpr (GATED) {
+                float u = total(NB / 2 + (n >> 4), n & 15, m);
+                if (bias != nullptr) u += Elem<T>::load(bias + F + n0 + n);
+                v = gate_act<GATE>(v) * u;
+            }
+            H[(m0 + m) * g.ldh + n0 + n] = Elem<T>::store(v);
+        }
+        __syncthreads();
+    }
+}
+
+unsigned blocks_for(int64_t items, int64_t per)
+{
+    const int64_t b = (items + per - 1) / per;
+    return (unsigned)(b < 1 ? 1 : b < 16384 ? b : 16384);
+}
+
+template <class T, int NB, int MB, int GROUP, int GATE>
+hipError_t launch_few(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
+{
+    const int64_t out = GATE >= 0 ? w.N / 2 : w.N, per = GATE >= 0 ? NB * 8 : NB * 16;
+    const dim3 grid((unsigned)((out + per - 1) / per), (unsigned)(w.n + (g.offsets != nullptr ? 1 : 0)));
+    hipLaunchKernelGGL((quant4_few_kernel<T, NB, MB, GROUP, GATE>), grid, dim3(NT), 0, stream, w, g);
+    return hipGetLastError();
+}
+
+template <class T, int GROUP, int GATE>
+hipError_t few_rows(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
+{
+    if (g.P <= 16 * w.n) return launch_few<T, 2, 1, GROUP, GATE>(w, g, stream);
+    return launch_few<T, 2, 2, GROUP, GATE>(w, g, stream);
+}
+
+template <class T, int GROUP>
+hipError_t few_gate(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
+{
+    switch (g.gate) {
+    case kSilu: return few_rows<T, GROUP, kSilu>(w, g, stream);
+    case kGelu: return few_rows<T, GROUP, kGelu>(w, g, stream);
+    case kGeluTanh: return few_rows<T, GROUP, kGeluTanh>(w, g, stream);
+    case kSigmoid: return few_rows<T, GROUP, kSigmoid>(w, g, stream);
+    case kRelu: return few_rows<T, GROUP, kRelu>(w, g, stream);
+    default: return few_rows<T, GROUP, -1>(w, g, stream);
+    }
+}
+
+template <class T>
+hipError_t few_group(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
+{
+    switch (w.group) {
+    case 32: return few_gate<T, 32>(w, g, stream);
+    case 64: return few_gate<T, 64>(w, g, stream);
+    default: return few_gate<T, 128>(w, g, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_quant4_quantize(int dtype, const Quant4 &w, const void *W, uint8_t *q, float *scale, uint8_t *zero,
+                                  hipStream_t stream)
+{
+    const int64_t groups = w.n * w.N * ((w.K + w.group - 1) / w.group);
+    if (groups == 0) return hipSuccess;
+    const dim3 grid(blocks_for(groups, 4));
+    if (dtype == kF32) hipLaunchKernelGGL(quantize_kernel<float>, grid, dim3(256), 0, stream, w, (const float *)W, q, scale, zero);
+    else hipLaunchKernelGGL(quantize_kernel<uint16_t>, grid, dim3(256), 0, stream, w, (const uint16_t *)W, q, scale, zero);
+    return hipGetLastError();
+}
+
+hipError_t launch_quant4_pack(const Quant4 &w, const uint8_t *q, const float *scale, const uint8_t *zero, void *packed,
+                              hipStream_t stream)
+{
+    const int64_t dwords = w.n * w.value_bytes() / 4;
+    if (dwords == 0) return hipSuccess;
+    hipLaunchKernelGGL(pack_values_kernel, dim3(blocks_for(dwords, 256)), dim3(256), 0, stream, w, q, (char *)packed);
+    hipLaunchKernelGGL(pack_scales_kernel, dim3(blocks_for(w.n * w.groups() * w.rows(), 256)), dim3(256), 0, stream, w,
+                       scale, zero, (char *)packed);
+    return hipGetLastError();
+}
+
+hipError_t launch_quant4_unpack(int dtype, const Quant4 &w, const void *packed, void *W, hipStream_t stream)
+{
+    const int64_t dwords = w.n * w.value_bytes() / 4;
+    if (dwords == 0) return hipSuccess;
+    const dim3 grid(blocks_for(dwords, 256));
+    if (dtype == kF32) hipLaunchKernelGGL(unpack_kernel<float>, grid, dim3(256), 0, stream, w, packed, (float *)W);
+    else hipLaunchKernelGGL(unpack_kernel<uint16_t>, grid, dim3(256), 0, stream, w, packed, (uint16_t *)W);
+    return hipGetLastError();
+}
+
+bool quant4_few(const Quant4 &w, int64_t P) { return P <= 64 || P <= 16 * w.n; }
+
+hipError_t launch_quant4_few(int dtype, const Quant4 &w, const Quant4Product &g, hipStream_t stream)
+{
+    if (g.P == 0 || w.N == 0) return hipSuccess;
+    return dtype == kF32 ? few_group<float>(w, g, stream) : few_group<uint16_t>(w, g, stream);
+}
+
+}  // namespace sgemm_emu_dev
