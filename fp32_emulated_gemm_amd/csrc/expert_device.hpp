@@ -104,29 +104,29 @@ struct Eight {
     }
 };
 
-// The parts of eight FP32 values, each stage rounded to nearest even by the
-// hardware's conversion; rounding beyond the largest BF16, Inf and NaN show in t
-// and take the exact path.
+// Rounded to BF16, two at a time; beyond the largest BF16 that, not Inf.
+__device__ __forceinline__ uint32_t pack2_finite(float a, float b)
+{
+    constexpr float MOST = 3.38953139e38f;
+    return pack2(__builtin_amdgcn_fmed3f(a, -MOST, MOST), __builtin_amdgcn_fmed3f(b, -MOST, MOST));
+}
+
+// The parts of eight FP32 values, x = x0 + 2^-8 x1 + 2^-16 x2, each stage rounded
+// to nearest even by the hardware's conversion.  x0 and x1 stay finite: an Inf or
+// NaN comes through in x2 (Inf - finite), so its products are those of IEEE.
 __device__ __forceinline__ void split8_nearest(const Eight<float> &in, u32x4_t (&p)[3])
 {
-    float x[8], t[8];
-    float probe = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(in.v[e >> 2][e & 3]);
-    uint32_t w0[4], w1[4], w2[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        w0[i] = pack2(x[2 * i], x[2 * i + 1]);
-        t[2 * i] = (x[2 * i] - u2f(w0[i] << 16)) * 256.0f;
-        t[2 * i + 1] = (x[2 * i + 1] - u2f(w0[i] & 0xFFFF0000u)) * 256.0f;
-        w1[i] = pack2(t[2 * i], t[2 * i + 1]);
-        const float a = (t[2 * i] - u2f(w1[i] << 16)) * 256.0f, b = (t[2 * i + 1] - u2f(w1[i] & 0xFFFF0000u)) * 256.0f;
-        w2[i] = pack_bf16x2(f2u(a), f2u(b));         // exact: 8 significant bits
-        probe += __builtin_fabsf(t[2 * i]) + __builtin_fabsf(t[2 * i + 1]);
+        const float x = __uint_as_float(in.v[i >> 1][2 * (i & 1)]), y = __uint_as_float(in.v[i >> 1][2 * (i & 1) + 1]);
+        const uint32_t w0 = pack2_finite(x, y);
+        const float t = (x - u2f(w0 << 16)) * 256.0f, u = (y - u2f(w0 & 0xFFFF0000u)) * 256.0f;
+        const uint32_t w1 = pack2_finite(t, u);
+        const float a = (t - u2f(w1 << 16)) * 256.0f, b = (u - u2f(w1 & 0xFFFF0000u)) * 256.0f;
+        p[0][i] = w0;
+        p[1][i] = w1;
+        p[2][i] = pack2(a, b);               // exact where finite: 8 significant bits
     }
-    if (!(probe < 3.0e38f)) split8_packed<true>(x, w0, w1, w2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { p[0][i] = w0[i]; p[1][i] = w1[i]; p[2][i] = w2[i]; }
 }
 
 }  // namespace sgemm_emu_dev

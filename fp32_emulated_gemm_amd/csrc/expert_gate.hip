@@ -36,7 +36,7 @@ __global__ __launch_bounds__(NT) void expert_gate_kernel(ExpertGate g)
     const int lane = threadIdx.x & 63, q = (threadIdx.x & 15) * 4, hi = threadIdx.x >> 4;
     const RowTile t = find_tile<ROWS>(g.offsets, g.n, g.P, (int)g.n, (int)blockIdx.x, lane);
     if (t.segment < 0) return;
-    const int64_t c = (int64_t)blockIdx.y * COLS + q, left = g.F - c, h = dz_pitch(g.F) / 2, zp = z_pitch(g.F);
+    const int64_t c = (int64_t)blockIdx.y * COLS + q, left = g.F - c, h = expert_dz_pitch(g.F) / 2, zp = z_pitch(g.F);
     float sg[4] = {0, 0, 0, 0}, su[4] = {0, 0, 0, 0};
     for (int i = 0; i < ROWS / 16; ++i) {
         const int64_t r = t.row + hi + 16 * i;
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(NT) void expert_sum_kernel(ExpertGate g, int64_t co
 template <class T, int GATE>
 hipError_t launch(const ExpertGate &g, hipStream_t stream)
 {
-    const int64_t width = GATE >= 0 ? dz_pitch(g.F) / 2 : g.F, tiles = expert_gate_tiles(g.P, g.n);
+    const int64_t width = GATE >= 0 ? expert_dz_pitch(g.F) / 2 : g.F, tiles = expert_gate_tiles(g.P, g.n);
     if (tiles > 0 && width > 0)
         hipLaunchKernelGGL((expert_gate_kernel<T, GATE>), dim3((unsigned)tiles, (unsigned)((width + COLS - 1) / COLS)),
                            dim3(NT), 0, stream, g);

@@ -25,7 +25,7 @@ namespace {
 constexpr int BK = 32;                       // K step: one MFMA's
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-enum { FORWARD, BACK_X, BACK_W };
+enum { FORWARD = kForward, BACK_X = kBackX, BACK_W = kBackW };
 
 // PLANES: BF16 parts of an element; BANDS: accumulators.
 template <class T>
@@ -360,18 +360,21 @@ hipError_t launch_forward(const ExpertProduct &g, hipStream_t stream)
 hipError_t launch_expert_forward(int dtype, const ExpertProduct &g, hipStream_t stream)
 {
     if (g.P == 0 || g.N == 0) return hipSuccess;
+    if (dtype == kBF16 && expert_lies(kForward, g)) return launch_expert_bf16(kForward, g, stream);
     return dtype == kF32 ? launch_forward<float>(g, stream) : launch_forward<uint16_t>(g, stream);
 }
 
 hipError_t launch_expert_dx(int dtype, const ExpertProduct &g, hipStream_t stream)
 {
     if (g.P == 0 || g.N == 0) return hipSuccess;
+    if (dtype == kBF16 && expert_lies(kBackX, g)) return launch_expert_bf16(kBackX, g, stream);
     return dtype == kF32 ? launch_op<float, BACK_X, -1>(g, stream) : launch_op<uint16_t, BACK_X, -1>(g, stream);
 }
 
 hipError_t launch_expert_dw(int dtype, const ExpertProduct &g, hipStream_t stream)
 {
     if (g.n == 0 || g.M == 0 || g.N == 0) return hipSuccess;
+    if (dtype == kBF16 && expert_lies(kBackW, g)) return launch_expert_bf16(kBackW, g, stream);
     return dtype == kF32 ? launch_op<float, BACK_W, -1>(g, stream) : launch_op<uint16_t, BACK_W, -1>(g, stream);
 }
 

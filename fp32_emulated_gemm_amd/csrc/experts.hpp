@@ -72,8 +72,17 @@ hipError_t launch_expert_dx(int dtype, const ExpertProduct &g, hipStream_t strea
 // C_e (map's rows x N) = A_e^T B_e over the rows of expert e: A = dZ (M columns), B = X (N columns).
 hipError_t launch_expert_dw(int dtype, const ExpertProduct &g, hipStream_t stream);
 
+// The three for bfloat16 operands whose rows start at 16-byte pieces and hold whole
+// ones (expert_bf16.hip); expert_lies() tells whether a product's do.
+enum { kForward, kBackX, kBackW };
+bool expert_lies(int op, const ExpertProduct &g);
+hipError_t launch_expert_bf16(int op, const ExpertProduct &g, hipStream_t stream);
+
 // ---------------------------------------------------------------- gate backward (expert_gate.hip)
-// dZ (rows of dz_pitch(F): gate from 0, up from dz_pitch / 2, zeros between and
+// Halves of a row of dZ are padded to whole tiles, so that no step over its columns
+// and no tile of them meets both.
+constexpr int64_t expert_dz_pitch(int64_t F) { return 2 * round_up(F, 128); }
+// dZ (rows of expert_dz_pitch(F): gate from 0, up from the half, zeros between and
 // after) from Z and dH, and the bias gradients' partial sums, a row of 2F floats
 // (N without a gate) for each tile of 64 rows of an expert; each may be null.
 struct ExpertGate {

@@ -66,7 +66,7 @@ struct BackwardWs {
     BackwardWs(void *ws, int dtype, int64_t P, int64_t N, int64_t n, int gate, bool dbias)
     {
         Carve c(ws);
-        dZ = gate >= 0 ? (void *)c.take<char>(P * dz_pitch(N / 2) * size_of(dtype)) : nullptr;
+        dZ = gate >= 0 ? (void *)c.take<char>(P * expert_dz_pitch(N / 2) * size_of(dtype)) : nullptr;
         sums = dbias ? c.take<float>(expert_gate_tiles(P, n) * N) : nullptr;
         bytes = c.bytes;
     }
@@ -244,7 +244,7 @@ int sgemm_emu_expert_linear_backward(int dtype, int64_t P, int64_t N, int64_t K,
         LAUNCH(launch_expert_gate(dtype, q, s));
     }
     const void *const dZ = gate >= 0 ? w.dZ : dH;
-    const int64_t pitch = gate >= 0 ? dz_pitch(outs) : N;
+    const int64_t pitch = gate >= 0 ? expert_dz_pitch(outs) : N;
     ExpertProduct g{};
     g.P = P; g.n = n;
     g.offsets = offsets;
