@@ -81,6 +81,34 @@ struct Operand {
     }
 };
 
+// A copy of 16 bytes a lane from `at` + off to LDS, as the builtin's, written out: the
+// compiler does not know how the transposing reads relate to copies in flight and
+// puts a wait for all of them before each group of reads, half a step too early.
+// Here the steps' own waits (step_barrier) order them.  The wait states are those
+// between a vector write of a scalar register, or a write of m0 (which nothing else
+// in these kernels uses), and its use.
+__device__ __forceinline__ void copy_untracked(uint32_t lds, const uint16_t *at, uint32_t off)
+{
+    const uint64_t p = (uint64_t)(uintptr_t)at;
+    const u32x4_t r = {(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p),
+                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)), 0xFFFFFFF0u, (uint32_t)RSRC_WORD3};
+    asm volatile("s_mov_b32 m0, %0\n\t"
+                 "s_nop 4\n\t"
+                 "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(r)
+                 : "memory");
+}
+
+// Which of a product's 256 x 256 tiles a launch covers: ALL (tiles of any size);
+// WHOLE, all of them or, where the last round would fill less than half of the CUs,
+// the rounds before it; REST, what WHOLE leaves, in quarters, two to a CU.  How many
+// there are is known on the device only.
+enum { ALL, WHOLE, REST };
+__device__ __forceinline__ int whole_rounds(int tiles, int slots)
+{
+    const int rest = tiles % slots;
+    return 2 * rest > slots ? tiles : tiles - rest;
+}
+
 // Rows of B behind tile row c of a gated product: see b_row in bf16_gemm.hip.
 template <bool GATED>
 __device__ __forceinline__ int64_t bank_row(int64_t N, int64_t n0, int c)
@@ -93,7 +121,7 @@ __device__ __forceinline__ int64_t bank_row(int64_t N, int64_t n0, int c)
     }
 }
 
-template <class T, int OP, int GATE>
+template <class T, int OP, int GATE, int PART>
 __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertProduct g)
 {
     constexpr bool GATED = GATE >= 0, A_KM = OP == kBackW, B_KM = OP != kForward;
@@ -103,30 +131,54 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
 
+    // Tile `index` of REST's 256 x 256 tiles or this launch's own, in the order of
+    // tile_of_index; of the former, this workgroup takes a quarter.
+    constexpr bool QUARTER = PART == REST;
+    constexpr int SIZE_M = QUARTER ? 256 : T::BM;
     int64_t e, m0, m_end, K, r0 = 0;
-    int tm, tn;
+    int rows, tiles, tm, tn;
+    RowTiles<SIZE_M> row_tiles(g.offsets, g.n, g.P, OP == kBackW ? 0 : (int)g.n + 1, lane);
     if constexpr (OP == kBackW) {
-        const int per = g.tiles_m * g.tiles_n, v = (int)blockIdx.x % per;
-        e = (int)blockIdx.x / per;
-        tm = v / g.tiles_n;
-        tn = v % g.tiles_n;
-        m0 = (int64_t)tm * T::BM;
+        rows = g.tiles_m;
+        tiles = (int)g.n * rows * g.tiles_n;
+    } else {
+        rows = row_tiles.total;
+        tiles = rows * g.tiles_n;
+    }
+    int index = QUARTER ? (int)blockIdx.x >> 2 : (int)blockIdx.x;
+    if constexpr (PART == ALL) {
+        if (index >= tiles) return;
+        if constexpr (OP != kBackW) index = xcd_order(index, tiles);
+    } else {
+        const int whole = whole_rounds(tiles, g.num_cus);
+        if (index >= (QUARTER ? tiles - whole : whole)) return;
+        index = QUARTER ? whole + index : OP == kBackW ? index : xcd_order(index, whole);
+    }
+    if constexpr (OP == kBackW) {
+        const int per = rows * g.tiles_n;
+        e = index / per;
+        // each expert's tiles over all XCDs: their lengths differ from expert to expert
+        tile_at(xcd_order(index - (int)e * per, per), rows, g.tiles_n, imin(rows, 8), tm, tn);
+        m0 = (int64_t)tm * SIZE_M;
         m_end = g.M;
         r0 = expert_start(g.offsets, e, g.P);
         K = expert_end(g.offsets, e, g.n, g.P) - r0;
     } else {
-        const int segments = (int)g.n + 1;
-        const int rows = all_tiles<T::BM>(g.offsets, g.n, g.P, segments, lane), tiles = rows * g.tiles_n;
-        if ((int)blockIdx.x >= tiles) return;
-        tile_of_index((int)blockIdx.x, tiles, rows, g.tiles_n, imin(rows, 8), tm, tn);
-        const RowTile r = find_tile<T::BM>(g.offsets, g.n, g.P, segments, tm, lane);
+        tile_at(index, rows, g.tiles_n, imin(rows, 8), tm, tn);
+        const RowTile r = row_tiles.find(tm);
         if (r.segment < 0) return;
         e = r.segment;
         m0 = r.row;
         m_end = r.end;
         K = e < g.n ? g.K : 0;                             // rows of no expert: zeros
     }
-    const int64_t n0 = (int64_t)tn * T::BN;
+    int64_t n0 = (int64_t)tn * (QUARTER ? 256 : T::BN);
+    if constexpr (QUARTER) {
+        static_assert(T::BM == 128 && T::BN == 128, "quarters of 256 x 256");
+        m0 += (blockIdx.x & 2) * 64;
+        n0 += (blockIdx.x & 1) * 128;
+        if (m0 >= m_end || n0 >= (GATED ? round_up(g.N, 32) : g.N)) return;
+    }
     const bool there = OP == kBackW || e < g.n;
     const uint16_t *const A = (const uint16_t *)g.A;
     const uint16_t *const B = (const uint16_t *)g.B + (OP == kBackW || !there ? 0 : e * g.bank);
@@ -140,11 +192,15 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
     if constexpr (B_KM) ob.columns(g.ldb, n0, g.N, wave, lane);
     else ob.rows(B, g.ldb, klast, wave, lane, [&](int c) { return bank_row<GATED>(g.N, n0, c); });
 
-    typedef __attribute__((address_space(3))) void lds_void_t;
     // One copy of 1 KB: by a lane's offset from `at`, `soff` bytes further.
     auto copy = [&](uint16_t *buf, int q, const uint16_t *at, uint32_t off, int soff) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(at, 0xFFFFFFF0ll), (lds_void_t *)(buf + q * 512), 16, (int)off,
-                                                 soff, 0, 0);
+        typedef __attribute__((address_space(3))) void lds_void_t;
+        if constexpr (OP == kForward) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(at, 0xFFFFFFF0ll), (lds_void_t *)(buf + q * 512), 16, (int)off,
+                                                     soff, 0, 0);
+        } else {
+            copy_untracked((uint32_t)(uintptr_t)(lds_void_t *)(buf + q * 512), at, off);
+        }
     };
     // Copies past the last step repeat it (nobody reads them).
     auto stage = [&](int kt) {
@@ -157,7 +213,7 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
         for (int d = 0; d < OA::COPIES; ++d) {
             const int q = wave * OA::COPIES + d;
             if constexpr (A_KM) copy(buf, q, A + (r0 + k0) * g.lda + m0, oa.row[d] < left ? oa.off[d] : OUT_OF_RANGE, 0);
-            else copy(buf, q, oa.p[d], last ? oa.end[d] : oa.off[d], k * (KS * 2));
+            else copy(buf, q, OP == kForward ? oa.p[d] : oa.p[d] + k0, last ? oa.end[d] : oa.off[d], k * (KS * 2));
         }
         // dX: a step lies in one half of dZ's columns (h is a multiple of KS, or K itself)
         const bool up = OP == kBackX && k0 >= g.map.h;
@@ -276,20 +332,17 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
     }
 }
 
-template <class T, int OP, int GATE>
-hipError_t launch_tile(ExpertProduct g, hipStream_t stream)
+template <class T, int OP, int GATE, int PART>
+hipError_t launch_part(ExpertProduct g, hipStream_t stream)
 {
-    g.tiles_n = (int)((g.N + T::BN - 1) / T::BN);
-    int64_t blocks;
-    if constexpr (OP == kBackW) {
-        g.tiles_m = (int)((g.M + T::BM - 1) / T::BM);
-        blocks = g.n * g.tiles_m * g.tiles_n;
-    } else {
-        const int64_t segments = g.n + 1;
-        blocks = (g.P / T::BM + (segments < g.P ? segments : g.P)) * g.tiles_n;
-    }
+    constexpr int BM = PART == REST ? 256 : T::BM, BN = PART == REST ? 256 : T::BN;
+    g.tiles_m = (int)((g.M + BM - 1) / BM);                // dW only: elsewhere from the offsets
+    g.tiles_n = (int)((g.N + BN - 1) / BN);
+    const int64_t segments = g.n + 1, rows = OP == kBackW ? g.n * g.tiles_m : g.P / BM + (segments < g.P ? segments : g.P);
+    int64_t blocks = rows * g.tiles_n;
+    if (PART == REST) blocks = 4 * (g.num_cus / 2 < blocks ? g.num_cus / 2 : blocks);
     if (blocks * T::NT >= (int64_t)1 << 32) return hipErrorInvalidValue;   // more work-items than a launch can have
-    hipLaunchKernelGGL((expert_bf16_kernel<T, OP, GATE>), dim3((unsigned)blocks), dim3(T::NT), 0, stream, g);
+    hipLaunchKernelGGL((expert_bf16_kernel<T, OP, GATE, PART>), dim3((unsigned)blocks), dim3(T::NT), 0, stream, g);
     return hipGetLastError();
 }
 
@@ -301,21 +354,19 @@ enum { TILE_64, TILE_128, TILE_256, TILES };
 int best_tile(int op, const ExpertProduct &g)
 {
     static const struct { int size, per_cu, step, fixed; } t[TILES] = {{64, 2, 38, 20}, {128, 2, 82, 50}, {256, 1, 138, 100}};
+    const int64_t steps = ((op == kBackW ? g.P / g.n : g.K) + KS - 1) / KS;
+    // kept pre-activations leave at a tile's end, 256 KB of a 256 x 256 tile
+    const int64_t keep = g.Z != nullptr ? 30 : 0;
+    auto round = [&](int i, int64_t step) { return steps * step + t[i].fixed * 10 + keep * t[i].size * t[i].size * t[i].per_cu / 800; };
     int best = TILE_64;
     int64_t least = INT64_MAX;
     for (int i = 0; i < TILES; ++i) {
-        const int64_t s = t[i].size, tn = (g.N + s - 1) / s, slots = (int64_t)g.num_cus * t[i].per_cu;
-        int64_t tiles, steps;
-        if (op == kBackW) {
-            tiles = g.n * ((g.M + s - 1) / s) * tn;
-            steps = (g.P / g.n + KS - 1) / KS;
-        } else {
-            const int64_t rows = g.P / s + (g.n + 1) / 2;
-            tiles = (rows > 0 ? rows : 1) * tn;
-            steps = (g.K + KS - 1) / KS;
-        }
-        const int64_t step = i == TILE_64 && tiles <= g.num_cus ? 22 : t[i].step;
-        const int64_t c = (tiles + slots - 1) / slots * (steps * step + t[i].fixed * 10);
+        const int64_t s = t[i].size, slots = (int64_t)g.num_cus * t[i].per_cu;
+        const int64_t rows = op == kBackW ? g.n * ((g.M + s - 1) / s) : g.P / s + (g.n + 1) / 2;
+        const int64_t tiles = (rows > 0 ? rows : 1) * ((g.N + s - 1) / s), rest = tiles % slots;
+        const int64_t one = round(i, i == TILE_64 && tiles <= g.num_cus ? 22 : t[i].step);
+        int64_t c = (tiles + slots - 1) / slots * one;
+        if (i == TILE_256 && 2 * rest <= slots) c = tiles / slots * one + (rest > 0 ? round(TILE_128, t[TILE_128].step) : 0) + 300;
         if (c < least) {
             least = c;
             best = i;
@@ -328,9 +379,12 @@ template <int OP, int GATE>
 hipError_t launch_op(const ExpertProduct &g, hipStream_t stream)
 {
     switch (best_tile(OP, g)) {
-    case TILE_256: return launch_tile<Tile256, OP, GATE>(g, stream);
-    case TILE_128: return launch_tile<Tile128, OP, GATE>(g, stream);
-    default: return launch_tile<Tile64, OP, GATE>(g, stream);
+    case TILE_256: {
+        const hipError_t e = launch_part<Tile256, OP, GATE, WHOLE>(g, stream);
+        return e != hipSuccess ? e : launch_part<Tile128, OP, GATE, REST>(g, stream);
+    }
+    case TILE_128: return launch_part<Tile128, OP, GATE, ALL>(g, stream);
+    default: return launch_part<Tile64, OP, GATE, ALL>(g, stream);
     }
 }
 

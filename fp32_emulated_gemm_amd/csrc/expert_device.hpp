@@ -42,43 +42,72 @@ __device__ __forceinline__ int count_tiles(const int32_t *offsets, int64_t n, in
     return e < segments ? (int)((expert_end(offsets, e, n, P) - expert_start(offsets, e, P) + BM - 1) / BM) : 0;
 }
 
-// Tiles of all segments; uniform over the wave.
+// The row tiles of all segments and where each lies, found by whole waves.
 template <int BM>
-__device__ __forceinline__ int all_tiles(const int32_t *offsets, int64_t n, int64_t P, int segments, int lane)
-{
-    int c = 0;
-    for (int e = lane; e < segments; e += 64) c += count_tiles<BM>(offsets, n, P, e, segments);
-    return __builtin_amdgcn_readfirstlane(wave_sum(c));
-}
+struct RowTiles {
+    const int32_t *offsets;
+    int64_t n, P;
+    int lane, segments;
+    int64_t start, end;      // of segment `lane`
+    int count, sum;          // its tiles, and those up to it
+    int total;               // of all segments; uniform
 
-// Tile `index`; all lanes of the wave take part and get the same.
-template <int BM>
-__device__ __forceinline__ RowTile find_tile(const int32_t *offsets, int64_t n, int64_t P, int segments, int index,
-                                             int lane)
-{
-    int base = 0;
-    for (int e0 = 0; e0 < segments; e0 += 64) {
-        const int c = count_tiles<BM>(offsets, n, P, e0 + lane, segments);
-        int sum = c;                                       // inclusive over the lanes
+    __device__ __forceinline__ RowTiles(const int32_t *o, int64_t n_, int64_t P_, int segments_, int lane_)
+        : offsets(o), n(n_), P(P_), lane(lane_), segments(segments_)
+    {
+        total = 0;
+        for (int e0 = (segments - 1) & ~63; e0 >= 0; e0 -= 64) total += scan(e0);   // ends with the first 64
+    }
+
+    // Segments e0 + lane; returns their tiles.
+    __device__ __forceinline__ int scan(int e0)
+    {
+        const int e = e0 + lane;
+        start = end = 0;
+        if (e < segments) {
+            // both loads at once: a workgroup starts with them
+            const int64_t s = offsets != nullptr ? offsets[lmin(e, n)] : e == 0 ? 0 : P;
+            const int64_t t = offsets != nullptr && e < n ? offsets[lmin(e + 1, n)] : P;
+            start = s < 0 ? 0 : lmin(s, P);
+            end = t < start ? start : lmin(t, P);
+        }
+        count = sum = (int)((end - start + BM - 1) / BM);
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int v = __shfl_up(sum, d);
             if (lane >= d) sum += v;
         }
-        const uint64_t past = __ballot(base + sum > index);
-        if (past != 0) {
-            const int l = __builtin_ctzll(past);
-            RowTile t;
-            t.segment = e0 + l;
-            t.first = base + __builtin_amdgcn_readlane(sum - c, l);
-            t.row = expert_start(offsets, t.segment, P) + (int64_t)(index - t.first) * BM;
-            t.end = expert_end(offsets, t.segment, n, P);
-            return t;
-        }
-        base += __builtin_amdgcn_readlane(sum, 63);
+        return __builtin_amdgcn_readlane(sum, 63);
     }
-    return RowTile{-1, 0, 0, 0};
-}
+
+    // Tile `index`; every lane gets the same.
+    __device__ __forceinline__ RowTile find(int index)
+    {
+        int base = 0;
+        for (int e0 = 0;;) {
+            const uint64_t past = __ballot(base + sum > index);
+            if (past != 0) {
+                const int l = __builtin_ctzll(past);
+                RowTile t;
+                t.segment = e0 + l;
+                t.first = base + __builtin_amdgcn_readlane(sum - count, l);
+                t.row = uniform(start, l) + (int64_t)(index - t.first) * BM;
+                t.end = uniform(end, l);
+                return t;
+            }
+            base += __builtin_amdgcn_readlane(sum, 63);
+            e0 += 64;
+            if (e0 >= segments) return RowTile{-1, 0, 0, 0};
+            scan(e0);
+        }
+    }
+
+    static __device__ __forceinline__ int64_t uniform(int64_t v, int l)
+    {
+        // rows are below 2^31
+        return __builtin_amdgcn_readlane((int)v, l);
+    }
+};
 
 // Eight consecutive elements in registers, `left` of them there (others zero).
 template <class T>
@@ -111,22 +140,62 @@ __device__ __forceinline__ uint32_t pack2_finite(float a, float b)
     return pack2(__builtin_amdgcn_fmed3f(a, -MOST, MOST), __builtin_amdgcn_fmed3f(b, -MOST, MOST));
 }
 
-// The parts of eight FP32 values, x = x0 + 2^-8 x1 + 2^-16 x2, each stage rounded
-// to nearest even by the hardware's conversion.  x0 and x1 stay finite: an Inf or
-// NaN comes through in x2 (Inf - finite), so its products are those of IEEE.
+// The parts of two FP32 values, x = x0 + 2^-8 x1 + 2^-16 x2, each stage rounded to
+// nearest even by the hardware's conversion.  x0 and x1 stay finite: an Inf or NaN
+// comes through in x2 (Inf - finite), so its products are those of IEEE.
+__device__ __forceinline__ void split2_nearest(float x, float y, uint32_t &p0, uint32_t &p1, uint32_t &p2)
+{
+    p0 = pack2_finite(x, y);
+    const float t = (x - u2f(p0 << 16)) * 256.0f, u = (y - u2f(p0 & 0xFFFF0000u)) * 256.0f;
+    p1 = pack2_finite(t, u);
+    const float a = (t - u2f(p1 << 16)) * 256.0f, b = (u - u2f(p1 & 0xFFFF0000u)) * 256.0f;
+    p2 = pack2(a, b);                        // exact where finite: 8 significant bits
+}
+
 __device__ __forceinline__ void split8_nearest(const Eight<float> &in, u32x4_t (&p)[3])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float x = __uint_as_float(in.v[i >> 1][2 * (i & 1)]), y = __uint_as_float(in.v[i >> 1][2 * (i & 1) + 1]);
-        const uint32_t w0 = pack2_finite(x, y);
-        const float t = (x - u2f(w0 << 16)) * 256.0f, u = (y - u2f(w0 & 0xFFFF0000u)) * 256.0f;
-        const uint32_t w1 = pack2_finite(t, u);
-        const float a = (t - u2f(w1 << 16)) * 256.0f, b = (u - u2f(w1 & 0xFFFF0000u)) * 256.0f;
-        p[0][i] = w0;
-        p[1][i] = w1;
-        p[2][i] = pack2(a, b);               // exact where finite: 8 significant bits
+        uint32_t p0, p1, p2;
+        split2_nearest(__uint_as_float(in.v[i >> 1][2 * (i & 1)]), __uint_as_float(in.v[i >> 1][2 * (i & 1) + 1]), p0, p1, p2);
+        p[0][i] = p0;
+        p[1][i] = p1;
+        p[2][i] = p2;
     }
+}
+
+// 16 bytes of a row in registers, `left` of its elements there (others zero).
+template <class T>
+__device__ __forceinline__ u32x4_t load_piece(const T *p, int64_t left)
+{
+    constexpr int V = Elem<T>::VEC;
+    u32x4_t v = {0, 0, 0, 0};
+    if (left >= V) {
+        v = *reinterpret_cast<const u32x4_any *>(p);
+    } else if (left > 0) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < left) {
+                if constexpr (sizeof(T) == 4) v[e] = __float_as_uint(p[e]);
+                else v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+            }
+    }
+    return v;
+}
+
+// tile_of_index (device_common.hpp) in its two halves: the tile that workgroup v of
+// T takes, so that each XCD has a run of them, and where tile t lies.
+__device__ __forceinline__ int xcd_order(int v, int T)
+{
+    const int per = T >> 3, extra = T & 7, xcd = v & 7;
+    return xcd * per + imin(xcd, extra) + (v >> 3);
+}
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int group_m, int &tm, int &tn)
+{
+    const int group = t / (group_m * tiles_n), first = group * group_m, gm = imin(tiles_m - first, group_m);
+    const int in = t - group * group_m * tiles_n;
+    tm = first + in % gm;
+    tn = in / gm;
 }
 
 }  // namespace sgemm_emu_dev

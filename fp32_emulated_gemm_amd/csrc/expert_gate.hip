@@ -11,11 +11,28 @@ namespace {
 
 constexpr int ROWS = 64, COLS = 64, NT = 256;
 
-template <class T>
-__device__ __forceinline__ void load4(float (&f)[4], const T *p, int64_t left)
+// Four elements of a row, `left` of them there (others zero).
+__device__ __forceinline__ void load4(float (&f)[4], const float *p, int64_t left)
 {
+    if (left >= 4) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_any *>(p);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = e < left ? Elem<T>::load(p + e) : 0.0f;
+        for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = e < left ? p[e] : 0.0f;
+    }
+}
+__device__ __forceinline__ void load4(float (&f)[4], const uint16_t *p, int64_t left)
+{
+    if (left >= 4) {
+        const u32x2_any v = *reinterpret_cast<const u32x2_any *>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = e < left ? bf2f(p[e]) : 0.0f;
+    }
 }
 
 // Four elements, columns c.. of a row of dZ (whose pitch is a multiple of 32).
@@ -34,35 +51,42 @@ __global__ __launch_bounds__(NT) void expert_gate_kernel(ExpertGate g)
     constexpr int PARTS = GATE >= 0 ? 2 : 1;
     __shared__ float sums[PARTS][16][COLS];
     const int lane = threadIdx.x & 63, q = (threadIdx.x & 15) * 4, hi = threadIdx.x >> 4;
-    const RowTile t = find_tile<ROWS>(g.offsets, g.n, g.P, (int)g.n, (int)blockIdx.x, lane);
+    const RowTile t = RowTiles<ROWS>(g.offsets, g.n, g.P, (int)g.n, lane).find((int)blockIdx.x);
     if (t.segment < 0) return;
     const int64_t c = (int64_t)blockIdx.y * COLS + q, left = g.F - c, h = expert_dz_pitch(g.F) / 2, zp = z_pitch(g.F);
     float sg[4] = {0, 0, 0, 0}, su[4] = {0, 0, 0, 0};
+    // all loads first; rows past the tile re-read its last one
+    float d[ROWS / 16][4], zg[ROWS / 16][4], zu[ROWS / 16][4];
+#pragma unroll
+    for (int i = 0; i < ROWS / 16; ++i) {
+        const int64_t r = lmin(t.row + hi + 16 * i, t.end - 1);
+        load4(d[i], (const T *)g.dH + r * g.lddh + c, left);
+        if constexpr (GATE >= 0) {
+            load4(zg[i], g.Z + r * zp + c, left);
+            load4(zu[i], g.Z + r * zp + zp / 2 + c, left);
+        }
+    }
+#pragma unroll
     for (int i = 0; i < ROWS / 16; ++i) {
         const int64_t r = t.row + hi + 16 * i;
         if (r >= t.end) break;
-        float d[4];
-        load4<T>(d, (const T *)g.dH + r * g.lddh + c, left);
         if constexpr (GATE < 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sg[e] += d[e];
+            for (int e = 0; e < 4; ++e) sg[e] += d[i][e];
         } else {
-            float zg[4], zu[4], a[4];
-            load4<float>(zg, g.Z + r * zp + c, left);
-            load4<float>(zu, g.Z + r * zp + zp / 2 + c, left);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float slope;
-                gate_act_grad<GATE>(zg[e], a[e], slope);
-                zg[e] = e < left ? d[e] * zu[e] * slope : 0.0f;
-                zu[e] = e < left ? d[e] * a[e] : 0.0f;
-                sg[e] += zg[e];
-                su[e] += zu[e];
+                float a, slope;
+                gate_act_grad<GATE>(zg[i][e], a, slope);
+                zg[i][e] = e < left ? d[i][e] * zu[i][e] * slope : 0.0f;
+                zu[i][e] = e < left ? d[i][e] * a : 0.0f;
+                sg[e] += zg[i][e];
+                su[e] += zu[i][e];
             }
             if (g.dZ != nullptr && c < h) {
                 T *const out = (T *)g.dZ + r * 2 * h + c;
-                store4(out, zg);
-                store4(out + h, zu);
+                store4(out, zg[i]);
+                store4(out + h, zu[i]);
             }
         }
     }

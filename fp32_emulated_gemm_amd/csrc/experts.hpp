@@ -65,16 +65,16 @@ struct ExpertProduct {
     int num_cus;
     int tiles_m, tiles_n;        // set by the launch
 };
-// C[r] = A[r] B_e^T (+ bias, gate) on the rows r of expert e, zeros on rows of none.
-hipError_t launch_expert_forward(int dtype, const ExpertProduct &g, hipStream_t stream);
-// C[r] = A[r] B_e with B_e's rows by `map`: A = dZ (columns K), N columns.
-hipError_t launch_expert_dx(int dtype, const ExpertProduct &g, hipStream_t stream);
-// C_e (map's rows x N) = A_e^T B_e over the rows of expert e: A = dZ (M columns), B = X (N columns).
-hipError_t launch_expert_dw(int dtype, const ExpertProduct &g, hipStream_t stream);
-
-// The three for bfloat16 operands whose rows start at 16-byte pieces and hold whole
-// ones (expert_bf16.hip); expert_lies() tells whether a product's do.
+// kForward: C[r] = A[r] B_e^T (+ bias, gate) on the rows r of expert e.
+// kBackX: C[r] = A[r] B_e with B_e's rows by `map`: A = dZ (K columns), N columns.
+// Both leave zeros on rows of no expert.
+// kBackW: C_e (map's rows x N) = A_e^T B_e over the rows of expert e: A = dZ (M
+// columns), B = X (N columns).
 enum { kForward, kBackX, kBackW };
+hipError_t launch_expert(int op, int dtype, const ExpertProduct &g, hipStream_t stream);
+hipError_t launch_expert_f32(int op, const ExpertProduct &g, hipStream_t stream);
+// For bfloat16 operands whose rows start at 16-byte pieces and hold whole ones;
+// expert_lies() tells whether a product's do.
 bool expert_lies(int op, const ExpertProduct &g);
 hipError_t launch_expert_bf16(int op, const ExpertProduct &g, hipStream_t stream);
 

@@ -196,7 +196,7 @@ int sgemm_emu_expert_linear(int dtype, int64_t P, int64_t N, int64_t K, int64_t 
     g.C = H; g.ldc = ldh;
     g.Z = Zkeep; g.ldz = z_pitch(outs);
     g.num_cus = cus;
-    LAUNCH(launch_expert_forward(dtype, g, (hipStream_t)stream));
+    LAUNCH(launch_expert(kForward, dtype, g, (hipStream_t)stream));
     return SGEMM_EMU_OK;
 }
 
@@ -257,13 +257,13 @@ int sgemm_emu_expert_linear_backward(int dtype, int64_t P, int64_t N, int64_t K,
         g.K = pitch;
         g.B = W; g.ldb = K; g.bank = N * K;
         g.C = dX; g.ldc = lddx;
-        LAUNCH(launch_expert_dx(dtype, g, s));
+        LAUNCH(launch_expert(kBackX, dtype, g, s));
     }
     if (dW != nullptr) {
         g.M = pitch;
         g.B = X; g.ldb = ldx; g.bank = N * K;
         g.C = dW; g.ldc = K;
-        LAUNCH(launch_expert_dw(dtype, g, s));
+        LAUNCH(launch_expert(kBackW, dtype, g, s));
     }
     return SGEMM_EMU_OK;
 }
@@ -354,7 +354,7 @@ int sgemm_emu_quant4_linear(int dtype, int64_t P, int64_t N, int64_t K, int64_t 
     g.gate = gate;
     g.C = H; g.ldc = ldh;
     g.num_cus = cus;
-    LAUNCH(launch_expert_forward(dtype, g, s));
+    LAUNCH(launch_expert(kForward, dtype, g, s));
     return SGEMM_EMU_OK;
 }
 

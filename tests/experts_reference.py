@@ -57,7 +57,7 @@ def combine(ys, places, weights, dy=None):
     """y (and dys, dw with dy)."""
     bf16 = ys.dtype == torch.bfloat16
     T, k = places.shape
-    Y, w = ys.double(), torch.ones(T, k, dtype=torch.float64) if weights is None else weights.double()
+    Y, w = ys.double(), torch.ones(T, k, dtype=torch.float64, device=x.device) if weights is None else weights.double()
     there = (places >= 0).double()
     rows = Y[places.long().clamp(min=0).reshape(-1)].view(T, k, -1) if Y.shape[0] else Y.new_zeros(T, k, Y.shape[1])
     # rows of pairs that come nowhere may hold anything
@@ -105,10 +105,10 @@ def experts(x, w, offsets, bias, gate, dh=None):
     n, N, K = w.shape
     P = x.shape[0]
     out_cols = N if gate is None else N // 2
-    h, eh = torch.zeros(P, out_cols, dtype=torch.float64), torch.zeros(P, out_cols, dtype=torch.float64)
+    h, eh = torch.zeros(P, out_cols, dtype=torch.float64, device=x.device), torch.zeros(P, out_cols, dtype=torch.float64, device=x.device)
     dx, edx = torch.zeros_like(X), torch.zeros_like(X)
     dw, edw = torch.zeros_like(W), torch.zeros_like(W)
-    db, edb = torch.zeros(n, N, dtype=torch.float64), torch.zeros(n, N, dtype=torch.float64)
+    db, edb = torch.zeros(n, N, dtype=torch.float64, device=x.device), torch.zeros(n, N, dtype=torch.float64, device=x.device)
     for e, (s, t) in enumerate(_spans(offsets)):
         if s == t:
             continue
@@ -161,7 +161,7 @@ def quant4(x, q, scale, zero, group, offsets, bias, gate, few):
     X = x.double()
     n, N, K = q.shape
     out_cols = N if gate is None else N // 2
-    h, eh = torch.zeros(x.shape[0], out_cols, dtype=torch.float64), torch.zeros(x.shape[0], out_cols, dtype=torch.float64)
+    h, eh = torch.zeros(x.shape[0], out_cols, dtype=torch.float64, device=x.device), torch.zeros(x.shape[0], out_cols, dtype=torch.float64, device=x.device)
     for e, (s, t) in enumerate(_spans(offsets)):
         if s == t:
             continue
