@@ -100,7 +100,8 @@ __host__ __device__ inline int64_t expert_gate_tiles(int64_t P, int64_t n) { ret
 hipError_t launch_expert_gate(int dtype, const ExpertGate &g, hipStream_t stream);
 
 // ---------------------------------------------------------------- 4-bit weights (quant4.hip)
-// A bank's packed bytes: values, scales, zeros (16 added), see quant4.hip.
+// A bank's packed bytes: values, scales, zeros (16 added), see quant4.hip; and spare
+// bytes behind, which a tile that begins inside another reads past the last row.
 struct Quant4 {
     int64_t n, N, K, group;
     bool zeros;
@@ -110,7 +111,7 @@ struct Quant4 {
     __host__ __device__ int64_t value_bytes() const { return rows() * blocks() * 64; }
     __host__ __device__ int64_t scale_bytes() const { return groups() * rows() * 4; }
     __host__ __device__ int64_t zero_bytes() const { return zeros ? round_up(groups() * rows(), 16) : 0; }
-    __host__ __device__ int64_t bank_bytes() const { return value_bytes() + scale_bytes() + zero_bytes(); }
+    __host__ __device__ int64_t bank_bytes() const { return value_bytes() + scale_bytes() + zero_bytes() + 64; }
 };
 hipError_t launch_quant4_quantize(int dtype, const Quant4 &w, const void *W, uint8_t *q, float *scale, uint8_t *zero,
                                   hipStream_t stream);

@@ -21,7 +21,6 @@ namespace sgemm_emu_dev {
 
 namespace {
 
-constexpr int WAVES = 8, NT = 64 * WAVES;
 constexpr int KB = 128;                      // columns of a tile
 
 // ---------------------------------------------------------------- quantise, pack, unpack
@@ -113,26 +112,53 @@ __global__ __launch_bounds__(256) void pack_scales_kernel(Quant4 w, const float 
     }
 }
 
-// One thread per dword of values: eight columns of a row.
+// A wave takes 16 rows by 128 columns: a tile in one contiguous read, its rows out
+// through LDS in whole pieces (a lane's own dwords belong to places 64 bytes apart:
+// stored one by one, 4096 x 4096 took 83 us).
 template <class T>
 __global__ __launch_bounds__(256) void unpack_kernel(Quant4 w, const void *packed, T *W)
 {
-    const int64_t per = w.value_bytes() / 4, total = w.n * per, rows = w.rows();
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
-        const int64_t bank = u / per, at = u - bank * per;
+    constexpr int PITCH = KB + 16 / sizeof(T);             // rows of LDS, 16 bytes longer
+    __shared__ __attribute__((aligned(16))) T buf[4][16 * PITCH];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t blocks = w.blocks(), rows = w.rows(), per = rows / 16 * blocks, total = w.n * per;
+    T *const out = buf[wave];
+    for (int64_t u = (int64_t)blockIdx.x * 4 + wave; u < total; u += (int64_t)gridDim.x * 4) {
+        const int64_t bank = u / per, at = u - bank * per, row0 = at / blocks * 16, c0 = at % blocks * KB;
         const Packed p = packed_bank(w, packed, bank);
-        const int64_t tile = at >> 8, blocks = w.blocks();
-        const int l = (int)(at >> 2) & 63, d = (int)at & 3;
-        const int64_t row = tile / blocks * 16 + (l & 15), c = tile % blocks * KB + d * 32 + (l >> 4) * 8;
-        if (row >= w.N) continue;
-        const uint32_t v = p.values[at];
-        const int64_t g = c / w.group * rows + row;
-        const float s = p.scale[g], z = w.zeros ? (float)(p.zero[g] - 16) : 8.0f;
+        const u32x4_t v = reinterpret_cast<const u32x4_t *>(p.values)[at * 64 + lane];
+        const int64_t row = row0 + (lane & 15);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c + e < w.K)
-                W[(bank * w.N + row) * w.K + c + e] =
-                    Elem<T>::store(((float)((v >> (4 * (e >> 1) + 16 * (e & 1))) & 15) - z) * s);
+        for (int d = 0; d < 4; ++d) {
+            const int64_t g = (c0 + d * 32) / w.group * rows + row;
+            const float s = p.scale[g], z = w.zeros ? (float)(p.zero[g] - 16) : 8.0f;
+            T e8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) e8[e] = Elem<T>::store(((float)((v[d] >> (4 * (e >> 1) + 16 * (e & 1))) & 15) - z) * s);
+            T *const to = out + (lane & 15) * PITCH + d * 32 + (lane >> 4) * 8;
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+                reinterpret_cast<u32x4_t *>(to)[i] = reinterpret_cast<const u32x4_t *>(e8)[i];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        constexpr int V = Elem<T>::VEC, PER = KB / V;      // pieces of a row
+#pragma unroll
+        for (int i = 0; i < 16 * PER / 64; ++i) {
+            const int q = i * 64 + lane, r = q / PER, c = q % PER * V;
+            const int64_t left = w.K - c0 - c;
+            const T *const from = out + r * PITCH + c;
+            T *const to = W + (bank * w.N + row0 + r) * w.K + c0 + c;
+            if (row0 + r < w.N && left > 0) {
+                if (left >= V) {
+                    *reinterpret_cast<u32x4_any *>(to) = *reinterpret_cast<const u32x4_t *>(from);
+                } else {
+                    for (int e = 0; e < left; ++e) to[e] = from[e];
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -149,24 +175,97 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t w)
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// The columns 8 (lane >> 4) .. + 7 of four steps of 32 of X's row `m`, as they come:
+// one row of a tile of 16 in each lane.
 template <class T>
-struct Xs {
-    static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+struct XBlock {
+    u32x4_t v[4][sizeof(T) / 2];
+
+    // LIES: rows at whole dwords, loaded through a descriptor that ends with the last
+    // element.  Rows past the last read zeros.
+    template <bool LIES>
+    __device__ __forceinline__ void load(const T *X, int64_t ldx, int64_t row, int64_t rows, int64_t k0, int64_t K, int lane)
+    {
+        constexpr int PIECES = sizeof(T) / 2;
+        if constexpr (LIES) {
+            // a descriptor for the tile's 16 rows; the row of this lane lies `lane & 15` further
+            const int64_t first = row - (lane & 15), left = rows - first;
+            const rsrc_t r = make_rsrc(X + first * ldx, left > 0 ? ((lmin(left, 16) - 1) * ldx + K) * (int64_t)sizeof(T) : 0);
+            const uint32_t off = row < rows ? (uint32_t)(((lane & 15) * ldx + (lane >> 4) * 8) * sizeof(T)) : 0xFFFFFFF0u;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+                    v[d][i] = bload_u32x4(r, off == 0xFFFFFFF0u ? off : off + (uint32_t)((k0 + d * 32) * sizeof(T) + i * 16), 0);
+            if (k0 + KB <= K) return;
+            // the last block: what the pieces hold behind K
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int64_t end = K - (k0 + d * 32 + (lane >> 4) * 8);
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if constexpr (sizeof(T) == 4) v[d][i][q] = i * 4 + q < end ? v[d][i][q] : 0u;
+                        else v[d][i][q] = 2 * q + 1 < end ? v[d][i][q] : 2 * q < end ? v[d][i][q] & 0xFFFFu : 0u;
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int64_t k = k0 + d * 32 + (lane >> 4) * 8;
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+                    v[d][i] = load_piece<T>(X + row * ldx + k + i * Elem<T>::VEC, row < rows ? K - k - i * Elem<T>::VEC : 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void parts(int d, u32x4_t (&p)[sizeof(T) == 4 ? 3 : 1]) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t p0, p1, p2;
+                split2_nearest(__uint_as_float(v[d][i >> 1][2 * (i & 1)]), __uint_as_float(v[d][i >> 1][2 * (i & 1) + 1]), p0,
+                               p1, p2);
+                p[0][i] = p0;
+                p[1][i] = p1;
+                p[2][i] = p2;
+            }
+        } else {
+            p[0] = v[d][0];
+        }
+    }
 };
+
+typedef uint32_t u32_any __attribute__((aligned(1)));
+
+__device__ __forceinline__ float gate_value(int gate, float z)
+{
+    switch (gate) {
+    case kSilu: return gate_act<kSilu>(z);
+    case kGelu: return gate_act<kGelu>(z);
+    case kGeluTanh: return gate_act<kGeluTanh>(z);
+    case kSigmoid: return gate_act<kSigmoid>(z);
+    default: return gate_act<kRelu>(z);
+    }
+}
 
 // GROUP columns share a scale.  A workgroup takes NB tiles of 16 rows of W (with a
 // gate, NB / 2 of the gate's and those of the up projection's same outputs) and 16 MB
-// rows of X at a time; its waves take the blocks of 128 columns in turn.
-template <class T, int NB, int MB, int GROUP, int GATE>
-__global__ __launch_bounds__(NT) void quant4_few_kernel(Quant4 w, Quant4Product g)
+// rows of X at a time; its waves take the blocks of 128 columns in turn, the next
+// block's values loaded under the products of the one before.
+template <class T, int WAVES, int NB, int MB, int GROUP, bool LIES>
+__global__ __launch_bounds__(64 * WAVES) void quant4_few_kernel(Quant4 w, Quant4Product g)
 {
-    constexpr int PARTS = Xs<T>::PARTS, STEPS = GROUP / 32, GROUPS = KB / GROUP;
-    constexpr bool GATED = GATE >= 0;
-    constexpr int OUT = GATED ? NB / 2 * 16 : NB * 16;
+    constexpr int NT = 64 * WAVES, PARTS = sizeof(T) == 4 ? 3 : 1, STEPS = GROUP / 32, GROUPS = KB / GROUP;
     __shared__ __attribute__((aligned(16))) f32x4_t sums[WAVES][NB][MB][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t e = blockIdx.y, F = GATED ? w.N / 2 : w.N, n0 = (int64_t)blockIdx.x * OUT;
+    const bool gated = g.gate >= 0;
+    const int OUT = gated ? NB / 2 * 16 : NB * 16;
+    const int64_t e = blockIdx.y, F = gated ? w.N / 2 : w.N, n0 = (int64_t)blockIdx.x * OUT;
     const int64_t r0 = expert_start(g.offsets, e, g.P), r1 = expert_end(g.offsets, e, w.n, g.P);
+    if (r0 >= r1) return;
     T *const H = (T *)g.H;
     if (e >= w.n) {                                        // rows of no expert
         for (int64_t o = threadIdx.x; o < (r1 - r0) * OUT; o += NT) {
@@ -177,14 +276,17 @@ __global__ __launch_bounds__(NT) void quant4_few_kernel(Quant4 w, Quant4Product 
     }
     const Packed p = packed_bank(w, g.packed, e);
     const int64_t blocks = w.blocks(), rows = w.rows();
-    // Rows of W behind each tile: a gate's up rows begin at F, inside a tile where F is
-    // no multiple of 16, so a lane's row is found one by one.
-    int64_t wrow[NB], srow[NB];
+    // First row of W of each tile.  Up rows begin at F, inside a packed tile where F is no
+    // multiple of 16.  Rows past the last are other rows' or the bank's spare bytes; their
+    // results are dropped.
+    const uint32_t *values[NB];
+    int64_t srow[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        const int64_t base = GATED ? (b < NB / 2 ? 0 : F) + n0 + (b % (NB / 2)) * 16 : n0 + b * 16;
-        wrow[b] = lmin(base + (lane & 15), rows - 1);
-        srow[b] = base + 4 * (lane >> 4);
+        const int64_t base = gated ? (b < NB / 2 ? b * 16 : F + (b - NB / 2) * 16) + n0 : n0 + b * 16;
+        const int64_t row = lmin(base + (lane & 15), rows - 1);
+        values[b] = p.values + (((row >> 4) * blocks) << 8) + (((lane & 48) | (row & 15)) << 2);
+        srow[b] = lmin(base, rows - 1) + 4 * (lane >> 4);
     }
     const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
     for (int64_t m0 = r0; m0 < r1; m0 += 16 * MB) {
@@ -193,12 +295,31 @@ __global__ __launch_bounds__(NT) void quant4_few_kernel(Quant4 w, Quant4Product 
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int m = 0; m < MB; ++m) acc[b][m] = f32x4_t{};
+        u32x4_t next[NB];
+        auto load_values = [&](int64_t kb) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) next[b] = *reinterpret_cast<const u32x4_t *>(values[b] + (kb << 8));
+        };
+        if (wave < blocks) load_values(wave);
         for (int64_t kb = wave; kb < blocks; kb += WAVES) {
             u32x4_t v[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-                v[b] = *reinterpret_cast<const u32x4_t *>(
-                    p.values + (((wrow[b] >> 4) * blocks + kb) << 8) + (((lane & 48) | (wrow[b] & 15)) << 2));
+            for (int b = 0; b < NB; ++b) v[b] = next[b];
+            XBlock<T> x[MB];
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                x[m].template load<LIES>((const T *)g.X, g.ldx, m0 + m * 16 + (lane & 15), r1, kb * KB, w.K, lane);
+            f32x4_t scale[GROUPS][NB];
+            uint32_t zero[GROUPS][NB];
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int64_t at = (kb * GROUPS + gr) * rows + srow[b];
+                    scale[gr][b] = __builtin_bit_cast(f32x4_t, (u32x4_t)*reinterpret_cast<const u32x4_any *>(p.scale + at));
+                    zero[gr][b] = w.zeros ? *reinterpret_cast<const u32_any *>(p.zero + at) : 0x18181818u;
+                }
+            if (kb + WAVES < blocks) load_values(kb + WAVES);
 #pragma unroll
             for (int gr = 0; gr < GROUPS; ++gr) {
                 f32x4_t part[PARTS][NB][MB], xs[PARTS][MB];
@@ -213,18 +334,13 @@ __global__ __launch_bounds__(NT) void quant4_few_kernel(Quant4 w, Quant4Product 
 #pragma unroll
                 for (int st = 0; st < STEPS; ++st) {
                     const int d = gr * STEPS + st;
-                    const int64_t k = kb * KB + d * 32 + 8 * (lane >> 4);
                     bf16x8_t wf[NB];
 #pragma unroll
                     for (int b = 0; b < NB; ++b) wf[b] = widen(v[b][d]);
 #pragma unroll
                     for (int m = 0; m < MB; ++m) {
-                        const int64_t row = m0 + m * 16 + (lane & 15);
-                        Eight<T> x;
-                        x.load((const T *)g.X + lmin(row, r1 - 1) * g.ldx + k, row < r1 ? w.K - k : 0);
                         u32x4_t xp[PARTS];
-                        if constexpr (PARTS == 3) split8_nearest(x, xp);
-                        else xp[0] = x.v[0];
+                        x[m].parts(d, xp);
 #pragma unroll
                         for (int q = 0; q < PARTS; ++q) {
                             const bf16x8_t xf = __builtin_bit_cast(bf16x8_t, xp[q]);
@@ -235,29 +351,24 @@ __global__ __launch_bounds__(NT) void quant4_few_kernel(Quant4 w, Quant4Product 
                         }
                     }
                 }
-                const int64_t at = (kb * GROUPS + gr) * rows;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float s[4], z[4];
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int64_t r = lmin(srow[b] + q, rows - 1);
-                        s[q] = p.scale[at + r];
-                        z[q] = w.zeros ? (float)p.zero[at + r] : 24.0f;
-                    }
+                        const float z = -(float)((zero[gr][b] >> (8 * q)) & 255u);
 #pragma unroll
-                    for (int m = 0; m < MB; ++m)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float t = __builtin_fmaf(-z[q], xs[0][m][q], part[0][b][m][q]);
+                        for (int m = 0; m < MB; ++m) {
+                            float t = __builtin_fmaf(z, xs[0][m][q], part[0][b][m][q]);
                             if constexpr (PARTS == 3) {
-                                const float t1 = __builtin_fmaf(-z[q], xs[1][m][q], part[1][b][m][q]);
-                                const float t2 = __builtin_fmaf(-z[q], xs[2][m][q], part[2][b][m][q]);
+                                const float t1 = __builtin_fmaf(z, xs[1][m][q], part[1][b][m][q]);
+                                const float t2 = __builtin_fmaf(z, xs[2][m][q], part[2][b][m][q]);
                                 t += __builtin_fmaf(t2, 0x1p-16f, t1 * 0x1p-8f);
                             }
-                            acc[b][m][q] = __builtin_fmaf(s[q], t, acc[b][m][q]);
+                            acc[b][m][q] = __builtin_fmaf(scale[gr][b][q], t, acc[b][m][q]);
                         }
-                }
+                    }
+                // one group's products at a time: all of a block's together would not fit the registers
+                if constexpr (GROUPS > 1) __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
@@ -272,15 +383,16 @@ __global__ __launch_bounds__(NT) void quant4_few_kernel(Quant4 w, Quant4Product 
             for (int i = 0; i < WAVES; ++i) v += sums[i][b][m >> 4][(n >> 2) * 16 + (m & 15)][n & 3];
             return v;
         };
-        for (int o = threadIdx.x; o < OUT * 16 * MB; o += NT) {
+        const int here = (int)lmin(r1 - m0, 16 * MB);
+        for (int o = threadIdx.x; o < OUT * here; o += NT) {
             const int n = o % OUT, m = o / OUT;
-            if (n0 + n >= F || m0 + m >= r1) continue;
+            if (n0 + n >= F) continue;
             float v = total(n >> 4, n & 15, m);
             if (bias != nullptr) v += Elem<T>::load(bias + n0 + n);
-            if constexpr (GATED) {
+            if (gated) {
                 float u = total(NB / 2 + (n >> 4), n & 15, m);
                 if (bias != nullptr) u += Elem<T>::load(bias + F + n0 + n);
-                v = gate_act<GATE>(v) * u;
+                v = gate_value(g.gate, v) * u;
             }
             H[(m0 + m) * g.ldh + n0 + n] = Elem<T>::store(v);
         }
@@ -294,42 +406,39 @@ unsigned blocks_for(int64_t items, int64_t per)
     return (unsigned)(b < 1 ? 1 : b < 16384 ? b : 16384);
 }
 
-template <class T, int NB, int MB, int GROUP, int GATE>
+template <class T, int WAVES, int NB, int MB, int GROUP, bool LIES>
 hipError_t launch_few(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
 {
-    const int64_t out = GATE >= 0 ? w.N / 2 : w.N, per = GATE >= 0 ? NB * 8 : NB * 16;
+    const int64_t out = g.gate >= 0 ? w.N / 2 : w.N, per = g.gate >= 0 ? NB * 8 : NB * 16;
     const dim3 grid((unsigned)((out + per - 1) / per), (unsigned)(w.n + (g.offsets != nullptr ? 1 : 0)));
-    hipLaunchKernelGGL((quant4_few_kernel<T, NB, MB, GROUP, GATE>), grid, dim3(NT), 0, stream, w, g);
+    hipLaunchKernelGGL((quant4_few_kernel<T, WAVES, NB, MB, GROUP, LIES>), grid, dim3(64 * WAVES), 0, stream, w, g);
     return hipGetLastError();
 }
 
-template <class T, int GROUP, int GATE>
+// Rows of W and X of a workgroup: 16 rows of X where an expert has about as many or
+// fewer, else as many as the registers hold beside the groups' scales, so that W
+// passes once or twice; of W the more the more rows of X are read beside it, as long
+// as there are workgroups for the CUs.
+template <class T, int GROUP>
 hipError_t few_rows(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
 {
-    if (g.P <= 16 * w.n) return launch_few<T, 2, 1, GROUP, GATE>(w, g, stream);
-    return launch_few<T, 2, 2, GROUP, GATE>(w, g, stream);
-}
-
-template <class T, int GROUP>
-hipError_t few_gate(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
-{
-    switch (g.gate) {
-    case kSilu: return few_rows<T, GROUP, kSilu>(w, g, stream);
-    case kGelu: return few_rows<T, GROUP, kGelu>(w, g, stream);
-    case kGeluTanh: return few_rows<T, GROUP, kGeluTanh>(w, g, stream);
-    case kSigmoid: return few_rows<T, GROUP, kSigmoid>(w, g, stream);
-    case kRelu: return few_rows<T, GROUP, kRelu>(w, g, stream);
-    default: return few_rows<T, GROUP, -1>(w, g, stream);
-    }
+    constexpr int MB = sizeof(T) == 2 && GROUP >= 64 ? 4 : 2, NB = GROUP == 128 || (sizeof(T) == 2 && GROUP == 64) ? 4 : 2;
+    const bool lies = sizeof(T) == 4 || (g.ldx % 2 == 0 && aligned(g.X, 4));
+    const int64_t each = w.n > 0 ? (g.P + w.n - 1) / w.n : 0, tiles = (w.N + 15) / 16 * (w.n < g.P ? w.n : g.P);
+    if (!lies) return each <= 16 ? launch_few<T, 8, 2, 1, GROUP, false>(w, g, stream) : launch_few<T, 8, 2, MB, GROUP, false>(w, g, stream);
+    if (each > 16) return launch_few<T, 8, 2, MB, GROUP, true>(w, g, stream);
+    if (NB > 2 && each > 4 && tiles >= 4 * g.num_cus) return launch_few<T, 8, NB, 1, GROUP, true>(w, g, stream);
+    if (g.gate >= 0 || tiles >= 2 * g.num_cus) return launch_few<T, 8, 2, 1, GROUP, true>(w, g, stream);
+    return launch_few<T, 16, 1, 1, GROUP, true>(w, g, stream);
 }
 
 template <class T>
 hipError_t few_group(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
 {
     switch (w.group) {
-    case 32: return few_gate<T, 32>(w, g, stream);
-    case 64: return few_gate<T, 64>(w, g, stream);
-    default: return few_gate<T, 128>(w, g, stream);
+    case 32: return few_rows<T, 32>(w, g, stream);
+    case 64: return few_rows<T, 64>(w, g, stream);
+    default: return few_rows<T, 128>(w, g, stream);
     }
 }
 
@@ -359,9 +468,9 @@ hipError_t launch_quant4_pack(const Quant4 &w, const uint8_t *q, const float *sc
 
 hipError_t launch_quant4_unpack(int dtype, const Quant4 &w, const void *packed, void *W, hipStream_t stream)
 {
-    const int64_t dwords = w.n * w.value_bytes() / 4;
-    if (dwords == 0) return hipSuccess;
-    const dim3 grid(blocks_for(dwords, 256));
+    const int64_t tiles = w.n * (w.rows() / 16) * w.blocks();
+    if (tiles == 0) return hipSuccess;
+    const dim3 grid(blocks_for(tiles, 4));
     if (dtype == kF32) hipLaunchKernelGGL(unpack_kernel<float>, grid, dim3(256), 0, stream, w, packed, (float *)W);
     else hipLaunchKernelGGL(unpack_kernel<uint16_t>, grid, dim3(256), 0, stream, w, packed, (uint16_t *)W);
     return hipGetLastError();
