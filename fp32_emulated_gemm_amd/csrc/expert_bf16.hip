@@ -136,11 +136,11 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
     constexpr bool QUARTER = PART == REST;
     constexpr int SIZE_M = QUARTER ? 256 : T::BM;
     int64_t e, m0, m_end, K, r0 = 0;
-    int rows, tiles, tm, tn;
+    int rows, tiles, tm, tn, chunk = 0;
     RowTiles<SIZE_M> row_tiles(g.offsets, g.n, g.P, OP == kBackW ? 0 : (int)g.n + 1, lane);
     if constexpr (OP == kBackW) {
         rows = g.tiles_m;
-        tiles = (int)g.n * rows * g.tiles_n;
+        tiles = (int)weight_chunks(g) * rows * g.tiles_n;
     } else {
         rows = row_tiles.total;
         tiles = rows * g.tiles_n;
@@ -156,13 +156,16 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
     }
     if constexpr (OP == kBackW) {
         const int per = rows * g.tiles_n;
-        e = index / per;
+        chunk = index / per;
         // each expert's tiles over all XCDs: their lengths differ from expert to expert
-        tile_at(xcd_order(index - (int)e * per, per), rows, g.tiles_n, imin(rows, 8), tm, tn);
+        tile_at(xcd_order(index - chunk * per, per), rows, g.tiles_n, imin(rows, 8), tm, tn);
         m0 = (int64_t)tm * SIZE_M;
         m_end = g.M;
-        r0 = expert_start(g.offsets, e, g.P);
-        K = expert_end(g.offsets, e, g.n, g.P) - r0;
+        const RowTile r = weight_rows(g, chunk, lane);
+        if (r.segment < 0) return;
+        e = r.segment;
+        r0 = r.row;
+        K = r.end - r0;
     } else {
         tile_at(index, rows, g.tiles_n, imin(rows, 8), tm, tn);
         const RowTile r = row_tiles.find(tm);
@@ -267,6 +270,21 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
     // acc[j][i][q]: row m0w + 16 i + (lane & 15), column n0w + 16 j + 4 (lane >> 4) + q
     const int64_t m0w = m0 + wm * T::TM, n0w = n0 + wn * T::TN;
     const int mlane = lane & 15, quad = 4 * (lane >> 4);
+    if constexpr (OP == kBackW && PART == ALL) {
+        if (g.partials != nullptr) {
+#pragma unroll
+            for (int i = 0; i < T::MI; ++i) {
+                const int64_t m = m0w + i * 16 + mlane;
+                if (m >= g.M) continue;
+#pragma unroll
+                for (int j = 0; j < T::NI; ++j) {
+                    const int64_t n = n0w + j * 16 + quad;   // N is a multiple of 8: four lie inside or outside
+                    if (n < g.N) *reinterpret_cast<f32x4_t *>(g.partials + (chunk * g.M + m) * g.N + n) = acc[j][i];
+                }
+            }
+            return;
+        }
+    }
     uint16_t *const out = lds + wave * T::EPI_WAVE;
     const uint16_t *const bias = OP == kForward && there && g.bias != nullptr ? (const uint16_t *)g.bias + e * g.N : nullptr;
     if constexpr (GATED) {
@@ -338,7 +356,7 @@ hipError_t launch_part(ExpertProduct g, hipStream_t stream)
     constexpr int BM = PART == REST ? 256 : T::BM, BN = PART == REST ? 256 : T::BN;
     g.tiles_m = (int)((g.M + BM - 1) / BM);                // dW only: elsewhere from the offsets
     g.tiles_n = (int)((g.N + BN - 1) / BN);
-    const int64_t segments = g.n + 1, rows = OP == kBackW ? g.n * g.tiles_m : g.P / BM + (segments < g.P ? segments : g.P);
+    const int64_t segments = g.n + 1, rows = OP == kBackW ? weight_chunks(g) * g.tiles_m : g.P / BM + (segments < g.P ? segments : g.P);
     int64_t blocks = rows * g.tiles_n;
     if (PART == REST) blocks = 4 * (g.num_cus / 2 < blocks ? g.num_cus / 2 : blocks);
     if (blocks * T::NT >= (int64_t)1 << 32) return hipErrorInvalidValue;   // more work-items than a launch can have
@@ -353,6 +371,7 @@ enum { TILE_64, TILE_128, TILE_256, TILES };
 // bf16_gemm.hip.  An expert's last row tile is half filled on average.
 int best_tile(int op, const ExpertProduct &g)
 {
+    if (op == kBackW && g.partials != nullptr) return TILE_128;
     static const struct { int size, per_cu, step, fixed; } t[TILES] = {{64, 2, 38, 20}, {128, 2, 82, 50}, {256, 1, 138, 100}};
     const int64_t steps = ((op == kBackW ? g.P / g.n : g.K) + KS - 1) / KS;
     // kept pre-activations leave at a tile's end, 256 KB of a 256 x 256 tile

@@ -43,17 +43,18 @@ __device__ __forceinline__ int count_tiles(const int32_t *offsets, int64_t n, in
 }
 
 // The row tiles of all segments and where each lies, found by whole waves.
-template <int BM>
+template <int BM_>
 struct RowTiles {
     const int32_t *offsets;
     int64_t n, P;
-    int lane, segments;
+    int lane, segments, BM;
     int64_t start, end;      // of segment `lane`
     int count, sum;          // its tiles, and those up to it
     int total;               // of all segments; uniform
 
-    __device__ __forceinline__ RowTiles(const int32_t *o, int64_t n_, int64_t P_, int segments_, int lane_)
-        : offsets(o), n(n_), P(P_), lane(lane_), segments(segments_)
+    // rows: of a tile, where BM_ is 0.
+    __device__ __forceinline__ RowTiles(const int32_t *o, int64_t n_, int64_t P_, int segments_, int lane_, int rows = 0)
+        : offsets(o), n(n_), P(P_), lane(lane_), segments(segments_), BM(BM_ != 0 ? BM_ : rows)
     {
         total = 0;
         for (int e0 = (segments - 1) & ~63; e0 >= 0; e0 -= 64) total += scan(e0);   // ends with the first 64
@@ -71,7 +72,7 @@ struct RowTiles {
             start = s < 0 ? 0 : lmin(s, P);
             end = t < start ? start : lmin(t, P);
         }
-        count = sum = (int)((end - start + BM - 1) / BM);
+        count = sum = (int)(((uint32_t)(end - start) + (uint32_t)BM - 1u) / (uint32_t)BM);   // rows are below 2^22
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int v = __shfl_up(sum, d);
@@ -181,6 +182,21 @@ __device__ __forceinline__ u32x4_t load_piece(const T *p, int64_t left)
             }
     }
     return v;
+}
+
+// Rows that a workgroup of a weight gradient takes: an expert's, or with partial sums
+// one of the pieces of g.chunk rows that all experts' rows are cut into.
+__device__ __forceinline__ RowTile weight_rows(const ExpertProduct &g, int chunk, int lane)
+{
+    RowTile t{chunk, 0, 0, 0};
+    if (g.partials == nullptr) {
+        t.row = expert_start(g.offsets, chunk, g.P);
+        t.end = expert_end(g.offsets, chunk, g.n, g.P);
+    } else {
+        t = RowTiles<0>(g.offsets, g.n, g.P, (int)g.n, lane, (int)g.chunk).find(chunk);
+        t.end = lmin(t.end, t.row + g.chunk);
+    }
+    return t;
 }
 
 // tile_of_index (device_common.hpp) in its two halves: the tile that workgroup v of

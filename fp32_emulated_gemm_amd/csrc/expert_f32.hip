@@ -7,16 +7,17 @@
 // cores in three bands of one weight each, summed in FP32 and added smallest first.
 //
 // One workgroup per output tile, in K steps of 32.  A step's operands are loaded two
-// steps ahead into one of two sets of registers, and split and written to the other
-// LDS buffer under the MFMAs of the step before, four vector instructions behind
-// each: the split costs about as much as the MFMAs (8192 elements, 48 MFMAs a wave),
-// so neither may wait for the other.  Loads go through descriptors that end with the
+// steps ahead, and split and written to the other LDS buffer among the MFMAs of the
+// step before: the split costs about as much as the MFMAs (8192 elements, 48 MFMAs a
+// wave), so neither may wait for the other.  Loads go through descriptors that end with the
 // last element, so nothing is read behind it, whatever K and the alignment; where K
 // ends inside a step, what a row's pieces hold behind it is cleared.
 //
 // Operands whose k are rows (W in dX, dZ and X in dW) keep that layout in LDS and are
 // read by ds_read_b64_tr_b16, four k of a column at a time: nothing is transposed in
 // memory, and an expert's rows may start anywhere.
+#include <type_traits>
+
 #include "expert_stage.hpp"
 
 namespace sgemm_emu_dev {
@@ -30,10 +31,19 @@ template <class S, bool KM>
 struct Pieces {
     const float *p[KM ? 1 : S::MINE];        // !KM: first row of the wave's eight, at k = 0
     uint32_t bytes[KM ? 1 : S::MINE];        // to the last element of the last of them
-    uint32_t off[S::MINE];
+    uint32_t off[KM ? 1 : S::MINE];          // KM: the next piece lies a fixed number of rows on
 };
 
 constexpr int64_t MOST_BYTES = 0xFFFFFFF0ll;
+
+// make_rsrc for a size that fits.
+__device__ __forceinline__ rsrc_t make_rsrc32(const void *base, uint32_t bytes)
+{
+    const uint64_t p = (uint64_t)(uintptr_t)base;
+    void *const ub = (void *)(uintptr_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) << 32) |
+                                         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p));
+    return __builtin_amdgcn_make_buffer_rsrc(ub, (short)0, (int)__builtin_amdgcn_readfirstlane(bytes), RSRC_WORD3);
+}
 
 template <class TL, int OP, int GATE>
 __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertProduct g)
@@ -48,14 +58,18 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
 
     int64_t e, m0, m_end, K, r0 = 0;
     int tm, tn;
+    int chunk = 0;
     if constexpr (OP == kBackW) {
         const int per = g.tiles_m * g.tiles_n;
-        e = (int)blockIdx.x / per;
-        tile_at(xcd_order((int)blockIdx.x - (int)e * per, per), g.tiles_m, g.tiles_n, imin(g.tiles_m, 8), tm, tn);
+        chunk = (int)blockIdx.x / per;
+        tile_at(xcd_order((int)blockIdx.x - chunk * per, per), g.tiles_m, g.tiles_n, imin(g.tiles_m, 8), tm, tn);
         m0 = (int64_t)tm * TL::BM;
         m_end = g.M;
-        r0 = expert_start(g.offsets, e, g.P);
-        K = expert_end(g.offsets, e, g.n, g.P) - r0;
+        const RowTile r = weight_rows(g, chunk, lane);
+        if (r.segment < 0) return;
+        e = r.segment;
+        r0 = r.row;
+        K = r.end - r0;
     } else {
         RowTiles<TL::BM> row_tiles(g.offsets, g.n, g.P, (int)g.n + 1, lane);
         const int rows = row_tiles.total, tiles = rows * g.tiles_n;
@@ -84,22 +98,27 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
         q.bytes[c] = (uint32_t)lmin(((last - first) * ld + K) * 4, MOST_BYTES);
         q.off[c] = (uint32_t)(((row(r) - first) * ld + piece % 8 * 4) * 4);
     };
+    if constexpr (A_KM) {
+        pa.off[0] = (uint32_t)(((int)threadIdx.x / SA::ROW * g.lda + (int)threadIdx.x % SA::ROW * 4) * 4);
+    } else {
 #pragma unroll
-    for (int c = 0; c < SA::MINE; ++c) {
-        const int piece = (int)threadIdx.x + c * NT;
-        if constexpr (A_KM) pa.off[c] = (uint32_t)((piece / SA::ROW * g.lda + piece % SA::ROW * 4) * 4);
-        else rows_of(pa, A, g.lda, c, [&](int r) { return lmin(m0 + r, m_end - 1); });
+        for (int c = 0; c < SA::MINE; ++c) rows_of(pa, A, g.lda, c, [&](int r) { return lmin(m0 + r, m_end - 1); });
     }
+    if constexpr (B_KM) {
+        pb.off[0] = (uint32_t)(((int)threadIdx.x / SB::ROW * g.ldb + (int)threadIdx.x % SB::ROW * 4) * 4);
+    } else {
 #pragma unroll
-    for (int c = 0; c < SB::MINE; ++c) {
-        const int piece = (int)threadIdx.x + c * NT;
-        if constexpr (B_KM) pb.off[c] = (uint32_t)((piece / SB::ROW * g.ldb + piece % SB::ROW * 4) * 4);
-        else rows_of(pb, B, g.ldb, c, [&](int r) { return GATED ? gated_row(g.N >> 1, n0, r) : lmin(n0 + r, g.N - 1); });
+        for (int c = 0; c < SB::MINE; ++c)
+            rows_of(pb, B, g.ldb, c, [&](int r) { return GATED ? gated_row(g.N >> 1, n0, r) : lmin(n0 + r, g.N - 1); });
     }
-    // Bytes of `rows` rows of ld elements, from column c0 of cols on, to the last element.
-    auto extent = [](int64_t rows, int64_t ld, int64_t cols, int64_t c0) {
-        return rows > 0 && cols > c0 ? lmin(((rows - 1) * ld + cols - c0) * 4, MOST_BYTES) : (int64_t)0;
+    // Bytes of `rows` rows of ld elements, from column c0 of cols on, to the last
+    // element.  The rows span less than 2^32 bytes, and nothing here branches: a branch
+    // would part the step's split from its MFMAs.
+    auto extent = [](int rows, int64_t ld, int64_t cols, int64_t c0) {
+        const uint32_t last = (uint32_t)(cols - c0) * 4u, before = (uint32_t)(rows - 1) * (uint32_t)(ld * 4);
+        return rows > 0 ? last + before : 0u;
     };
+    auto rows_left = [](int64_t left) { return (int)(left < BK ? left : BK); };
 
     struct Set {
         u32x4_t a[SA::MINE], b[SB::MINE];
@@ -107,24 +126,24 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
     auto load = [&](Set &s, int kt) {
         const int64_t k0 = (int64_t)kt * BK;
         if constexpr (A_KM) {
-            const rsrc_t r = make_rsrc(A + (r0 + k0) * g.lda + m0, extent(lmin(K - k0, BK), g.lda, g.M, m0));
+            const rsrc_t r = make_rsrc32(A + (r0 + k0) * g.lda + m0, extent(rows_left(K - k0), g.lda, g.M, m0));
 #pragma unroll
-            for (int c = 0; c < SA::MINE; ++c) s.a[c] = bload_u32x4(r, pa.off[c], 0);
+            for (int c = 0; c < SA::MINE; ++c) s.a[c] = bload_u32x4(r, pa.off[0] + (uint32_t)(c * (NT / SA::ROW) * g.lda * 4), 0);
         } else {
 #pragma unroll
-            for (int c = 0; c < SA::MINE; ++c) s.a[c] = bload_u32x4(make_rsrc(pa.p[c], pa.bytes[c]), pa.off[c], (uint32_t)(k0 * 4));
+            for (int c = 0; c < SA::MINE; ++c) s.a[c] = bload_u32x4(make_rsrc32(pa.p[c], pa.bytes[c]), pa.off[c] + (uint32_t)(k0 * 4), 0);
         }
         if constexpr (B_KM) {
             // dX: a step lies in one half of dZ's columns (h is a multiple of BK, or K itself)
             const bool up = OP == kBackX && k0 >= g.map.h;
             const int64_t in = up ? k0 - g.map.h : k0, row = OP == kBackW ? r0 + k0 : up ? g.map.F + in : in;
             const int64_t left = OP == kBackW ? K - k0 : g.map.F - in;
-            const rsrc_t r = make_rsrc(B + row * g.ldb + n0, extent(lmin(left, BK), g.ldb, g.N, n0));
+            const rsrc_t r = make_rsrc32(B + row * g.ldb + n0, extent(rows_left(left), g.ldb, g.N, n0));
 #pragma unroll
-            for (int c = 0; c < SB::MINE; ++c) s.b[c] = bload_u32x4(r, pb.off[c], 0);
+            for (int c = 0; c < SB::MINE; ++c) s.b[c] = bload_u32x4(r, pb.off[0] + (uint32_t)(c * (NT / SB::ROW) * g.ldb * 4), 0);
         } else {
 #pragma unroll
-            for (int c = 0; c < SB::MINE; ++c) s.b[c] = bload_u32x4(make_rsrc(pb.p[c], pb.bytes[c]), pb.off[c], (uint32_t)(k0 * 4));
+            for (int c = 0; c < SB::MINE; ++c) s.b[c] = bload_u32x4(make_rsrc32(pb.p[c], pb.bytes[c]), pb.off[c] + (uint32_t)(k0 * 4), 0);
         }
     };
     // What a row's pieces hold behind K, in the step where it ends.
@@ -147,9 +166,9 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
     };
     auto put = [&](uint16_t *buf, const Set &s) {
 #pragma unroll
-        for (int c = 0; c < SA::MINE; ++c) put_piece<float, SA>(buf, (int)threadIdx.x + c * NT, s.a[c]);
+        for (int c = 0; c < SA::MINE; ++c) put_piece<float, SA>(buf, SA::piece((int)threadIdx.x, c), s.a[c]);
 #pragma unroll
-        for (int c = 0; c < SB::MINE; ++c) put_piece<float, SB>(buf + SA::ELEMS, (int)threadIdx.x + c * NT, s.b[c]);
+        for (int c = 0; c < SB::MINE; ++c) put_piece<float, SB>(buf + SA::ELEMS, SB::piece((int)threadIdx.x, c), s.b[c]);
     };
 
     f32x4_t acc[PL][TL::NI][TL::MI];
@@ -161,10 +180,11 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
             for (int i = 0; i < TL::MI; ++i) acc[b][j][i] = f32x4_t{};
 
     // Step kt: its operands lie in `buf`; `next` takes those of kt + 1 from `s`, which
-    // then loads those of kt + 3.
-    auto step = [&](int kt, const uint16_t *buf, uint16_t *next, Set &s) {
-        // The planes in turn, so that the fragments of two are held at a time; a band's
-        // products need no order among them.
+    // then loads those of kt + 3.  MORE: 0 for the last step, 2 where kt + 1 is the
+    // last, which may end inside K.  The planes' fragments are read in turn, two planes
+    // held at a time; a band's products need no order among them.
+    auto step = [&](int kt, const uint16_t *buf, uint16_t *next, Set &s, auto more) {
+        constexpr int MORE = decltype(more)::value;
         bf16x8_t fa[2][TL::MI], fb[2][TL::NI];
         auto read = [&](int into, int q) {
 #pragma unroll
@@ -182,31 +202,57 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
         };
         read(0, 0);
         read(1, 1);
-        clear_tail(s, kt + 1);
-        put(next, s);                        // whose readers passed the last barrier
         multiply(0, 0, 0);
         multiply(1, 0, 1);
         multiply(1, 1, 0);
         multiply(2, 1, 1);
         read(1, 2);
+        if constexpr (MORE == 2) clear_tail(s, kt + 1);
+        if constexpr (MORE != 0) put(next, s);   // whose readers passed the last barrier
+        if constexpr (MORE == 1) load(s, kt + 3);   // past the last step: nothing that is used
         multiply(2, 0, 1);
         multiply(2, 1, 0);
-        load(s, kt + 3);                     // past the last step: nothing inside the descriptors
+        if constexpr (MORE == 1) {
+            constexpr int MFMAS = 6 * TL::MI * TL::NI, PUTS = SA::MINE + SB::MINE, EACH = MFMAS / PUTS;
+#pragma unroll
+            for (int q = 0; q < PUTS; ++q) {
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // an MFMA
+                    __builtin_amdgcn_sched_group_barrier(0x002, (56 + EACH - 1) / EACH, 0);  // vector instructions
+                }
+                __builtin_amdgcn_sched_group_barrier(0x200, 3, 0);                           // a piece's three parts
+            }
+        }
         lds_barrier();
     };
     if (steps > 0) {
+        constexpr auto MAIN = std::integral_constant<int, 1>();
         Set s0, s1;
         load(s0, 0);
         load(s1, 1);
-        clear_tail(s0, 0);
+        if (steps == 1) clear_tail(s0, 0);
         put(lds[0], s0);
         load(s0, 2);
         lds_barrier();
-        for (int kt = 0; kt < steps; kt += 2) {
-            step(kt, lds[0], lds[1], s1);
-            if (kt + 1 >= steps) break;
-            step(kt + 1, lds[1], lds[0], s0);
+        int kt = 0;
+        for (; kt + 3 < steps; kt += 2) {
+            step(kt, lds[0], lds[1], s1, MAIN);
+            step(kt + 1, lds[1], lds[0], s0, MAIN);
         }
+        int at = 0;
+        if (kt + 2 < steps) {
+            step(kt, lds[0], lds[1], s1, MAIN);
+            s1 = s0;
+            at = 1;
+            ++kt;
+        }
+        if (kt + 1 < steps) {
+            step(kt, lds[at], lds[at ^ 1], s1, std::integral_constant<int, 2>());
+            at ^= 1;
+            ++kt;
+        }
+        step(kt, lds[at], nullptr, s1, std::integral_constant<int, 0>());
     }
 
     // acc[..][j][i][q]: row 16 i + (lane & 15), column 16 j + 4 (lane >> 4) + q of the wave's block
@@ -233,13 +279,19 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
             int64_t m = m0 + wm * TL::TM + i * 16 + mlane;
             bool in = m < m_end && n < F;
             float *row = (float *)g.C;
+            int64_t ld = g.ldc;
             if constexpr (OP == kBackW) {
-                m = g.map.row(m);
-                in = in && m >= 0;
-                row += e * g.bank;
+                if (g.partials != nullptr) {
+                    row = g.partials + chunk * g.M * g.N;
+                    ld = g.N;
+                } else {
+                    m = g.map.row(m);
+                    in = in && m >= 0;
+                    row += e * g.bank;
+                }
             }
             if (!in) continue;
-            row += m * g.ldc + n;
+            row += m * ld + n;
             float v[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[q] = total(j, i, q) + b[q];
@@ -269,19 +321,20 @@ hipError_t launch_tile(ExpertProduct g, hipStream_t stream)
     g.tiles_m = (int)((g.M + TL::BM - 1) / TL::BM);        // dW only: elsewhere from the offsets
     g.tiles_n = (int)((g.N + TL::BN - 1) / TL::BN);
     const int64_t segments = g.n + 1;
-    const int64_t rows = OP == kBackW ? g.n * g.tiles_m : g.P / TL::BM + (segments < g.P ? segments : g.P);
+    const int64_t rows = OP == kBackW ? weight_chunks(g) * g.tiles_m : g.P / TL::BM + (segments < g.P ? segments : g.P);
     const int64_t blocks = rows * g.tiles_n;
     if (blocks * TL::NT >= (int64_t)1 << 32) return hipErrorInvalidValue;   // more work-items than a launch can have
     hipLaunchKernelGGL((expert_f32_kernel<TL, OP, GATE>), dim3((unsigned)blocks), dim3(TL::NT), 0, stream, g);
     return hipGetLastError();
 }
 
-// 128 x 128 tiles where they fill the CUs, else 64 x 64.
+// 128 x 128 tiles where they fill half of the CUs, else 64 x 64 (dX of 12288 x 1024 -> 256,
+// 208 tiles: 62 us against 90).
 template <int OP, int GATE>
 hipError_t launch_op(const ExpertProduct &g, hipStream_t stream)
 {
-    const int64_t tm = OP == kBackW ? g.n * ((g.M + 127) / 128) : g.P / 128, tn = (g.N + 127) / 128;
-    if (tm * tn >= (OP == kBackW ? 4 : 1) * g.num_cus) return launch_tile<Tile128, OP, GATE>(g, stream);
+    const int64_t tm = OP == kBackW ? weight_chunks(g) * ((g.M + 127) / 128) : g.P / 128, tn = (g.N + 127) / 128;
+    if (2 * tm * tn >= g.num_cus) return launch_tile<Tile128, OP, GATE>(g, stream);
     return launch_tile<Tile64, OP, GATE>(g, stream);
 }
 

@@ -121,6 +121,7 @@ __global__ __launch_bounds__(NT) void expert_sum_kernel(ExpertGate g, int64_t co
     const int64_t c = (int64_t)blockIdx.x * NT + threadIdx.x;
     if (c >= cols) return;
     float v = 0.0f;
+#pragma unroll 8
     for (int t = 0; t < tiles; ++t) v += g.sums[(int64_t)(before + t) * cols + c];
     ((T *)g.dbias)[(int64_t)e * cols + c] = Elem<T>::store(v);
 }

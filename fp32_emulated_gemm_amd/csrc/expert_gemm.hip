@@ -104,9 +104,9 @@ __global__ __launch_bounds__(TL::NT) void expert_kernel(ExpertProduct g)
     };
     auto put = [&](uint16_t *buf) {
 #pragma unroll
-        for (int c = 0; c < SA::MINE; ++c) put_piece<T, SA>(buf, (int)threadIdx.x + c * NT, a[c]);
+        for (int c = 0; c < SA::MINE; ++c) put_piece<T, SA>(buf, SA::piece((int)threadIdx.x, c), a[c]);
 #pragma unroll
-        for (int c = 0; c < SB::MINE; ++c) put_piece<T, SB>(buf + SA::ELEMS, (int)threadIdx.x + c * NT, b[c]);
+        for (int c = 0; c < SB::MINE; ++c) put_piece<T, SB>(buf + SA::ELEMS, SB::piece((int)threadIdx.x, c), b[c]);
     };
     if (steps > 0) {
         load(0);
@@ -218,6 +218,36 @@ hipError_t launch_op(const ExpertProduct &g, hipStream_t stream)
     return launch_tile<Tile64, OP, GATE>(g, stream);
 }
 
+// dW_e = the sum of its pieces' products, in order; zeros without one.
+constexpr int SUM_ROWS = 8;
+template <class D>
+__global__ __launch_bounds__(256) void sum_chunks_kernel(ExpertProduct g)
+{
+    const int lane = threadIdx.x & 63, e = (int)blockIdx.y, across = (int)((g.N + 255) / 256);
+    int before = 0;
+    for (int i = lane; i < e; i += 64) before += (int)((expert_end(g.offsets, i, g.n, g.P) - expert_start(g.offsets, i, g.P) + g.chunk - 1) / g.chunk);
+    before = __builtin_amdgcn_readfirstlane(wave_sum(before));
+    // offsets that do not ascend may count more pieces than there are
+    const int most = (int)weight_chunks(g), first = imin(before, most);
+    const int64_t rows = expert_end(g.offsets, e, g.n, g.P) - expert_start(g.offsets, e, g.P);
+    const int count = imin((int)((rows + g.chunk - 1) / g.chunk), most - first);
+    const int64_t n = (int64_t)((int)blockIdx.x % across) * 256 + threadIdx.x, m0 = (int64_t)((int)blockIdx.x / across) * SUM_ROWS;
+    if (n >= g.N) return;
+    float v[SUM_ROWS];
+#pragma unroll
+    for (int i = 0; i < SUM_ROWS; ++i) v[i] = 0.0f;
+    for (int c = 0; c < count; ++c) {
+        const float *const p = g.partials + (first + c) * g.M * g.N + n;
+#pragma unroll
+        for (int i = 0; i < SUM_ROWS; ++i) v[i] += p[lmin(m0 + i, g.M - 1) * g.N];
+    }
+#pragma unroll
+    for (int i = 0; i < SUM_ROWS; ++i) {
+        const int64_t m = m0 + i < g.M ? g.map.row(m0 + i) : -1;
+        if (m >= 0) ((D *)g.C)[e * g.bank + m * g.ldc + n] = Elem<D>::store(v[i]);
+    }
+}
+
 hipError_t launch(int op, const ExpertProduct &g, hipStream_t stream)
 {
     if (op == BACK_X) return launch_op<BACK_X, -1>(g, stream);
@@ -238,8 +268,16 @@ hipError_t launch_expert(int op, int dtype, const ExpertProduct &g, hipStream_t 
 {
     if (op == kBackW ? g.n == 0 || g.M == 0 : g.P == 0) return hipSuccess;
     if (g.N == 0) return hipSuccess;
-    if (dtype == kF32) return launch_expert_f32(op, g, stream);
-    return expert_lies(op, g) ? launch_expert_bf16(op, g, stream) : launch(op, g, stream);
+    const bool lies = dtype == kF32 || expert_lies(op, g);
+    ExpertProduct q = g;
+    if (!lies || q.chunk == 0) q.partials = nullptr;
+    const hipError_t e = dtype == kF32 ? launch_expert_f32(op, q, stream)
+                         : lies ? launch_expert_bf16(op, q, stream) : launch(op, q, stream);
+    if (e != hipSuccess || q.partials == nullptr) return e;
+    const dim3 grid((unsigned)(((g.N + 255) / 256) * ((g.M + SUM_ROWS - 1) / SUM_ROWS)), (unsigned)g.n);
+    if (dtype == kF32) hipLaunchKernelGGL(sum_chunks_kernel<float>, grid, dim3(256), 0, stream, q);
+    else hipLaunchKernelGGL(sum_chunks_kernel<uint16_t>, grid, dim3(256), 0, stream, q);
+    return hipGetLastError();
 }
 
 }  // namespace sgemm_emu_dev

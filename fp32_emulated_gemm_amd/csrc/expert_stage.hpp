@@ -36,11 +36,14 @@ struct Stage {
     // Offset of chunk c of LDS row `row` in a plane.
     static __device__ __forceinline__ int at(int row, int c) { return row * WIDE * 8 + slot(row, c) * 8; }
 
-    // Offset of piece `p` in a plane.
-    static __device__ __forceinline__ int piece(int p)
+    // Offset in a plane of a thread's piece c.  The permutation repeats after 16 rows: one
+    // address serves all pieces where they lie so far apart.
+    static __device__ __forceinline__ int piece(int thread, int c)
     {
-        const int c = p % ROW * V;
-        return at(p / ROW, c >> 3) + (c & 7);
+        constexpr int ROWS = NT / ROW;
+        const int k = thread % ROW * V;
+        if constexpr (ROWS % 16 == 0) return at(thread / ROW, k >> 3) + (k & 7) + c * NT * V;
+        else return at(thread / ROW + c * ROWS, k >> 3) + (k & 7);
     }
 
     // Fragment: k 8 (lane >> 4) .. + 7 of index base + (lane & 15).
@@ -62,11 +65,10 @@ struct Stage {
     }
 };
 
-// A piece to its place in the planes.
+// A piece to offset `at` of the planes.
 template <class T, class S>
-__device__ __forceinline__ void put_piece(uint16_t *buf, int p, const u32x4_t &v)
+__device__ __forceinline__ void put_piece(uint16_t *buf, int at, const u32x4_t &v)
 {
-    uint16_t *const at = buf + S::piece(p);
     if constexpr (sizeof(T) == 4) {
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         u32x2 w[3];
@@ -79,9 +81,9 @@ __device__ __forceinline__ void put_piece(uint16_t *buf, int p, const u32x4_t &v
             w[2][i] = p2;
         }
 #pragma unroll
-        for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x2 *>(at + q * S::PLANE) = w[q];
+        for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x2 *>(buf + at + q * S::PLANE) = w[q];
     } else {
-        *reinterpret_cast<u32x4_t *>(at) = v;
+        *reinterpret_cast<u32x4_t *>(buf + at) = v;
     }
 }
 

@@ -62,9 +62,24 @@ struct ExpertProduct {
     float *Z;                    // with a gate: pre-activations (see z_pitch), or null
     int64_t ldz;
     Halves map;                  // dX: rows of B behind k; dW: rows of the weight behind dZ's columns
+    float *partials;             // dW: sums of pieces of `chunk` rows, M x N each, or null
+    int64_t chunk;
     int num_cus;
     int tiles_m, tiles_n;        // set by the launch
 };
+// A weight gradient with few tiles runs over pieces of the experts' rows, so that one
+// expert with many rows does not hold the others up: rows of a piece (0: the tiles
+// suffice), such that there are about two tiles to a CU, and the pieces at most.
+constexpr int64_t kPlanCus = 256;            // MI355X
+constexpr int64_t weight_chunk(int64_t P, int64_t M, int64_t N, int64_t n)
+{
+    const int64_t per = ((M + 127) / 128) * ((N + 127) / 128), even = round_up(P * per / (2 * kPlanCus), 64);
+    return n * per >= 3 * kPlanCus || P <= 256 || per == 0 ? 0 : even < 256 ? 256 : even >= P ? 0 : even;
+}
+__host__ __device__ inline int64_t weight_chunks(const ExpertProduct &g)
+{
+    return g.partials == nullptr ? g.n : g.P / g.chunk + (g.n < g.P ? g.n : g.P);
+}
 // kForward: C[r] = A[r] B_e^T (+ bias, gate) on the rows r of expert e.
 // kBackX: C[r] = A[r] B_e with B_e's rows by `map`: A = dZ (K columns), N columns.
 // Both leave zeros on rows of no expert.

@@ -61,13 +61,16 @@ struct SortWs {
 
 struct BackwardWs {
     void *dZ;
-    float *sums;
-    int64_t bytes;
-    BackwardWs(void *ws, int dtype, int64_t P, int64_t N, int64_t n, int gate, bool dbias)
+    float *sums, *partials;
+    int64_t chunk, bytes;
+    BackwardWs(void *ws, int dtype, int64_t P, int64_t N, int64_t K, int64_t n, int gate, bool dbias)
     {
         Carve c(ws);
         dZ = gate >= 0 ? (void *)c.take<char>(P * expert_dz_pitch(N / 2) * size_of(dtype)) : nullptr;
         sums = dbias ? c.take<float>(expert_gate_tiles(P, n) * N) : nullptr;
+        const int64_t M = gate >= 0 ? expert_dz_pitch(N / 2) : N;
+        chunk = weight_chunk(P, M, K, n);
+        partials = chunk > 0 ? c.take<float>((P / chunk + (n < P ? n : P)) * M * K) : nullptr;
         bytes = c.bytes;
     }
 };
@@ -205,7 +208,7 @@ int64_t sgemm_emu_expert_linear_backward_workspace(int dtype, int64_t P, int64_t
 {
     if (!dtype_ok(dtype) || !extent_ok(P) || !bank_ok(n, N, K)) return SGEMM_EMU_EINVAL;
     CHECK(check_gate(gate, N));
-    return BackwardWs(nullptr, dtype, P, N, n, gate, dbias != 0).bytes;
+    return BackwardWs(nullptr, dtype, P, N, K, n, gate, dbias != 0).bytes;
 }
 
 int sgemm_emu_expert_linear_backward(int dtype, int64_t P, int64_t N, int64_t K, int64_t n, const void *X, int64_t ldx,
@@ -226,7 +229,7 @@ int sgemm_emu_expert_linear_backward(int dtype, int64_t P, int64_t N, int64_t K,
     CHECK(check_operand(dtype, P, K, dX, lddx, true));
     CHECK(check_vector(n * N * K, dW, elem, true));
     CHECK(check_vector(n * N, dbias, elem, true));
-    const BackwardWs w(ws, dtype, P, N, n, gate, dbias != nullptr);
+    const BackwardWs w(ws, dtype, P, N, K, n, gate, dbias != nullptr);
     CHECK(check_ws(ws, ws_bytes, w.bytes));
     int cus = 0;
     CHECK(current_cus(&cus));
@@ -263,6 +266,7 @@ int sgemm_emu_expert_linear_backward(int dtype, int64_t P, int64_t N, int64_t K,
         g.M = pitch;
         g.B = X; g.ldb = ldx; g.bank = N * K;
         g.C = dW; g.ldc = K;
+        g.partials = w.partials; g.chunk = w.chunk;
         LAUNCH(launch_expert(kBackW, dtype, g, s));
     }
     return SGEMM_EMU_OK;

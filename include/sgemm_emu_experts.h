@@ -72,8 +72,8 @@ int sgemm_emu_combine_tokens_backward(int dtype, int64_t T, int64_t k, int64_t K
  *   H = act(Z[:, :F]) * Z[:, F:].
  *   X: P x K; W: n x N x K contiguous; bias: n x N contiguous or NULL; H: P x N, or
  *   P x F with a gate.  FP32: the six leading products of a three-way BF16 split to
- *   nearest (what is left out is below 2^-25 of a product), or FP32 matrix
- *   instructions where a call has few rows; summed in FP32.
+ *   nearest (what is left out is below 2^-25 of a product), summed in FP32; an Inf or
+ *   NaN reaches the outputs of its row or expert only.
  *   Zkeep: NULL, or with a gate P rows of 2 pad8(F) floats as in
  *   sgemm_emu_gated_linear, for the backward.
  */
