@@ -476,7 +476,7 @@ hipError_t launch_quant4_unpack(int dtype, const Quant4 &w, const void *packed, 
     return hipGetLastError();
 }
 
-bool quant4_few(const Quant4 &w, int64_t P) { return P <= 64 || P <= 16 * w.n; }
+bool quant4_few(const Quant4 &w, int64_t P) { return P <= kFewRows || P <= 16 * w.n; }
 
 hipError_t launch_quant4_few(int dtype, const Quant4 &w, const Quant4Product &g, hipStream_t stream)
 {

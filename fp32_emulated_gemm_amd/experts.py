@@ -20,6 +20,7 @@ from .ops import (DTYPES, GATES, addr, check_tensor, forward_mode, ok, ops_lib, 
 
 SGEMM_EMU_MAX_EXPERTS = 1024
 SGEMM_EMU_GATE_NONE = -1
+SORT_IN_ONE = 1024   # pairs that the sort takes without workspace, at least: those calls need not ask
 
 EXPERTS_EXPORTS = ("sgemm_emu_sort_tokens_workspace", "sgemm_emu_sort_tokens", "sgemm_emu_gather_tokens",
                    "sgemm_emu_combine_tokens", "sgemm_emu_combine_tokens_backward", "sgemm_emu_expert_linear",
@@ -80,22 +81,30 @@ class ExpertOrder:
     `offsets` [n + 1]: expert e's rows are [offsets[e], offsets[e + 1]); `pairs` [T k]: sorted row -> pair
     t k + j, -1 behind the last; `places` [T, k]: pair -> sorted row, -1 where it comes nowhere.  int32."""
 
-    __slots__ = ("offsets", "pairs", "places", "experts", "tokens", "choices")
+    __slots__ = ("offsets", "pairs", "places", "experts", "tokens", "choices", "rows", "device_index")
 
     def __init__(self, offsets, pairs, places, experts):
         self.offsets, self.pairs, self.places, self.experts = offsets, pairs, places, experts
         self.tokens, self.choices = places.shape
-
-    @property
-    def rows(self):
-        return self.tokens * self.choices
+        self.rows = self.tokens * self.choices
+        self.device_index = offsets.get_device() if offsets.is_cuda else None
 
 
 def check_order(order):
     if not isinstance(order, ExpertOrder):
         raise TypeError(f"order: expected an ExpertOrder (of sort_tokens), got {type(order).__name__}")
-    if not order.offsets.is_cuda or order.offsets.get_device() != torch.cuda.current_device():
+    if order.device_index is None or order.device_index != torch.cuda.current_device():
         raise ValueError(f"order: expected one on the current HIP device, got {order.offsets.device}")
+
+
+def _fits(t, order, rows):
+    """check_order and check_tensor of a tensor of `rows` rows in one expression, for the calls where the
+    host's time counts."""
+    try:
+        return (t.dtype in DTYPES and t.dim() == 2 and t.shape[0] == rows
+                and t.get_device() == order.device_index == torch.cuda.current_device())
+    except (AttributeError, RuntimeError):       # RuntimeError: no device
+        return False
 
 
 def sort_tokens(ids, experts):
@@ -103,21 +112,26 @@ def sort_tokens(ids, experts):
     of one expert keep their order; an id outside [0, experts) comes nowhere."""
     if not isinstance(ids, torch.Tensor):
         raise TypeError(f"ids: expected a torch tensor, got {type(ids).__name__}")
-    if ids.dim() not in (1, 2):
-        raise ValueError(f"ids: expected one or two dimensions, got {ids.dim()}")
-    check_tensor(ids, "ids", torch.int32, ids.shape)
+    dims = ids.dim()
+    if dims not in (1, 2):
+        raise ValueError(f"ids: expected one or two dimensions, got {dims}")
+    if ids.dtype is not torch.int32 or not ids.is_cuda or ids.get_device() != torch.cuda.current_device():
+        check_tensor(ids, "ids", torch.int32, ids.shape)
     if not 0 <= experts <= SGEMM_EMU_MAX_EXPERTS:
         raise ValueError(f"experts: expected 0 to {SGEMM_EMU_MAX_EXPERTS}, got {experts}")
     L = experts_lib()
     ids = ids.contiguous()
     T, P = ids.shape[0], ids.numel()
     out = ids.new_empty(2 * P + experts + 1)
-    offsets, pairs, places = out.split((experts + 1, P, P))
-    nws = ok(L.sgemm_emu_sort_tokens_workspace(P, experts), "sgemm_emu_sort_tokens_workspace")
+    offsets, pairs, places = out.split_with_sizes((experts + 1, P, P))
+    nws = 0
+    if P > SORT_IN_ONE:
+        nws = ok(L.sgemm_emu_sort_tokens_workspace(P, experts), "sgemm_emu_sort_tokens_workspace")
     ws = scratch(nws, ids)
-    ok(L.sgemm_emu_sort_tokens(P, experts, addr(ids), addr(offsets), addr(pairs), addr(places), addr(ws), nws,
+    at = out.data_ptr()
+    ok(L.sgemm_emu_sort_tokens(P, experts, addr(ids), at, at + 4 * (experts + 1), at + 4 * (experts + 1 + P), addr(ws), nws,
                                stream_of(ids.get_device())), "sgemm_emu_sort_tokens")
-    return ExpertOrder(offsets, pairs, places.view(T, ids.shape[1] if ids.dim() == 2 else 1), experts)
+    return ExpertOrder(offsets, pairs, places.view(T, ids.shape[1] if dims == 2 else 1), experts)
 
 
 def _gather(x, order):
@@ -180,8 +194,9 @@ class _CombineFn(torch.autograd.Function):
 def gather_tokens(x, order):
     """Rows x[t] of x [T, K] (float32 or bfloat16) in the order of their experts: [T k, K], zeros behind the
     last.  Differentiable in x, in reverse mode."""
-    check_order(order)
-    check_tensor(x, "x", value_type(x, "x"), (order.tokens, None))
+    if not _fits(x, order, getattr(order, "tokens", None)):
+        check_order(order)
+        check_tensor(x, "x", value_type(x, "x"), (order.tokens, None))
     return _GatherFn.apply(x, order) if _differentiable(x) else _gather(x, order)
 
 
@@ -189,10 +204,12 @@ def combine_tokens(ys, order, weights=None):
     """y[t] = sum over j of weights[t, j] ys[row of pair (t, j)] for ys [T k, K] (float32 or bfloat16), summed
     in 32 bits with j ascending; weights: float32 [T, k], or None (1).  Pairs that come nowhere add nothing.
     Differentiable in ys and weights, in reverse mode."""
-    check_order(order)
-    check_tensor(ys, "ys", value_type(ys, "ys"), (order.rows, None))
+    if not _fits(ys, order, getattr(order, "rows", None)):
+        check_order(order)
+        check_tensor(ys, "ys", value_type(ys, "ys"), (order.rows, None))
     if weights is not None:
-        check_tensor(weights, "weights", torch.float32, (order.tokens, order.choices))
+        if not (_fits(weights, order, order.tokens) and weights.dtype is torch.float32 and weights.shape[1] == order.choices):
+            check_tensor(weights, "weights", torch.float32, (order.tokens, order.choices))
         weights = weights.contiguous()
     return _CombineFn.apply(ys, order, weights) if _differentiable(ys, weights) else _combine(ys, order, weights)
 
@@ -264,9 +281,10 @@ def expert_linear(x, weight, order, bias=None, gate=None):
     "gelu_tanh", "sigmoid", "relu") act(x Wg^T + bg) * (x Wu^T + bu), weight[e] = [Wg; Wu]; zeros on rows of
     no expert.  x [T k, K] sorted (gather_tokens), weight [n, N, K], bias [n, N] or None, all float32 or all
     bfloat16 on the current HIP device.  Differentiable in x, weight and bias, in reverse mode."""
-    check_order(order)
-    dt = value_type(x, "x")
-    check_tensor(x, "x", dt, (order.rows, None))
+    if not _fits(x, order, getattr(order, "rows", None)):
+        check_order(order)
+        check_tensor(x, "x", value_type(x, "x"), (order.rows, None))
+    dt = x.dtype
     check_tensor(weight, "weight", dt, (order.experts, None, x.shape[1]))
     if bias is not None:
         check_tensor(bias, "bias", dt, weight.shape[:2])

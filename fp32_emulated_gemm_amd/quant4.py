@@ -11,6 +11,7 @@ served, not trained.  The calls are those of include/sgemm_emu_experts.h.
 """
 import torch
 
+from . import ops
 from .experts import (ExpertFeedForward, check_order, combine_tokens, experts_lib, gate_code, gather_tokens,
                       sort_tokens, value_type)
 from .ops import DTYPES, addr, check_tensor, forward_mode, ok, rows_of, scratch, stream_of
@@ -21,15 +22,12 @@ GROUPS = (32, 64, 128)
 class Quant4Weight:
     """A weight [N, K] or a bank of experts' [n, N, K] held in 4 bits, laid out by quantize or pack."""
 
-    __slots__ = ("packed", "shape", "group", "zeros")
+    __slots__ = ("packed", "shape", "group", "zeros", "bank")
 
     def __init__(self, packed, shape, group, zeros):
         self.packed, self.shape, self.group, self.zeros = packed, tuple(shape), group, zeros
-
-    @property
-    def bank(self):
-        """(experts, rows, columns), one expert for a layer's weight."""
-        return self.shape if len(self.shape) == 3 else (1, *self.shape)
+        # (experts, rows, columns), one expert for a layer's weight
+        self.bank = self.shape if len(self.shape) == 3 else (1, *self.shape)
 
     def dequantize(self, dtype=torch.float32):
         """The weights that it stands for, rounded to `dtype` (float32 or bfloat16)."""
@@ -106,13 +104,13 @@ def quant4_linear(x, weight, bias=None, gate=None, order=None):
         raise TypeError(f"weight: expected a Quant4Weight (of quantize or pack), got {type(weight).__name__}")
     dt = value_type(x, "x")
     n, N, K = weight.bank
+    shape, d = x.shape, x.get_device()
     if order is None:
         if len(weight.shape) != 2:
             raise ValueError("weight: a bank of experts needs the rows' order")
-        if x.dim() < 1:
+        if len(shape) < 1:
             raise ValueError("x: expected at least one dimension")
-        check_tensor(x, "x", dt, (*x.shape[:-1], K))
-        P = x.shape[:-1].numel()
+        P = shape[0] if len(shape) == 2 else shape[:-1].numel()
     else:
         check_order(order)
         if len(weight.shape) != 3:
@@ -120,10 +118,11 @@ def quant4_linear(x, weight, bias=None, gate=None, order=None):
         if n != order.experts:
             raise ValueError(f"weight: expected a bank of {order.experts} experts, got {n}")
         P = order.rows
-        check_tensor(x, "x", dt, (P, K))
+    if not (x.is_cuda and shape[-1] == K and d == torch.cuda.current_device() and (order is None or tuple(shape) == (P, K))):
+        check_tensor(x, "x", dt, (*shape[:-1], K) if order is None else (P, K))
     if bias is not None:
         check_tensor(bias, "bias", dt, (N,) if order is None else (n, N))
-    if weight.packed.device != x.device:
+    if weight.packed.get_device() != d:
         raise ValueError(f"weight: expected one on {x.device}, got {weight.packed.device}")
     act = gate_code(gate, N)
     if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)):
@@ -133,18 +132,20 @@ def quant4_linear(x, weight, bias=None, gate=None, order=None):
             if t is not None and torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
                 raise NotImplementedError("quant4_linear has no forward-mode derivative")
     L = experts_lib()
-    x2d, xld = rows_of(x if x.dim() == 2 else x.reshape(P, K))
+    x2d, xld = rows_of(x if len(shape) == 2 else x.reshape(P, K))
     bias = None if bias is None else bias.contiguous()
     out = N // 2 if gate is not None else N
     h = x.new_empty((P, out))
     code = DTYPES[dt]
-    nws = ok(L.sgemm_emu_quant4_linear_workspace(code, P, N, K, n, weight.group, weight.zeros),
-             "sgemm_emu_quant4_linear_workspace")
+    nws = 0
+    if P > ops.FEW_ROWS:                 # fewer read the packed weight
+        nws = ok(L.sgemm_emu_quant4_linear_workspace(code, P, N, K, n, weight.group, weight.zeros),
+                 "sgemm_emu_quant4_linear_workspace")
     ws = scratch(nws, x)
     ok(L.sgemm_emu_quant4_linear(code, P, N, K, n, weight.group, weight.zeros, addr(x2d), xld, addr(weight.packed),
                                  addr(bias), act, None if order is None else addr(order.offsets), addr(h),
-                                 max(out, 1), addr(ws), nws, stream_of(x.get_device())), "sgemm_emu_quant4_linear")
-    return h if x.dim() == 2 else h.reshape(*x.shape[:-1], out)
+                                 max(out, 1), addr(ws), nws, stream_of(d)), "sgemm_emu_quant4_linear")
+    return h if len(shape) == 2 else h.reshape(*shape[:-1], out)
 
 
 class _Held(torch.nn.Module):

@@ -57,7 +57,7 @@ def combine(ys, places, weights, dy=None):
     """y (and dys, dw with dy)."""
     bf16 = ys.dtype == torch.bfloat16
     T, k = places.shape
-    Y, w = ys.double(), torch.ones(T, k, dtype=torch.float64, device=x.device) if weights is None else weights.double()
+    Y, w = ys.double(), torch.ones(T, k, dtype=torch.float64, device=ys.device) if weights is None else weights.double()
     there = (places >= 0).double()
     rows = Y[places.long().clamp(min=0).reshape(-1)].view(T, k, -1) if Y.shape[0] else Y.new_zeros(T, k, Y.shape[1])
     # rows of pairs that come nowhere may hold anything

@@ -97,7 +97,7 @@ def test_strides(dtype):
     for ys in (tall[:, 3:K + 3], tall[:, :K], tall[:1, :K].expand(T * k, K)):
         ref.check(combine_tokens(ys, order, weights), xr.combine(ys.cpu(), places, weights.cpu())["y"], "y")
     leaf = tall[:, 3:K + 3].detach().requires_grad_(True)
-    dy = across.t().expand(T, K) if False else across.t()
+    dy = across.t()
     grad, = torch.autograd.grad(combine_tokens(leaf, order, weights), (leaf,), dy)
     ref.check(grad, xr.combine(leaf.detach().cpu(), places, weights.cpu(), dy.cpu())["dys"], "dys")
 
