@@ -31,6 +31,7 @@ struct Route {
     T *rows_out;                 // sorted rows: Xs, dYs (or null)
     int64_t ldr_out;
     float *dweights;             // or null
+    bool past;                   // set by the launch
 };
 hipError_t launch_route(int what, const Route<float> &a, hipStream_t stream);
 hipError_t launch_route(int what, const Route<uint16_t> &a, hipStream_t stream);

@@ -86,6 +86,8 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_place_kernel(Sort a)
 #pragma unroll
             for (int w = 0; w < SORT_WAVES; ++w) all += at[w][e];
         } else {
+            // loads of several workgroups' counts under way at a time
+#pragma unroll 16
             for (int b = 0; b < a.blocks; ++b) {
                 const int c = a.counts[(int64_t)b * (n + 1) + e];
                 before += b < (int)blockIdx.x ? c : 0;
@@ -125,6 +127,7 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_place_kernel(Sort a)
     if (e == SORT_THREADS - 1) {
         int pos = total;
         if constexpr (!ONE)
+#pragma unroll 16
             for (int b = 0; b < (int)blockIdx.x; ++b) pos += a.counts[(int64_t)b * (n + 1) + n];
 #pragma unroll
         for (int w = 0; w < SORT_WAVES; ++w) {
@@ -167,7 +170,8 @@ struct Piece {
     static constexpr int V = Elem<T>::VEC, COLS = 64 * V * PIECES;
     u32x4_t v[PIECES];
 
-    // Columns c0.. of a row; past K zeros.
+    // Columns c0.. of a row; past K zeros.  ONCE: nobody reads them again.
+    template <bool ONCE = false>
     __device__ __forceinline__ void load(const T *row, int64_t c0, int64_t K, int lane)
     {
 #pragma unroll
@@ -175,7 +179,8 @@ struct Piece {
             const int64_t c = c0 + (i * 64 + lane) * V;
             v[i] = u32x4_t{0, 0, 0, 0};
             if (c + V <= K) {
-                v[i] = *reinterpret_cast<const u32x4_any *>(row + c);
+                const u32x4_any *const p = reinterpret_cast<const u32x4_any *>(row + c);
+                v[i] = ONCE ? __builtin_nontemporal_load(p) : *p;
             } else {
                 for (int e = 0; e < V; ++e)
                     if (c + e < K) {
@@ -185,13 +190,15 @@ struct Piece {
             }
         }
     }
-    __device__ __forceinline__ void store(T *row, int64_t c0, int64_t K, int lane) const
+    // past: past the caches, for outputs that they would not hold until they are read.
+    __device__ __forceinline__ void store(T *row, int64_t c0, int64_t K, int lane, bool past = false) const
     {
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             const int64_t c = c0 + (i * 64 + lane) * V;
             if (c + V <= K) {
-                *reinterpret_cast<u32x4_any *>(row + c) = v[i];
+                if (past) __builtin_nontemporal_store(v[i], reinterpret_cast<u32x4_t *>(row + c));
+                else *reinterpret_cast<u32x4_any *>(row + c) = v[i];
             } else {
                 for (int e = 0; e < V; ++e)
                     if (c + e < K) {
@@ -249,7 +256,7 @@ __device__ __forceinline__ void clear_rest(const Route<T> &a, T *rows, int64_t l
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) zero.v[i] = u32x4_t{0, 0, 0, 0};
     for (int64_t r = (last < 0 ? 0 : last) + unit; r < a.P; r += units)
-        for (int64_t c = c0; c < c1; c += Piece<T>::COLS) zero.store(rows + r * ld, c, a.K, lane);
+        for (int64_t c = c0; c < c1; c += Piece<T>::COLS) zero.store(rows + r * ld, c, a.K, lane, a.past);
 }
 
 template <class T>
@@ -263,7 +270,7 @@ __global__ __launch_bounds__(NT) void gather_kernel(Route<T> a)
     const int32_t *const place = a.places + t * a.k;
     for (int64_t j = 0; j < a.k; ++j) {
         const int64_t r = place[j];
-        if (r >= 0 && r < a.P) x.store(a.rows_out + r * a.ldr_out, c0, a.K, lane);
+        if (r >= 0 && r < a.P) x.store(a.rows_out + r * a.ldr_out, c0, a.K, lane, a.past);
     }
     clear_rest(a, a.rows_out, a.ldr_out, t, a.tokens, c0, c0 + 1, lane);
 }
@@ -292,7 +299,7 @@ __global__ __launch_bounds__(NT) void combine_kernel(Route<T> a)
             const int64_t r = j0 + q < a.k ? place[j0 + q] : -1;
             in[q] = r >= 0 && r < a.P;
             if (in[q]) {
-                y[q].load(a.rows + r * a.ldr, c0, a.K, lane);
+                y[q].template load<true>(a.rows + r * a.ldr, c0, a.K, lane);
                 w[q] = WEIGHTS ? a.weights[t * a.k + j0 + q] : 1.0f;
             }
         }
@@ -308,7 +315,7 @@ __global__ __launch_bounds__(NT) void combine_kernel(Route<T> a)
     }
     Piece<T> out;
     out.put(acc);
-    out.store(a.x_out + t * a.ldx_out, c0, a.K, lane);
+    out.store(a.x_out + t * a.ldx_out, c0, a.K, lane, a.past);
 }
 
 // One wave per pair: the token's gradient is read once from memory and by its
@@ -346,7 +353,7 @@ __global__ __launch_bounds__(NT) void combine_backward_kernel(Route<T> a)
 #pragma unroll
                     for (int e = 0; e < V; ++e) g[i][e] *= w;
                 dy.put(g);
-                dy.store(a.rows_out + r * a.ldr_out, c0, a.K, lane);
+                dy.store(a.rows_out + r * a.ldr_out, c0, a.K, lane, a.past);
             }
         }
     }
@@ -364,9 +371,18 @@ dim3 token_grid(const Route<T> &a)
     return dim3((unsigned)((a.tokens + WAVES - 1) / WAVES), (unsigned)((a.K + Piece<T>::COLS - 1) / Piece<T>::COLS));
 }
 
+// With sorted rows of more than half of the last-level cache (256 MB) outputs go past
+// it: what was written first would be gone before the next kernel reads it, and its
+// way out competes with reads (65536 x 2048 bfloat16 gathered, then as many summed:
+// 187 us in all, 161 past the caches).  Rows of whole 16-byte pieces only: others
+// would be stored element by element.
 template <class T>
-hipError_t route(int what, const Route<T> &a, hipStream_t stream)
+hipError_t route(int what, const Route<T> &args, hipStream_t stream)
 {
+    Route<T> a = args;
+    const void *const to = what == kCombine ? (const void *)a.x_out : a.rows_out;
+    const int64_t ld = what == kCombine ? a.ldx_out : a.ldr_out;
+    a.past = a.P * a.K * (int64_t)sizeof(T) > (int64_t)128 << 20 && ld * (int64_t)sizeof(T) % 16 == 0 && aligned(to, 16);
     if (a.tokens == 0 || a.K == 0) return hipSuccess;
     const bool w = a.weights != nullptr;
     const dim3 tokens = token_grid(a), pairs((unsigned)((a.P + WAVES - 1) / WAVES));
