@@ -372,11 +372,12 @@ enum { TILE_64, TILE_128, TILE_256, TILES };
 int best_tile(int op, const ExpertProduct &g)
 {
     if (op == kBackW && g.partials != nullptr) return TILE_128;
-    static const struct { int size, per_cu, step, fixed; } t[TILES] = {{64, 2, 38, 20}, {128, 2, 82, 50}, {256, 1, 138, 100}};
+    static const struct { int size, per_cu, step, fixed, keep; } t[TILES] = {
+        {64, 2, 38, 20, 60}, {128, 2, 82, 50, 210}, {256, 1, 138, 100, 280}};
     const int64_t steps = ((op == kBackW ? g.P / g.n : g.K) + KS - 1) / KS;
-    // kept pre-activations leave at a tile's end, 256 KB of a 256 x 256 tile
-    const int64_t keep = g.Z != nullptr ? 30 : 0;
-    auto round = [&](int i, int64_t step) { return steps * step + t[i].fixed * 10 + keep * t[i].size * t[i].size * t[i].per_cu / 800; };
+    // kept pre-activations leave at a tile's end: 16382 x 2048 -> 2 x 1365 takes 250 us in
+    // three whole rounds of 256 x 256 tiles and 38 for the rest, 310 in six of 128 x 128
+    auto round = [&](int i, int64_t step) { return steps * step + (t[i].fixed + (g.Z != nullptr ? t[i].keep : 0)) * 10; };
     int best = TILE_64;
     int64_t least = INT64_MAX;
     for (int i = 0; i < TILES; ++i) {
