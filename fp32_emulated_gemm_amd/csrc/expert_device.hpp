@@ -142,8 +142,10 @@ __device__ __forceinline__ uint32_t pack2_finite(float a, float b)
 }
 
 // The parts of two FP32 values, x = x0 + 2^-8 x1 + 2^-16 x2, each stage rounded to
-// nearest even by the hardware's conversion.  x0 and x1 stay finite: an Inf or NaN
-// comes through in x2 (Inf - finite), so its products are those of IEEE.
+// nearest even by the hardware's conversion.  x0 and x1 stay finite, so that a value
+// beyond the largest BF16 keeps its own; an Inf or NaN comes through in x2, and what it
+// reaches is Inf or NaN (NaN where the largest BF16 times the other operand's smaller
+// part overflows to the other side).
 __device__ __forceinline__ void split2_nearest(float x, float y, uint32_t &p0, uint32_t &p1, uint32_t &p2)
 {
     p0 = pack2_finite(x, y);

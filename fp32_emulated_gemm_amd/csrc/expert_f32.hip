@@ -1,10 +1,13 @@
 // expert_f32.hip -- the experts' FP32 products.
 //
 // Each operand is split into three BF16 parts as it is staged, x = x0 + 2^-8 x1 +
-// 2^-16 x2, every stage rounded to nearest even.  Then |x1| <= |x| / 2 and |x2| <=
-// |x| / 4, so the three products x1 w2, x2 w1 and x2 w2 together stay below 2^-25
-// |x w|, half of an FP32 rounding, and are left out: six products on the BF16 matrix
-// cores in three bands of one weight each, summed in FP32 and added smallest first.
+// 2^-16 x2, every stage rounded to nearest even.  With 2^e <= |x| < 2^(e+1) the first
+// rounding leaves at most 2^(e-8), so |x1| <= 2^e <= |x|, and the second 2^(e-9) of
+// that, so |x2| <= 2^(e-1) <= |x| / 2.  The products x1 w2 and x2 w1, of weight 2^-24,
+// are each at most |x w| / 2 (x2 w2 is 2^-10 of them): together at most 2^-24 |x w|,
+// an FP32 product's own rounding, and a tenth of it on average.  They are left out:
+// six products on the BF16 matrix cores in three bands of one weight each, summed in
+// FP32 and added smallest first.
 //
 // One workgroup per output tile, in K steps of 32.  A step's operands are loaded two
 // steps ahead, and split and written to the other LDS buffer among the MFMAs of the

@@ -35,13 +35,16 @@ __global__ __launch_bounds__(256) void quantize_kernel(Quant4 w, const T *W, uin
         const int64_t row = u / groups, c = (u - row * groups) * w.group;
         const int64_t left = lmin(w.group, w.K - c);
         float v[2], lo = 0.0f, hi = 0.0f;
+        bool finite = true;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int at = lane + 64 * i;
             v[i] = at < left ? Elem<T>::load(W + row * w.K + c + at) : 0.0f;
             lo = fminf(lo, v[i]);
             hi = fmaxf(hi, v[i]);
+            finite = finite && __builtin_fabsf(v[i]) <= 3.40282347e38f;
         }
+        finite = __all(finite);
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) {
             lo = fminf(lo, __shfl_xor(lo, d));
@@ -54,6 +57,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(Quant4 w, const T *W, uin
         } else {
             s = fmaxf(hi, -lo) * (1.0f / 7.0f);
         }
+        if (!finite) s = __builtin_nanf("");
         const float most = zero != nullptr ? 15.0f - z : 7.0f, least = zero != nullptr ? -z : -7.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -155,7 +155,8 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_place_kernel(Sort a)
             const int64_t p = sort_pair(s);
             pos += rank;
             a.places[p] = key[s] < n ? pos : -1;
-            a.pairs[pos] = key[s] < n ? (int32_t)p : -1;
+            // ids that change while they are sorted must not lead outside
+            if (pos < a.P) a.pairs[pos] = key[s] < n ? (int32_t)p : -1;
         }
     }
 }

@@ -72,8 +72,9 @@ int sgemm_emu_combine_tokens_backward(int dtype, int64_t T, int64_t k, int64_t K
  *   H = act(Z[:, :F]) * Z[:, F:].
  *   X: P x K; W: n x N x K contiguous; bias: n x N contiguous or NULL; H: P x N, or
  *   P x F with a gate.  FP32: the six leading products of a three-way BF16 split to
- *   nearest (what is left out is below 2^-25 of a product), summed in FP32; an Inf or
- *   NaN reaches the outputs of its row or expert only.
+ *   nearest (what is left out is at most 2^-24 of a product, an FP32 product's own
+ *   rounding), summed in FP32; an Inf or NaN makes the outputs that it reaches, of
+ *   its row or expert only, Inf or NaN.
  *   Zkeep: NULL, or with a gate P rows of 2 pad8(F) floats as in
  *   sgemm_emu_gated_linear, for the backward.
  */
@@ -104,7 +105,8 @@ int sgemm_emu_expert_linear_backward(int dtype, int64_t P, int64_t N, int64_t K,
  * sgemm_emu_quant4_quantize -- nearest such weights of W (n x N x K contiguous):
  *   zero NULL: symmetric, scale = max|w| / 7 and q - 8 in -7..7; else scale =
  *   (max(w, 0) - min(w, 0)) / 15, zero = -min / scale rounded.  Groups of zeros take
- *   scale 0.  Values are rounded to nearest, ties to even.
+ *   scale 0, groups with a NaN or an Inf stand for NaN.  Values are rounded to
+ *   nearest, ties to even.
  * sgemm_emu_quant4_pack -- lays them out for sgemm_emu_quant4_linear: `packed` of
  *   sgemm_emu_quant4_bytes bytes, 16-byte aligned.  q's high four bits are ignored,
  *   and so are zero's.
@@ -122,8 +124,9 @@ int sgemm_emu_quant4_unpack(int dtype, int64_t n, int64_t N, int64_t K, int64_t 
 /*
  * sgemm_emu_quant4_linear -- sgemm_emu_expert_linear with such weights.  offsets NULL:
  *   one layer (n = 1) on all P rows.  Few rows read the packed weights and sum
- *   (q - zero) x in FP32, scaled group by group; more rows (ws_bytes > 0) unpack
- *   the weights into ws first, rounded to the call's type.
+ *   (q - zero) x in FP32, scaled group by group (an Inf in a row of X makes that
+ *   row's outputs NaN); more rows (ws_bytes > 0) unpack the weights into ws first,
+ *   rounded to the call's type.
  */
 int64_t sgemm_emu_quant4_linear_workspace(int dtype, int64_t P, int64_t N, int64_t K, int64_t n, int64_t group,
                                           int zeros);

@@ -3,7 +3,9 @@ with the elementwise error bounds that the GPU tests hold the kernels to.
 
 Bounds, derived from the arithmetic as in ops_reference (u = 2^-24):
   a product of K terms summed in FP32: 2 K u sum|a b|; from FP32 operands in three BF16
-  parts the three smallest of nine products are left out, below 2^-25 = u / 2 of a term;
+  parts the three smallest of nine products are left out: with 2^e <= |x| < 2^(e+1) the
+  parts are |x1| <= 2^e <= |x| and |x2| <= 2^(e-1) <= |x| / 2 (8 bits to nearest leave
+  half of the last), so 2^-24 (x1 w2 + x2 w1) is at most 2^-24 |x w| = u of a term;
   4-bit weights with few rows: each group of g columns sums (16 + q) x and (16 + zero) x,
   2 (g + 4) u of their magnitudes, scaled; the groups' sums 2 (G + 16) u more, G groups
   in eight waves' parts;
@@ -100,7 +102,7 @@ def _epilogue(z, ez, gate, bf16):
 def experts(x, w, offsets, bias, gate, dh=None):
     """{name: (reference, bound)} of H (and dx, dw, db with dh); CPU tensors of one type."""
     bf16 = x.dtype == torch.bfloat16
-    left = 0.0 if bf16 else 0.5                       # products left out, in u of a term
+    left = 0.0 if bf16 else 1.0                       # products left out, in u of a term
     X, W = x.double(), w.double()
     n, N, K = w.shape
     P = x.shape[0]
@@ -171,7 +173,7 @@ def quant4(x, q, scale, zero, group, offsets, bias, gate, few):
             G = -(-K // group)
             ez = 2 * (group + 4) * U * (xe.abs() @ mags[e].T) + 2 * (G + 16) * U * mag
         else:
-            ez = (2 * K + 1.5) * U * mag + (BF if bf16 else U) * mag
+            ez = (2 * K + 2) * U * mag + (BF if bf16 else U) * mag
         if bias is not None:
             z = z + bias[e].double()
             ez = ez + U * z.abs()

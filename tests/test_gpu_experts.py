@@ -67,3 +67,35 @@ def test_other_gates(dtype, gate):
 @pytest.mark.parametrize("gate", [None, "silu"])
 def test_empty(dtype, T, k, n, N, K, gate):
     _check(dtype, T, k, n, N, K, gate, True, "none" if n == 0 else "mixed")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [20, 700])
+def test_values_that_are_not_finite_stay_in_their_rows(dtype, T):
+    """Inf and NaN in one expert's weights and in one row of X reach the outputs and gradients of those
+    alone, and make them Inf or NaN."""
+    from fp32_emulated_gemm_amd.experts import expert_linear, sort_tokens
+    n, N, K = 3, 40, 72
+    ids = (torch.arange(T) % n).int().unsqueeze(1)
+    offsets = xr.order(ids, n)[0].tolist()
+    order = sort_tokens(ids.cuda(), n)
+    x, w, _, dh = _inputs(dtype, T, N, K, n, None, False)
+    clean = xr.experts(x, w, torch.tensor(offsets), None, None, dh)
+    w[1, 7, 5] = float("inf")
+    x[offsets[3] - 1, 9] = float("-inf")
+    x[0, 3] = float("nan")
+    xd, wd = x.cuda().requires_grad_(True), w.cuda().requires_grad_(True)
+    h = expert_linear(xd, wd, order)
+    dx, dw = torch.autograd.grad(h, (xd, wd), dh.cuda())
+    h, dx, dw = h.detach().cpu(), dx.cpu(), dw.cpu()
+    s, t = offsets[1], offsets[2]
+    rows = torch.ones(T, dtype=torch.bool)
+    rows[0] = rows[-1] = False
+    assert h[0].isnan().all() and not h[-1].isfinite().any() and not h[s:t, 7].isfinite().any()
+    ok = rows.unsqueeze(1).expand(T, N).clone()
+    ok[s:t, 7] = False
+    bad = (h.double() - clean["h"][0]).abs() > clean["h"][1]
+    assert not (bad & ok).any()
+    other = torch.cat((torch.arange(s), torch.arange(t, T)))
+    assert ((dx.double() - clean["dx"][0]).abs() <= clean["dx"][1])[other].all()
+    assert ((dw.double() - clean["dw"][0]).abs() <= clean["dw"][1])[1].all()

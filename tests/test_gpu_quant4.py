@@ -73,6 +73,18 @@ def test_quantized_to_nearest(dtype, group, symmetric, shape):
     assert (w4[..., 0, :] == 0).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("symmetric", [True, False])
+def test_groups_that_are_not_finite_stand_for_nan(bad, symmetric):
+    from fp32_emulated_gemm_amd.quant4 import quantize
+    w = torch.randn(3, 100, device="cuda")
+    w[1, 40] = bad
+    got = quantize(w, 32, symmetric).dequantize()
+    assert got[1, 32:64].isnan().all()
+    got[1, 32:64] = 0.0
+    assert got.isfinite().all()
+
+
 def _products(dtype, T, k, n, N, K, group, zeros, gate, bias, kind="mixed", seed=0):
     """k = 0: a layer."""
     from fp32_emulated_gemm_amd.experts import sort_tokens
