@@ -140,7 +140,9 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
             // dX: a step lies in one half of dZ's columns (h is a multiple of BK, or K itself)
             const bool up = OP == kBackX && k0 >= g.map.h;
             const int64_t in = up ? k0 - g.map.h : k0, row = OP == kBackW ? r0 + k0 : up ? g.map.F + in : in;
-            const int64_t left = OP == kBackW ? K - k0 : g.map.F - in;
+            // a step past the last (loaded ahead, never used) has no rows: without a gate the
+            // rows behind W's last would seem to be an up half
+            const int64_t left = OP == kBackW ? K - k0 : lmin(g.map.F - in, K - k0);
             const rsrc_t r = make_rsrc32(B + row * g.ldb + n0, extent(rows_left(left), g.ldb, g.N, n0));
 #pragma unroll
             for (int c = 0; c < SB::MINE; ++c) s.b[c] = bload_u32x4(r, pb.off[0] + (uint32_t)(c * (NT / SB::ROW) * g.ldb * 4), 0);
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
         read(1, 2);
         if constexpr (MORE == 2) clear_tail(s, kt + 1);
         if constexpr (MORE != 0) put(next, s);   // whose readers passed the last barrier
-        if constexpr (MORE == 1) load(s, kt + 3);   // past the last step: nothing that is used
+        if constexpr (MORE == 1) load(s, kt + 3);   // past the last step: nothing inside the descriptors that is used
         multiply(2, 0, 1);
         multiply(2, 1, 0);
         if constexpr (MORE == 1) {

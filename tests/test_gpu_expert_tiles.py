@@ -55,7 +55,9 @@ def test_bfloat16_tiles(counts, spare, N, K, gate):
 
 
 @pytest.mark.parametrize("counts,spare,N,K,gate", [
-    ([700, 0, 1300, 250], 30, 1024, 256, "gelu"), ([2100, 1800, 900], 20, 1030, 131, None), ([4000], 0, 512, 512, None)])
+    ([700, 0, 1300, 250], 30, 1024, 256, "gelu"), ([2100, 1800, 900], 20, 1030, 131, None), ([4000], 0, 512, 512, None),
+    # weights of whole allocations, whose ends the steps loaded ahead must not pass
+    ([512], 0, 2048, 2048, None), ([128], 0, 1024, 1024, None)])
 def test_float32_tiles(counts, spare, N, K, gate):
     _compare("f32", counts, spare, N, K, gate)
 
