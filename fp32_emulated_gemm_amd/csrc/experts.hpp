@@ -148,7 +148,7 @@ struct Quant4Product {
     int num_cus;
 };
 // Whether a call of P rows reads the packed weights (else it unpacks them first).
-bool quant4_few(const Quant4 &w, int64_t P);
+bool quant4_few(int dtype, const Quant4 &w, int64_t P);
 hipError_t launch_quant4_few(int dtype, const Quant4 &w, const Quant4Product &g, hipStream_t stream);
 
 }  // namespace sgemm_emu_dev

@@ -321,7 +321,7 @@ int64_t sgemm_emu_quant4_linear_workspace(int dtype, int64_t P, int64_t N, int64
                                           int zeros)
 {
     if (!dtype_ok(dtype) || !extent_ok(P) || !bank_ok(n, N, K) || !group_ok(group)) return SGEMM_EMU_EINVAL;
-    return quant4_few(quant4(n, N, K, group, zeros), P) ? 0 : round_up(n * N * K * size_of(dtype), 256);
+    return quant4_few(dtype, quant4(n, N, K, group, zeros), P) ? 0 : round_up(n * N * K * size_of(dtype), 256);
 }
 
 int sgemm_emu_quant4_linear(int dtype, int64_t P, int64_t N, int64_t K, int64_t n, int64_t group, int zeros,
@@ -343,7 +343,7 @@ int sgemm_emu_quant4_linear(int dtype, int64_t P, int64_t N, int64_t K, int64_t 
     CHECK(current_cus(&cus));
     const Quant4 w = quant4(n, N, K, group, zeros);
     const hipStream_t s = (hipStream_t)stream;
-    if (quant4_few(w, P)) {
+    if (quant4_few(dtype, w, P)) {
         Quant4Product g{P, X, ldx, packed, bias, gate, offsets, H, ldh, cus};
         LAUNCH(launch_quant4_few(dtype, w, g, s));
         return SGEMM_EMU_OK;

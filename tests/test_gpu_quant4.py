@@ -112,7 +112,8 @@ def _products(dtype, T, k, n, N, K, group, zeros, gate, bias, kind="mixed", seed
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("T,N,K", [(1, 2, 1), (1, 64, 128), (1, 130, 1000), (3, 34, 129), (16, 96, 256), (17, 66, 500),
-                                   (33, 48, 64), (64, 320, 384), (65, 96, 160), (300, 130, 257)])
+                                   (33, 48, 64), (64, 320, 384), (65, 96, 160), (128, 48, 200),
+                                   (129, 64, 96), (300, 130, 257)])
 @pytest.mark.parametrize("gate,bias,zeros", [(None, True, True), ("silu", False, True), ("gelu", True, False)])
 def test_layers(dtype, group, T, N, K, gate, bias, zeros):
     _products(dtype, T, 0, 1, N, K, group, zeros, gate, bias, seed=T + K)
