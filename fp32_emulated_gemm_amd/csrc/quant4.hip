@@ -185,8 +185,8 @@ template <class T>
 struct XBlock {
     u32x4_t v[4][sizeof(T) / 2];
 
-    // LIES: rows at whole dwords, loaded through a descriptor that ends with the last
-    // element.  Rows past the last read zeros.
+    // LIES: rows at whole dwords, loaded through a descriptor that ends with the dword of
+    // the last element.  Rows past the last read zeros.
     template <bool LIES>
     __device__ __forceinline__ void load(const T *X, int64_t ldx, int64_t row, int64_t rows, int64_t k0, int64_t K, int lane)
     {
@@ -194,7 +194,8 @@ struct XBlock {
         if constexpr (LIES) {
             // a descriptor for the tile's 16 rows; the row of this lane lies `lane & 15` further
             const int64_t first = row - (lane & 15), left = rows - first;
-            const rsrc_t r = make_rsrc(X + first * ldx, left > 0 ? ((lmin(left, 16) - 1) * ldx + K) * (int64_t)sizeof(T) : 0);
+            const int64_t bytes = ((lmin(left, 16) - 1) * ldx + K) * (int64_t)sizeof(T);
+            const rsrc_t r = make_rsrc(X + first * ldx, left > 0 ? (bytes + 3) & ~3ll : 0);
             const uint32_t off = row < rows ? (uint32_t)(((lane & 15) * ldx + (lane >> 4) * 8) * sizeof(T)) : 0xFFFFFFF0u;
 #pragma unroll
             for (int d = 0; d < 4; ++d)

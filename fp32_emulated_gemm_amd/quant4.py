@@ -118,7 +118,7 @@ def quant4_linear(x, weight, bias=None, gate=None, order=None):
         if n != order.experts:
             raise ValueError(f"weight: expected a bank of {order.experts} experts, got {n}")
         P = order.rows
-    if not (x.is_cuda and shape[-1] == K and d == torch.cuda.current_device() and (order is None or tuple(shape) == (P, K))):
+    if not (x.is_cuda and shape[-1:] == (K,) and d == torch.cuda.current_device() and (order is None or tuple(shape) == (P, K))):
         check_tensor(x, "x", dt, (*shape[:-1], K) if order is None else (P, K))
     if bias is not None:
         check_tensor(bias, "bias", dt, (N,) if order is None else (n, N))

@@ -208,6 +208,34 @@ def test_layouts(dtype, T):
             assert (got.double() - want.double()).abs().max() <= (2.0 ** -7 if dtype == "bf16" else 2.0 ** -18) * want.abs().max()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("P,K,ld", [(1, 129, 130), (2, 129, 130), (5, 63, 66), (17, 1, 2), (40, 255, 258), (65, 33, 40)])
+def test_odd_rows_at_even_strides(dtype, P, K, ld):
+    """The last element of the last row, and nothing behind it (NaN there), in each product."""
+    from fp32_emulated_gemm_amd.experts import expert_linear, sort_tokens
+    from fp32_emulated_gemm_amd.quant4 import quant4_linear, quantize
+    g = torch.Generator("cuda").manual_seed(P + K)
+    wide = torch.full((P, ld), float("nan"), device="cuda", dtype=xr.DT[dtype])
+    wide[:, :K] = torch.randn(P, K, generator=g, device="cuda").to(wide.dtype)
+    wide[:, K - 1] = 8.0                         # a lost last column shows
+    x = wide[:, :K]
+    weight = torch.randn(1, 32, K, generator=g, device="cuda").to(wide.dtype)
+    order = sort_tokens(torch.zeros(P, device="cuda", dtype=torch.int32), 1)
+    w4 = quantize(weight, 32)
+    one = quantize(weight[0], 32)
+    for got, w in ((expert_linear(x, weight, order), weight[0]), (quant4_linear(x, w4, order=order), w4.dequantize()[0]),
+                   (quant4_linear(x, one), one.dequantize())):
+        want = x.double() @ w.double().t()
+        # the sums' roundings, of terms up to 31 scales in 4 bits (a scale: at most 2/15 of the
+        # largest weight); in bfloat16 also the result's, and an unpacked weight's
+        w = w.double().abs()
+        room = x.double().abs() @ (w + 62 / 15 * w.amax(1, keepdim=True)).t()
+        tol = (K / 4 + 8) * 2.0 ** -24 * room
+        if dtype == "bf16":
+            tol = tol + 2.0 ** -8 * (want.abs() + x.double().abs() @ w.t())
+        assert ((got.double() - want).abs() <= tol).all()
+
+
 def test_refusals():
     from fp32_emulated_gemm_amd.experts import combine_tokens, expert_linear, gather_tokens, sort_tokens
     from fp32_emulated_gemm_amd.quant4 import quant4_linear, quantize
@@ -222,6 +250,7 @@ def test_refusals():
                 lambda: expert_linear(ys, w, order, torch.zeros(3, 5, device="cuda")),
                 lambda: expert_linear(ys, w.cpu(), order), lambda: quant4_linear(x, bank), lambda: quant4_linear(ys, w4, order=order),
                 lambda: quant4_linear(x[:, :4], w4), lambda: quant4_linear(x, w4, torch.zeros(5, device="cuda")),
+                lambda: quant4_linear(x[0, 0], bank, order=order),
                 lambda: quant4_linear(x, quantize(w[0, :5]), gate="silu")):
         with pytest.raises(ValueError):
             bad()
