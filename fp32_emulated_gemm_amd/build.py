@@ -26,7 +26,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsgemm_emu.so")
 DEBUG_LIB = os.path.join(HERE, "libsgemm_emu_serial_lds.so")
 SOURCES = ["api.hip", "gemm.hip", "gemm_fused.hip", "split.hip", "ieee.hip", "ops_api.hip", "bf16_gemm.hip", "lowrank.hip", "layouts.hip",
-           "experts_api.hip", "route.hip", "expert_gemm.hip", "expert_bf16.hip", "expert_f32.hip", "expert_gate.hip", "quant4.hip"]
+           "experts_api.hip", "route.hip", "expert_gemm.hip", "expert_bf16.hip", "expert_f32.hip", "expert_few.hip",
+           "expert_gate.hip", "quant4.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero", "-mcode-object-version=5",

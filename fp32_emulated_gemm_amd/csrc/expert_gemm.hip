@@ -268,6 +268,7 @@ hipError_t launch_expert(int op, int dtype, const ExpertProduct &g, hipStream_t 
 {
     if (op == kBackW ? g.n == 0 || g.M == 0 : g.P == 0) return hipSuccess;
     if (g.N == 0) return hipSuccess;
+    if (op == kForward && expert_few(dtype, g)) return launch_expert_few(dtype, g, stream);
     const bool lies = dtype == kF32 || expert_lies(op, g);
     ExpertProduct q = g;
     if (!lies || q.chunk == 0) q.partials = nullptr;

@@ -93,6 +93,9 @@ hipError_t launch_expert_f32(int op, const ExpertProduct &g, hipStream_t stream)
 // expert_lies() tells whether a product's do.
 bool expert_lies(int op, const ExpertProduct &g);
 hipError_t launch_expert_bf16(int op, const ExpertProduct &g, hipStream_t stream);
+// Whether a forward product of few rows takes the kernel made for them.
+bool expert_few(int dtype, const ExpertProduct &g);
+hipError_t launch_expert_few(int dtype, const ExpertProduct &g, hipStream_t stream);
 
 // ---------------------------------------------------------------- gate backward (expert_gate.hip)
 // Halves of a row of dZ are padded to whole tiles, so that no step over its columns

@@ -15,7 +15,7 @@
 // formed in FP32 and scaled once a group.  The offset of 16 costs two or three of
 // FP32's 24 bits (128 + q, one shift less, would cost five).  FP32 rows of X come in
 // three BF16 parts; a weight is one, so three products in three bands.
-#include "expert_device.hpp"
+#include "expert_rows.hpp"
 
 namespace sgemm_emu_dev {
 
@@ -179,82 +179,7 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t w)
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// The columns 8 (lane >> 4) .. + 7 of four steps of 32 of X's row `m`, as they come:
-// one row of a tile of 16 in each lane.
-template <class T>
-struct XBlock {
-    u32x4_t v[4][sizeof(T) / 2];
-
-    // LIES: rows at whole dwords, loaded through a descriptor that ends with the dword of
-    // the last element.  Rows past the last read zeros.
-    template <bool LIES>
-    __device__ __forceinline__ void load(const T *X, int64_t ldx, int64_t row, int64_t rows, int64_t k0, int64_t K, int lane)
-    {
-        constexpr int PIECES = sizeof(T) / 2;
-        if constexpr (LIES) {
-            // a descriptor for the tile's 16 rows; the row of this lane lies `lane & 15` further
-            const int64_t first = row - (lane & 15), left = rows - first;
-            const int64_t bytes = ((lmin(left, 16) - 1) * ldx + K) * (int64_t)sizeof(T);
-            const rsrc_t r = make_rsrc(X + first * ldx, left > 0 ? (bytes + 3) & ~3ll : 0);
-            const uint32_t off = row < rows ? (uint32_t)(((lane & 15) * ldx + (lane >> 4) * 8) * sizeof(T)) : 0xFFFFFFF0u;
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-#pragma unroll
-                for (int i = 0; i < PIECES; ++i)
-                    v[d][i] = bload_u32x4(r, off == 0xFFFFFFF0u ? off : off + (uint32_t)((k0 + d * 32) * sizeof(T) + i * 16), 0);
-            if (k0 + KB <= K) return;
-            // the last block: what the pieces hold behind K
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const int64_t end = K - (k0 + d * 32 + (lane >> 4) * 8);
-#pragma unroll
-                for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if constexpr (sizeof(T) == 4) v[d][i][q] = i * 4 + q < end ? v[d][i][q] : 0u;
-                        else v[d][i][q] = 2 * q + 1 < end ? v[d][i][q] : 2 * q < end ? v[d][i][q] & 0xFFFFu : 0u;
-                    }
-            }
-        } else {
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const int64_t k = k0 + d * 32 + (lane >> 4) * 8;
-#pragma unroll
-                for (int i = 0; i < PIECES; ++i)
-                    v[d][i] = load_piece<T>(X + row * ldx + k + i * Elem<T>::VEC, row < rows ? K - k - i * Elem<T>::VEC : 0);
-            }
-        }
-    }
-    __device__ __forceinline__ void parts(int d, u32x4_t (&p)[sizeof(T) == 4 ? 3 : 1]) const
-    {
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t p0, p1, p2;
-                split2_nearest(__uint_as_float(v[d][i >> 1][2 * (i & 1)]), __uint_as_float(v[d][i >> 1][2 * (i & 1) + 1]), p0,
-                               p1, p2);
-                p[0][i] = p0;
-                p[1][i] = p1;
-                p[2][i] = p2;
-            }
-        } else {
-            p[0] = v[d][0];
-        }
-    }
-};
-
 typedef uint32_t u32_any __attribute__((aligned(1)));
-
-__device__ __forceinline__ float gate_value(int gate, float z)
-{
-    switch (gate) {
-    case kSilu: return gate_act<kSilu>(z);
-    case kGelu: return gate_act<kGelu>(z);
-    case kGeluTanh: return gate_act<kGeluTanh>(z);
-    case kSigmoid: return gate_act<kSigmoid>(z);
-    default: return gate_act<kRelu>(z);
-    }
-}
 
 // GROUP columns share a scale.  A workgroup takes NB tiles of 16 rows of W (with a
 // gate, NB / 2 of the gate's and those of the up projection's same outputs) and 16 MB
@@ -310,7 +235,7 @@ __global__ __launch_bounds__(64 * WAVES) void quant4_few_kernel(Quant4 w, Quant4
             u32x4_t v[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) v[b] = next[b];
-            XBlock<T> x[MB];
+            RowBlock<T> x[MB];
 #pragma unroll
             for (int m = 0; m < MB; ++m)
                 x[m].template load<LIES>((const T *)g.X, g.ldx, m0 + m * 16 + (lane & 15), r1, kb * KB, w.K, lane);
