@@ -74,6 +74,15 @@ def _differentiable(*tensors):
     return forward_mode() or (torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in tensors]))
 
 
+def once(backward):
+    """torch's once_differentiable, whose own time a backward pass that records nothing is spared."""
+    recorded = torch.autograd.function.once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return (recorded if torch.is_grad_enabled() else backward)(ctx, *grads)
+    return run
+
+
 # ---------------------------------------------------------------- tokens
 
 class ExpertOrder:
@@ -163,7 +172,7 @@ class _GatherFn(torch.autograd.Function):
         return _gather(x, order)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @once
     def backward(ctx, dxs):
         return _combine(dxs, ctx.order, None), None
 
@@ -176,7 +185,7 @@ class _CombineFn(torch.autograd.Function):
         return _combine(ys, order, weights)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @once
     def backward(ctx, dy):
         (ys, weights), order = ctx.saved_tensors, ctx.order
         L = experts_lib()
@@ -241,7 +250,7 @@ class _ExpertFn(torch.autograd.Function):
         return h
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @once
     def backward(ctx, dh):
         x, weight, z = ctx.saved_tensors
         gate, order = ctx.gate, ctx.order
