@@ -8,6 +8,11 @@
 // are permuted by its number so that the 8 rows of half a wave lie on all banks.
 // Rows past an expert's last are not copied: their lanes' offsets lie past the
 // descriptor and read zeros.
+//
+// The matrix cores bound it at the clock that the card's power allows: 32768 x 4096 ->
+// 2048 over 16 experts takes 550 us, 1.0 PFLOP/s (the library's 8192^3 product on the
+// same card: 1.13).  16382 x 2048 -> 2 x 1365: gated with Z 284 us, 645 TFLOP/s and 179 MB
+// of Z; dX 234, 780; dW 226, 810.
 #include "bf16_tile.hpp"
 #include "expert_device.hpp"
 

@@ -19,6 +19,11 @@
 // Operands whose k are rows (W in dX, dZ and X in dW) keep that layout in LDS and are
 // read by ds_read_b64_tr_b16, four k of a column at a time: nothing is transposed in
 // memory, and an expert's rows may start anywhere.
+//
+// What bounds it is the split beside the MFMAs: 2048^3 in one expert runs at 146 TFLOP/s
+// (the platform's FP32 product: 124; 154 at 8192^3).  12288 x 256 -> 1024 over eight
+// experts, gated, with Z: 84 us; dX 65, dW 64 and 11 for its pieces' sums: eight K steps
+// of a tile do not hide its start and end.
 #include <type_traits>
 
 #include "expert_stage.hpp"

@@ -110,21 +110,26 @@ int64_t row_tiles(const ExpertProduct &g) { return g.P / 16 + (g.n + 1 < g.P ? g
 
 }  // namespace
 
-// Up to 256 rows, where this kernel's time for a block of columns is below the tiles':
+// Up to 1024 rows, where this kernel's time for a block of columns is below the tiles':
 // hundredths of a us, at least those of one workgroup or tile alone, beyond that in
-// proportion to how many a CU has, with the rows evenly among the experts.  Times on
+// proportion to how many a CU has, with the rows evenly among the experts (beyond 256
+// rows: tiles as if one expert had all, where they are fewest).  Times on
 // 4096 x 4096, here and in 64 x 64 tiles: FP32 1 row 20 and 104 us, 64 rows 73 and 105,
 // 128 rows 132 and 108; bfloat16 1 row 9 and 18, 16 rows 11 and 18, 64 rows 32 and 18.
+// 512 rows of 128 x 2720: FP32 19 and 70, bfloat16 7 and 13.  bfloat16 rows that do not
+// lie in pieces, 1024 x 1001 over 8 experts: 1 row 5 and 13, 128 rows 12 and 17, 256 20 and 17.
 bool expert_few(int dtype, const ExpertProduct &g)
 {
-    if (g.P > 256 || g.n == 0) return false;
+    if (g.P > 1024 || g.n == 0) return false;
     const bool lies = dtype == kF32 || expert_lies(kForward, g);
     const int64_t with = g.n < g.P ? g.n : g.P, each = (g.P + with - 1) / with, cus = g.num_cus;
-    const int64_t here = with * ((each + 15) / 16) * ((g.N + 15) / 16), tiles = with * ((each + 63) / 64) * ((g.N + 63) / 64);
+    const int64_t here = with * ((each + 15) / 16) * ((g.N + 15) / 16);
+    const int64_t rows = g.P <= 256 ? with * ((each + 63) / 64) : (g.P + 63) / 64;
+    const int64_t tiles = rows * ((g.N + 63) / 64);
     auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
     if (dtype == kF32) return 50 * most(cus, here) < most(320 * cus, 270 * tiles);
     if (lies) return 20 * most(cus, here) < most(44 * cus, 68 * tiles);
-    return 25 * most(cus, here) < 120 * most(cus, tiles);
+    return 50 * most(cus, here) < 120 * most(cus, tiles);
 }
 
 hipError_t launch_expert_few(int dtype, const ExpertProduct &args, hipStream_t stream)

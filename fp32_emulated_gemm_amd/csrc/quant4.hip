@@ -15,6 +15,11 @@
 // formed in FP32 and scaled once a group.  The offset of 16 costs two or three of
 // FP32's 24 bits (128 + q, one shift less, would cost five).  FP32 rows of X come in
 // three BF16 parts; a weight is one, so three products in three bands.
+//
+// Few rows are bounded by the loads' latency, then by the weights' bytes: one bfloat16
+// row of 4096 x 4096 takes 6 us (9 MB); 64 rows over 64 experts of 2816 x 2048, gated,
+// 34 us, 123 MB at 3.7 TB/s; 16 float32 rows of 8192 x 1024 in groups of 32 9 us.
+// Unpacking 4096 x 4096 to bfloat16 takes 13 us, 42 MB at 3.3 TB/s.
 #include "expert_rows.hpp"
 
 namespace sgemm_emu_dev {
@@ -183,8 +188,8 @@ typedef uint32_t u32_any __attribute__((aligned(1)));
 
 // GROUP columns share a scale.  A workgroup takes NB tiles of 16 rows of W (with a
 // gate, NB / 2 of the gate's and those of the up projection's same outputs) and 16 MB
-// rows of X at a time; its waves take the blocks of 128 columns in turn, the next
-// block's values loaded under the products of the one before.
+// rows of X at a time, its share of the expert's; its waves take the blocks of 128
+// columns in turn, the next block's values loaded under the products of the one before.
 template <class T, int WAVES, int NB, int MB, int GROUP, bool LIES>
 __global__ __launch_bounds__(64 * WAVES) void quant4_few_kernel(Quant4 w, Quant4Product g)
 {
@@ -195,7 +200,8 @@ __global__ __launch_bounds__(64 * WAVES) void quant4_few_kernel(Quant4 w, Quant4
     const int OUT = gated ? NB / 2 * 16 : NB * 16;
     const int64_t e = blockIdx.y, F = gated ? w.N / 2 : w.N, n0 = (int64_t)blockIdx.x * OUT;
     const int64_t r0 = expert_start(g.offsets, e, g.P), r1 = expert_end(g.offsets, e, w.n, g.P);
-    if (r0 >= r1) return;
+    const int64_t first = r0 + (int64_t)blockIdx.z * 16 * MB;
+    if (first >= r1 || (e >= w.n && blockIdx.z > 0)) return;
     T *const H = (T *)g.H;
     if (e >= w.n) {                                        // rows of no expert
         for (int64_t o = threadIdx.x; o < (r1 - r0) * OUT; o += NT) {
@@ -219,7 +225,7 @@ __global__ __launch_bounds__(64 * WAVES) void quant4_few_kernel(Quant4 w, Quant4
         srow[b] = lmin(base, rows - 1) + 4 * (lane >> 4);
     }
     const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-    for (int64_t m0 = r0; m0 < r1; m0 += 16 * MB) {
+    for (int64_t m0 = first; m0 < r1; m0 += 16 * MB * (int64_t)gridDim.z) {
         f32x4_t acc[NB][MB];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -340,7 +346,16 @@ template <class T, int WAVES, int NB, int MB, int GROUP, bool LIES>
 hipError_t launch_few(const Quant4 &w, const Quant4Product &g, hipStream_t stream)
 {
     const int64_t out = g.gate >= 0 ? w.N / 2 : w.N, per = g.gate >= 0 ? NB * 8 : NB * 16;
-    const dim3 grid((unsigned)((out + per - 1) / per), (unsigned)(w.n + (g.offsets != nullptr ? 1 : 0)));
+    // an expert's rows over as many workgroups as the CUs have room for: one after the other
+    // they would wait for the same loads again
+    const int64_t across = (out + per - 1) / per, with = w.n < g.P ? w.n : g.P;
+    int64_t parts = 1;
+    if (with > 0) {
+        const int64_t each = (g.P + with - 1) / with, most = g.num_cus / (across * with);
+        parts = (each + 16 * MB - 1) / (16 * MB);
+        parts = parts < most ? parts : most < 1 ? 1 : most;
+    }
+    const dim3 grid((unsigned)across, (unsigned)(w.n + (g.offsets != nullptr ? 1 : 0)), (unsigned)parts);
     hipLaunchKernelGGL((quant4_few_kernel<T, WAVES, NB, MB, GROUP, LIES>), grid, dim3(64 * WAVES), 0, stream, w, g);
     return hipGetLastError();
 }
@@ -408,9 +423,10 @@ hipError_t launch_quant4_unpack(int dtype, const Quant4 &w, const void *packed, 
 
 // A layer's calls of up to 64 rows read the packed weight, and so do a bank's with up to
 // 16 rows an expert.  64 rows of 4096 x 4096 take 23 us in bfloat16 (groups of 128),
-// unpacked 38 whatever the rows up to 256.  float32 rows, whose unpacked product is
-// slow with few tiles, stay up to 128 with the larger groups: 64 rows 47 to 53 us,
-// unpacked 130; with groups of 32 they take 70, twice that at 128 rows.
+// unpacked 38 whatever the rows up to 256.  float32 rows stay up to 128 with the larger
+// groups: 128 rows of 4096 x 4096 take 50 to 57 us, unpacked 130; of 11008 x 4096 184 to
+// 207, unpacked 232.  With groups of 32, 64 rows of those take 41 and 135, unpacked 105
+// and 193, and twice the rows twice as long.
 bool quant4_few(int dtype, const Quant4 &w, int64_t P)
 {
     const int64_t most = dtype == kF32 && w.group >= 64 ? 2 * kFewRows : kFewRows;

@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("T,k,n,N,K", [
     (1, 1, 1, 2, 3), (1, 1, 1, 34, 127), (1, 3, 7, 30, 129), (2, 1, 1, 16, 1024), (7, 2, 5, 18, 2050), (15, 1, 1, 64, 128),
     (16, 1, 2, 96, 250), (17, 1, 1, 98, 385), (64, 4, 3, 62, 136), (256, 1, 1, 128, 72), (257, 1, 1, 128, 72),
-    (128, 2, 40, 66, 1025), (129, 2, 40, 66, 1025), (3, 2, 1024, 32, 64)])
+    (128, 2, 40, 66, 1025), (129, 2, 40, 66, 1025), (3, 2, 1024, 32, 64),
+    (1000, 1, 1, 34, 333), (512, 2, 3, 48, 700), (1025, 1, 2, 34, 333)])
 @pytest.mark.parametrize("gate,bias", [(None, True), ("silu", True), ("relu", False)])
 def test_few_rows(dtype, T, k, n, N, K, gate, bias):
     _check(dtype, T, k, n, N, K, gate, bias, "mixed", seed=T + N)
