@@ -5,7 +5,8 @@
 // expert and 16 outputs, and its waves take the blocks of 128 columns in turn: both
 // operands go from memory into MFMA fragments, nothing is shared but the sums at the
 // end.  FP32 operands come in three parts and six products, as in expert_f32.hip.
-// What bounds it: the loads' latency, then W's way in.
+// What bounds it: the loads' latency, then W's way in; one row of 4096 x 4096 takes 20 us
+// in FP32, 9 in bfloat16, 3.3 and 3.7 TB/s of W.
 #include "expert_rows.hpp"
 
 namespace sgemm_emu_dev {

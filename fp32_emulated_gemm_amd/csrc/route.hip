@@ -12,7 +12,7 @@
 // added (combine).  Memory bounds both: 16384 tokens of 2048 bfloat16, four experts each,
 // are gathered in 78 us and added up again in 75, 335 MB either way, 4.3 to 4.5 TB/s (a
 // large copy on this card: 5.2); 8191 tokens of 2044, eight experts each, added with
-// weights in 67, 4.5 TB/s.  The sort of 65536 pairs takes 5 + 7 us, of 32 pairs 4.
+// weights in 68, 4.4 TB/s.  The sort of 65536 pairs takes 5 + 7 us, of 32 pairs 4.
 #include "ops_device.hpp"
 #include "experts.hpp"
 
