@@ -208,6 +208,25 @@ def test_layouts(dtype, T):
             assert (got.double() - want.double()).abs().max() <= (2.0 ** -7 if dtype == "bf16" else 2.0 ** -18) * want.abs().max()
 
 
+@pytest.mark.parametrize("loss", [lambda y: y.sum(), lambda y: y.square().sum()])
+def test_second_derivatives_are_refused(loss):
+    """A recorded backward pass gives the gradients of one that is not, and no derivative of its own (torch
+    refuses at the backward node, or has no node where the incoming gradient is a constant)."""
+    from fp32_emulated_gemm_amd.experts import ExpertFeedForward
+    torch.manual_seed(1)
+    m = ExpertFeedForward(24, 16, 3, device="cuda")
+    x = torch.randn(5, 24, device="cuda", requires_grad=True)
+    ids = (torch.arange(10, device="cuda").view(5, 2) % 3).int()
+    weights = torch.rand(5, 2, device="cuda", requires_grad=True)
+    leaves = (x, weights, *m.parameters())
+    plain = torch.autograd.grad(loss(m(x, ids, weights)), leaves)
+    recorded = torch.autograd.grad(loss(m(x, ids, weights)), leaves, create_graph=True)
+    for a, b in zip(plain, recorded):
+        assert torch.equal(a, b)
+        with pytest.raises(RuntimeError):
+            b.sum().backward(retain_graph=True)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("P,K,ld", [(1, 129, 130), (2, 129, 130), (5, 63, 66), (17, 1, 2), (40, 255, 258), (65, 33, 40)])
 def test_odd_rows_at_even_strides(dtype, P, K, ld):
