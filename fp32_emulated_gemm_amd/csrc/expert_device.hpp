@@ -56,7 +56,8 @@ struct RowTiles {
     __device__ __forceinline__ RowTiles(const int32_t *o, int64_t n_, int64_t P_, int segments_, int lane_, int rows = 0)
         : offsets(o), n(n_), P(P_), lane(lane_), segments(segments_), BM(BM_ != 0 ? BM_ : rows)
     {
-        total = 0;
+        start = end = 0;                                                            // without a segment there is no tile
+        count = sum = total = 0;
         for (int e0 = (segments - 1) & ~63; e0 >= 0; e0 -= 64) total += scan(e0);   // ends with the first 64
     }
 
