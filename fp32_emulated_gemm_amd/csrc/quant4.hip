@@ -20,6 +20,8 @@
 // row of 4096 x 4096 takes 6 us (9 MB); 64 rows over 64 experts of 2816 x 2048, gated,
 // 34 us, 123 MB at 3.7 TB/s; 16 float32 rows of 8192 x 1024 in groups of 32 9 us.
 // Unpacking 4096 x 4096 to bfloat16 takes 13 us, 42 MB at 3.3 TB/s.
+#include <type_traits>
+
 #include "expert_rows.hpp"
 
 namespace sgemm_emu_dev {
@@ -118,6 +120,8 @@ __global__ __launch_bounds__(256) void pack_scales_kernel(Quant4 w, const float 
         char *const p = packed + bank * w.bank_bytes() + w.value_bytes();
         ((float *)p)[at] = in ? scale[src] : 0.0f;
         if (w.zeros) ((uint8_t *)(p + w.scale_bytes()))[at] = in ? 16 + (zero[src] & 15) : 24;
+        // spare bytes, read as scales of rows behind the last: nothing that is not finite
+        if (at < 16) ((uint32_t *)(p + w.scale_bytes() + w.zero_bytes()))[at] = 0;
     }
 }
 
@@ -173,18 +177,21 @@ __global__ __launch_bounds__(256) void unpack_kernel(Quant4 w, const void *packe
 
 // ---------------------------------------------------------------- few rows
 
-// Eight values 16 + q of a dword as BF16.
+// Eight values 16 + q of a dword as BF16; SIXTEEN: 16 times a power of two, twice.
+template <uint32_t SIXTEEN>
 __device__ __forceinline__ bf16x8_t widen(uint32_t w)
 {
     u32x4_t v;
-    v[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-    v[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-    v[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-    v[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+    v[0] = ((w << 3) & 0x00780078u) | SIXTEEN;
+    v[1] = ((w >> 1) & 0x00780078u) | SIXTEEN;
+    v[2] = ((w >> 5) & 0x00780078u) | SIXTEEN;
+    v[3] = ((w >> 9) & 0x00780078u) | SIXTEEN;
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
 typedef uint32_t u32_any __attribute__((aligned(1)));
+
+__device__ __forceinline__ bool is_finite(float x) { return __builtin_fabsf(x) <= 3.40282347e38f; }
 
 // GROUP columns share a scale.  A workgroup takes NB tiles of 16 rows of W (with a
 // gate, NB / 2 of the gate's and those of the up projection's same outputs) and 16 MB
@@ -224,93 +231,120 @@ __global__ __launch_bounds__(64 * WAVES) void quant4_few_kernel(Quant4 w, Quant4
         values[b] = p.values + (((row >> 4) * blocks) << 8) + (((lane & 48) | (row & 15)) << 2);
         srow[b] = lmin(base, rows - 1) + 4 * (lane >> 4);
     }
-    const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
     for (int64_t m0 = first; m0 < r1; m0 += 16 * MB * (int64_t)gridDim.z) {
-        f32x4_t acc[NB][MB];
+        // The sums over this wave's blocks, of weights times 2^-DOWN.
+        auto sum_blocks = [&](f32x4_t (&acc)[NB][MB], auto down) {
+            constexpr uint32_t DOWN = decltype(down)::value * 0x00800080u, ONE = 0x3F803F80u - DOWN, SIXTEEN = 0x41804180u - DOWN;
+            const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{ONE, ONE, ONE, ONE});
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int m = 0; m < MB; ++m) acc[b][m] = f32x4_t{};
-        u32x4_t next[NB];
-        auto load_values = [&](int64_t kb) {
+                for (int m = 0; m < MB; ++m) acc[b][m] = f32x4_t{};
+            u32x4_t next[NB];
+            auto load_values = [&](int64_t kb) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b) next[b] = *reinterpret_cast<const u32x4_t *>(values[b] + (kb << 8));
-        };
-        if (wave < blocks) load_values(wave);
-        for (int64_t kb = wave; kb < blocks; kb += WAVES) {
-            u32x4_t v[NB];
+                for (int b = 0; b < NB; ++b) next[b] = *reinterpret_cast<const u32x4_t *>(values[b] + (kb << 8));
+            };
+            if (wave < blocks) load_values(wave);
+            for (int64_t kb = wave; kb < blocks; kb += WAVES) {
+                u32x4_t v[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) v[b] = next[b];
-            RowBlock<T> x[MB];
+                for (int b = 0; b < NB; ++b) v[b] = next[b];
+                RowBlock<T> x[MB];
 #pragma unroll
-            for (int m = 0; m < MB; ++m)
-                x[m].template load<LIES>((const T *)g.X, g.ldx, m0 + m * 16 + (lane & 15), r1, kb * KB, w.K, lane);
-            f32x4_t scale[GROUPS][NB];
-            uint32_t zero[GROUPS][NB];
+                for (int m = 0; m < MB; ++m)
+                    x[m].template load<LIES>((const T *)g.X, g.ldx, m0 + m * 16 + (lane & 15), r1, kb * KB, w.K, lane);
+                f32x4_t scale[GROUPS][NB];
+                uint32_t zero[GROUPS][NB];
 #pragma unroll
-            for (int gr = 0; gr < GROUPS; ++gr)
+                for (int gr = 0; gr < GROUPS; ++gr)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int64_t at = (kb * GROUPS + gr) * rows + srow[b];
-                    scale[gr][b] = __builtin_bit_cast(f32x4_t, (u32x4_t)*reinterpret_cast<const u32x4_any *>(p.scale + at));
-                    zero[gr][b] = w.zeros ? *reinterpret_cast<const u32_any *>(p.zero + at) : 0x18181818u;
-                }
-            if (kb + WAVES < blocks) load_values(kb + WAVES);
-#pragma unroll
-            for (int gr = 0; gr < GROUPS; ++gr) {
-                f32x4_t part[PARTS][NB][MB], xs[PARTS][MB];
-#pragma unroll
-                for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        xs[q][m] = f32x4_t{};
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) part[q][b][m] = f32x4_t{};
+                    for (int b = 0; b < NB; ++b) {
+                        const int64_t at = (kb * GROUPS + gr) * rows + srow[b];
+                        scale[gr][b] = __builtin_bit_cast(f32x4_t, (u32x4_t)*reinterpret_cast<const u32x4_any *>(p.scale + at));
+                        zero[gr][b] = w.zeros ? *reinterpret_cast<const u32_any *>(p.zero + at) : 0x18181818u;
                     }
+                if (kb + WAVES < blocks) load_values(kb + WAVES);
 #pragma unroll
-                for (int st = 0; st < STEPS; ++st) {
-                    const int d = gr * STEPS + st;
-                    bf16x8_t wf[NB];
+                for (int gr = 0; gr < GROUPS; ++gr) {
+                    f32x4_t part[PARTS][NB][MB], xs[PARTS][MB];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) wf[b] = widen(v[b][d]);
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        u32x4_t xp[PARTS];
-                        x[m].parts(d, xp);
-#pragma unroll
-                        for (int q = 0; q < PARTS; ++q) {
-                            const bf16x8_t xf = __builtin_bit_cast(bf16x8_t, xp[q]);
-                            xs[q][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf, xs[q][m], 0, 0, 0);
-#pragma unroll
-                            for (int b = 0; b < NB; ++b)
-                                part[q][b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[b], xf, part[q][b][m], 0, 0, 0);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float z = -(float)((zero[gr][b] >> (8 * q)) & 255u);
+                    for (int q = 0; q < PARTS; ++q)
 #pragma unroll
                         for (int m = 0; m < MB; ++m) {
-                            float t = __builtin_fmaf(z, xs[0][m][q], part[0][b][m][q]);
-                            if constexpr (PARTS == 3) {
-                                const float t1 = __builtin_fmaf(z, xs[1][m][q], part[1][b][m][q]);
-                                const float t2 = __builtin_fmaf(z, xs[2][m][q], part[2][b][m][q]);
-                                t += __builtin_fmaf(t2, 0x1p-16f, t1 * 0x1p-8f);
-                            }
-                            acc[b][m][q] = __builtin_fmaf(scale[gr][b][q], t, acc[b][m][q]);
+                            xs[q][m] = f32x4_t{};
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) part[q][b][m] = f32x4_t{};
                         }
+#pragma unroll
+                    for (int st = 0; st < STEPS; ++st) {
+                        const int d = gr * STEPS + st;
+                        bf16x8_t wf[NB];
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) wf[b] = widen<SIXTEEN>(v[b][d]);
+#pragma unroll
+                        for (int m = 0; m < MB; ++m) {
+                            u32x4_t xp[PARTS];
+                            x[m].parts(d, xp);
+#pragma unroll
+                            for (int q = 0; q < PARTS; ++q) {
+                                const bf16x8_t xf = __builtin_bit_cast(bf16x8_t, xp[q]);
+                                xs[q][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf, xs[q][m], 0, 0, 0);
+#pragma unroll
+                                for (int b = 0; b < NB; ++b)
+                                    part[q][b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[b], xf, part[q][b][m], 0, 0, 0);
+                            }
+                        }
+                        if constexpr (DOWN != 0) __builtin_amdgcn_sched_barrier(0);   // rare: in few registers
                     }
-                // one group's products at a time: all of a block's together would not fit the registers
-                if constexpr (GROUPS > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float z = -(float)((zero[gr][b] >> (8 * q)) & 255u);
+#pragma unroll
+                            for (int m = 0; m < MB; ++m) {
+                                float t = __builtin_fmaf(z, xs[0][m][q], part[0][b][m][q]);
+                                if constexpr (PARTS == 3) {
+                                    const float t1 = __builtin_fmaf(z, xs[1][m][q], part[1][b][m][q]);
+                                    const float t2 = __builtin_fmaf(z, xs[2][m][q], part[2][b][m][q]);
+                                    t += __builtin_fmaf(t2, 0x1p-16f, t1 * 0x1p-8f);
+                                }
+                                acc[b][m][q] = __builtin_fmaf(scale[gr][b][q], t, acc[b][m][q]);
+                            }
+                        }
+                    // one group's products at a time: all of a block's together would not fit the registers
+                    if constexpr (GROUPS > 1) __builtin_amdgcn_sched_barrier(0);
+                }
             }
-        }
+        };
+        f32x4_t acc[NB][MB];
+        sum_blocks(acc, std::integral_constant<int, 0>());
+        float lost = 0.0f;                                 // NaN where a sum is not finite
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int m = 0; m < MB; ++m) sums[wave][b][m][lane] = acc[b][m];
+            for (int m = 0; m < MB; ++m) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) lost = __builtin_fmaf(acc[b][m][q], 0.0f, lost);
+                sums[wave][b][m][lane] = acc[b][m];
+            }
+        // The sums of (16 + q) x and (16 + zero) x reach 31 * 128 < 2^12 times the largest |x|.
+        // Where that passes the largest float they leave Inf or NaN, though the product may be
+        // neither: such a wave takes its blocks again, the weights times 2^-12, for the sums that
+        // were lost.
+        if (__builtin_expect(__any(lost != lost), 0)) {
+            sum_blocks(acc, std::integral_constant<int, 12>());
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    f32x4_t v = sums[wave][b][m][lane];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = is_finite(v[q]) ? v[q] : acc[b][m][q] * 0x1p12f;
+                    sums[wave][b][m][lane] = v;
+                }
+        }
         __syncthreads();
         const T *const bias = g.bias != nullptr ? (const T *)g.bias + e * w.N : nullptr;
         auto total = [&](int b, int n, int m) {            // row n of tile b, row m of X

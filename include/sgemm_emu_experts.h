@@ -124,8 +124,8 @@ int sgemm_emu_quant4_unpack(int dtype, int64_t n, int64_t N, int64_t K, int64_t 
 /*
  * sgemm_emu_quant4_linear -- sgemm_emu_expert_linear with such weights.  offsets NULL:
  *   one layer (n = 1) on all P rows.  Few rows read the packed weights and sum
- *   (q - zero) x in FP32, scaled group by group (an Inf in a row of X makes that
- *   row's outputs NaN); more rows (ws_bytes > 0) unpack the weights into ws first,
+ *   (q - zero) x in FP32, scaled group by group, for finite X of any size (an Inf in
+ *   a row of X makes that row's outputs NaN); more rows (ws_bytes > 0) unpack the weights into ws first,
  *   rounded to the call's type.
  */
 int64_t sgemm_emu_quant4_linear_workspace(int dtype, int64_t P, int64_t N, int64_t K, int64_t n, int64_t group,
