@@ -12,6 +12,7 @@ served, not trained.  The calls are those of include/sgemm_emu_experts.h.
 import torch
 
 from . import ops
+from .adapters import AdapterLinear
 from .experts import (ExpertFeedForward, check_order, combine_tokens, experts_lib, gate_code, gather_tokens,
                       sort_tokens, value_type)
 from .ops import DTYPES, addr, check_tensor, forward_mode, ok, rows_of, scratch, stream_of
@@ -171,7 +172,12 @@ class Quant4Linear(_Held):
 
     @classmethod
     def from_linear(cls, layer, group=128, symmetric=False):
-        """From a torch.nn.Linear, or this package's Linear or GatedLinear (its gate with it)."""
+        """From a torch.nn.Linear, or this package's Linear or GatedLinear (its gate with it).  Layers that compute
+        more, by a fused activation or adapters, are refused."""
+        if getattr(layer, "activation", None) is not None:
+            raise ValueError(f"layer: its activation {layer.activation!r} would be lost; apply it to the served layer's output")
+        if isinstance(layer, AdapterLinear):
+            raise ValueError("layer: its adapters would be lost; quantize its weight alone")
         return cls(quantize(layer.weight, group, symmetric), layer.bias, getattr(layer, "gate", None))
 
     @property
