@@ -150,7 +150,7 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
         rows = row_tiles.total;
         tiles = rows * g.tiles_n;
     }
-    int index = QUARTER ? (int)blockIdx.x >> 2 : (int)blockIdx.x;
+    int index = QUARTER ? (int)blockIdx.x >> 2 : workgroup();
     if constexpr (PART == ALL) {
         if (index >= tiles) return;
         if constexpr (OP != kBackW) index = xcd_order(index, tiles);
@@ -364,8 +364,8 @@ hipError_t launch_part(ExpertProduct g, hipStream_t stream)
     const int64_t segments = g.n + 1, rows = OP == kBackW ? weight_chunks(g) * g.tiles_m : g.P / BM + (segments < g.P ? segments : g.P);
     int64_t blocks = rows * g.tiles_n;
     if (PART == REST) blocks = 4 * (g.num_cus / 2 < blocks ? g.num_cus / 2 : blocks);
-    if (blocks * T::NT >= (int64_t)1 << 32) return hipErrorInvalidValue;   // more work-items than a launch can have
-    hipLaunchKernelGGL((expert_bf16_kernel<T, OP, GATE, PART>), dim3((unsigned)blocks), dim3(T::NT), 0, stream, g);
+    if (!grid_ok(blocks)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((expert_bf16_kernel<T, OP, GATE, PART>), grid_of(blocks), dim3(T::NT), 0, stream, g);
     return hipGetLastError();
 }
 

@@ -22,6 +22,9 @@ __device__ __forceinline__ int64_t expert_end(const int32_t *offsets, int64_t e,
     return v < s ? s : v;
 }
 
+// This workgroup's number in a grid of grid_of(), whose last ones may lie past `blocks`.
+__device__ __forceinline__ int workgroup() { return (int)(blockIdx.y * kGridX + blockIdx.x); }
+
 // Row tiles of BM rows, counted through the segments 0 .. segments - 1.
 struct RowTile {
     int segment;             // -1: there is no such tile

@@ -69,8 +69,9 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
     int chunk = 0;
     if constexpr (OP == kBackW) {
         const int per = g.tiles_m * g.tiles_n;
-        chunk = (int)blockIdx.x / per;
-        tile_at(xcd_order((int)blockIdx.x - chunk * per, per), g.tiles_m, g.tiles_n, imin(g.tiles_m, 8), tm, tn);
+        chunk = workgroup() / per;
+        if (chunk >= weight_chunks(g)) return;
+        tile_at(xcd_order(workgroup() - chunk * per, per), g.tiles_m, g.tiles_n, imin(g.tiles_m, 8), tm, tn);
         m0 = (int64_t)tm * TL::BM;
         m_end = g.M;
         const RowTile r = weight_rows(g, chunk, lane);
@@ -81,8 +82,8 @@ __global__ __launch_bounds__(TL::NT, TL::PER_CU) void expert_f32_kernel(ExpertPr
     } else {
         RowTiles<TL::BM> row_tiles(g.offsets, g.n, g.P, (int)g.n + 1, lane);
         const int rows = row_tiles.total, tiles = rows * g.tiles_n;
-        if ((int)blockIdx.x >= tiles) return;
-        tile_at(xcd_order((int)blockIdx.x, tiles), rows, g.tiles_n, imin(rows, 8), tm, tn);
+        if (workgroup() >= tiles) return;
+        tile_at(xcd_order(workgroup(), tiles), rows, g.tiles_n, imin(rows, 8), tm, tn);
         const RowTile r = row_tiles.find(tm);
         if (r.segment < 0) return;
         e = r.segment;
@@ -333,8 +334,8 @@ hipError_t launch_tile(ExpertProduct g, hipStream_t stream)
     const int64_t segments = g.n + 1;
     const int64_t rows = OP == kBackW ? weight_chunks(g) * g.tiles_m : g.P / TL::BM + (segments < g.P ? segments : g.P);
     const int64_t blocks = rows * g.tiles_n;
-    if (blocks * TL::NT >= (int64_t)1 << 32) return hipErrorInvalidValue;   // more work-items than a launch can have
-    hipLaunchKernelGGL((expert_f32_kernel<TL, OP, GATE>), dim3((unsigned)blocks), dim3(TL::NT), 0, stream, g);
+    if (!grid_ok(blocks)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((expert_f32_kernel<TL, OP, GATE>), grid_of(blocks), dim3(TL::NT), 0, stream, g);
     return hipGetLastError();
 }
 

@@ -22,9 +22,9 @@ __global__ __launch_bounds__(NT) void expert_few_kernel(ExpertProduct g)
     constexpr int NB = GATED ? 2 : 1, BANDS = sizeof(T) == 4 ? 3 : 1;
     __shared__ __attribute__((aligned(16))) f32x4_t sums[WAVES][NB][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const RowTile t = RowTiles<16>(g.offsets, g.n, g.P, (int)g.n + 1, lane).find((int)blockIdx.x / g.tiles_n);
+    const RowTile t = RowTiles<16>(g.offsets, g.n, g.P, (int)g.n + 1, lane).find(workgroup() / g.tiles_n);
     if (t.segment < 0) return;
-    const int64_t F = GATED ? g.N / 2 : g.N, n0 = (int64_t)((int)blockIdx.x % g.tiles_n) * 16;
+    const int64_t F = GATED ? g.N / 2 : g.N, n0 = (int64_t)(workgroup() % g.tiles_n) * 16;
     const int here = (int)lmin(t.end - t.row, 16);
     T *const C = (T *)g.C;
     if (t.segment >= g.n) {                                // rows of no expert
@@ -138,8 +138,8 @@ hipError_t launch_expert_few(int dtype, const ExpertProduct &args, hipStream_t s
     ExpertProduct g = args;
     g.tiles_n = (int)(((g.gate >= 0 ? g.N / 2 : g.N) + 15) / 16);
     const int64_t blocks = row_tiles(g) * g.tiles_n;
-    if (blocks * NT >= (int64_t)1 << 32) return hipErrorInvalidValue;   // more work-items than a launch can have
-    const dim3 grid((unsigned)blocks);
+    if (!grid_ok(blocks)) return hipErrorInvalidValue;
+    const dim3 grid = grid_of(blocks);
     const bool lies = g.lda % 2 == 0 && g.ldb % 2 == 0 && g.bank % 2 == 0 && aligned(g.A, 4) && aligned(g.B, 4) &&
                       (g.gate < 0 || (g.N / 2 * g.ldb) % 2 == 0);
     if (dtype == kF32) launch<float, true>(g, grid, stream);

@@ -66,8 +66,9 @@ __global__ __launch_bounds__(TL::NT) void expert_kernel(ExpertProduct g)
     int tm, tn;
     if constexpr (OP == BACK_W) {
         const int per = g.tiles_m * g.tiles_n;
-        const int v = (int)blockIdx.x % per;
-        t.e = (int)blockIdx.x / per;
+        const int v = workgroup() % per;
+        t.e = workgroup() / per;
+        if (t.e >= g.n) return;
         tile_at(xcd_order(v, per), g.tiles_m, g.tiles_n, imin(g.tiles_m, 8), tm, tn);
         t.m0 = (int64_t)tm * TL::BM;
         t.m_end = g.M;
@@ -76,8 +77,8 @@ __global__ __launch_bounds__(TL::NT) void expert_kernel(ExpertProduct g)
     } else {
         RowTiles<TL::BM> row_tiles(g.offsets, g.n, g.P, (int)g.n + 1, lane);
         const int rows = row_tiles.total, tiles = rows * g.tiles_n;
-        if ((int)blockIdx.x >= tiles) return;
-        tile_at(xcd_order((int)blockIdx.x, tiles), rows, g.tiles_n, imin(rows, 8), tm, tn);
+        if (workgroup() >= tiles) return;
+        tile_at(xcd_order(workgroup(), tiles), rows, g.tiles_n, imin(rows, 8), tm, tn);
         const RowTile r = row_tiles.find(tm);
         if (r.segment < 0) return;
         t.e = r.segment;
@@ -204,8 +205,8 @@ hipError_t launch_tile(ExpertProduct g, hipStream_t stream)
         const int64_t segments = g.n + 1;
         blocks = (g.P / TL::BM + (segments < g.P ? segments : g.P)) * g.tiles_n;
     }
-    if (blocks * TL::NT >= (int64_t)1 << 32) return hipErrorInvalidValue;   // more work-items than a launch can have
-    hipLaunchKernelGGL((expert_kernel<TL, OP, GATE>), dim3((unsigned)blocks), dim3(TL::NT), 0, stream, g);
+    if (!grid_ok(blocks)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((expert_kernel<TL, OP, GATE>), grid_of(blocks), dim3(TL::NT), 0, stream, g);
     return hipGetLastError();
 }
 

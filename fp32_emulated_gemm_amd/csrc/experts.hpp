@@ -8,6 +8,15 @@
 
 namespace sgemm_emu_dev {
 
+// A launch holds fewer than 2^32 work-items along x, which many experts beside wide
+// weights pass: workgroups go on along y (expert_device.hpp: workgroup()).
+constexpr int kGridX = 1 << 22;              // of up to 512 work-items
+inline bool grid_ok(int64_t blocks) { return blocks < (int64_t)1 << 31; }
+inline dim3 grid_of(int64_t blocks)
+{
+    return dim3((unsigned)(blocks < kGridX ? blocks : kGridX), (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+
 constexpr int kMaxExperts = 1024;            // SGEMM_EMU_MAX_EXPERTS
 
 // ---------------------------------------------------------------- tokens (route.hip)
