@@ -181,7 +181,8 @@ class _CombineFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, order, weights):
         ctx.order = order
-        ctx.save_for_backward(ys, weights)
+        # rows are read by the weights' gradient alone
+        ctx.save_for_backward(ys if ctx.needs_input_grad[2] else None, weights)
         return _combine(ys, order, weights)
 
     @staticmethod
@@ -189,14 +190,14 @@ class _CombineFn(torch.autograd.Function):
     def backward(ctx, dy):
         (ys, weights), order = ctx.saved_tensors, ctx.order
         L = experts_lib()
-        (ys, yld), (dy, dyld) = rows_of(ys), rows_of(dy)
-        K = ys.shape[1]
-        dys = ys.new_empty((order.rows, K)) if ctx.needs_input_grad[0] else None
-        dw = torch.empty_like(weights) if weights is not None and ctx.needs_input_grad[2] else None
-        ok(L.sgemm_emu_combine_tokens_backward(DTYPES[ys.dtype], order.tokens, order.choices, K, order.experts,
+        (ys, yld), (dy, dyld) = (None, 1) if ys is None else rows_of(ys), rows_of(dy)
+        K = dy.shape[1]
+        dys = dy.new_empty((order.rows, K)) if ctx.needs_input_grad[0] else None
+        dw = None if ys is None else torch.empty_like(weights)
+        ok(L.sgemm_emu_combine_tokens_backward(DTYPES[dy.dtype], order.tokens, order.choices, K, order.experts,
                                                addr(ys), yld, addr(order.offsets), addr(order.places), addr(weights),
                                                addr(dy), dyld, addr(dys), max(K, 1), addr(dw),
-                                               stream_of(ys.get_device())), "sgemm_emu_combine_tokens_backward")
+                                               stream_of(dy.get_device())), "sgemm_emu_combine_tokens_backward")
         return dys, None, dw
 
 
@@ -245,8 +246,10 @@ class _ExpertFn(torch.autograd.Function):
         weight = weight.contiguous()
         bias = None if bias is None else bias.contiguous()
         h, z = _forward(x, xld, weight, bias, gate, order, True)
-        ctx.save_for_backward(x, weight, z)
-        ctx.gate, ctx.order, ctx.has_bias = gate, order, bias is not None
+        # rows are read by the weight's gradient alone, the weight by the rows' alone
+        need_x, need_w, _ = ctx.needs_input_grad[:3]
+        ctx.save_for_backward(x if need_w else None, weight if need_x else None, z)
+        ctx.gate, ctx.order, ctx.has_bias, ctx.dims = gate, order, bias is not None, (*weight.shape, x.shape[0])
         return h
 
     @staticmethod
@@ -257,18 +260,18 @@ class _ExpertFn(torch.autograd.Function):
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
         need_b = need_b and ctx.has_bias
         L = experts_lib()
-        dt = DTYPES[x.dtype]
-        (P, K), (n, N, _) = x.shape, weight.shape
-        (x, xld), (dh, dhld) = rows_of(x), rows_of(dh)
-        dx = x.new_empty((P, K)) if need_x else None
-        dw = torch.empty_like(weight) if need_w else None
-        db = x.new_empty((n, N)) if need_b else None
+        dt = DTYPES[dh.dtype]
+        n, N, K, P = ctx.dims
+        (x, xld), (dh, dhld) = (None, max(K, 1)) if x is None else rows_of(x), rows_of(dh)
+        dx = dh.new_empty((P, K)) if need_x else None
+        dw = dh.new_empty((n, N, K)) if need_w else None
+        db = dh.new_empty((n, N)) if need_b else None
         nws = ok(L.sgemm_emu_expert_linear_backward_workspace(dt, P, N, K, n, gate, need_b),
                  "sgemm_emu_expert_linear_backward_workspace")
-        ws = scratch(nws, x)
+        ws = scratch(nws, dh)
         ok(L.sgemm_emu_expert_linear_backward(dt, P, N, K, n, addr(x), xld, addr(weight), addr(z), gate,
                                               addr(order.offsets), addr(dh), dhld, addr(dx), max(K, 1), addr(dw),
-                                              addr(db), addr(ws), nws, stream_of(x.get_device())),
+                                              addr(db), addr(ws), nws, stream_of(dh.get_device())),
            "sgemm_emu_expert_linear_backward")
         return dx, dw, db, None, None
 
