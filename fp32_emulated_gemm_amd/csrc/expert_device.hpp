@@ -114,30 +114,6 @@ struct RowTiles {
     }
 };
 
-// Eight consecutive elements in registers, `left` of them there (others zero).
-template <class T>
-struct Eight {
-    u32x4_t v[sizeof(T) / 2];
-
-    __device__ __forceinline__ void load(const T *p, int64_t left)
-    {
-        constexpr int V = Elem<T>::VEC;
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = u32x4_t{0, 0, 0, 0};
-        if (left >= 8) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = *reinterpret_cast<const u32x4_any *>(p + i * V);
-        } else if (left > 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < left) {
-                    if constexpr (sizeof(T) == 4) v[e >> 2][e & 3] = __float_as_uint(p[e]);
-                    else v[0][e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
-                }
-        }
-    }
-};
-
 // Rounded to BF16, two at a time; beyond the largest BF16 that, not Inf.
 __device__ __forceinline__ uint32_t pack2_finite(float a, float b)
 {
@@ -157,18 +133,6 @@ __device__ __forceinline__ void split2_nearest(float x, float y, uint32_t &p0, u
     p1 = pack2_finite(t, u);
     const float a = (t - u2f(p1 << 16)) * 256.0f, b = (u - u2f(p1 & 0xFFFF0000u)) * 256.0f;
     p2 = pack2(a, b);                        // exact where finite: 8 significant bits
-}
-
-__device__ __forceinline__ void split8_nearest(const Eight<float> &in, u32x4_t (&p)[3])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t p0, p1, p2;
-        split2_nearest(__uint_as_float(in.v[i >> 1][2 * (i & 1)]), __uint_as_float(in.v[i >> 1][2 * (i & 1) + 1]), p0, p1, p2);
-        p[0][i] = p0;
-        p[1][i] = p1;
-        p[2][i] = p2;
-    }
 }
 
 // 16 bytes of a row in registers, `left` of its elements there (others zero).
