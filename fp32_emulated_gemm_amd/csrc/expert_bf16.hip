@@ -90,8 +90,11 @@ struct Operand {
 // compiler does not know how the transposing reads relate to copies in flight and
 // puts a wait for all of them before each group of reads, half a step too early.
 // Here the steps' own waits (step_barrier) order them.  The wait states are those
-// between a vector write of a scalar register, or a write of m0 (which nothing else
-// in these kernels uses), and its use.
+// between a vector write of a scalar register, or a write of m0, and its use.  m0 is
+// listed so that no value of the compiler's own is kept in it across a copy; its
+// warning is that it saves none there either, which nothing here needs.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_untracked(uint32_t lds, const uint16_t *at, uint32_t off)
 {
     const uint64_t p = (uint64_t)(uintptr_t)at;
@@ -100,8 +103,9 @@ __device__ __forceinline__ void copy_untracked(uint32_t lds, const uint16_t *at,
     asm volatile("s_mov_b32 m0, %0\n\t"
                  "s_nop 4\n\t"
                  "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(r)
-                 : "memory");
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Which of a product's 256 x 256 tiles a launch covers: ALL (tiles of any size);
 // WHOLE, all of them or, where the last round would fill less than half of the CUs,
