@@ -87,3 +87,25 @@ def test_infinities_stay_in_their_rows(dtype, P, bad):
     assert bool(got[P // 2].isnan().all())
     rest = torch.arange(P, device="cuda") != P // 2
     assert bool(want.isfinite().all()) and torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("P", [1, 8, 40])
+def test_the_last_expert_of_a_bank_past_32_bits(dtype, group, P):
+    """Values, scales and zeros of more than 2^32 bytes of packed weights, at the derived bounds."""
+    from fp32_emulated_gemm_amd.experts import sort_tokens
+    from fp32_emulated_gemm_amd.quant4 import pack, quant4_linear
+    n, N, K, rows = 72, 10240, 12288, 16
+    q, scale, zero = _weights(1, rows, K, group, True, P)
+    full = torch.zeros(n, N, K, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(n, N, K // group, device="cuda")
+    zeros = torch.zeros(n, N, K // group, dtype=torch.uint8, device="cuda")
+    full[-1, -rows:], scales[-1, -rows:], zeros[-1, -rows:] = q[0].cuda(), scale[0].cuda(), zero[0].cuda()
+    w4 = pack(full, scales, zeros, group)
+    assert w4.packed.numel() > 1 << 32
+    del full, scales, zeros
+    x = torch.randn(P, K, generator=torch.Generator().manual_seed(P)).to(xr.DT[dtype])
+    y = quant4_linear(x.cuda(), w4, order=sort_tokens(torch.full((P,), n - 1, dtype=torch.int32, device="cuda"), n))
+    assert not bool(y[:, :-rows].any())
+    ref.check(y[:, -rows:], xr.quant4(x, q, scale, zero, group, torch.tensor([0, P]), None, None, True), "y")
