@@ -64,6 +64,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(Quant4 w, const T *W, uin
         } else {
             s = fmaxf(hi, -lo) * (1.0f / 7.0f);
         }
+        // no level past the largest BF16, which the weights may be rounded to
+        s = fminf(s, 3.38953139e38f / (zero != nullptr ? fmaxf(z, 15.0f - z) : 7.0f));
         if (!finite) s = __builtin_nanf("");
         const float most = zero != nullptr ? 15.0f - z : 7.0f, least = zero != nullptr ? -z : -7.0f;
 #pragma unroll

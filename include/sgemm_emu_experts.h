@@ -106,7 +106,7 @@ int sgemm_emu_expert_linear_backward(int dtype, int64_t P, int64_t N, int64_t K,
  *   zero NULL: symmetric, scale = max|w| / 7 and q - 8 in -7..7; else scale =
  *   (max(w, 0) - min(w, 0)) / 15, zero = -min / scale rounded.  Groups of zeros take
  *   scale 0, groups with a NaN or an Inf stand for NaN.  Values are rounded to
- *   nearest, ties to even.
+ *   nearest, ties to even.  No level passes the largest BF16: scales end there.
  * sgemm_emu_quant4_pack -- lays them out for sgemm_emu_quant4_linear: `packed` of
  *   sgemm_emu_quant4_bytes bytes, 16-byte aligned.  q's high four bits are ignored,
  *   and so are zero's.

@@ -109,3 +109,31 @@ def test_the_last_expert_of_a_bank_past_32_bits(dtype, group, P):
     y = quant4_linear(x.cuda(), w4, order=sort_tokens(torch.full((P,), n - 1, dtype=torch.int32, device="cuda"), n))
     assert not bool(y[:, :-rows].any())
     ref.check(y[:, -rows:], xr.quant4(x, q, scale, zero, group, torch.tensor([0, P]), None, None, True), "y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("symmetric", [True, False])
+def test_the_largest_weights_stay_finite(dtype, symmetric):
+    """Groups up to the largest float stand for finite weights, in both types, a step off at most."""
+    from fp32_emulated_gemm_amd.quant4 import pack, quantize_values
+    most = float(torch.finfo(xr.DT[dtype]).max)
+    w = torch.randn(6, 256, generator=torch.Generator().manual_seed(1)).double()
+    w = w / w.abs().amax(1, keepdim=True) * most
+    w[0], w[1, ::2], w[1, 1::2] = most, most, -most
+    w[2], w[3] = -most, w[3].abs()
+    w[4, :] = torch.where(torch.arange(256) % 32 == 0, -most / 64, most)
+    w = w.clamp(-most, most).to(xr.DT[dtype])
+    q, scale, zero = quantize_values(w.cuda(), 32, symmetric)
+    w4 = pack(q, scale, zero, 32)
+    assert bool(scale.isfinite().all())
+    for out in (torch.float32, torch.bfloat16):
+        got = w4.dequantize(out)
+        assert bool(got.isfinite().all())
+        # half a step, another half where the zero point is rounded, and what the limited scale s leaves out:
+        # the levels end at m s = B, the largest bfloat16, m = max(z, 15 - z) from 8 to 15, the weights at
+        # B (1 + 2^-8), m 2^-8 s further; the scale without the limit is at most z (1 + 2^-8) / (z - 1/2) s,
+        # so that the other end lies at most 7.5 8 / 7.5 (1 + 2^-8) - 7 < 1 + 15 2^-8 steps off (z = 8).
+        # In bfloat16 the weight's own rounding comes to it.
+        step = scale.double().repeat_interleave(32, 1).cpu()
+        room = step * ((0.5 if symmetric else 1.0) + 15 * 2.0 ** -8) + (2.0 ** -8 * got.double().cpu().abs() if out is torch.bfloat16 else 0)
+        assert bool(((got.double().cpu() - w.double()).abs() <= room).all())
