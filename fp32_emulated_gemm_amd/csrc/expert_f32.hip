@@ -11,8 +11,8 @@
 //
 // One workgroup per output tile, in K steps of 32.  A step's operands are loaded two
 // steps ahead, and split and written to the other LDS buffer among the MFMAs of the
-// step before: the split costs about as much as the MFMAs (8192 elements, 48 MFMAs a
-// wave), so neither may wait for the other.  Loads go through descriptors that end with the
+// step before: vector instructions, the split's for the most part, take 1.25 times the
+// MFMAs' cycles (dX below), so neither may wait for the other.  Loads go through descriptors that end with the
 // last element, so nothing is read behind it, whatever K and the alignment; where K
 // ends inside a step, what a row's pieces hold behind it is cleared.
 //
@@ -22,8 +22,9 @@
 //
 // What bounds it is the split beside the MFMAs: 2048^3 in one expert runs at 146 TFLOP/s
 // (the platform's FP32 product: 124; 154 at 8192^3).  12288 x 256 -> 1024 over eight
-// experts, gated, with Z: 84 us; dX 65, dW 64 and 11 for its pieces' sums: eight K steps
-// of a tile do not hide its start and end.
+// experts, gated, with Z: 85 us; dX 66, dW 67 and 11 for its pieces' sums.  There vector
+// instructions and MFMAs take 29 and 23 % of the SIMDs' cycles in dX, 35 and 18 % in the
+// forward pass (its gate and Z besides), and waves wait in a quarter to a third of theirs.
 #include <type_traits>
 
 #include "expert_stage.hpp"

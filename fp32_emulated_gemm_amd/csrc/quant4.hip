@@ -16,10 +16,13 @@
 // FP32's 24 bits (128 + q, one shift less, would cost five).  FP32 rows of X come in
 // three BF16 parts; a weight is one, so three products in three bands.
 //
-// Few rows are bounded by the loads' latency, then by the weights' bytes: one bfloat16
-// row of 4096 x 4096 takes 6 us (9 MB); 64 rows over 64 experts of 2816 x 2048, gated,
-// 34 us, 123 MB at 3.7 TB/s; 16 float32 rows of 8192 x 1024 in groups of 32 9 us.
-// Unpacking 4096 x 4096 to bfloat16 takes 13 us, 42 MB at 3.3 TB/s.
+// One bfloat16 row of 4096 x 4096 takes 6.4 us (9 MB), bounded by the loads' latency;
+// 64 rows over 64 experts of 2816 x 2048, gated, 34.6 us, 123 MB at 3.6 TB/s: vector
+// instructions (widening, scales, sums) issue in half of the SIMDs' cycles, MFMAs in a
+// twelfth, and waves wait in 37 % of theirs; 16 float32 rows of 8192 x 1024 in groups of
+// 32 9.0 us, each wave splitting its rows anew.  Unpacking 4096 x 4096 to bfloat16 takes
+// 12.6 us, 42 MB at 3.3 TB/s, a bank of 64 of 2816 x 2048 174, 5.3 TB/s.  Quantising that
+// bank takes 728 us, packing 659: once a weight, element by element.
 #include <type_traits>
 
 #include "expert_rows.hpp"
@@ -130,6 +133,12 @@ __global__ __launch_bounds__(256) void pack_scales_kernel(Quant4 w, const float 
 // A wave takes 16 rows by 128 columns: a tile in one contiguous read, its rows out
 // through LDS in whole pieces (a lane's own dwords belong to places 64 bytes apart:
 // stored one by one, 4096 x 4096 took 83 us).
+//
+// In bfloat16 the weight (q - zero) scale is rounded to its 8 bits here, as the operand of
+// a bfloat16 product, where the calls of few rows keep it exact: 2047 rows of 4096 x 4096
+// have a relative error of 0.00235 against 0.00166 of the output's rounding alone.  Two
+// parts (16 bits) reach 0.00166 too, but make the product two: 121 us for 66, and 100 for
+// 56 of 512 rows of 11008 x 4096.  float32 calls round once, to 24 bits.
 template <class T>
 __global__ __launch_bounds__(256) void unpack_kernel(Quant4 w, const void *packed, T *W)
 {
@@ -463,6 +472,14 @@ hipError_t launch_quant4_unpack(int dtype, const Quant4 &w, const void *packed, 
 // groups: 128 rows of 4096 x 4096 take 50 to 57 us, unpacked 130; of 11008 x 4096 184 to
 // 207, unpacked 232.  With groups of 32, 64 rows of those take 41 and 135, unpacked 105
 // and 193, and twice the rows twice as long.
+//
+// A bank's with its rows spread evenly, packed and unpacked (groups of 128): 1024 rows over
+// 64 experts of 2816 x 2048, gated, 85 and 359 us in bfloat16, 138 and 978 in float32; 128
+// over eight of those 16 and 42, 25 and 87; 4096 over 256 of 1024 x 512 76 and 154, 95 and
+// 432.  With nine rows in ten on one expert, whose workgroups then take their rows one pass
+// of W after the other, packing gains up to about 8 n rows (512 over the 64: 151 and 281) and
+// loses beyond: 302 and 343, but 208 and 57 over 64 of 1024 x 1024, 679 and 160 over the 256.
+// The host does not know which it is.
 bool quant4_few(int dtype, const Quant4 &w, int64_t P)
 {
     const int64_t most = dtype == kF32 && w.group >= 64 ? 2 * kFewRows : kFewRows;

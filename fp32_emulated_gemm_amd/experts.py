@@ -292,7 +292,8 @@ def expert_linear(x, weight, order, bias=None, gate=None):
     """On the rows of expert e (order.offsets): x weight[e]^T + bias[e], or with a gate ("silu", "gelu",
     "gelu_tanh", "sigmoid", "relu") act(x Wg^T + bg) * (x Wu^T + bu), weight[e] = [Wg; Wu]; zeros on rows of
     no expert.  x [T k, K] sorted (gather_tokens), weight [n, N, K], bias [n, N] or None, all float32 or all
-    bfloat16 on the current HIP device.  Differentiable in x, weight and bias, in reverse mode."""
+    bfloat16 on the current HIP device.  Differentiable in x, weight and bias, in reverse mode; of a bfloat16 gate,
+    the gradients of x and weight are products of its pre-activations' gradient rounded to bfloat16."""
     if not _fits(x, order, getattr(order, "rows", None)):
         check_order(order)
         check_tensor(x, "x", value_type(x, "x"), (order.rows, None))

@@ -5,9 +5,11 @@
     y = quant4_linear(x, w4, bias)              # x [..., K]
     h = quant4_linear(xs, w4, gate="silu", order=order)     # experts, on sorted rows
 
-A few rows (single tokens) read the packed weights in one pass and sum (q - zero) x
-in 32 bits; longer calls unpack them first.  Forward only: weights of 4 bits are
-served, not trained.  The calls are those of include/sgemm_emu_experts.h.
+A few rows (single tokens: up to 64, float32 with groups of 64 or 128 up to 128, or 16 an
+expert) read the packed weights in one pass and sum (q - zero) x in 32 bits.  Longer calls
+unpack them first, rounded to the rows' type: in bfloat16 the weight then has 8 bits, and the
+outputs' relative error is 0.0024 where it is 0.0017 with few rows.  Forward only: weights of
+4 bits are served, not trained.  The calls are those of include/sgemm_emu_experts.h.
 """
 import torch
 
@@ -100,7 +102,8 @@ def quantize(weight, group=128, symmetric=False):
 def quant4_linear(x, weight, bias=None, gate=None, order=None):
     """x W^T + bias, or with a gate act(x Wg^T + bg) * (x Wu^T + bu), W = [Wg; Wu] the Quant4Weight `weight`.
     Without `order`: x [..., K], weight [N, K], bias [N].  With it (sort_tokens): x [T k, K] sorted, weight
-    [n, N, K], bias [n, N], as in experts.expert_linear.  x and bias float32 or bfloat16.  Forward only."""
+    [n, N, K], bias [n, N], as in experts.expert_linear.  x and bias float32 or bfloat16; with more rows than
+    read the packed weight, W is rounded to that type.  Forward only."""
     if not isinstance(weight, Quant4Weight):
         raise TypeError(f"weight: expected a Quant4Weight (of quantize or pack), got {type(weight).__name__}")
     dt = value_type(x, "x")
