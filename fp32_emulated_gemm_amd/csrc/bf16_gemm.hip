@@ -38,17 +38,12 @@ namespace {
 
 enum { EPI_PLAIN = 0, EPI_GATED = 1, EPI_ADAPTER = 2, EPI_PARTIAL = 3 };
 
-// Row of B behind tile row c (see the file's head): block c / 16 is gate rows
-// for an even block, up rows for an odd one.
+// Row of B behind tile row c (see the file's head).
 template <int EPI>
 __device__ __forceinline__ int64_t b_row(const Bf16Gemm &g, int64_t n0, int c)
 {
-    if constexpr (EPI == EPI_GATED) {
-        const int64_t F = g.N >> 1, f = lmin((n0 >> 1) + ((c >> 5) << 4) + (c & 15), F - 1);
-        return (c & 16) ? F + f : f;
-    } else {
-        return lmin(n0 + c, g.N - 1);
-    }
+    if constexpr (EPI == EPI_GATED) return gated_row(g.N >> 1, n0, c);
+    else return lmin(n0 + c, g.N - 1);
 }
 
 // The accumulators' start: the adapters' part, up[i][n][:] . S[m][:] for the

@@ -118,18 +118,6 @@ __device__ __forceinline__ int whole_rounds(int tiles, int slots)
     return 2 * rest > slots ? tiles : tiles - rest;
 }
 
-// Rows of B behind tile row c of a gated product: see b_row in bf16_gemm.hip.
-template <bool GATED>
-__device__ __forceinline__ int64_t bank_row(int64_t N, int64_t n0, int c)
-{
-    if constexpr (GATED) {
-        const int64_t F = N >> 1, f = lmin((n0 >> 1) + ((c >> 5) << 4) + (c & 15), F - 1);
-        return (c & 16) ? F + f : f;
-    } else {
-        return lmin(n0 + c, N - 1);
-    }
-}
-
 template <class T, int OP, int GATE, int PART>
 __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertProduct g)
 {
@@ -202,7 +190,7 @@ __global__ __launch_bounds__(T::NT, T::PER_CU) void expert_bf16_kernel(ExpertPro
     if constexpr (A_KM) oa.columns(g.lda, m0, g.M, wave, lane);
     else oa.rows(A, g.lda, klast, wave, lane, [&](int c) { return lmin(m0 + c, m_end - 1); });
     if constexpr (B_KM) ob.columns(g.ldb, n0, g.N, wave, lane);
-    else ob.rows(B, g.ldb, klast, wave, lane, [&](int c) { return bank_row<GATED>(g.N, n0, c); });
+    else ob.rows(B, g.ldb, klast, wave, lane, [&](int c) { return GATED ? gated_row(g.N >> 1, n0, c) : lmin(n0 + c, g.N - 1); });
 
     // One copy of 1 KB: by a lane's offset from `at`, `soff` bytes further.
     auto copy = [&](uint16_t *buf, int q, const uint16_t *at, uint32_t off, int soff) {

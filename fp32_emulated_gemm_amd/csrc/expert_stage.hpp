@@ -87,14 +87,6 @@ __device__ __forceinline__ void put_piece(uint16_t *buf, int at, const u32x4_t &
     }
 }
 
-// Row of the bank behind tile column c of a gated forward product: alternating
-// blocks of 16 gate and 16 up rows, so that both of an output meet in one lane.
-__device__ __forceinline__ int64_t gated_row(int64_t F, int64_t n0, int c)
-{
-    const int64_t f = lmin((n0 >> 1) + ((c >> 5) << 4) + (c & 15), F - 1);
-    return (c & 16) ? F + f : f;
-}
-
 // Four results, columns n.. of a row, `left` of them there.
 template <class T>
 __device__ __forceinline__ void store4(T *p, const float (&f)[4], int64_t left)

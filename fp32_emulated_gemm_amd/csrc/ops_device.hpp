@@ -40,6 +40,15 @@ struct Elem<uint16_t> {
     static __device__ __forceinline__ uint16_t store(float v) { return f2bf(v); }
 };
 
+// Row of a gated weight (F gate rows, then F up rows) behind row n0 + c of a product's
+// tile: alternating blocks of 16 gate and 16 up rows, so that both of an output meet in
+// one lane.  Rows past the last are the last.
+__device__ __forceinline__ int64_t gated_row(int64_t F, int64_t n0, int c)
+{
+    const int64_t f = lmin((n0 >> 1) + ((c >> 5) << 4) + (c & 15), F - 1);
+    return (c & 16) ? F + f : f;
+}
+
 // 1 / (1 + exp(-z)) on the hardware's exp2 and reciprocal (1 ulp each): the
 // rounding of z log2(e) leaves |z| 2^-24 or so of relative error.
 __device__ __forceinline__ float sigmoidf(float z)
