@@ -73,8 +73,9 @@ int sgemm_emu_combine_tokens_backward(int dtype, int64_t T, int64_t k, int64_t K
  *   X: P x K; W: n x N x K contiguous; bias: n x N contiguous or NULL; H: P x N, or
  *   P x F with a gate.  FP32: the six leading products of a three-way BF16 split to
  *   nearest (what is left out is at most 2^-24 of a product, an FP32 product's own
- *   rounding), summed in FP32; an Inf or NaN makes the outputs that it reaches, of
- *   its row or expert only, Inf or NaN.
+ *   rounding), summed in FP32 (in three bands, which hold at most 2.01 times the sum of
+ *   |x w|: outputs where it passes 2^126 may be Inf or NaN); an Inf or NaN makes the outputs
+ *   that it reaches, of its row or expert only, Inf or NaN.
  *   Zkeep: NULL, or with a gate P rows of 2 pad8(F) floats as in
  *   sgemm_emu_gated_linear, for the backward.
  */
